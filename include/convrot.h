@@ -57,6 +57,9 @@ extern "C" {
 
 #define CONVROT_BLOCK 256          /* rotation block (ConvRot256)           */
 #define CONVROT_MAX_KP 65536       /* largest padded K accepted             */
+#define CONVROT_MAX_HEAD 1024      /* largest head width (qk_norm_rope)     */
+#define CONVROT_MAX_AXES 4         /* most position axes (qk_norm_rope)     */
+#define CONVROT_FEW_TOKENS 64      /* most rows with S8 codes (gemm_fused)  */
 
 typedef enum {
     CONVROT_OK = 0,
@@ -70,6 +73,14 @@ typedef enum {
 typedef enum { CONVROT_BF16 = 0, CONVROT_FP16 = 1, CONVROT_FP32 = 2 } convrot_dtype;
 
 typedef enum { CONVROT_CODES_S8 = 0, CONVROT_CODES_F16 = 1 } convrot_codes;
+
+typedef enum {
+    CONVROT_ACT_NONE = 0,
+    CONVROT_ACT_RELU = 1,
+    CONVROT_ACT_SILU = 2,          /* x / (1 + exp(-x))                              */
+    CONVROT_ACT_GELU = 3,          /* x/2 (1 + erf(x / sqrt 2))                      */
+    CONVROT_ACT_GELU_TANH = 4      /* x/2 (1 + tanh(sqrt(2/pi) (x + 0.044715 x^3)))  */
+} convrot_act;
 
 /* K rounded up to a multiple of CONVROT_BLOCK; 0 for K <= 0. */
 int convrot_padded_k(int K);
@@ -200,6 +211,131 @@ int convrot_gemm(const void* a_q, int64_t ld_aq, const float* a_scale,
                  const float* bias, int M, int N, int K_p,
                  void* out, convrot_dtype out_dtype, int64_t ld_out,
                  cudaStream_t stream);
+
+/*
+ * The operators around the layer's linear products in a video DiT block: the
+ * norm before one (convrot_rms_norm_quant), the per-head norm and rotary
+ * positions of q and k after the qkv product (convrot_qk_norm_rope), and the
+ * product with its bias, activation, gate and residual (convrot_gemm_fused).
+ * The conventions at the top of this file hold for them; like the layer's
+ * calls they only enqueue kernels and can be captured in a CUDA graph (after
+ * one eager call of the same kind on the device).
+ */
+
+/*
+ * Residual addition, RMS norm, ConvRot256 rotation and row-scaled S8
+ * quantisation of token rows, in one pass:
+ *
+ *     h = round(x + residual)                  (h = x without a residual)
+ *     u = h * weight / sqrt(mean_k(h^2) + eps)
+ *     codes, scale = convrot_quant_act of u, without rounding u
+ *
+ *   x       [M][ld_x] in `dtype` (BF16 / FP16 / FP32), ld_x >= K.
+ *   residual  NULL, or [M][ld_residual] in `dtype`, ld_residual >= K.  The sum
+ *           is rounded to `dtype` before the norm sees it, so that the codes
+ *           are those of the stored stream.
+ *   h       NULL, or [M][ld_h] in `dtype`: receives h (columns 0..K-1).  It
+ *           may be x or residual itself (same pointer and pitch), not overlap
+ *           them otherwise.
+ *   weight  NULL (ones), or [K] FP32 (16-byte aligned).
+ *   eps     > 0 and finite.
+ *   a_q, fmt, ld_aq, a_scale, a_norm   as for convrot_quant_act.
+ *
+ * The sum of squares and all arithmetic are FP32.  A row of zeros gives zero
+ * codes and scale 0.  A row that holds an Inf or NaN, or whose sum of squares
+ * leaves FP32's range (values beyond about 1e17), gets unspecified codes and
+ * scale (h is written all the same).  x, residual and h need only element
+ * alignment; where all their rows start on 16 bytes the vectorised path runs.
+ */
+int convrot_rms_norm_quant(const void* x, convrot_dtype dtype, int64_t ld_x,
+                           const void* residual, int64_t ld_residual,
+                           void* h, int64_t ld_h, const float* weight,
+                           float eps, int M, int K,
+                           void* a_q, convrot_codes fmt, int64_t ld_aq,
+                           float* a_scale, float* a_norm, cudaStream_t stream);
+
+/*
+ * Rotation frequencies (host helper): for every axis a with axis_pairs[a]
+ * pairs, theta^(-j / axis_pairs[a]) for j = 0 .. axis_pairs[a] - 1, the axes
+ * one after another, into the HOST array inv_freq [sum of axis_pairs].
+ * theta > 0 and finite; 1 <= naxes <= CONVROT_MAX_AXES.
+ */
+int convrot_rope_inv_freq(const int* axis_pairs, int naxes, double theta,
+                          double* inv_freq);
+
+/*
+ * RMS norm of every head of q and k (optional) and rotary positions with up
+ * to CONVROT_MAX_AXES axes (time, height, width, ...).  For token m and a
+ * head's D values x:
+ *
+ *     u = x * weight / sqrt(mean_d(x^2) + eps)       (u = x without a weight)
+ *     phi_i = pos[m][axis of pair i] * inv_freq[i]   for i < P = sum axis_pairs
+ *     (u_a, u_b) -> (u_a cos phi_i - u_b sin phi_i, u_b cos phi_i + u_a sin phi_i)
+ *
+ * with (a, b) = (i, i + P), or (2i, 2i + 1) if `interleaved`.  The pairs of
+ * axis 0 come first, then those of axis 1, and so on.  Values 2P .. D-1 are
+ * not rotated.  FP32 arithmetic, rounded once to `dtype`; angles are exact to
+ * about 1e-7 radians for every int32 position (negative ones too).
+ *
+ *   q, k    heads_q and heads_k heads of D values (contiguous) per token, in
+ *           `dtype`; the token and head strides (in elements, >= 0) are free,
+ *           so they can be views of the packed qkv output.  heads_k (or
+ *           heads_q) may be 0, its pointers NULL then.
+ *   q_out, k_out   the same layout with strides of their own, whose heads do
+ *           not overlap.  Each may be its input itself (same pointer and
+ *           strides: in place), not overlap any input otherwise.
+ *   q_weight, k_weight   NULL (no norm), or [D] FP32 (4-byte aligned).
+ *   D       1 .. CONVROT_MAX_HEAD; 2P <= D.
+ *   pos     [M][ld_pos] int32 (4-byte aligned), ld_pos >= naxes.
+ *   axis_pairs  HOST array [naxes] of pairs per axis (each >= 0).
+ *   inv_freq  [P] FP64, device (8-byte aligned): radians per unit of position.
+ *   eps     > 0 and finite where a weight is given.
+ */
+int convrot_qk_norm_rope(const void* q, int64_t q_tok, int64_t q_head,
+                         void* q_out, int64_t q_out_tok, int64_t q_out_head,
+                         int heads_q, const float* q_weight,
+                         const void* k, int64_t k_tok, int64_t k_head,
+                         void* k_out, int64_t k_out_tok, int64_t k_out_head,
+                         int heads_k, const float* k_weight,
+                         convrot_dtype dtype, int M, int D,
+                         const int32_t* pos, int64_t ld_pos,
+                         const int* axis_pairs, int naxes,
+                         const double* inv_freq, float eps, int interleaved,
+                         cudaStream_t stream);
+
+/*
+ * The integer product of convrot_gemm with a longer epilogue:
+ *
+ *     y[m, n] = residual[m, n] + gate[n] * act(fp32(acc) * s_a[m] * s_w[n] + bias[n])
+ *
+ * in FP32, rounded once to out_dtype; acc is the exact int32 sum over K_p.
+ * Without activation, gate and residual it equals convrot_gemm bit for bit.
+ *
+ *   a_q, w_q  [M][ld_aq] and [N][ld_wq] codes, both in `fmt`.
+ *           CONVROT_CODES_F16: any M.  CONVROT_CODES_S8 (weights resident at
+ *           one byte per code, for serving a few tokens): M up to
+ *           CONVROT_FEW_TOKENS; for more rows widen the weight's codes once
+ *           (convrot_widen_codes) and pass FP16 codes.
+ *   a_scale [M], w_scale [N] FP32 (w_scale 16-byte aligned).
+ *   bias, gate  NULL, or [N] FP32 (16-byte aligned).
+ *   act     one of convrot_act.
+ *   residual  NULL, or [M][ld_residual] in out_dtype, ld_residual >= N.  It
+ *           may be out itself (same pointer and pitch), not overlap it
+ *           otherwise.
+ *   K_p     a multiple of 256, <= CONVROT_MAX_KP.
+ *   out     [M][ld_out] in out_dtype; ld_out >= N.  Only columns 0..N-1 of
+ *           rows 0..M-1 are written.
+ * Alignment: a_q and w_q 16-byte aligned, ld_aq and ld_wq whole 16-byte
+ * pieces (multiples of 8 F16 or 16 S8 codes); out and residual need only
+ * element alignment.
+ */
+int convrot_gemm_fused(const void* a_q, int64_t ld_aq, const float* a_scale,
+                       const void* w_q, int64_t ld_wq, const float* w_scale,
+                       convrot_codes fmt, const float* bias, convrot_act act,
+                       const float* gate, const void* residual,
+                       int64_t ld_residual, int M, int N, int K_p,
+                       void* out, convrot_dtype out_dtype, int64_t ld_out,
+                       cudaStream_t stream);
 
 /*
  * W8A8 with resident weights: widens S8 codes (CONVROT_CODES_S8, e.g. weight

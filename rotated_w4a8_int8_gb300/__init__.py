@@ -18,15 +18,20 @@ __all__ = [
     "device_error", "ConvRotError", "BF16", "FP16",
     "FP32", "CODES_S8",
     "CODES_F16", "LIB_PATH", "EXPORTS",
+    "rms_norm_quant", "rope_inv_freq", "qk_norm_rope", "gemm_fused",
+    "ACT_NONE", "ACT_RELU", "ACT_SILU", "ACT_GELU", "ACT_GELU_TANH", "FEW_TOKENS",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libconvrot.so")
 BF16, FP16, FP32 = 0, 1, 2
 CODES_S8, CODES_F16 = 0, 1
+ACT_NONE, ACT_RELU, ACT_SILU, ACT_GELU, ACT_GELU_TANH = 0, 1, 2, 3, 4
+FEW_TOKENS = 64          # most token rows gemm_fused takes with int8 codes
 EXPORTS = ("convrot_padded_k", "convrot_status_string", "convrot_prepare_weight",
            "convrot_quant_act", "convrot_gemm", "convrot_gemm_i32", "convrot_device_error",
            "convrot_last_error", "convrot_gemm_timeout_selftest", "convrot_widen_codes", "convrot_int8_mma_probe",
-           "convrot_decode_gemm_probe")
+           "convrot_decode_gemm_probe", "convrot_rms_norm_quant", "convrot_rope_inv_freq", "convrot_qk_norm_rope",
+           "convrot_gemm_fused")
 
 _lib = None
 
@@ -68,6 +73,17 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.convrot_int8_mma_probe.restype = i32
     lib.convrot_decode_gemm_probe.argtypes = [vp, vp, vp, vp, i32, i32, i32, i32, vp, i64, i32, vp, vp]
     lib.convrot_decode_gemm_probe.restype = i32
+    lib.convrot_rms_norm_quant.argtypes = [vp, i32, i64, vp, i64, vp, i64, vp, ctypes.c_float, i32, i32, vp, i32, i64,
+                                           vp, vp, vp]
+    lib.convrot_rms_norm_quant.restype = i32
+    lib.convrot_rope_inv_freq.argtypes = [vp, i32, ctypes.c_double, vp]
+    lib.convrot_rope_inv_freq.restype = i32
+    lib.convrot_qk_norm_rope.argtypes = [vp, i64, i64, vp, i64, i64, i32, vp, vp, i64, i64, vp, i64, i64, i32, vp,
+                                         i32, i32, i32, vp, i64, vp, i32, vp, ctypes.c_float, i32, vp]
+    lib.convrot_qk_norm_rope.restype = i32
+    lib.convrot_gemm_fused.argtypes = [vp, i64, vp, vp, i64, vp, i32, vp, i32, vp, vp, i64, i32, i32, i32, vp, i32,
+                                       i64, vp]
+    lib.convrot_gemm_fused.restype = i32
     lib.convrot_last_error.argtypes = []
     lib.convrot_last_error.restype = ctypes.c_char_p
     lib.convrot_device_error.argtypes = [vp, ctypes.POINTER(i32)]
@@ -125,6 +141,29 @@ def _codes_fmt(t) -> int:
     return {torch.int8: CODES_S8, torch.float16: CODES_F16}[t.dtype]
 
 
+def _matrix(fn: str, name: str, t, rows: int, cols: int, dtype=None) -> None:
+    """A device matrix of at least rows x cols with contiguous rows, of `dtype` where one is asked for."""
+    if t is None:
+        return
+    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] < cols:
+        raise ValueError(f"{fn}: {name} has shape {tuple(t.shape)}, [{rows}, >= {cols}] is needed")
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{fn}: the rows of {name} must be contiguous")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{fn}: {name} is {t.dtype}, {dtype} is needed")
+    if not t.is_cuda:
+        raise ValueError(f"{fn}: {name} must be a CUDA tensor")
+
+
+def _vector(fn: str, name: str, t, n: int, dtype) -> None:
+    """A contiguous device vector of n values of `dtype`, or None."""
+    if t is None:
+        return
+    if t.dim() != 1 or t.shape[0] != n or t.dtype != dtype or not t.is_cuda or (n > 1 and t.stride(0) != 1):
+        raise ValueError(f"{fn}: {name} must be a contiguous {dtype} CUDA vector of {n}, "
+                         f"not {t.dtype} {tuple(t.shape)} on {t.device}")
+
+
 def prepare_weight(w_fp4, w_sf, w_tensor_scale, K: int, w_q, w_scale, w_norm=None, stream=None) -> None:
     """convrot_prepare_weight: w_fp4 uint8 [N, K_s/2], w_sf uint8 [N, K_s/16],
     w_tensor_scale float32 [1], w_q int8 or float16 [N, >=K_p], w_scale float32 [N],
@@ -164,6 +203,86 @@ def gemm_i32(a_q, w_q, acc, K_p: int | None = None, a_norm=None, w_norm=None, st
     _check("convrot_gemm_i32", load_library().convrot_gemm_i32(
         _ptr(a_q), _ld(a_q), _ptr(a_norm), _ptr(w_q), _ld(w_q), _ptr(w_norm), M, N, int(K_p), _ptr(acc),
         _ld(acc), _stream(stream)))
+
+
+def rms_norm_quant(x, K: int, a_q, a_scale, residual=None, h=None, weight=None, eps: float = 1e-6, a_norm=None,
+                   stream=None) -> None:
+    """convrot_rms_norm_quant: x bf16/fp16/fp32 [M, >=K], residual and h None or the same type [M, >=K] (h receives
+    x + residual and may be either of them), weight None or float32 [K], a_q int8 or float16 [M, >=K_p],
+    a_scale float32 [M], a_norm None or float32 [M]."""
+    import torch
+    fn, M, K = "rms_norm_quant", x.shape[0], int(K)
+    _matrix(fn, "x", x, M, K)
+    _matrix(fn, "residual", residual, M, K, x.dtype)
+    _matrix(fn, "h", h, M, K, x.dtype)
+    _matrix(fn, "a_q", a_q, M, padded_k(K))
+    _vector(fn, "a_scale", a_scale, M, torch.float32)
+    _vector(fn, "a_norm", a_norm, M, torch.float32)
+    _vector(fn, "weight", weight, K, torch.float32)
+    _check("convrot_rms_norm_quant", load_library().convrot_rms_norm_quant(
+        _ptr(x), _dtype_code(x), _ld(x), _ptr(residual), 0 if residual is None else _ld(residual),
+        _ptr(h), 0 if h is None else _ld(h), _ptr(weight), float(eps), M, K,
+        _ptr(a_q), _codes_fmt(a_q), _ld(a_q), _ptr(a_scale), _ptr(a_norm), _stream(stream)))
+
+
+def rope_inv_freq(axis_pairs, theta: float = 10000.0) -> list[float]:
+    """convrot_rope_inv_freq: radians per unit of position of every pair, axis after axis (host values; put them in
+    a float64 device tensor for qk_norm_rope)."""
+    out = (ctypes.c_double * max(1, sum(axis_pairs)))()
+    _check("convrot_rope_inv_freq", load_library().convrot_rope_inv_freq(
+        (ctypes.c_int * len(axis_pairs))(*axis_pairs), len(axis_pairs), float(theta), out))
+    return list(out)[:sum(axis_pairs)]
+
+
+def qk_norm_rope(q, k, pos, inv_freq, axis_pairs, q_out, k_out, q_weight=None, k_weight=None, eps: float = 1e-6,
+                 interleaved: bool = False, stream=None) -> None:
+    """convrot_qk_norm_rope: q and k bf16/fp16/fp32 [M, heads, D] views (values of a head contiguous; k and k_out may
+    be None), q_out and k_out of the same shapes and type (may be q and k themselves), pos int32 [M, axes],
+    inv_freq float64 [sum(axis_pairs)], axis_pairs pairs per axis, q_weight / k_weight None or float32 [D]."""
+    import torch
+    fn = "qk_norm_rope"
+    M, heads_q, D = q.shape
+    heads_k = 0 if k is None else k.shape[1]
+    if (k is None) != (k_out is None):
+        raise ValueError(f"{fn}: k and k_out belong together")
+    views = []
+    for name, t, shape in (("q", q, (M, heads_q, D)), ("q_out", q_out, (M, heads_q, D)),
+                           ("k", k, (M, heads_k, D)), ("k_out", k_out, (M, heads_k, D))):
+        if t is None:
+            views += [0, 0, 0]
+            continue
+        if t.shape != shape or t.dtype != q.dtype or not t.is_cuda or (D > 1 and t.stride(2) != 1):
+            raise ValueError(f"{fn}: {name} must be a {q.dtype} CUDA tensor {shape} with contiguous heads")
+        views += [t.data_ptr(), t.stride(0), t.stride(1)]
+    _matrix(fn, "pos", pos, M, len(axis_pairs), torch.int32)
+    _vector(fn, "inv_freq", inv_freq, sum(axis_pairs), torch.float64)
+    _vector(fn, "q_weight", q_weight, D, torch.float32)
+    _vector(fn, "k_weight", k_weight, D, torch.float32)
+    _check("convrot_qk_norm_rope", load_library().convrot_qk_norm_rope(
+        *views[:6], heads_q, _ptr(q_weight), *views[6:], heads_k, _ptr(k_weight), _dtype_code(q), M, D, _ptr(pos),
+        _ld(pos), (ctypes.c_int * len(axis_pairs))(*axis_pairs), len(axis_pairs), _ptr(inv_freq), float(eps),
+        int(bool(interleaved)), _stream(stream)))
+
+
+def gemm_fused(a_q, a_scale, w_q, w_scale, out, K_p: int | None = None, bias=None, act: int = ACT_NONE, gate=None,
+               residual=None, stream=None) -> None:
+    """convrot_gemm_fused: a_q and w_q codes [M, >=K_p] and [N, >=K_p], both float16 or (M <= FEW_TOKENS) both int8,
+    out bf16/fp16/fp32 [M, >=N] = residual + gate * act(dequantised product + bias); bias and gate None or
+    float32 [N], act an ACT_* code, residual None or out's type [M, >=N] (may be out)."""
+    import torch
+    fn, M, N = "gemm_fused", a_q.shape[0], w_q.shape[0]
+    K_p = a_q.shape[1] if K_p is None else int(K_p)
+    _matrix(fn, "a_q", a_q, M, K_p)
+    _matrix(fn, "w_q", w_q, N, K_p, a_q.dtype)
+    _matrix(fn, "out", out, M, N)
+    _matrix(fn, "residual", residual, M, N, out.dtype)
+    _vector(fn, "a_scale", a_scale, M, torch.float32)
+    for name, t in (("w_scale", w_scale), ("bias", bias), ("gate", gate)):
+        _vector(fn, name, t, N, torch.float32)
+    _check("convrot_gemm_fused", load_library().convrot_gemm_fused(
+        _ptr(a_q), _ld(a_q), _ptr(a_scale), _ptr(w_q), _ld(w_q), _ptr(w_scale), _codes_fmt(a_q), _ptr(bias), int(act),
+        _ptr(gate), _ptr(residual), 0 if residual is None else _ld(residual), M, N, K_p, _ptr(out),
+        _dtype_code(out), _ld(out), _stream(stream)))
 
 
 def widen_codes(src, dst, cols: int | None = None, stream=None) -> None:
