@@ -10,6 +10,14 @@
 // and max|z| of the rotated z = (h * weight) H together, and multiplies by r
 // only in the quantiser.  One read of the row, one reduction.
 //
+// Bound by HBM: per element the row, the residual, h and an FP16-held code,
+// 8 bytes with 16-bit storage.  The row's elements are read and h is written
+// in whole coalesced accesses and handed to the rotation through shared
+// memory; a thread's own 32 elements (two sectors of a row per thread) read
+// and written directly took 257 us where this takes 155 us (19989 x 5376,
+// BF16, residual: 82% of the copy bandwidth), and it keeps rows of any
+// alignment coalesced.
+//
 // The sum and the norm's statistics are FP32; h is rounded to the storage
 // type before anything else uses it, so that the codes are those of the
 // stored residual stream.  The rotation, the quantiser and the layout of a
@@ -41,65 +49,151 @@ struct NormArgs {
   float eps, inv_k, half_sqrt_kp;
 };
 
-// Storage word(s) of two values rounded to the type (16-bit types).
-template <int DT>
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-  if constexpr (DT == DT_BF16) {
-    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&v);
-  } else {
-    const __half2 v = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&v);
-  }
-}
+// Access of V neighbouring elements of one storage type as FP32 (V elements
+// are 16 bytes, 4 bytes or one element; the address is aligned to the whole).
+template <int DT, int V>
+struct Chunk {
+  static constexpr int BYTES = V * (DT == DT_FP32 ? 4 : 2);
+  static constexpr int W = BYTES < 4 ? 1 : BYTES / 4;
+  uint32_t w[W];
 
-// a = round(a + b), element by element, in storage words.
-template <int DT>
-__device__ __forceinline__ void add_raw(Raw<DT>& a, const Raw<DT>& b) {
-#pragma unroll
-  for (int i = 0; i < Raw<DT>::N; ++i) {
-    if constexpr (DT == DT_FP32) {
-      a.w[i] = __float_as_uint(__uint_as_float(a.w[i]) + __uint_as_float(b.w[i]));
+  // Plain (coherent) loads: h may be x or the residual, which this kernel then writes.
+  __device__ __forceinline__ void load(const char* p) {
+    if constexpr (BYTES == 16) {
+      const uint4 v = *reinterpret_cast<const uint4*>(p);
+      w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
+    } else if constexpr (BYTES == 4) {
+      w[0] = *reinterpret_cast<const uint32_t*>(p);
     } else {
-      a.w[i] = pack2<DT>(raw_elem<DT>(a, 2 * i) + raw_elem<DT>(b, 2 * i),
-                         raw_elem<DT>(a, 2 * i + 1) + raw_elem<DT>(b, 2 * i + 1));
+      w[0] = *reinterpret_cast<const uint16_t*>(p);
     }
   }
-}
-
-// Stores the elements [c0, c0 + 32) of a row below K.
-template <int DT, int VEC>
-__device__ __forceinline__ void store_raw(char* row, int c0, int K, const Raw<DT>& r) {
-  constexpr int esz = (DT == DT_FP32) ? 4 : 2;
-  if (c0 >= K) return;
-  if (VEC > 0 && c0 + 32 <= K) {
-    uint4* p = reinterpret_cast<uint4*>(row + static_cast<size_t>(c0) * esz);
-#pragma unroll
-    for (int u = 0; u < Raw<DT>::N / 4; ++u) p[u] = make_uint4(r.w[4 * u], r.w[4 * u + 1], r.w[4 * u + 2], r.w[4 * u + 3]);
-    return;
+  __device__ __forceinline__ void store(char* p) const {
+    if constexpr (BYTES == 16) *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    else if constexpr (BYTES == 4) *reinterpret_cast<uint32_t*>(p) = w[0];
+    else *reinterpret_cast<uint16_t*>(p) = static_cast<uint16_t>(w[0]);
   }
-#pragma unroll
-  for (int e = 0; e < 32; ++e) {
-    if (c0 + e >= K) continue;
-    if constexpr (DT == DT_FP32) reinterpret_cast<uint32_t*>(row)[c0 + e] = r.w[e];
-    else reinterpret_cast<uint16_t*>(row)[c0 + e] = static_cast<uint16_t>(r.w[e >> 1] >> (16 * (e & 1)));
+  __device__ __forceinline__ float get(int e) const {
+    if constexpr (DT == DT_FP32) return __uint_as_float(w[e]);
+    else if constexpr (DT == DT_BF16) return __uint_as_float((e & 1) ? (w[e >> 1] & 0xffff0000u) : (w[e >> 1] << 16));
+    else return __half2float(__ushort_as_half(static_cast<unsigned short>((e & 1) ? (w[e >> 1] >> 16) : (w[e >> 1] & 0xffffu))));
   }
-}
-
-// Plain (coherent) loads: h may be x or the residual, which this kernel then
-// writes.
-template <int DT, int VEC>
-__device__ __forceinline__ void load_row_raw(const char* row, int c0, int K, Raw<DT>& r) {
-  if (VEC > 0 && c0 + 32 <= K) {
-    const uint4* p = reinterpret_cast<const uint4*>(row + static_cast<size_t>(c0) * (DT == DT_FP32 ? 4 : 2));
+  // this = round(this + b), element by element
+  __device__ __forceinline__ void add(const Chunk& b) {
+    if constexpr (DT == DT_FP32) {
 #pragma unroll
-    for (int u = 0; u < Raw<DT>::N / 4; ++u) {
-      const uint4 v = p[u];
-      r.w[4 * u] = v.x; r.w[4 * u + 1] = v.y; r.w[4 * u + 2] = v.z; r.w[4 * u + 3] = v.w;
+      for (int i = 0; i < V; ++i) w[i] = __float_as_uint(get(i) + b.get(i));
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; i += 2) {
+        const float lo = get(i) + b.get(i), hi = V > 1 ? get(i + 1) + b.get(i + 1) : 0.f;
+        if constexpr (DT == DT_BF16) {
+          const __nv_bfloat162 t = __floats2bfloat162_rn(lo, hi);
+          w[i >> 1] = *reinterpret_cast<const uint32_t*>(&t);
+        } else {
+          const __half2 t = __floats2half2_rn(lo, hi);
+          w[i >> 1] = *reinterpret_cast<const uint32_t*>(&t);
+        }
+      }
     }
-    return;
   }
-  load_raw<DT, 0>(row, c0, K, r);
+};
+
+// The row's h * weight in shared memory, FP32, one kSlotBytes region per
+// 256-block (the block's transpose buffer, which the rotation reuses): element
+// 32 t + 4 u + j of a block at float 32 t + 4 (u ^ t) + j, so that neither the
+// row-wise writes nor the rotation's reads (thread t reads its 32 elements,
+// 16 bytes at a time) meet bank conflicts.
+__device__ __forceinline__ float* row_slot(char* rows, int e) {
+  const int t = (e >> 5) & 7, u = (e >> 2) & 7;
+  return reinterpret_cast<float*>(rows + (e >> 8) * kSlotBytes) + 32 * t + 4 * (u ^ t) + (e & 3);
+}
+
+// First pass over this CTA's elements [e0, e0 + n): coalesced accesses of V
+// elements whatever the row's alignment; h = round(x + residual) is written,
+// its squares are summed, and h * weight goes to shared memory (zeros at and
+// past K).  Returns this thread's share of the sum of squares.
+template <int DT, bool RES, int V>
+__device__ __forceinline__ float stage_row(const NormArgs& a, int row, int e0, int n, char* rows) {
+  constexpr int64_t es = (DT == DT_FP32) ? 4 : 2;
+  // accesses in flight per thread and operand (with a residual two measured
+  // faster than four: 155.4 against 161.9 us; without one, slower)
+  constexpr int BATCH = V == 1 ? 8 : RES ? 2 : 4;
+  const char* x = a.x + (row * a.ld_x + e0) * es;
+  const char* r = RES ? a.res + (row * a.ld_res + e0) * es : nullptr;
+  char* h = a.h ? a.h + (row * a.ld_h + e0) * es : nullptr;
+  const int left = a.K - e0;                 // elements of the row from e0 on
+  float ss = 0.f;
+  for (int base = threadIdx.x * V; base < n; base += blockDim.x * V * BATCH) {
+    Chunk<DT, V> cx[BATCH], cr[RES ? BATCH : 1];
+#pragma unroll
+    for (int b = 0; b < BATCH; ++b) {
+      const int e = base + b * blockDim.x * V;
+      if (e + V <= left) {
+        cx[b].load(x + e * es);
+        if constexpr (RES) cr[b].load(r + e * es);
+      }
+    }
+#pragma unroll
+    for (int b = 0; b < BATCH; ++b) {
+      const int e = base + b * blockDim.x * V;
+      if (e >= n) break;
+      float v[V];
+      if (e + V <= left) {
+        if constexpr (RES) cx[b].add(cr[b]);
+        if (h) cx[b].store(h + e * es);
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] = cx[b].get(i);
+      } else {
+        // the row's end: element by element, zeros past it
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          v[i] = 0.f;
+          if (e + i < left) {
+            Chunk<DT, 1> c1, r1;
+            c1.load(x + (e + i) * es);
+            if constexpr (RES) {
+              r1.load(r + (e + i) * es);
+              c1.add(r1);
+            }
+            if (h) c1.store(h + (e + i) * es);
+            v[i] = c1.get(0);
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < V; ++i) ss = fmaf(v[i], v[i], ss);
+      if (a.weight) {
+        const float* w = a.weight + e0 + e;
+        if (e + V <= left) {
+          if constexpr (V >= 4) {
+#pragma unroll
+            for (int i = 0; i < V; i += 4) {
+              const float4 f = __ldg(reinterpret_cast<const float4*>(w + i));
+              v[i] *= f.x; v[i + 1] *= f.y; v[i + 2] *= f.z; v[i + 3] *= f.w;
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i) v[i] *= __ldg(w + i);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < V; ++i)
+            if (e + i < left) v[i] *= __ldg(w + i);
+        }
+      }
+      if constexpr (V >= 4) {
+#pragma unroll
+        for (int i = 0; i < V; i += 4)
+          *reinterpret_cast<float4*>(row_slot(rows, e + i)) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+      } else if constexpr (V == 2) {
+        *reinterpret_cast<float2*>(row_slot(rows, e)) = make_float2(v[0], v[1]);
+      } else {
+        *row_slot(rows, e) = v[0];
+      }
+    }
+  }
+  return ss;
 }
 
 // Row reduction of (max|z|, sum h^2, sum z^2) over the CTA (SPLIT == 1) or
@@ -161,44 +255,47 @@ __device__ __forceinline__ void norm_reduce(float amax, float ssh, float ssz, co
   __syncthreads();
 }
 
-template <int DT, bool RES, int VEC, int NBMAX, int SPLIT>
+template <int DT, bool RES, int V, int NBMAX, int SPLIT>
 __global__ void __launch_bounds__(kMaxThreads) norm_quant_kernel(const NormArgs a) {
   extern __shared__ __align__(16) char smem[];
-  float* red = reinterpret_cast<float*>(smem + a.S * kSlotBytes);
+  constexpr int64_t es = (DT == DT_FP32) ? 4 : 2;
   const int slot = threadIdx.x >> 3, lane8 = threadIdx.x & 7;
-  constexpr int64_t esize = (DT == DT_FP32) ? 4 : 2;
   const int row = blockIdx.x / SPLIT, part = blockIdx.x % SPLIT;
   const int nbl = (a.nblocks + SPLIT - 1) / SPLIT;
   const int blk0 = part * nbl, nloc = min(nbl, a.nblocks - blk0);
+  float* red = reinterpret_cast<float*>(smem + nbl * kSlotBytes);
 
-  Raw<DT> hx[NBMAX], hr[RES ? NBMAX : 1];
+  const float ssh = stage_row<DT, RES, V>(a, row, blk0 * kBlock, nloc * kBlock, smem);
+  // this CTA's share of a later row, into L2 (see l2_prefetch)
+  if (const int later = row + a.pf_dist; later < a.M) {
+    const size_t rb = static_cast<size_t>(a.K) * es, share = (rb + SPLIT - 1) / SPLIT;
+    const size_t b0 = part * share, b1 = b0 + share < rb ? b0 + share : rb;
+    l2_prefetch(a.x + later * a.ld_x * es + b0, b1 - b0);
+    if constexpr (RES) l2_prefetch(a.res + later * a.ld_res * es + b0, b1 - b0);
+  }
+  __syncthreads();
+
+  BlockCols c[NBMAX];
+  float amax = 0.f, ssz = 0.f;
 #pragma unroll
   for (int i = 0; i < NBMAX; ++i) {
     const int li = slot + a.S * i;
-    if (slot < a.S && li < nloc) {
-      const int c0 = (blk0 + li) * kBlock + 32 * lane8;
-      load_row_raw<DT, VEC>(a.x + row * a.ld_x * esize, c0, a.K, hx[i]);
-      if constexpr (RES) load_row_raw<DT, VEC>(a.res + row * a.ld_res * esize, c0, a.K, hr[i]);
-    }
-  }
-  BlockCols c[NBMAX];
-  float amax = 0.f, ssh = 0.f, ssz = 0.f;
-#pragma unroll
-  for (int i = 0; i < NBMAX; ++i) {
-    const int li = slot + a.S * i, c0 = (blk0 + li) * kBlock + 32 * lane8;
     const bool active = (slot < a.S) && (li < nloc);
-    float2 P[16];
+    char* mine = smem + (active ? li : 0) * kSlotBytes;
+    float2 P[16];                                  // (element b, element 16 + b) of the thread's 32
     if (active) {
-      if constexpr (RES) add_raw<DT>(hx[i], hr[i]);
-      if (a.h) store_raw<DT, VEC>(a.h + row * a.ld_h * esize, c0, a.K, hx[i]);
-      pairs_from_raw<DT>(hx[i], P);
-      float2 s2 = make_float2(0.f, 0.f);
+      const float4* line = reinterpret_cast<const float4*>(mine) + 8 * lane8;
 #pragma unroll
-      for (int b = 0; b < 16; ++b) s2 = fma2(P[b], P[b], s2);
-      ssh += s2.x + s2.y;
-      if (a.weight) apply_pre_scale(a.weight, c0, a.K, P);
+      for (int u = 0; u < 4; ++u) {
+        const float4 lo = line[u ^ lane8], hi = line[(u + 4) ^ lane8];
+        P[4 * u] = make_float2(lo.x, hi.x);
+        P[4 * u + 1] = make_float2(lo.y, hi.y);
+        P[4 * u + 2] = make_float2(lo.z, hi.z);
+        P[4 * u + 3] = make_float2(lo.w, hi.w);
+      }
     }
-    rotate_block(P, c[i], smem + slot * kSlotBytes, lane8, active);
+    __syncwarp();                                  // the block is read before its region becomes the transpose buffer
+    rotate_block(P, c[i], mine, lane8, active);
     if (active) {
       amax = absmax_cols(amax, c[i]);
       if (a.norm) ssz = sumsq_cols(ssz, c[i]);
@@ -222,17 +319,27 @@ __global__ void __launch_bounds__(kMaxThreads) norm_quant_kernel(const NormArgs 
   if constexpr (SPLIT == 2) cluster_exit_wait();
 }
 
-template <int DT, bool RES, int VEC>
+template <int DT, bool RES, int V>
 static cudaError_t launch_norm_cfg(const RowGeometry& g, const NormArgs& a, cudaStream_t st) {
-  if (g.split == 1) return launch_rows(norm_quant_kernel<DT, RES, VEC, 1, 1>, g, a.M, st, a);
-  if (g.nbmax == 1) return launch_rows(norm_quant_kernel<DT, RES, VEC, 1, 2>, g, a.M, st, a);
-  return launch_rows(norm_quant_kernel<DT, RES, VEC, 2, 2>, g, a.M, st, a);
+  if (g.split == 1) return launch_rows(norm_quant_kernel<DT, RES, V, 1, 1>, g, a.M, st, a);
+  if (g.nbmax == 1) return launch_rows(norm_quant_kernel<DT, RES, V, 1, 2>, g, a.M, st, a);
+  return launch_rows(norm_quant_kernel<DT, RES, V, 2, 2>, g, a.M, st, a);
 }
 
+template <int DT, int V>
+static cudaError_t launch_norm(const RowGeometry& g, const NormArgs& a, cudaStream_t st) {
+  return a.res ? launch_norm_cfg<DT, true, V>(g, a, st) : launch_norm_cfg<DT, false, V>(g, a, st);
+}
+
+// `align`: the bytes that every row of x, residual and h starts on.
 template <int DT>
-static cudaError_t launch_norm(const RowGeometry& g, const NormArgs& a, bool vec, cudaStream_t st) {
-  if (a.res) return vec ? launch_norm_cfg<DT, true, 1>(g, a, st) : launch_norm_cfg<DT, true, 0>(g, a, st);
-  return vec ? launch_norm_cfg<DT, false, 1>(g, a, st) : launch_norm_cfg<DT, false, 0>(g, a, st);
+static cudaError_t launch_norm_dt(const RowGeometry& g, const NormArgs& a, int align, cudaStream_t st) {
+  if constexpr (DT == DT_FP32) {
+    return align >= 16 ? launch_norm<DT, 4>(g, a, st) : launch_norm<DT, 1>(g, a, st);
+  } else {
+    if (align >= 16) return launch_norm<DT, 8>(g, a, st);
+    return align >= 4 ? launch_norm<DT, 2>(g, a, st) : launch_norm<DT, 1>(g, a, st);
+  }
 }
 
 }  // namespace convrot
@@ -258,7 +365,8 @@ extern "C" int convrot_rms_norm_quant(const void* x, convrot_dtype dtype, int64_
   if (off(a_scale, 4) || off(weight, 16) || off(a_norm, 4)) return CONVROT_ERR_MISALIGNED;
   RowGeometry g;
   if (!row_geometry(K_p, kMaxSlots, &g)) return CONVROT_ERR_UNSUPPORTED;
-  g.smem = static_cast<size_t>(g.S) * kSlotBytes + kNormRedFloats * sizeof(float);
+  const int nbl = (g.nblocks + g.split - 1) / g.split;
+  g.smem = static_cast<size_t>(nbl) * kSlotBytes + kNormRedFloats * sizeof(float);
   NormArgs a = {};
   a.x = static_cast<const char*>(x);
   a.res = static_cast<const char*>(residual);
@@ -280,14 +388,16 @@ extern "C" int convrot_rms_norm_quant(const void* x, convrot_dtype dtype, int64_
   a.eps = eps;
   a.inv_k = 1.0f / static_cast<float>(K);
   a.half_sqrt_kp = 0.5001f * std::sqrt(static_cast<float>(K_p));
-  // vector path: every row of x, residual and h starts on 16 bytes
-  auto rows16 = [&](const void* p, int64_t ld) { return !p || (!off(p, 16) && (ld * static_cast<int64_t>(es)) % 16 == 0); };
-  const bool vec = rows16(x, ld_x) && rows16(residual, ld_residual) && rows16(h, ld_h);
+  auto rows_on = [&](const void* p, int64_t ld, int64_t n) {
+    return !p || (!off(p, n) && (M == 1 || ld * static_cast<int64_t>(es) % n == 0));
+  };
+  auto all_on = [&](int64_t n) { return rows_on(x, ld_x, n) && rows_on(residual, ld_residual, n) && rows_on(h, ld_h, n); };
+  const int align = all_on(16) ? 16 : all_on(4) ? 4 : 2;
   cudaError_t e;
   switch (dtype) {
-    case CONVROT_BF16: e = launch_norm<DT_BF16>(g, a, vec, stream); break;
-    case CONVROT_FP16: e = launch_norm<DT_FP16>(g, a, vec, stream); break;
-    default: e = launch_norm<DT_FP32>(g, a, vec, stream); break;
+    case CONVROT_BF16: e = launch_norm_dt<DT_BF16>(g, a, align, stream); break;
+    case CONVROT_FP16: e = launch_norm_dt<DT_FP16>(g, a, align, stream); break;
+    default: e = launch_norm_dt<DT_FP32>(g, a, align, stream); break;
   }
   return e == cudaSuccess ? CONVROT_OK : convrot::record_cuda_error("rms_norm_quant launch", e);
 }

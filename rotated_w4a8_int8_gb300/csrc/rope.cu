@@ -129,11 +129,194 @@ __global__ void __launch_bounds__(32 * kAnyWarps) rope_any_kernel(const Params p
   }
 }
 
+// Head widths in whole 16-element pieces, on 16-byte boundaries.  A lane holds
+// one piece: 8 pairs, as two runs of 8 elements (pairs i .. i+7 at i and at
+// i + P, or 16 neighbouring elements), G = D / 16 rounded up to a power of two
+// lanes hold a head, and a warp 32 / G heads of one token at a time.  The
+// turns of the CTA's tokens and the norm's weights sit in shared memory, in
+// runs of four with the second runs of four behind the first ones, so that
+// the 16-byte reads of a head's lanes are free of bank conflicts and shared
+// by the warp's heads.
+constexpr int kWarps = 8;
+
+__device__ __forceinline__ int spread(int i, int n) { return ((i >> 2) & 1) * (n / 2) + (i >> 3) * 4 + (i & 3); }
+
 template <int DT>
-static cudaError_t launch(const Params& p, bool interleaved, cudaStream_t st) {
-  if (interleaved) rope_any_kernel<DT, true><<<p.M, 32 * kAnyWarps, 0, st>>>(p);
-  else rope_any_kernel<DT, false><<<p.M, 32 * kAnyWarps, 0, st>>>(p);
+struct Piece {
+  static constexpr int W = DT == CONVROT_FP32 ? 8 : 4;     // words of one run of 8 elements
+  uint32_t w[2][W];
+};
+
+template <int DT>
+__device__ __forceinline__ void load_piece(const void* x, int64_t off, int j0, int j1, Piece<DT>& r) {
+  using T = typename Elem<DT>::T;
+  const T* p = static_cast<const T*>(x) + off;
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int u = 0; u < Piece<DT>::W / 4; ++u) {
+      const uint4 v = *(reinterpret_cast<const uint4*>(p + (h ? j1 : j0)) + u);
+      r.w[h][4 * u] = v.x; r.w[h][4 * u + 1] = v.y; r.w[h][4 * u + 2] = v.z; r.w[h][4 * u + 3] = v.w;
+    }
+}
+
+template <int DT>
+__device__ __forceinline__ float piece_elem(const Piece<DT>& r, int h, int e) {
+  if constexpr (DT == CONVROT_FP32) return __uint_as_float(r.w[h][e]);
+  else if constexpr (DT == CONVROT_BF16) return __uint_as_float((e & 1) ? (r.w[h][e >> 1] & 0xffff0000u) : (r.w[h][e >> 1] << 16));
+  else return __half2float(__ushort_as_half(static_cast<unsigned short>((e & 1) ? (r.w[h][e >> 1] >> 16) : (r.w[h][e >> 1] & 0xffffu))));
+}
+
+template <int DT>
+__device__ __forceinline__ void store_piece(void* y, int64_t off, int j0, int j1, const float (&v)[2][8]) {
+  using T = typename Elem<DT>::T;
+  T* p = static_cast<T*>(y) + off;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint4* d = reinterpret_cast<uint4*>(p + (h ? j1 : j0));
+    if constexpr (DT == CONVROT_FP32) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+        d[u] = make_uint4(__float_as_uint(v[h][4 * u]), __float_as_uint(v[h][4 * u + 1]),
+                          __float_as_uint(v[h][4 * u + 2]), __float_as_uint(v[h][4 * u + 3]));
+    } else {
+      uint32_t w[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        if constexpr (DT == CONVROT_BF16) {
+          const __nv_bfloat162 t = __floats2bfloat162_rn(v[h][2 * u], v[h][2 * u + 1]);
+          w[u] = *reinterpret_cast<const uint32_t*>(&t);
+        } else {
+          const __half2 t = __floats2half2_rn(v[h][2 * u], v[h][2 * u + 1]);
+          w[u] = *reinterpret_cast<const uint32_t*>(&t);
+        }
+      }
+      d[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
+}
+
+__device__ __forceinline__ void load8(const float* base, int n, int i, float (&v)[8]) {   // i a multiple of 8
+  const float4 a = *reinterpret_cast<const float4*>(base + i / 2);
+  const float4 b = *reinterpret_cast<const float4*>(base + n / 2 + i / 2);
+  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+}
+
+// T tokens per CTA (1, 2, 4 or 8), kWarps / T warps each; gridDim.y CTAs share a token's heads.
+template <int DT, bool INTERLEAVED, int G, int T>
+__global__ void __launch_bounds__(32 * kWarps, 6) rope_kernel(const Params p) {
+  extern __shared__ __align__(16) float smem[];
+  float* cs = smem;                          // [T][2][P]: cosines, sines
+  float* ws = smem + T * 2 * p.P;            // [2][D]: weights of q and k
+  constexpr int HPW = 32 / G;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int m0 = blockIdx.x * T;
+  for (int i = threadIdx.x; i < T * p.P; i += 32 * kWarps) {
+    const int t = i / p.P, j = i - t * p.P;
+    if (m0 + t < p.M) {
+      const float2 v = pair_turn(p, m0 + t, j);
+      cs[t * 2 * p.P + spread(j, p.P)] = v.x;
+      cs[t * 2 * p.P + p.P + spread(j, p.P)] = v.y;
+    }
+  }
+  for (int i = threadIdx.x; i < 2 * p.D; i += 32 * kWarps) {
+    const float* w = i < p.D ? p.q.weight : p.k.weight;
+    const int j = i < p.D ? i : i - p.D;
+    if (w) ws[(i < p.D ? 0 : p.D) + spread(j, p.D)] = __ldg(w + j);
+  }
+  __syncthreads();
+  constexpr int WPT = kWarps / T;            // warps per token
+  const int t = warp / WPT, m = m0 + t;
+  if (m >= p.M) return;
+  const int c = lane % G, hl = lane / G;
+  const bool piece = 16 * c < p.D;           // lanes past the head's pieces idle
+  const bool turns = 8 * c < p.P;            // this piece is rotated
+  // the piece's two runs: a rotated piece of the split layout lies in both halves
+  const int j0 = !turns || INTERLEAVED ? 16 * c : 8 * c;
+  const int j1 = !turns || INTERLEAVED ? 16 * c + 8 : 8 * c + p.P;
+  const float* tcs = cs + t * 2 * p.P;
+  const int gq = (p.q.heads + HPW - 1) / HPW, gk = (p.k.heads + HPW - 1) / HPW;
+  const int step = WPT * gridDim.y;
+  for (int g = blockIdx.y * WPT + warp % WPT; g < gq + gk; g += step) {
+    const bool is_q = g < gq;
+    const Operand& o = is_q ? p.q : p.k;
+    const int head = (is_q ? g : g - gq) * HPW + hl;
+    const bool active = piece && head < o.heads;
+    Piece<DT> r = {};
+    if (active) load_piece<DT>(o.x, m * o.x_tok + head * o.x_head, j0, j1, r);
+    float v[2][8];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[h][e] = piece_elem<DT>(r, h, e);
+    if (o.weight) {
+      float ss = 0.f;
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) ss = fmaf(v[h][e], v[h][e], ss);
+#pragma unroll
+      for (int s = G / 2; s > 0; s >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, s);
+      const float f = rsqrtf(ss / static_cast<float>(p.D) + p.eps);
+      if (piece) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float w[8];
+          load8(ws + (is_q ? 0 : p.D), p.D, h ? j1 : j0, w);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[h][e] *= f * w[e];
+        }
+      }
+    }
+    if (turns) {
+      float co[8], si[8];
+      load8(tcs, p.P, 8 * c, co);
+      load8(tcs + p.P, p.P, 8 * c, si);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        float& a = INTERLEAVED ? v[e >> 2][2 * (e & 3)] : v[0][e];
+        float& b = INTERLEAVED ? v[e >> 2][2 * (e & 3) + 1] : v[1][e];
+        const float ta = a * co[e] - b * si[e], tb = b * co[e] + a * si[e];
+        a = ta;
+        b = tb;
+      }
+    }
+    if (active) store_piece<DT>(o.y, m * o.y_tok + head * o.y_head, j0, j1, v);
+  }
+}
+
+template <int DT, bool INTERLEAVED, int G>
+static cudaError_t launch_g(const Params& p, cudaStream_t st) {
+  const int per_warp = 32 / G, groups = (p.q.heads + per_warp - 1) / per_warp + (p.k.heads + per_warp - 1) / per_warp;
+  auto smem = [&](int T) { return static_cast<size_t>(T * 2 * p.P + 2 * p.D) * sizeof(float); };
+  if (p.M >= 4 * 2 * 152) {
+    rope_kernel<DT, INTERLEAVED, G, 4><<<(p.M + 3) / 4, 32 * kWarps, smem(4), st>>>(p);
+  } else {
+    // few tokens: their heads over several CTAs, up to one warp per group of heads
+    int y = (4 * 152 + p.M - 1) / p.M;
+    const int most = (groups + kWarps - 1) / kWarps;
+    if (y > most) y = most;
+    rope_kernel<DT, INTERLEAVED, G, 1><<<dim3(p.M, y), 32 * kWarps, smem(1), st>>>(p);
+  }
   return cudaGetLastError();
+}
+
+template <int DT, bool INTERLEAVED>
+static cudaError_t launch_layout(const Params& p, bool vec, cudaStream_t st) {
+  if (vec) {
+    const int pieces = p.D / 16;
+    if (pieces <= 4) return launch_g<DT, INTERLEAVED, 4>(p, st);
+    if (pieces <= 8) return launch_g<DT, INTERLEAVED, 8>(p, st);
+    if (pieces <= 16) return launch_g<DT, INTERLEAVED, 16>(p, st);
+  }
+  rope_any_kernel<DT, INTERLEAVED><<<p.M, 32 * kAnyWarps, 0, st>>>(p);
+  return cudaGetLastError();
+}
+
+template <int DT>
+static cudaError_t launch(const Params& p, bool interleaved, bool vec, cudaStream_t st) {
+  return interleaved ? launch_layout<DT, true>(p, vec, st) : launch_layout<DT, false>(p, vec, st);
 }
 
 }  // namespace crrope
@@ -207,11 +390,20 @@ extern "C" int convrot_qk_norm_rope(const void* q, int64_t q_tok, int64_t q_head
   p.ld_pos = ld_pos;
   p.inv_freq = inv_freq;
   p.eps = eps;
+  // vector path: whole 16-element pieces on 16-byte boundaries
+  const int64_t e16 = 16 / static_cast<int64_t>(es);
+  auto on16 = [&](const void* t, int64_t tok, int64_t head, int heads) {
+    return reinterpret_cast<uintptr_t>(t) % 16 == 0 && (M == 1 || tok % e16 == 0) && (heads <= 1 || head % e16 == 0);
+  };
+  bool vec = D % 16 == 0 && pairs % 8 == 0;
+  for (const Operand* o : {&p.q, &p.k})
+    if (o->heads > 0)
+      vec = vec && on16(o->x, o->x_tok, o->x_head, o->heads) && on16(o->y, o->y_tok, o->y_head, o->heads);
   cudaError_t e;
   switch (dtype) {
-    case CONVROT_BF16: e = launch<CONVROT_BF16>(p, interleaved != 0, stream); break;
-    case CONVROT_FP16: e = launch<CONVROT_FP16>(p, interleaved != 0, stream); break;
-    default: e = launch<CONVROT_FP32>(p, interleaved != 0, stream); break;
+    case CONVROT_BF16: e = launch<CONVROT_BF16>(p, interleaved != 0, vec, stream); break;
+    case CONVROT_FP16: e = launch<CONVROT_FP16>(p, interleaved != 0, vec, stream); break;
+    default: e = launch<CONVROT_FP32>(p, interleaved != 0, vec, stream); break;
   }
   return e == cudaSuccess ? CONVROT_OK : convrot::record_cuda_error("qk_norm_rope launch", e);
 }
