@@ -2,6 +2,19 @@
 //
 // One to CONVROT_FEW_TOKENS token rows against a whole weight: each weight
 // code is read once and used M times, so the bytes of the weight bound it.
+//
+// A CTA owns 16 MT weight rows; its eight warps take the K units (64 bytes of
+// every row) in turn.  The products run on the warp-level tensor instruction
+// (mma.sync m16n8k16, FP16 in, FP32 out) with the weight as its 16-row operand
+// and the tokens, eight to a tile, as the other one: at one to a few dozen
+// tokens a tcgen05 tile would be mostly padding.  Which k an operand's slot
+// holds does not matter as long as both operands agree, so a lane feeds the
+// instruction from 16 contiguous bytes of its rows: no shared memory, no
+// shuffles, and every load is a full 16 bytes.  One-byte codes become FP16 in
+// registers (1024 + 128 + code is a byte permute away, an exact subtraction
+// leaves the code).  Sums are exact integers: FP32 partial sums over at most
+// 1024 codes stay below 2^24, then go to int32 registers; the warps' sums meet
+// in shared memory by integer addition, whose order does not matter.
 #include <cstdint>
 #include <cuda_runtime.h>
 #include <cuda_fp16.h>
@@ -12,86 +25,161 @@
 
 namespace crfused {
 
+template <int V>
+struct Kind {
+  static constexpr int value = V;
+};
+
 constexpr int WARPS = 8;
+constexpr int EXACT_CODES = 1024;        // codes per exact FP32 partial sum
 
-// Sixteen codes as four words of signed bytes.
+// 16 bytes of a weight row: read once, kept out of L1.
+__device__ __forceinline__ uint4 load_weight(const char* p) {
+  uint4 v;
+  asm("ld.global.nc.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
+      : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+
+// Four signed bytes -> four FP16 integers.
+__device__ __forceinline__ void widen4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  const uint32_t x = w ^ 0x80808080u;                     // code + 128
+  const uint32_t a = __byte_perm(x, 0x64646464u, 0x5140), b = __byte_perm(x, 0x64646464u, 0x5342);   // 1024 + 128 + code
+  const __half2 off = __float2half2_rn(1152.0f);
+  const __half2 l = __hsub2(*reinterpret_cast<const __half2*>(&a), off);
+  const __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&b), off);
+  lo = *reinterpret_cast<const uint32_t*>(&l);
+  hi = *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// The operand words of step s of a lane's 16 bytes: four codes, two and two.
 template <bool S8>
-__device__ __forceinline__ int4 load_codes16(const void* row, int k) {
+__device__ __forceinline__ void step_words(const uint4& v, int s, uint32_t& lo, uint32_t& hi) {
   if constexpr (S8) {
-    return __ldg(reinterpret_cast<const int4*>(static_cast<const int8_t*>(row) + k));
+    widen4(s == 0 ? v.x : s == 1 ? v.y : s == 2 ? v.z : v.w, lo, hi);
   } else {
-    const __half* p = static_cast<const __half*>(row) + k;
-    int w[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint2 v = __ldg(reinterpret_cast<const uint2*>(p + 4 * j));
-      // 1536 + code has the code's two's complement in its low byte
-      const __half2 m = __float2half2_rn(1536.0f);
-      const __half2 a = __hadd2(*reinterpret_cast<const __half2*>(&v.x), m);
-      const __half2 b = __hadd2(*reinterpret_cast<const __half2*>(&v.y), m);
-      w[j] = __byte_perm(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b), 0x6420);
-    }
-    return make_int4(w[0], w[1], w[2], w[3]);
+    lo = s == 0 ? v.x : v.z;
+    hi = s == 0 ? v.y : v.w;
   }
 }
 
-// One warp per weight row, all tokens in turn, four at a time.
-template <int OUT, bool S8>
-__global__ void __launch_bounds__(32 * WARPS) few_kernel(const void* a_q, int64_t ld_aq, const void* w_q, int64_t ld_wq,
-                                                         int K_p, const Epilogue e) {
-  using namespace crgemm;
-  using T = typename OutT<OUT>::T;
-  constexpr int64_t es = S8 ? 1 : 2;
-  const int n = blockIdx.x * WARPS + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  if (n >= e.N) return;
-  const char* w = static_cast<const char*>(w_q) + n * ld_wq * es;
-  for (int m0 = 0; m0 < e.M; m0 += 4) {
-    int acc[4] = {0, 0, 0, 0};
-    for (int k = 16 * lane; k < K_p; k += 512) {
-      const int4 b = load_codes16<S8>(w, k);
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// NT tiles of eight tokens, MT tiles of 16 weight rows, U units in flight per warp.
+template <bool S8, int NT, int MT, int U>
+__global__ void __launch_bounds__(32 * WARPS)
+few_kernel(const char* __restrict__ a_q, int64_t a_pitch, const char* __restrict__ w_q, int64_t w_pitch, int units,
+           int out_dtype, const Epilogue e) {
+  constexpr int ROWS = 16 * MT, TOKENS = 8 * NT, PITCH = ROWS + 4;   // pad: no bank conflicts below
+  constexpr int STEPS = S8 ? 4 : 2, CODES = S8 ? 64 : 32;            // per unit of 64 bytes
+  __shared__ __align__(16) int sums[TOKENS * PITCH];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
+  for (int i = threadIdx.x; i < TOKENS * PITCH; i += 32 * WARPS) sums[i] = 0;
+  const int n0 = blockIdx.x * ROWS;
+  // rows and tokens past the matrix repeat the last one; their sums are not used
+  const char *wr[2 * MT], *ar[NT];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (m0 + i >= e.M) continue;
-        const int4 a = load_codes16<S8>(static_cast<const char*>(a_q) + (m0 + i) * ld_aq * es, k);
-        acc[i] = __dp4a(a.x, b.x, __dp4a(a.y, b.y, __dp4a(a.z, b.z, __dp4a(a.w, b.w, acc[i]))));
+  for (int i = 0; i < 2 * MT; ++i) wr[i] = w_q + min(n0 + 8 * i + g, e.N - 1) * w_pitch + 16 * q;
+#pragma unroll
+  for (int t = 0; t < NT; ++t) ar[t] = a_q + min(8 * t + g, e.M - 1) * a_pitch + 16 * q;
+  int total[MT][NT][4] = {};
+  for (int first = warp; first < units; first += WARPS * (EXACT_CODES / CODES)) {
+    const int end = min(units, first + WARPS * (EXACT_CODES / CODES));
+    float acc[MT][NT][4] = {};
+    for (int u0 = first; u0 < end; u0 += WARPS * U) {
+      uint4 wv[U][2 * MT], av[U][NT];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int at = u0 + u * WARPS;
+        if (at < end) {
+#pragma unroll
+          for (int i = 0; i < 2 * MT; ++i) wv[u][i] = load_weight(wr[i] + static_cast<int64_t>(at) * 64);
+#pragma unroll
+          for (int t = 0; t < NT; ++t) av[u][t] = __ldg(reinterpret_cast<const uint4*>(ar[t] + static_cast<int64_t>(at) * 64));
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (u0 + u * WARPS >= end) break;                // uniform in the warp
+#pragma unroll
+        for (int s = 0; s < STEPS; ++s) {
+          uint32_t b[NT][2];
+#pragma unroll
+          for (int t = 0; t < NT; ++t) step_words<S8>(av[u][t], s, b[t][0], b[t][1]);
+#pragma unroll
+          for (int i = 0; i < MT; ++i) {
+            uint32_t a0, a1, a2, a3;
+            step_words<S8>(wv[u][2 * i], s, a0, a2);
+            step_words<S8>(wv[u][2 * i + 1], s, a1, a3);
+#pragma unroll
+            for (int t = 0; t < NT; ++t) mma16816(acc[i][t], a0, a1, a2, a3, b[t][0], b[t][1]);
+          }
+        }
       }
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      acc[i] = __reduce_add_sync(0xffffffffu, acc[i]);
-      const int m = m0 + i;
-      if (lane != 0 || m >= e.M) continue;
-      float y = __fmul_rn(__fmul_rn(static_cast<float>(acc[i]), __ldg(e.a_scale + m)), __ldg(e.w_scale + n));
-      if (e.bias) y = __fadd_rn(y, __ldg(e.bias + n));
-      y = activate(y, e.act);
-      if (e.gate) y = __fmul_rn(y, __ldg(e.gate + n));
-      if (e.residual) {
-        const T r = static_cast<const T*>(e.residual)[m * e.ld_res + n];
-        y = __fadd_rn(y, static_cast<float>(r));
-      }
-      static_cast<T*>(e.out)[m * e.ld_out + n] = to_out<OUT>(y);
-    }
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) total[i][t][j] += __float2int_rn(acc[i][t][j]);     // exact
+  }
+  __syncthreads();                                       // sums are zero
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        atomicAdd(&sums[(8 * t + 2 * q + (j & 1)) * PITCH + 16 * i + g + 8 * (j >> 1)], total[i][t][j]);
+  __syncthreads();
+  for (int i = threadIdx.x; i < e.M * (ROWS / 4); i += 32 * WARPS) {
+    const int m = i / (ROWS / 4), r = 4 * (i % (ROWS / 4)), n = n0 + r;
+    if (n >= e.N) continue;
+    const int4 v = *reinterpret_cast<const int4*>(&sums[m * PITCH + r]);
+    const float4 f = make_float4(static_cast<float>(v.x), static_cast<float>(v.y), static_cast<float>(v.z),
+                                 static_cast<float>(v.w));
+    const ColumnTerms t = load_columns(e, n);
+    const float sa = __ldg(e.a_scale + m);
+    auto finish = [&](auto kind) {
+      constexpr int OUT = decltype(kind)::value;
+      ResidualWords<OUT> res = {};
+      if (e.residual) res = load_residual<OUT>(e, m, n);
+      finish4<OUT>(e, t, f, sa, res, m, n);
+    };
+    if (out_dtype == CONVROT_BF16) finish(Kind<CONVROT_BF16>{});
+    else if (out_dtype == CONVROT_FP16) finish(Kind<CONVROT_FP16>{});
+    else finish(Kind<CONVROT_FP32>{});
   }
 }
 
-template <int OUT>
-static cudaError_t launch_few(const void* a_q, int64_t ld_aq, const void* w_q, int64_t ld_wq, bool s8, int K_p,
+template <bool S8, int NT, int MT, int U>
+static cudaError_t launch_few(const void* a_q, int64_t ld_aq, const void* w_q, int64_t ld_wq, int K_p, int out_dtype,
                               const Epilogue& e, cudaStream_t st) {
-  const int blocks = (e.N + WARPS - 1) / WARPS;
-  if (s8) few_kernel<OUT, true><<<blocks, 32 * WARPS, 0, st>>>(a_q, ld_aq, w_q, ld_wq, K_p, e);
-  else few_kernel<OUT, false><<<blocks, 32 * WARPS, 0, st>>>(a_q, ld_aq, w_q, ld_wq, K_p, e);
+  constexpr int es = S8 ? 1 : 2;
+  few_kernel<S8, NT, MT, U><<<(e.N + 16 * MT - 1) / (16 * MT), 32 * WARPS, 0, st>>>(
+      static_cast<const char*>(a_q), ld_aq * es, static_cast<const char*>(w_q), ld_wq * es, K_p * es / 64, out_dtype, e);
   return cudaGetLastError();
+}
+
+template <bool S8>
+static cudaError_t launch_tokens(const void* a_q, int64_t ld_aq, const void* w_q, int64_t ld_wq, int K_p, int out_dtype,
+                                 const Epilogue& e, cudaStream_t st) {
+  if (e.M <= 8) return launch_few<S8, 1, 1, 4>(a_q, ld_aq, w_q, ld_wq, K_p, out_dtype, e, st);
+  if (e.M <= 16) return launch_few<S8, 2, 1, 4>(a_q, ld_aq, w_q, ld_wq, K_p, out_dtype, e, st);
+  if (e.M <= 32) return launch_few<S8, 4, 2, 2>(a_q, ld_aq, w_q, ld_wq, K_p, out_dtype, e, st);
+  return launch_few<S8, 8, 2, 1>(a_q, ld_aq, w_q, ld_wq, K_p, out_dtype, e, st);
 }
 
 int gemm_few(const void* a_q, int64_t ld_aq, const void* w_q, int64_t ld_wq, convrot_codes fmt, int K_p,
              const Epilogue& e, convrot_dtype out_dtype, cudaStream_t st) {
-  const bool s8 = fmt == CONVROT_CODES_S8;
-  cudaError_t r;
-  switch (out_dtype) {
-    case CONVROT_BF16: r = launch_few<CONVROT_BF16>(a_q, ld_aq, w_q, ld_wq, s8, K_p, e, st); break;
-    case CONVROT_FP16: r = launch_few<CONVROT_FP16>(a_q, ld_aq, w_q, ld_wq, s8, K_p, e, st); break;
-    default: r = launch_few<CONVROT_FP32>(a_q, ld_aq, w_q, ld_wq, s8, K_p, e, st); break;
-  }
+  const cudaError_t r = fmt == CONVROT_CODES_S8 ? launch_tokens<true>(a_q, ld_aq, w_q, ld_wq, K_p, out_dtype, e, st)
+                                                : launch_tokens<false>(a_q, ld_aq, w_q, ld_wq, K_p, out_dtype, e, st);
   return r == cudaSuccess ? CONVROT_OK : convrot::record_cuda_error("few-token GEMM launch", r);
 }
 
@@ -135,6 +223,6 @@ extern "C" int convrot_gemm_fused(const void* a_q, int64_t ld_aq, const float* a
   e.act = act;
   e.vec_out = !off(out, 4 * es) && ld_out % 4 == 0;
   e.vec_res = !off(residual, 4 * es) && ld_residual % 4 == 0;
-  if (fmt == CONVROT_CODES_S8 || M <= 16) return gemm_few(a_q, ld_aq, w_q, ld_wq, fmt, K_p, e, out_dtype, stream);
+  if (fmt == CONVROT_CODES_S8 || M <= CONVROT_FEW_TOKENS) return gemm_few(a_q, ld_aq, w_q, ld_wq, fmt, K_p, e, out_dtype, stream);
   return gemm_many(a_q, ld_aq, w_q, ld_wq, K_p, e, out_dtype, stream);
 }

@@ -408,7 +408,7 @@ static cudaError_t resident_clusters(int split, int* out) {
     e = cudaOccupancyMaxActiveClusters(&n, k, &cfg);
     if (e != cudaSuccess || n <= 0) {
       (void)cudaGetLastError();
-      n = sms / (2 * split);
+      n = split == 1 ? sms / 2 : -1;             // -1: clusters of this size do not fit
     }
     if (dev < kMaxDevices) known[dev][split] = n;
   }
@@ -444,10 +444,50 @@ static int launch(const void* a_q, int64_t ld_aq, const void* w_q, int64_t ld_wq
   return e == cudaSuccess ? CONVROT_OK : convrot::record_cuda_error("fused GEMM launch", e);
 }
 
+// Tile width and pairs per tile.
+struct Shape {
+  int bn, split;
+};
+
+template <int OUT>
+static int pick_shape(const Params& p, Shape* best) {
+  // model of a tile's time in microseconds (a 64-deep step of a 256- and a 128-wide tile; joining a split tile)
+  constexpr double step256 = 0.33, step128 = 0.20, join = 2.0;
+  double least = 0;
+  for (int bn : {256, 128}) {
+    const int items = p.num_m2 * ((p.e.N + bn - 1) / bn);
+    const double step = bn == 256 ? step256 : step128;
+    for (int split = 1; split <= MAX_SPLIT; ++split) {
+      if (split > 1 && p.k_steps < 8 * split) break;
+      int resident = 0;
+      cudaError_t e = bn == 256 ? (split == 1 ? resident_clusters<OUT, 256, false>(1, &resident)
+                                              : resident_clusters<OUT, 256, true>(split, &resident))
+                                : (split == 1 ? resident_clusters<OUT, 128, false>(1, &resident)
+                                              : resident_clusters<OUT, 128, true>(split, &resident));
+      if (e != cudaSuccess) return convrot::record_cuda_error("fused GEMM set-up", e);
+      if (split > 1 && items > resident) break;
+      const int rounds = (items + resident - 1) / resident, steps = (p.k_steps + split - 1) / split;
+      const double t = rounds * steps * step + (split > 1 ? join : 0.0);
+      if (least == 0 || t < least) {
+        least = t;
+        *best = {bn, split};
+      }
+    }
+  }
+  return CONVROT_OK;
+}
+
 template <int OUT>
 static int launch_out(const void* a_q, int64_t ld_aq, const void* w_q, int64_t ld_wq, int K_p, Params p,
                       cudaStream_t st) {
-  return launch<OUT, 256, false>(a_q, ld_aq, w_q, ld_wq, K_p, p, 1, st);
+  Shape s = {256, 1};
+  const int r = pick_shape<OUT>(p, &s);
+  if (r != CONVROT_OK) return r;
+  if (s.bn == 256)
+    return s.split == 1 ? launch<OUT, 256, false>(a_q, ld_aq, w_q, ld_wq, K_p, p, 1, st)
+                        : launch<OUT, 256, true>(a_q, ld_aq, w_q, ld_wq, K_p, p, s.split, st);
+  return s.split == 1 ? launch<OUT, 128, false>(a_q, ld_aq, w_q, ld_wq, K_p, p, 1, st)
+                      : launch<OUT, 128, true>(a_q, ld_aq, w_q, ld_wq, K_p, p, s.split, st);
 }
 
 int gemm_many(const void* a_q, int64_t ld_aq, const void* w_q, int64_t ld_wq, int K_p, const Epilogue& ep,
