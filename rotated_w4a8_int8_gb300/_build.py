@@ -17,12 +17,13 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libconvrot.so")
 # (source, object, defines): quant.cu is compiled twice, once without and once
-# with the kernels that write code-norm bounds
+# with the kernels that write code-norm bounds; gemm_fused.cu once per output type
 SOURCES = [("api.cu", "api", []), ("quant.cu", "quant", []),
            ("quant.cu", "quant_norm", ["-DCONVROT_QUANT_NORM=1"]), ("gemm.cu", "gemm", []),
            ("int8_probe.cu", "int8_probe", []), ("decode_gemm_probe.cu", "decode_gemm_probe", []),
-           ("norm_quant.cu", "norm_quant", []), ("rope.cu", "rope", []), ("gemm_fused.cu", "gemm_fused", []),
-           ("gemm_few.cu", "gemm_few", [])]
+           ("norm_quant.cu", "norm_quant", []), ("rope.cu", "rope", []), ("gemm_few.cu", "gemm_few", []),
+           *(("gemm_fused.cu", f"gemm_fused_{name}", [f"-DCONVROT_FUSED_OUT=CONVROT_{name.upper()}"])
+             for name in ("bf16", "fp16", "fp32"))]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
          "-I", os.path.join(ROOT, "include")]

@@ -25,11 +25,6 @@
 
 namespace crfused {
 
-template <int V>
-struct Kind {
-  static constexpr int value = V;
-};
-
 constexpr int WARPS = 8;
 constexpr int EXACT_CODES = 1024;        // codes per exact FP32 partial sum
 
@@ -70,17 +65,40 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// NT tiles of eight tokens, MT tiles of 16 weight rows, U units in flight per warp.
+__device__ __forceinline__ int ld_cluster(const int* p, uint32_t rank) {
+  int v;
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(crgemm::map_to_rank(crgemm::smem_u32(p), rank)) : "memory");
+  return v;
+}
+
+// NT tiles of eight tokens, MT tiles of 16 weight rows, U units in flight per
+// warp.  A cluster of `split` CTAs shares the K units of a row tile; each
+// finishes its part of the tile's outputs from all of their sums.
 template <bool S8, int NT, int MT, int U>
-__global__ void __launch_bounds__(32 * WARPS)
+__global__ void __launch_bounds__(32 * WARPS, MT == 1 ? 3 : 1)
 few_kernel(const char* __restrict__ a_q, int64_t a_pitch, const char* __restrict__ w_q, int64_t w_pitch, int units,
-           int out_dtype, const Epilogue e) {
+           int split, int out_dtype, const Epilogue e) {
   constexpr int ROWS = 16 * MT, TOKENS = 8 * NT, PITCH = ROWS + 4;   // pad: no bank conflicts below
   constexpr int STEPS = S8 ? 4 : 2, CODES = S8 ? 64 : 32;            // per unit of 64 bytes
   __shared__ __align__(16) int sums[TOKENS * PITCH];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
   for (int i = threadIdx.x; i < TOKENS * PITCH; i += 32 * WARPS) sums[i] = 0;
-  const int n0 = blockIdx.x * ROWS;
+  const int part = blockIdx.x % split;
+  const int n0 = static_cast<int>(blockIdx.x / split) * ROWS;
+  // Each thread finishes output group `mine` (token, four weight rows), and
+  // more for many tokens.  What that needs is asked for now: fetched at the
+  // end, it is a DRAM latency per CTA.
+  const int groups = e.M * (ROWS / 4), mine = threadIdx.x * split + part;
+  if (mine < groups && n0 + 4 * (mine % (ROWS / 4)) < e.N) {
+    const int m = mine / (ROWS / 4), n = n0 + 4 * (mine % (ROWS / 4));
+    warm_l1(e.w_scale + n);
+    warm_l1(e.a_scale + m);
+    if (e.bias) warm_l1(e.bias + n);
+    if (e.gate) warm_l1(e.gate + n);
+    if (e.residual)
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const char*>(e.residual) +
+                                                    (m * e.ld_res + n) * (out_dtype == CONVROT_FP32 ? 4 : 2)));
+  }
   // rows and tokens past the matrix repeat the last one; their sums are not used
   const char *wr[2 * MT], *ar[NT];
 #pragma unroll
@@ -88,14 +106,15 @@ few_kernel(const char* __restrict__ a_q, int64_t a_pitch, const char* __restrict
 #pragma unroll
   for (int t = 0; t < NT; ++t) ar[t] = a_q + min(8 * t + g, e.M - 1) * a_pitch + 16 * q;
   int total[MT][NT][4] = {};
-  for (int first = warp; first < units; first += WARPS * (EXACT_CODES / CODES)) {
-    const int end = min(units, first + WARPS * (EXACT_CODES / CODES));
+  const int wstep = WARPS * split;                       // the tile's warps take the units in turn
+  for (int first = part * WARPS + warp; first < units; first += wstep * (EXACT_CODES / CODES)) {
+    const int end = min(units, first + wstep * (EXACT_CODES / CODES));
     float acc[MT][NT][4] = {};
-    for (int u0 = first; u0 < end; u0 += WARPS * U) {
+    for (int u0 = first; u0 < end; u0 += wstep * U) {
       uint4 wv[U][2 * MT], av[U][NT];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int at = u0 + u * WARPS;
+        const int at = u0 + u * wstep;
         if (at < end) {
 #pragma unroll
           for (int i = 0; i < 2 * MT; ++i) wv[u][i] = load_weight(wr[i] + static_cast<int64_t>(at) * 64);
@@ -105,7 +124,7 @@ few_kernel(const char* __restrict__ a_q, int64_t a_pitch, const char* __restrict
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        if (u0 + u * WARPS >= end) break;                // uniform in the warp
+        if (u0 + u * wstep >= end) break;                // uniform in the warp
 #pragma unroll
         for (int s = 0; s < STEPS; ++s) {
           uint32_t b[NT][2];
@@ -137,43 +156,72 @@ few_kernel(const char* __restrict__ a_q, int64_t a_pitch, const char* __restrict
 #pragma unroll
       for (int j = 0; j < 4; ++j)
         atomicAdd(&sums[(8 * t + 2 * q + (j & 1)) * PITCH + 16 * i + g + 8 * (j >> 1)], total[i][t][j]);
-  __syncthreads();
-  for (int i = threadIdx.x; i < e.M * (ROWS / 4); i += 32 * WARPS) {
+  if (split > 1) crgemm::cluster_sync();
+  else __syncthreads();
+  for (int i = mine; i < groups; i += 32 * WARPS * split) {
     const int m = i / (ROWS / 4), r = 4 * (i % (ROWS / 4)), n = n0 + r;
     if (n >= e.N) continue;
-    const int4 v = *reinterpret_cast<const int4*>(&sums[m * PITCH + r]);
+    int4 v = *reinterpret_cast<const int4*>(&sums[m * PITCH + r]);
+    for (int c = 1; c < split; ++c) {
+      const uint32_t peer = part + c < split ? part + c : part + c - split;
+      v.x += ld_cluster(&sums[m * PITCH + r], peer);
+      v.y += ld_cluster(&sums[m * PITCH + r + 1], peer);
+      v.z += ld_cluster(&sums[m * PITCH + r + 2], peer);
+      v.w += ld_cluster(&sums[m * PITCH + r + 3], peer);
+    }
     const float4 f = make_float4(static_cast<float>(v.x), static_cast<float>(v.y), static_cast<float>(v.z),
                                  static_cast<float>(v.w));
     const ColumnTerms t = load_columns(e, n);
     const float sa = __ldg(e.a_scale + m);
+    float y[4] = {f.x, f.y, f.z, f.w};
+    with_act(e.act, [&](auto act) { activate4<decltype(act)::value>(e, t, y, sa); });
     auto finish = [&](auto kind) {
       constexpr int OUT = decltype(kind)::value;
       ResidualWords<OUT> res = {};
-      if (e.residual) res = load_residual<OUT>(e, m, n);
-      finish4<OUT>(e, t, f, sa, res, m, n);
+      if (e.residual) res = load_residual<OUT, false>(e, m, n);
+      finish4<OUT, false>(e, y, res, m, n);
     };
     if (out_dtype == CONVROT_BF16) finish(Kind<CONVROT_BF16>{});
     else if (out_dtype == CONVROT_FP16) finish(Kind<CONVROT_FP16>{});
     else finish(Kind<CONVROT_FP32>{});
   }
+  if (split > 1) crgemm::cluster_sync();                 // the peers have read this CTA's sums
 }
 
 template <bool S8, int NT, int MT, int U>
 static cudaError_t launch_few(const void* a_q, int64_t ld_aq, const void* w_q, int64_t ld_wq, int K_p, int out_dtype,
                               const Epilogue& e, cudaStream_t st) {
   constexpr int es = S8 ? 1 : 2;
-  few_kernel<S8, NT, MT, U><<<(e.N + 16 * MT - 1) / (16 * MT), 32 * WARPS, 0, st>>>(
-      static_cast<const char*>(a_q), ld_aq * es, static_cast<const char*>(w_q), ld_wq * es, K_p * es / 64, out_dtype, e);
-  return cudaGetLastError();
+  const int tiles = (e.N + 16 * MT - 1) / (16 * MT), units = K_p * es / 64;
+  // Few row tiles: up to eight CTAs share one, as long as all fit the GPU at
+  // once (152 SMs, FIT each) and every warp keeps a full batch of loads.
+  constexpr int FIT = MT == 1 ? 3 : 1;
+  int split = 1;
+  while (split < 8 && tiles * 2 * split <= 152 * FIT && units >= 2 * split * WARPS * U) split *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = split;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.gridDim = dim3(tiles * split);
+  cfg.blockDim = dim3(32 * WARPS);
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = split > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, few_kernel<S8, NT, MT, U>, static_cast<const char*>(a_q), ld_aq * es,
+                            static_cast<const char*>(w_q), ld_wq * es, units, split, out_dtype, e);
 }
 
 template <bool S8>
 static cudaError_t launch_tokens(const void* a_q, int64_t ld_aq, const void* w_q, int64_t ld_wq, int K_p, int out_dtype,
                                  const Epilogue& e, cudaStream_t st) {
-  if (e.M <= 8) return launch_few<S8, 1, 1, 4>(a_q, ld_aq, w_q, ld_wq, K_p, out_dtype, e, st);
-  if (e.M <= 16) return launch_few<S8, 2, 1, 4>(a_q, ld_aq, w_q, ld_wq, K_p, out_dtype, e, st);
-  if (e.M <= 32) return launch_few<S8, 4, 2, 2>(a_q, ld_aq, w_q, ld_wq, K_p, out_dtype, e, st);
-  return launch_few<S8, 8, 2, 1>(a_q, ld_aq, w_q, ld_wq, K_p, out_dtype, e, st);
+  if (e.M <= 8) return launch_few<S8, 1, 1, 3>(a_q, ld_aq, w_q, ld_wq, K_p, out_dtype, e, st);
+  if (e.M <= 16) return launch_few<S8, 2, 1, 2>(a_q, ld_aq, w_q, ld_wq, K_p, out_dtype, e, st);
+  if constexpr (S8) {
+    if (e.M <= 32) return launch_few<S8, 4, 2, 2>(a_q, ld_aq, w_q, ld_wq, K_p, out_dtype, e, st);
+    return launch_few<S8, 8, 2, 1>(a_q, ld_aq, w_q, ld_wq, K_p, out_dtype, e, st);
+  }
+  return cudaErrorInvalidValue;                          // FP16 codes of more tokens go to gemm_many
 }
 
 int gemm_few(const void* a_q, int64_t ld_aq, const void* w_q, int64_t ld_wq, convrot_codes fmt, int K_p,
@@ -223,6 +271,21 @@ extern "C" int convrot_gemm_fused(const void* a_q, int64_t ld_aq, const float* a
   e.act = act;
   e.vec_out = !off(out, 4 * es) && ld_out % 4 == 0;
   e.vec_res = !off(residual, 4 * es) && ld_residual % 4 == 0;
-  if (fmt == CONVROT_CODES_S8 || M <= CONVROT_FEW_TOKENS) return gemm_few(a_q, ld_aq, w_q, ld_wq, fmt, K_p, e, out_dtype, stream);
-  return gemm_many(a_q, ld_aq, w_q, ld_wq, K_p, e, out_dtype, stream);
+  if (fmt == CONVROT_CODES_S8 || M <= 16) return gemm_few(a_q, ld_aq, w_q, ld_wq, fmt, K_p, e, out_dtype, stream);
+  switch (out_dtype) {
+    case CONVROT_BF16: return gemm_many<CONVROT_BF16>(a_q, ld_aq, w_q, ld_wq, K_p, e, stream);
+    case CONVROT_FP16: return gemm_many<CONVROT_FP16>(a_q, ld_aq, w_q, ld_wq, K_p, e, stream);
+    default: return gemm_many<CONVROT_FP32>(a_q, ld_aq, w_q, ld_wq, K_p, e, stream);
+  }
 }
+
+namespace convrot {
+cudaError_t take_fused_error_word(int* v) {
+  int each[3] = {0, 0, 0};
+  cudaError_t e = crfused::take_fused_error_word<CONVROT_BF16>(&each[0]);
+  if (e == cudaSuccess) e = crfused::take_fused_error_word<CONVROT_FP16>(&each[1]);
+  if (e == cudaSuccess) e = crfused::take_fused_error_word<CONVROT_FP32>(&each[2]);
+  *v = each[0] ? each[0] : each[1] ? each[1] : each[2];
+  return e;
+}
+}  // namespace convrot

@@ -8,13 +8,21 @@
 // integer below 2^24), chunks added in int32 registers, CTA pairs with a
 // 256 x BN output tile (BN = 256 or 128), TMA-fed stages, persistent clusters.
 //
-// Epilogue.  A thread's accumulators are one row of 32-column boxes; a box
-// (32 rows x 32 columns of FP32 bits) goes through 4 KiB of swizzled shared
-// memory so that eight lanes then cover a row's 32 columns, four each.  In that layout
-// the weight scale, bias and gate of a lane's four columns are loaded once
-// per box, residual reads and output writes are 64- or 128-byte row pieces of
-// any alignment, and the activation's code is one rolled loop.  The
-// arithmetic is FP32, rounded once to the output type.
+// Epilogue.  Sixteen warps, each with 32 rows and a quarter of the tile's
+// columns: 64 accumulators per thread leave registers for the functions, and
+// four warps per scheduler hide their latency.  A thread owns a row.  The
+// output goes out in boxes of 32 rows x 64 bytes (32 bytes for split tiles)
+// that each warp fills in swizzled shared memory and hands to a TMA tensor
+// store; the residual's box is brought into the same buffer first (by a TMA
+// load that is issued while the tile is still being multiplied) and is
+// replaced value by value.  Rows that do not start on 16 bytes are copied by
+// the warp instead, 8, 4 or 2 bytes per lane.  (Writing the output from
+// registers, 8 bytes per lane and 64 bytes per row, took 469 us where this
+// takes 334 us, 365 us with the tanh form of GELU: 8192 x 28672, K = 1024,
+// BF16.  Sixteen warps and one copy of a box's code matter as much: eight
+// warps with every box unrolled took 435 us and 548 us.)  The arithmetic is FP32,
+// rounded once to the output type.  While this phase runs, the tensor core can
+// fill two chunks ahead and no more.
 //
 // Few output tiles.  With fewer tiles than CTA pairs, a cluster of S pairs
 // (2 <= S <= 4) shares one tile: each pair multiplies a slice of K, then
@@ -39,13 +47,16 @@ using namespace crgemm;
 constexpr int BM = 128, BK = 64;
 constexpr int KCHUNK_STEPS = 16;                 // 16 * 64 = 1024 K per exact FP32 chunk
 constexpr int A_BYTES = BM * BK * 2;
-constexpr int NUM_EPI_WARPS = 8;
-constexpr int THREADS = 64 + NUM_EPI_WARPS * 32; // 320; registers as for gemm.cu's 384-thread bound
-constexpr int THREADS_BOUND = 384;
+constexpr int NUM_EPI_WARPS = 16;
+constexpr int THREADS = 64 + NUM_EPI_WARPS * 32; // 576
+// Eighteen warps put at most five on one SM sub-partition (16K registers): the
+// launch bound is declared for 640 threads so that a thread has 96 registers.
+constexpr int THREADS_BOUND = 640;
 constexpr int GROUP_M2 = 16;                     // tile raster: 16 pair rows share each B tile
 constexpr int MAX_SPLIT = 4;
-constexpr int BOX_COLS = 32;
-constexpr int BOX_BYTES = 32 * BOX_COLS * 4;     // 4 KiB: 32 rows x 32 columns
+constexpr int UNIT = 16;                         // columns of a split tile's unit of ownership
+constexpr int UNIT_BYTES = 32 * UNIT * 4;        // 2 KiB: int32 sums of 32 rows x 16 columns
+constexpr int BOX_BYTES = 2048;                  // output staging per epilogue warp
 constexpr int STAGING = NUM_EPI_WARPS * BOX_BYTES;
 
 template <int BN>
@@ -53,22 +64,24 @@ struct Tile {
   static constexpr int B_BYTES = (BN / 2) * BK * 2;
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
   static constexpr int STAGES = BN == 256 ? 6 : 8;
-  static constexpr int BOXES = BN / 2 / BOX_COLS;            // per epilogue thread
+  static constexpr int COLS = BN / 4;                        // per epilogue warp
+  static constexpr int UNITS = COLS / UNIT;
   static constexpr int TMEM_COLS = 2 * BN;                   // two accumulator buffers
-  static constexpr int SMEM = STAGES * STAGE_BYTES + STAGING + 1024 /*align*/ + 256 /*barriers*/;
+  static constexpr int SMEM = STAGES * STAGE_BYTES + STAGING + 1024 /*align*/ + 512 /*barriers*/;
   static constexpr uint32_t IDESC = (1u << 4)                // D FP32, A and B FP16, K-major, M = 256
                                     | (static_cast<uint32_t>(BN >> 3) << 17)
                                     | (static_cast<uint32_t>((2 * BM) >> 4) << 24);
-  static_assert((2 * STAGES + 7) * 8 <= 256, "barrier area");
-  // partial sums received by a CTA of a split tile: (S - 1) senders x owned boxes x 8 warps
-  static_assert(2 * ((BOXES + 2) / 3) * STAGING <= STAGES * STAGE_BYTES, "split buffers");
-  static_assert(3 * ((BOXES + 3) / 4) * STAGING <= STAGES * STAGE_BYTES, "split buffers");
-  static_assert(((BOXES + 1) / 2) * STAGING <= STAGES * STAGE_BYTES, "split buffers");
+  static_assert((2 * STAGES + 7 + 2 * NUM_EPI_WARPS) * 8 <= 512, "barrier area");
+  // partial sums received by a CTA of a split tile: (S - 1) senders x owned units x 16 warps
+  static_assert(2 * ((UNITS + 2) / 3) * STAGING <= STAGES * STAGE_BYTES, "split buffers");
+  static_assert(3 * ((UNITS + 3) / 4) * STAGING <= STAGES * STAGE_BYTES, "split buffers");
+  static_assert(((UNITS + 1) / 2) * STAGING <= STAGES * STAGE_BYTES, "split buffers");
 };
 
 struct Params {
   Epilogue e;
   int k_steps, num_m2, num_n, num_items, split;
+  int out_piece, res_piece;     // 16: boxes by TMA; else bytes per lane of the warp's copy (8, 4 or 2)
 };
 
 __device__ __forceinline__ void work_coords(const Params& p, int item, int& m2, int& nt) {
@@ -86,44 +99,137 @@ __device__ __forceinline__ void st_cluster_v4(uint32_t addr, int a, int b, int c
                : "memory");
 }
 
-// One box of a warp: FP32 bits in `acc` (this lane's row, 32 columns) through
-// shared memory to the epilogue's layout, then finished and written.
-template <int OUT>
-__device__ __forceinline__ void finish_box(const Epilogue& e, const int32_t* acc, uint8_t* box, int lane, int m_base,
-                                           int n0, float sa) {
-  // 16-byte piece c of row r sits at piece c ^ (r & 7): no bank conflicts either way
-  uint8_t* mine = box + lane * (BOX_COLS * 4);
-#pragma unroll
-  for (int c = 0; c < 8; ++c)
-    *reinterpret_cast<int4*>(mine + ((c ^ (lane & 7)) << 4)) =
-        make_int4(acc[4 * c], acc[4 * c + 1], acc[4 * c + 2], acc[4 * c + 3]);
-  __syncwarp();
-  const int c = lane & 7, n = n0 + 4 * c;
-  const ColumnTerms t = load_columns(e, n);
-#pragma unroll 1
-  for (int half = 0; half < 2; ++half) {
-    const int r0 = half * 16 + (lane >> 3);
-    ResidualWords<OUT> rv[4] = {};
-    if (e.residual) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) rv[i] = load_residual<OUT>(e, m_base + r0 + 4 * i, n);
-    }
-#pragma unroll 1
-    for (int i = 0; i < 4; ++i) {
-      const int r = r0 + 4 * i;
-      const float4 v = *reinterpret_cast<const float4*>(box + r * (BOX_COLS * 4) + ((c ^ (r & 7)) << 4));
-      finish4<OUT>(e, t, v, __shfl_sync(0xffffffffu, sa, r), rv[0], m_base + r, n);
-      rv[0] = rv[1];
-      rv[1] = rv[2];
-      rv[2] = rv[3];
-    }
-  }
-  __syncwarp();                               // box read before it is refilled
+__device__ __forceinline__ void tma_load_box(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];"
+      ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y)
+      : "memory");
 }
 
-template <int OUT, int BN, bool SPLITK>
+// A warp's output box: 32 rows of CPB columns, row r at r * RB bytes, its
+// 16-byte pieces swizzled as the tensor maps have it (64-byte rows: piece
+// ^ (r >> 1) & 3; 32-byte rows: piece ^ (r >> 2) & 1).
+template <int OUT, bool SPLITK>
+struct Box {
+  static constexpr int ES = OUT == CONVROT_FP32 ? 4 : 2;
+  static constexpr int CPB = SPLITK ? UNIT : 64 / ES;
+  static constexpr int RB = CPB * ES;
+  static constexpr int BUFS = BOX_BYTES / (32 * RB);      // boxes in a warp's staging
+  static __device__ __forceinline__ uint32_t piece(int r, int q) {
+    return r * RB + ((q ^ (RB == 64 ? (r >> 1) & 3 : (r >> 2) & 1)) << 4);
+  }
+  static __device__ __forceinline__ uint32_t at(int r, int byte) { return piece(r, byte >> 4) + (byte & 15); }
+};
+
+// Copies a box between shared memory and the matrix, W bytes per lane, rows in
+// turn; elements outside the matrix are skipped (zeros on the way in).
+template <int OUT, bool SPLITK, typename W, bool IN>
+__device__ __forceinline__ void copy_box(const Epilogue& e, uint8_t* box, int lane, int m_base, int nb) {
+  using B = Box<OUT, SPLITK>;
+  constexpr int PER_ROW = B::RB / sizeof(W), ROWS = 32 / PER_ROW;    // lanes per row, rows per step
+  constexpr int EPL = sizeof(W) / B::ES;                              // elements per lane
+  const int n = nb + (lane % PER_ROW) * EPL;
+#pragma unroll 4
+  for (int r = lane / PER_ROW; r < 32; r += ROWS) {
+    W* s = reinterpret_cast<W*>(box + B::at(r, (lane % PER_ROW) * static_cast<int>(sizeof(W))));
+    const bool row = m_base + r < e.M;
+    char* g = IN ? const_cast<char*>(static_cast<const char*>(e.residual)) + ((m_base + r) * e.ld_res + n) * B::ES
+                 : static_cast<char*>(e.out) + ((m_base + r) * e.ld_out + n) * B::ES;
+    if (row && n + EPL <= e.N) {
+      if (IN) *s = *reinterpret_cast<const W*>(g);
+      else *reinterpret_cast<W*>(g) = *s;
+    } else {
+      using T = typename OutT<OUT>::T;
+#pragma unroll
+      for (int j = 0; j < EPL; ++j) {
+        T* se = reinterpret_cast<T*>(s) + j;
+        if (row && n + j < e.N) {
+          if (IN) *se = reinterpret_cast<const T*>(g)[j];
+          else reinterpret_cast<T*>(g)[j] = *se;
+        } else if (IN) {
+          *se = T(0.f);
+        }
+      }
+    }
+  }
+}
+
+template <int OUT, bool SPLITK, bool IN>
+__device__ __forceinline__ void copy_box_by(int piece, const Epilogue& e, uint8_t* box, int lane, int m_base, int nb) {
+  if (piece == 8) copy_box<OUT, SPLITK, uint2, IN>(e, box, lane, m_base, nb);
+  else if (piece == 4) copy_box<OUT, SPLITK, uint32_t, IN>(e, box, lane, m_base, nb);
+  else if constexpr (OUT != CONVROT_FP32) copy_box<OUT, SPLITK, uint16_t, IN>(e, box, lane, m_base, nb);
+}
+
+// What is neutral to the last bit: x + -0 = x and x * 1 = x for every x.
+__device__ const float4 kNoBias = {-0.f, -0.f, -0.f, -0.f}, kNoGate = {1.f, 1.f, 1.f, 1.f};
+
+// Values of a box from acc[0 .. CPB-1] (FP32 bits), in place over the
+// residual's values.  WHOLE: all of its columns lie inside the matrix; the
+// code then has no branches but the one on the residual, so that a box's 32
+// columns per thread overlap.
+template <int OUT, int ACT, bool SPLITK, bool WHOLE, int COLS>
+__device__ __forceinline__ void fill_box(const Epilogue& e, const int32_t (&acc)[COLS], uint8_t* box, int lane, int nb,
+                                         float sa) {
+  using B = Box<OUT, SPLITK>;
+  constexpr int V = 16 / B::ES;                      // columns per 16-byte piece
+  const float* sw = e.w_scale + nb;
+  const float* bias = e.bias ? e.bias + nb : reinterpret_cast<const float*>(&kNoBias);
+  const float* gate = e.gate ? e.gate + nb : reinterpret_cast<const float*>(&kNoGate);
+  const int bstep = e.bias ? 4 : 0, gstep = e.gate ? 4 : 0;
+  constexpr uint32_t kNone = OUT == CONVROT_FP32 ? 0x80000000u : 0x80008000u;     // -0: adding it changes nothing
+#pragma unroll
+  for (int q = 0; q < B::RB / 16; ++q) {
+    uint4* cell = reinterpret_cast<uint4*>(box + B::piece(lane, q));
+    uint4 w = make_uint4(kNone, kNone, kNone, kNone);
+    if (e.residual) w = *cell;
+    const uint32_t rv[4] = {w.x, w.y, w.z, w.w};
+    uint32_t out[4];
+#pragma unroll
+    for (int h = 0; h < V / 4; ++h) {
+      const int j = q * V + 4 * h;
+      float ts[4], tb[4], tg[4];
+      if constexpr (WHOLE) {
+        const float4 a = __ldg(reinterpret_cast<const float4*>(sw + j));
+        const float4 b = __ldg(reinterpret_cast<const float4*>(bias + (j / 4) * bstep));
+        const float4 g = __ldg(reinterpret_cast<const float4*>(gate + (j / 4) * gstep));
+        ts[0] = a.x; ts[1] = a.y; ts[2] = a.z; ts[3] = a.w;
+        tb[0] = b.x; tb[1] = b.y; tb[2] = b.z; tb[3] = b.w;
+        tg[0] = g.x; tg[1] = g.y; tg[2] = g.z; tg[3] = g.w;
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const bool in = nb + j + i < e.N;
+          ts[i] = in ? __ldg(sw + j + i) : 0.f;
+          tb[i] = in ? __ldg(bias + (j / 4) * bstep + i) : 0.f;
+          tg[i] = in ? __ldg(gate + (j / 4) * gstep + i) : 0.f;
+        }
+      }
+      ResidualWords<OUT> r;
+#pragma unroll
+      for (int i = 0; i < 16 / V; ++i) r.w[i] = rv[(16 / V) * h + i];
+      float y[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        y[i] = __fadd_rn(__fmul_rn(__fmul_rn(__int_as_float(acc[j + i]), sa), ts[i]), tb[i]);
+        y[i] = __fadd_rn(__fmul_rn(activate<ACT>(y[i]), tg[i]), residual_value<OUT>(r, i));
+      }
+      if constexpr (OUT == CONVROT_FP32) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) out[i] = __float_as_uint(y[i]);
+      } else {
+        out[2 * h] = to_out2<OUT>(y[0], y[1]);
+        out[2 * h + 1] = to_out2<OUT>(y[2], y[3]);
+      }
+    }
+    *cell = make_uint4(out[0], out[1], out[2], out[3]);
+  }
+}
+
+template <int OUT, int ACT, int BN, bool SPLITK>
 __global__ void __launch_bounds__(THREADS_BOUND, 1)
-fused_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_b, const Params p) {
+fused_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_b,
+             const __grid_constant__ CUtensorMap tmap_out, const __grid_constant__ CUtensorMap tmap_res, const Params p) {
   using L = Tile<BN>;
   constexpr int STAGES = L::STAGES;
   extern __shared__ uint8_t smem_raw[];
@@ -135,6 +241,7 @@ fused_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__
   const uint32_t drain = smem_u32(bars + 2 * STAGES + 4);
   volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(bars + 2 * STAGES + 5);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + 2 * STAGES + 6);
+  const uint32_t resf0 = smem_u32(bars + 2 * STAGES + 7);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
@@ -153,6 +260,7 @@ fused_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__
       mbar_init(acce0 + 8 * b, 2 * NUM_EPI_WARPS);   // epilogue warps of both CTAs of the pair
     }
     mbar_init(drain, 1);
+    for (int w = 0; w < 2 * NUM_EPI_WARPS; ++w) mbar_init(resf0 + 8 * w, 1);   // a warp's residual box has landed
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -269,20 +377,61 @@ fused_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__
     }
   } else {
     // ---------------------------------------------------------------- epilogue
-    const int ew = warp - 2;                  // 0..7
+    const int ew = warp - 2;                  // 0..15
     const int quarter = warp & 3;             // TMEM lanes this warp may access
-    const int col_half = ew >> 2;             // which half of the tile's columns
+    const int col0 = (ew >> 2) * L::COLS;     // this warp's columns of the tile
     const uint32_t lane_addr = static_cast<uint32_t>(quarter * 32) << 16;
-    uint8_t* box = staging + ew * BOX_BYTES;
+    using B = Box<OUT, SPLITK>;
+    constexpr int BOXES = L::COLS / B::CPB;
+    uint8_t* wstage = staging + ew * BOX_BYTES;
+    const uint32_t resf = resf0 + 8 * B::BUFS * ew;
+    const bool out_tma = p.out_piece == 16, res_tma = p.e.residual != nullptr && p.res_piece == 16;
+    // boxes of this warp: `asked` residual boxes were asked for by TMA, `done` are finished; box i uses buffer i % BUFS
+    uint32_t asked = 0, done = 0;
     uint32_t chunk = 0;
     bool ok = true;
     const uint32_t lacce0 = map_to_rank(acce0, leader);   // the even CTA's acc_empty barriers
     for (int tile = cluster_id; tile < p.num_items && ok; tile += num_clusters) {
       int m2, nt;
       work_coords(p, tile, m2, nt);
-      int32_t acc[BN / 2];
+      const int m_base = (2 * m2 + static_cast<int>(half)) * BM + quarter * 32;
+      const int n0 = nt * BN + col0;
+      // box b's residual into the buffer of the warp's `asked`-th box
+      auto request = [&](int b) {
+        if (lane == 0) {
+          const uint32_t buf = asked % B::BUFS;
+          if (out_tma) bulk_wait_read<0>();     // the buffer's last store has read it
+          mbar_arrive_expect_tx(resf + 8 * buf, 32 * B::RB);
+          tma_load_box(smem_u32(wstage + buf * (32 * B::RB)), &tmap_res, resf + 8 * buf, n0 + b * B::CPB, m_base);
+        }
+        ++asked;
+      };
+      const int b_first = SPLITK ? static_cast<int>(pair) : 0;
+      auto wanted = [&](int b) { return b < BOXES && m_base < p.e.M && n0 + b * B::CPB < p.e.N; };
+      // the first boxes' residual comes while the tile is multiplied, the rest waits in L2
+      if (res_tma) {
 #pragma unroll
-      for (int j = 0; j < BN / 2; ++j) acc[j] = 0;
+        for (int i = 0; i < B::BUFS; ++i)
+          if (wanted(b_first + i * S)) request(b_first + i * S);
+      }
+      if (p.e.residual && m_base + lane < p.e.M && n0 < p.e.N) {
+        const char* r = static_cast<const char*>(p.e.residual) + ((m_base + lane) * p.e.ld_res + n0) * B::ES;
+        const char* end = r + min(L::COLS, p.e.N - n0) * B::ES;
+        for (; r < end; r += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(r));
+      }
+      // what the output phase reads, asked for while the tile is multiplied
+      const float sa = m_base + lane < p.e.M ? __ldg(p.e.a_scale + m_base + lane) : 0.f;
+      for (int j = lane; j < L::COLS && n0 + j < p.e.N; j += 32) {
+        warm_l1(p.e.w_scale + n0 + j);
+        if (p.e.bias) warm_l1(p.e.bias + n0 + j);
+        if (p.e.gate) warm_l1(p.e.gate + n0 + j);
+      }
+      // A single chunk is the exact integer sum in FP32 already: its bits are
+      // kept, without the two conversions.
+      const bool keep_bits = !SPLITK && nchunks == 1;
+      int32_t acc[L::COLS];
+#pragma unroll
+      for (int j = 0; j < L::COLS; ++j) acc[j] = 0;
       for (int c = 0; c < nchunks; ++c, ++chunk) {
         const uint32_t buf = chunk & 1u, use = chunk >> 1;
         int got = 1;
@@ -290,14 +439,25 @@ fused_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__
         got = __shfl_sync(0xffffffffu, got, 0);
         if (!got) { ok = false; break; }
         tc_fence_after();
-        const uint32_t t_base = tmem_base + lane_addr + buf * BN + col_half * (BN / 2);
+        const uint32_t t_base = tmem_base + lane_addr + buf * BN + col0;
+        if (keep_bits) {
 #pragma unroll
-        for (int g = 0; g < BN / 32; ++g) {
-          uint32_t r[16];
-          tmem_ld_32x32b_x16(t_base + g * 16, r);
-          tmem_ld_wait();
+          for (int g = 0; g < L::COLS / 16; ++g) {
+            uint32_t r[16];
+            tmem_ld_32x32b_x16(t_base + g * 16, r);
+            tmem_ld_wait();
 #pragma unroll
-          for (int j = 0; j < 16; ++j) acc[g * 16 + j] += __float2int_rn(__uint_as_float(r[j]));   // exact
+            for (int j = 0; j < 16; ++j) acc[g * 16 + j] = static_cast<int32_t>(r[j]);
+          }
+        } else {
+#pragma unroll
+          for (int g = 0; g < L::COLS / 16; ++g) {
+            uint32_t r[16];
+            tmem_ld_32x32b_x16(t_base + g * 16, r);
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 16; ++j) acc[g * 16 + j] += __float2int_rn(__uint_as_float(r[j]));   // exact
+          }
         }
         tc_fence_before();
         __syncwarp();
@@ -306,55 +466,99 @@ fused_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__
       if constexpr (SPLITK) {
         // one tile per cluster: the stages of every CTA are free once all have their sums
         cluster_sync();
-        const int slots = (L::BOXES + S - 1) / S;          // boxes a pair owns, at most
+        const int slots = (L::UNITS + S - 1) / S;          // units a pair owns, at most
         if (ok) {
 #pragma unroll
-          for (int b = 0; b < L::BOXES; ++b) {
+          for (int b = 0; b < L::UNITS; ++b) {
             const uint32_t owner = b % S;
             if (owner == pair) continue;
             const uint32_t from = pair < owner ? pair : pair - 1;
-            const uint32_t local = smem_u32(smem) + ((from * slots + b / S) * NUM_EPI_WARPS + ew) * BOX_BYTES + lane * 16;
+            const uint32_t local = smem_u32(smem) + ((from * slots + b / S) * NUM_EPI_WARPS + ew) * UNIT_BYTES + lane * 16;
             const uint32_t dst = map_to_rank(local, 2 * owner + half);
 #pragma unroll
-            for (int q = 0; q < 8; ++q)
-              st_cluster_v4(dst + q * 512, acc[b * 32 + 4 * q], acc[b * 32 + 4 * q + 1], acc[b * 32 + 4 * q + 2],
-                            acc[b * 32 + 4 * q + 3]);
+            for (int q = 0; q < 4; ++q)
+              st_cluster_v4(dst + q * 512, acc[b * 16 + 4 * q], acc[b * 16 + 4 * q + 1], acc[b * 16 + 4 * q + 2],
+                            acc[b * 16 + 4 * q + 3]);
           }
         }
         cluster_sync();
         if (ok) {
 #pragma unroll
-          for (int b = 0; b < L::BOXES; ++b) {
+          for (int b = 0; b < L::UNITS; ++b) {
             if (b % S != static_cast<int>(pair)) continue;
             for (int from = 0; from < S - 1; ++from) {
-              const uint8_t* src = smem + ((from * slots + b / S) * NUM_EPI_WARPS + ew) * BOX_BYTES + lane * 16;
+              const uint8_t* src = smem + ((from * slots + b / S) * NUM_EPI_WARPS + ew) * UNIT_BYTES + lane * 16;
 #pragma unroll
-              for (int q = 0; q < 8; ++q) {
+              for (int q = 0; q < 4; ++q) {
                 const int4 v = *reinterpret_cast<const int4*>(src + q * 512);
-                acc[b * 32 + 4 * q] += v.x;
-                acc[b * 32 + 4 * q + 1] += v.y;
-                acc[b * 32 + 4 * q + 2] += v.z;
-                acc[b * 32 + 4 * q + 3] += v.w;
+                acc[b * 16 + 4 * q] += v.x;
+                acc[b * 16 + 4 * q + 1] += v.y;
+                acc[b * 16 + 4 * q + 2] += v.z;
+                acc[b * 16 + 4 * q + 3] += v.w;
               }
             }
           }
         }
       }
       if (!ok) break;
-      const int m_base = (2 * m2 + static_cast<int>(half)) * BM + quarter * 32;
-      const int n0 = nt * BN + col_half * (BN / 2);
-      const float sa = (m_base + lane < p.e.M) ? __ldg(p.e.a_scale + m_base + lane) : 0.f;
-      if (m_base < p.e.M) {
+      if (m_base >= p.e.M) continue;
+      if (!keep_bits) {
 #pragma unroll
-        for (int b = 0; b < L::BOXES; ++b) {
-          if (SPLITK && b % S != static_cast<int>(pair)) continue;
-          if (n0 + b * BOX_COLS >= p.e.N) continue;
-#pragma unroll
-          for (int j = 0; j < 32; ++j) acc[b * 32 + j] = __float_as_int(static_cast<float>(acc[b * 32 + j]));
-          finish_box<OUT>(p.e, acc + b * 32, box, lane, m_base, n0 + b * BOX_COLS, sa);
+        for (int j = 0; j < L::COLS; ++j) acc[j] = __float_as_int(static_cast<float>(acc[j]));
+      }
+      // The boxes run through one copy of the code: the box in work is always
+      // acc[0 .. CPB-1], and the others move up behind it.
+#pragma unroll 1
+      for (int b = 0; b < BOXES; ++b) {
+        const int nb = n0 + b * B::CPB;
+        if ((!SPLITK || b % S == static_cast<int>(pair)) && nb < p.e.N) {
+          const uint32_t buf = done % B::BUFS;
+          uint8_t* box = wstage + buf * (32 * B::RB);
+          if (res_tma) {
+            if (asked == done) request(b);
+            // every lane waits: each reads what the load wrote
+            const bool got = mbar_wait(resf + 8 * buf, (done / B::BUFS) & 1u, ERR_WAIT_FULL, abort_flag);
+            if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
+          } else {
+            if (out_tma && lane == 0) bulk_wait_read<B::BUFS - 1>();    // this buffer's last store has read it
+            __syncwarp();
+            if (p.e.residual) {
+              copy_box_by<OUT, SPLITK, true>(p.res_piece, p.e, box, lane, m_base, nb);
+              __syncwarp();
+            }
+          }
+          ++done;
+          if (nb + B::CPB <= p.e.N) fill_box<OUT, ACT, SPLITK, true>(p.e, acc, box, lane, nb, sa);
+          else fill_box<OUT, ACT, SPLITK, false>(p.e, acc, box, lane, nb, sa);
+          if (out_tma) {
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              tma_store_2d(&tmap_out, smem_u32(box), nb, m_base);
+              bulk_commit();
+            }
+          } else {
+            __syncwarp();
+            copy_box_by<OUT, SPLITK, false>(p.out_piece, p.e, box, lane, m_base, nb);
+            // the copy's reads of the box before the next residual lands in it
+            if (res_tma) fence_proxy_async_smem();
+            __syncwarp();
+          }
         }
+#pragma unroll
+        for (int j = 0; j < L::COLS - B::CPB; ++j) acc[j] = acc[j + B::CPB];
       }
     }
+    // every TMA store of this warp must have read its box before the CTA exits,
+    // and residual boxes asked for before an abort must have landed
+    if (lane == 0) {
+      bulk_wait_read<0>();
+      for (; done < asked; ++done) {
+        const uint64_t t0 = globaltimer();
+        while (!mbar_try_wait(resf + 8 * (done % B::BUFS), (done / B::BUFS) & 1u) && globaltimer() - t0 < kWaitLimitNs) {}
+      }
+    }
+    __syncwarp();
   }
 
   tc_fence_before();
@@ -380,10 +584,28 @@ static bool make_map(CUtensorMap* map, const void* base, int rows, int cols, int
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Box map over the output or the residual: 32 rows x CPB columns.
+template <int OUT, bool SPLITK>
+static bool make_box_map(CUtensorMap* map, const void* base, int M, int N, int64_t ld) {
+  using B = Box<OUT, SPLITK>;
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  constexpr CUtensorMapDataType dt = OUT == CONVROT_FP32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                     : OUT == CONVROT_FP16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                           : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  cuuint64_t dims[2] = {static_cast<cuuint64_t>(N), static_cast<cuuint64_t>(M)};
+  cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * B::ES};
+  cuuint32_t box[2] = {static_cast<cuuint32_t>(B::CPB), 32};
+  cuuint32_t estr[2] = {1, 1};
+  return fn(map, dt, 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            B::RB == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 constexpr int kMaxDevices = 64;
 
 // Clusters of 2 * split CTAs of this kernel that are resident at once.
-template <int OUT, int BN, bool SPLITK>
+template <int OUT, int ACT, int BN, bool SPLITK>
 static cudaError_t resident_clusters(int split, int* out) {
   static int known[kMaxDevices][MAX_SPLIT + 1] = {};
   int dev = 0;
@@ -391,7 +613,7 @@ static cudaError_t resident_clusters(int split, int* out) {
   if (e != cudaSuccess) return e;
   int n = dev < kMaxDevices ? known[dev][split] : 0;
   if (n == 0) {
-    auto k = fused_kernel<OUT, BN, SPLITK>;
+    auto k = fused_kernel<OUT, ACT, BN, SPLITK>;
     if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, Tile<BN>::SMEM)) != cudaSuccess) return e;
     int sms = 0;
     if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
@@ -416,17 +638,29 @@ static cudaError_t resident_clusters(int split, int* out) {
   return cudaSuccess;
 }
 
-template <int OUT, int BN, bool SPLITK>
+template <int OUT, int ACT, int BN, bool SPLITK>
 static int launch(const void* a_q, int64_t ld_aq, const void* w_q, int64_t ld_wq, int K_p, Params p, int split,
                   cudaStream_t st) {
   p.split = split;
   p.num_n = (p.e.N + BN - 1) / BN;
   p.num_items = p.num_m2 * p.num_n;
-  CUtensorMap ma, mb;
+  // 16-byte rows go by TMA, others by the warps' copies
+  auto piece = [](const void* base, int64_t ld) {
+    const int64_t es = OUT == CONVROT_FP32 ? 4 : 2;
+    for (int n : {16, 8, 4})
+      if (reinterpret_cast<uintptr_t>(base) % n == 0 && ld * es % n == 0) return n;
+    return 2;
+  };
+  p.out_piece = piece(p.e.out, p.e.ld_out);
+  p.res_piece = p.e.residual ? piece(p.e.residual, p.e.ld_res) : 0;
+  CUtensorMap ma, mb, mo = {}, mr = {};
+  if ((p.out_piece == 16 && !make_box_map<OUT, SPLITK>(&mo, p.e.out, p.e.M, p.e.N, p.e.ld_out)) ||
+      (p.res_piece == 16 && !make_box_map<OUT, SPLITK>(&mr, p.e.residual, p.e.M, p.e.N, p.e.ld_res)))
+    return convrot::record_error("cuTensorMapEncodeTiled failed for the output or the residual");
   if (!make_map(&ma, a_q, p.e.M, K_p, ld_aq, BM) || !make_map(&mb, w_q, p.e.N, K_p, ld_wq, BN / 2))
     return convrot::record_error("cuTensorMapEncodeTiled failed for an operand map");
   int resident = 0;
-  cudaError_t e = resident_clusters<OUT, BN, SPLITK>(split, &resident);
+  cudaError_t e = resident_clusters<OUT, ACT, BN, SPLITK>(split, &resident);
   if (e != cudaSuccess) return convrot::record_cuda_error("fused GEMM set-up", e);
   const int clusters = SPLITK ? p.num_items : (p.num_items < resident ? p.num_items : resident);
   cudaLaunchConfig_t cfg = {};
@@ -440,7 +674,7 @@ static int launch(const void* a_q, int64_t ld_aq, const void* w_q, int64_t ld_wq
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   cfg.gridDim = dim3(clusters * 2 * split);
-  e = cudaLaunchKernelEx(&cfg, fused_kernel<OUT, BN, SPLITK>, ma, mb, p);
+  e = cudaLaunchKernelEx(&cfg, fused_kernel<OUT, ACT, BN, SPLITK>, ma, mb, mo, mr, p);
   return e == cudaSuccess ? CONVROT_OK : convrot::record_cuda_error("fused GEMM launch", e);
 }
 
@@ -449,7 +683,7 @@ struct Shape {
   int bn, split;
 };
 
-template <int OUT>
+template <int OUT, int ACT>
 static int pick_shape(const Params& p, Shape* best) {
   // model of a tile's time in microseconds (a 64-deep step of a 256- and a 128-wide tile; joining a split tile)
   constexpr double step256 = 0.33, step128 = 0.20, join = 2.0;
@@ -460,10 +694,10 @@ static int pick_shape(const Params& p, Shape* best) {
     for (int split = 1; split <= MAX_SPLIT; ++split) {
       if (split > 1 && p.k_steps < 8 * split) break;
       int resident = 0;
-      cudaError_t e = bn == 256 ? (split == 1 ? resident_clusters<OUT, 256, false>(1, &resident)
-                                              : resident_clusters<OUT, 256, true>(split, &resident))
-                                : (split == 1 ? resident_clusters<OUT, 128, false>(1, &resident)
-                                              : resident_clusters<OUT, 128, true>(split, &resident));
+      cudaError_t e = bn == 256 ? (split == 1 ? resident_clusters<OUT, ACT, 256, false>(1, &resident)
+                                              : resident_clusters<OUT, ACT, 256, true>(split, &resident))
+                                : (split == 1 ? resident_clusters<OUT, ACT, 128, false>(1, &resident)
+                                              : resident_clusters<OUT, ACT, 128, true>(split, &resident));
       if (e != cudaSuccess) return convrot::record_cuda_error("fused GEMM set-up", e);
       if (split > 1 && items > resident) break;
       const int rounds = (items + resident - 1) / resident, steps = (p.k_steps + split - 1) / split;
@@ -477,34 +711,44 @@ static int pick_shape(const Params& p, Shape* best) {
   return CONVROT_OK;
 }
 
-template <int OUT>
-static int launch_out(const void* a_q, int64_t ld_aq, const void* w_q, int64_t ld_wq, int K_p, Params p,
+template <int OUT, int ACT>
+static int launch_act(const void* a_q, int64_t ld_aq, const void* w_q, int64_t ld_wq, int K_p, Params p,
                       cudaStream_t st) {
   Shape s = {256, 1};
-  const int r = pick_shape<OUT>(p, &s);
+  const int r = pick_shape<OUT, ACT>(p, &s);
   if (r != CONVROT_OK) return r;
   if (s.bn == 256)
-    return s.split == 1 ? launch<OUT, 256, false>(a_q, ld_aq, w_q, ld_wq, K_p, p, 1, st)
-                        : launch<OUT, 256, true>(a_q, ld_aq, w_q, ld_wq, K_p, p, s.split, st);
-  return s.split == 1 ? launch<OUT, 128, false>(a_q, ld_aq, w_q, ld_wq, K_p, p, 1, st)
-                      : launch<OUT, 128, true>(a_q, ld_aq, w_q, ld_wq, K_p, p, s.split, st);
+    return s.split == 1 ? launch<OUT, ACT, 256, false>(a_q, ld_aq, w_q, ld_wq, K_p, p, 1, st)
+                        : launch<OUT, ACT, 256, true>(a_q, ld_aq, w_q, ld_wq, K_p, p, s.split, st);
+  return s.split == 1 ? launch<OUT, ACT, 128, false>(a_q, ld_aq, w_q, ld_wq, K_p, p, 1, st)
+                      : launch<OUT, ACT, 128, true>(a_q, ld_aq, w_q, ld_wq, K_p, p, s.split, st);
 }
 
-int gemm_many(const void* a_q, int64_t ld_aq, const void* w_q, int64_t ld_wq, int K_p, const Epilogue& ep,
-              convrot_dtype out_dtype, cudaStream_t st) {
+// This file is compiled once per output type (CONVROT_FUSED_OUT): the
+// activation is a compile-time choice too, since all of them in one kernel
+// exceed its registers.
+#ifndef CONVROT_FUSED_OUT
+#error "compile with -DCONVROT_FUSED_OUT=<convrot_dtype>"
+#endif
+
+template <>
+int gemm_many<CONVROT_FUSED_OUT>(const void* a_q, int64_t ld_aq, const void* w_q, int64_t ld_wq, int K_p,
+                                 const Epilogue& ep, cudaStream_t st) {
+  constexpr int OUT = CONVROT_FUSED_OUT;
   Params p = {};
   p.e = ep;
   p.k_steps = K_p / BK;
   p.num_m2 = (ep.M + 2 * BM - 1) / (2 * BM);
-  switch (out_dtype) {
-    case CONVROT_BF16: return launch_out<CONVROT_BF16>(a_q, ld_aq, w_q, ld_wq, K_p, p, st);
-    case CONVROT_FP16: return launch_out<CONVROT_FP16>(a_q, ld_aq, w_q, ld_wq, K_p, p, st);
-    default: return launch_out<CONVROT_FP32>(a_q, ld_aq, w_q, ld_wq, K_p, p, st);
+  switch (ep.act) {
+    case CONVROT_ACT_RELU: return launch_act<OUT, CONVROT_ACT_RELU>(a_q, ld_aq, w_q, ld_wq, K_p, p, st);
+    case CONVROT_ACT_SILU: return launch_act<OUT, CONVROT_ACT_SILU>(a_q, ld_aq, w_q, ld_wq, K_p, p, st);
+    case CONVROT_ACT_GELU: return launch_act<OUT, CONVROT_ACT_GELU>(a_q, ld_aq, w_q, ld_wq, K_p, p, st);
+    case CONVROT_ACT_GELU_TANH: return launch_act<OUT, CONVROT_ACT_GELU_TANH>(a_q, ld_aq, w_q, ld_wq, K_p, p, st);
+    default: return launch_act<OUT, CONVROT_ACT_NONE>(a_q, ld_aq, w_q, ld_wq, K_p, p, st);
   }
 }
 
-}  // namespace crfused
+template <>
+cudaError_t take_fused_error_word<CONVROT_FUSED_OUT>(int* v) { return crgemm::take_error_word(v); }
 
-namespace convrot {
-cudaError_t take_fused_error_word(int* v) { return crgemm::take_error_word(v); }
-}  // namespace convrot
+}  // namespace crfused

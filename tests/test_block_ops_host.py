@@ -1,6 +1,7 @@
 """Host-side refusals of rms_norm_quant, qk_norm_rope and gemm_fused: every
 bad argument is turned away before anything reaches the GPU."""
 import ctypes
+import math
 
 import pytest
 import torch
@@ -103,33 +104,52 @@ def test_gemm_fused_rejects_bad_arguments(lib):
 
 
 def test_binding_refuses_wrong_tensors(lib):
-    # on the CPU every tensor is already wrong; shapes and types are checked before that
     f32, f16, i32 = torch.float32, torch.float16, torch.int32
-    x, q, s = torch.zeros(4, 300), torch.zeros(4, 512, dtype=f16), torch.zeros(4)
-    with pytest.raises(ValueError, match="x has shape"):
-        cr.rms_norm_quant(x, 400, q, s)
-    with pytest.raises(ValueError, match="contiguous"):
-        cr.rms_norm_quant(torch.zeros(300, 4).t(), 300, q, s)
-    with pytest.raises(ValueError, match="CUDA"):
-        cr.rms_norm_quant(x, 300, q, s)
-    with pytest.raises(ValueError, match="w_q is"):
-        cr.gemm_fused(_fake(4, 256, f16), s, _fake(8, 256, torch.int8), torch.zeros(8), _fake(4, 8, f32))
-    with pytest.raises(ValueError, match="must be a"):
-        cr.qk_norm_rope(torch.zeros(4, 2, 8), None, torch.zeros(4, 1, dtype=i32), torch.zeros(4, dtype=torch.float64), [4],
-                        torch.zeros(4, 2, 9), None)
+    s4 = _Fake((4,), f32)
+    x, q = _Fake((4, 300), f32), _Fake((4, 512), f16)
+    for bad in (_Fake((4, 299), f32), _Fake((3, 300), f32), _Fake((4, 300), f32, (1, 4)), _Fake((4, 300), f16),
+                _Fake((4, 300), f32, cuda=False), _Fake((300,), f32)):
+        with pytest.raises(ValueError, match="residual must be"):
+            cr.rms_norm_quant(x, 300, q, s4, residual=bad)
+    with pytest.raises(ValueError, match="a_scale must be"):
+        cr.rms_norm_quant(x, 300, q, _Fake((5,), f32))
+    with pytest.raises(ValueError, match="a_q must be"):
+        cr.rms_norm_quant(x, 300, _Fake((4, 512), f32), s4)
+    with pytest.raises(ValueError, match="w_q must be"):          # one kind of codes for both operands
+        cr.gemm_fused(_Fake((4, 256), f16), s4, _Fake((8, 256), torch.int8), _Fake((8,), f32), _Fake((4, 8), f32))
+    with pytest.raises(ValueError, match="bias must be"):
+        cr.gemm_fused(_Fake((4, 256), f16), s4, _Fake((8, 256), f16), _Fake((8,), f32), _Fake((4, 8), f32),
+                      bias=_Fake((8,), f16))
+    pos, freq = _Fake((4, 1), i32), _Fake((4,), torch.float64)
+    h = _Fake((4, 2, 8), f16)
+    with pytest.raises(ValueError, match="q_out must be"):
+        cr.qk_norm_rope(h, None, pos, freq, [4], _Fake((4, 2, 9), f16), None)
+    with pytest.raises(ValueError, match="pos must be"):
+        cr.qk_norm_rope(h, None, _Fake((4, 1), torch.int64), freq, [4], h, None)
+    with pytest.raises(ValueError, match="inv_freq must be"):
+        cr.qk_norm_rope(h, None, pos, _Fake((4,), f32), [4], h, None)
     with pytest.raises(ValueError, match="belong together"):
-        cr.qk_norm_rope(torch.zeros(4, 2, 8), torch.zeros(4, 2, 8), torch.zeros(4, 1, dtype=i32),
-                        torch.zeros(4, dtype=torch.float64), [4], torch.zeros(4, 2, 8), None)
+        cr.qk_norm_rope(h, h, pos, freq, [4], h, None)
 
 
-class _fake:
-    """A tensor that says it is on the GPU."""
+class _Fake:
+    """What a CUDA tensor says of itself; no call below gets past the checks."""
 
-    def __init__(self, rows, cols, dtype):
-        self.shape, self.dtype, self.is_cuda = (rows, cols), dtype, True
+    def __init__(self, shape, dtype, strides=None, cuda=True):
+        self.shape, self.dtype, self.is_cuda, self.device = shape, dtype, cuda, "cuda:0" if cuda else "cpu"
+        self.strides = strides or tuple(math.prod(shape[i + 1:]) for i in range(len(shape)))
 
-    def dim(self):
-        return 2
+    def stride(self):
+        return self.strides
 
-    def stride(self, d):
-        return (self.shape[1], 1)[d]
+    def numel(self):
+        return math.prod(self.shape)
+
+    def is_contiguous(self):
+        return self.strides == tuple(math.prod(self.shape[i + 1:]) for i in range(len(self.shape)))
+
+    def data_ptr(self):
+        return P
+
+    def get_device(self):
+        return 0
