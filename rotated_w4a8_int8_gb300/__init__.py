@@ -34,7 +34,7 @@ EXPORTS = ("convrot_padded_k", "convrot_status_string", "convrot_prepare_weight"
            "convrot_gemm_fused")
 
 _lib = None
-_types = None
+_block_ops = None
 
 
 class ConvRotError(RuntimeError):
@@ -142,58 +142,30 @@ def _codes_fmt(t) -> int:
     return {torch.int8: CODES_S8, torch.float16: CODES_F16}[t.dtype]
 
 
-# A call of the operators below costs the host some microseconds, more than a
-# small kernel takes: each tensor is checked and its pointer and pitch taken in
-# one go, and a refusal is worded only once there is one.
 def _refuse(fn: str, name: str, t, need: str):
     raise ValueError(f"{fn}: {name} must be {need}, not {t.dtype} {tuple(t.shape)} with strides {tuple(t.stride())} "
                      f"on {t.device}")
 
 
-def _matrix(fn: str, name: str, t, rows: int, cols: int, dtype) -> tuple[int, int]:
-    """Pointer and row pitch of a device matrix of `dtype`, rows x at least cols, with contiguous rows."""
-    if t is None:
-        return 0, 0
-    shape, stride = t.shape, t.stride()
-    if (len(shape) != 2 or shape[0] != rows or shape[1] < cols or (stride[1] != 1 and cols > 1) or t.dtype != dtype
-            or not t.is_cuda):
-        _refuse(fn, name, t, f"a {dtype} CUDA matrix [{rows}, >= {cols}] with contiguous rows")
-    return t.data_ptr(), stride[0] if rows > 1 else max(stride[0], shape[1])
-
-
-def _vector(fn: str, name: str, t, n: int, dtype) -> int:
-    """Pointer of a contiguous device vector of n values of `dtype`; 0 for None."""
-    if t is None:
-        return 0
-    if t.numel() != n or t.dtype != dtype or not t.is_cuda or not t.is_contiguous():
-        _refuse(fn, name, t, f"a contiguous {dtype} CUDA vector of {n}")
-    return t.data_ptr()
-
-
-def _dtypes():
-    """torch, {storage type: its code} and {codes' type: its code}, looked up once."""
-    global _types
-    if _types is None:
+def _operators():
+    """The compiled marshalling of the block operators (csrc/marshal.c), bound to the library once."""
+    global _block_ops
+    if _block_ops is None:
         import torch
-        _types = (torch, {torch.bfloat16: BF16, torch.float16: FP16, torch.float32: FP32},
-                  {torch.int8: CODES_S8, torch.float16: CODES_F16})
-    return _types
+        lib = load_library()
+        try:
+            from . import _marshal as m
+        except ImportError as e:
+            raise ImportError("the marshalling module is not built: run __graft_entry__.build() first") from e
 
-
-def _code(fn: str, name: str, t, codes) -> int:
-    code = codes.get(t.dtype)
-    if code is None:
-        _refuse(fn, name, t, "one of " + ", ".join(str(d) for d in codes))
-    return code
-
-
-def _stream_of(t, stream) -> int:
-    """The given stream, or the current one of the tensor's device."""
-    if stream is not None:
-        return int(getattr(stream, "cuda_stream", stream))
-    torch = _dtypes()[0]
-    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    return raw(t.get_device()) if raw is not None else torch.cuda.current_stream(t.device).cuda_stream
+        def current(device: int) -> int:
+            return torch.cuda.current_stream(device).cuda_stream
+        m.bind(*(ctypes.cast(f, ctypes.c_void_p).value
+                 for f in (lib.convrot_rms_norm_quant, lib.convrot_qk_norm_rope, lib.convrot_gemm_fused)),
+               _refuse, getattr(torch._C, "_cuda_getCurrentRawStream", current), torch.bfloat16, torch.float16,
+               torch.float32, torch.float64, torch.int8, torch.int32)
+        _block_ops = m
+    return _block_ops
 
 
 def prepare_weight(w_fp4, w_sf, w_tensor_scale, K: int, w_q, w_scale, w_norm=None, stream=None) -> None:
@@ -242,14 +214,9 @@ def rms_norm_quant(x, K: int, a_q, a_scale, residual=None, h=None, weight=None, 
     """convrot_rms_norm_quant: x bf16/fp16/fp32 [M, >=K], residual and h None or the same type [M, >=K] (h receives
     x + residual and may be either of them), weight None or float32 [K], a_q int8 or float16 [M, >=K_p],
     a_scale float32 [M], a_norm None or float32 [M]."""
-    torch, storage, codes = _dtypes()
-    fn, M, K, dt = "rms_norm_quant", x.shape[0], int(K), x.dtype
-    dtype, fmt = _code(fn, "x", x, storage), _code(fn, "a_q", a_q, codes)
-    _check("convrot_rms_norm_quant", (_lib or load_library()).convrot_rms_norm_quant(
-        (px := _matrix(fn, "x", x, M, K, dt))[0], dtype, px[1], *_matrix(fn, "residual", residual, M, K, dt),
-        *_matrix(fn, "h", h, M, K, dt), _vector(fn, "weight", weight, K, torch.float32), eps, M, K,
-        (pq := _matrix(fn, "a_q", a_q, M, K, a_q.dtype))[0], fmt, pq[1], _vector(fn, "a_scale", a_scale, M, torch.float32),
-        _vector(fn, "a_norm", a_norm, M, torch.float32), _stream_of(x, stream)))
+    status = (_block_ops or _operators()).rms_norm_quant(x, K, a_q, a_scale, residual, h, weight, eps, a_norm, stream)
+    if status:
+        _check("convrot_rms_norm_quant", status)
 
 
 def rope_inv_freq(axis_pairs, theta: float = 10000.0) -> list[float]:
@@ -266,26 +233,10 @@ def qk_norm_rope(q, k, pos, inv_freq, axis_pairs, q_out, k_out, q_weight=None, k
     """convrot_qk_norm_rope: q and k bf16/fp16/fp32 [M, heads, D] views (values of a head contiguous; k and k_out may
     be None), q_out and k_out of the same shapes and type (may be q and k themselves), pos int32 [M, axes],
     inv_freq float64 [sum(axis_pairs)], axis_pairs pairs per axis, q_weight / k_weight None or float32 [D]."""
-    torch, storage, _ = _dtypes()
-    fn, (M, heads_q, D), dt = "qk_norm_rope", q.shape, q.dtype
-    heads_k = 0 if k is None else k.shape[1]
-    if (k is None) != (k_out is None):
-        raise ValueError(f"{fn}: k and k_out belong together")
-
-    def view(name, t, heads):
-        if t is None:
-            return 0, 0, 0
-        stride = t.stride()
-        if t.shape != (M, heads, D) or t.dtype != dt or not t.is_cuda or (stride[2] != 1 and D > 1):
-            _refuse(fn, name, t, f"a {dt} CUDA tensor {(M, heads, D)} with contiguous heads")
-        return t.data_ptr(), stride[0], stride[1]
-    axes = len(axis_pairs)
-    _check("convrot_qk_norm_rope", (_lib or load_library()).convrot_qk_norm_rope(
-        *view("q", q, heads_q), *view("q_out", q_out, heads_q), heads_q, _vector(fn, "q_weight", q_weight, D, torch.float32),
-        *view("k", k, heads_k), *view("k_out", k_out, heads_k), heads_k, _vector(fn, "k_weight", k_weight, D, torch.float32),
-        _code(fn, "q", q, storage), M, D, *_matrix(fn, "pos", pos, M, axes, torch.int32),
-        (ctypes.c_int * axes)(*axis_pairs), axes, _vector(fn, "inv_freq", inv_freq, sum(axis_pairs), torch.float64), eps,
-        bool(interleaved), _stream_of(q, stream)))
+    status = (_block_ops or _operators()).qk_norm_rope(q, k, pos, inv_freq, axis_pairs, q_out, k_out, q_weight, k_weight,
+                                                     eps, interleaved, stream)
+    if status:
+        _check("convrot_qk_norm_rope", status)
 
 
 def gemm_fused(a_q, a_scale, w_q, w_scale, out, K_p: int | None = None, bias=None, act: int = ACT_NONE, gate=None,
@@ -293,16 +244,10 @@ def gemm_fused(a_q, a_scale, w_q, w_scale, out, K_p: int | None = None, bias=Non
     """convrot_gemm_fused: a_q and w_q codes [M, >=K_p] and [N, >=K_p], both float16 or (M <= FEW_TOKENS) both int8,
     out bf16/fp16/fp32 [M, >=N] = residual + gate * act(dequantised product + bias); bias and gate None or
     float32 [N], act an ACT_* code, residual None or out's type [M, >=N] (may be out)."""
-    torch, storage, codes = _dtypes()
-    fn, M, N, f32 = "gemm_fused", a_q.shape[0], w_q.shape[0], torch.float32
-    K_p = a_q.shape[1] if K_p is None else int(K_p)
-    fmt, dtype = _code(fn, "a_q", a_q, codes), _code(fn, "out", out, storage)
-    _check("convrot_gemm_fused", (_lib or load_library()).convrot_gemm_fused(
-        *_matrix(fn, "a_q", a_q, M, K_p, a_q.dtype), _vector(fn, "a_scale", a_scale, M, f32),
-        *_matrix(fn, "w_q", w_q, N, K_p, a_q.dtype), _vector(fn, "w_scale", w_scale, N, f32), fmt,
-        _vector(fn, "bias", bias, N, f32), act, _vector(fn, "gate", gate, N, f32),
-        *_matrix(fn, "residual", residual, M, N, out.dtype), M, N, K_p,
-        (po := _matrix(fn, "out", out, M, N, out.dtype))[0], dtype, po[1], _stream_of(out, stream)))
+    status = (_block_ops or _operators()).gemm_fused(a_q, a_scale, w_q, w_scale, out, K_p, bias, act, gate, residual,
+                                                   stream)
+    if status:
+        _check("convrot_gemm_fused", status)
 
 
 def widen_codes(src, dst, cols: int | None = None, stream=None) -> None:

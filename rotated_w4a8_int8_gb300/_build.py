@@ -10,12 +10,14 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libconvrot.so")
+MARSHAL = os.path.join(HERE, "_marshal.so")
 # (source, object, defines): quant.cu is compiled twice, once without and once
 # with the kernels that write code-norm bounds; gemm_fused.cu once per output type
 SOURCES = [("api.cu", "api", []), ("quant.cu", "quant", []),
@@ -48,15 +50,31 @@ def _compile(unit, extra: list[str]) -> str:
     return obj
 
 
+def _compile_marshal(_=None) -> None:
+    """The CPython extension that marshals the block operators' arguments."""
+    cc = shutil.which("gcc") or shutil.which("cc")
+    if cc is None:
+        raise RuntimeError("no C compiler found for the marshalling module")
+    tmp = MARSHAL + ".tmp"
+    cmd = [cc, "-O2", "-std=c11", "-shared", "-fPIC", "-I", sysconfig.get_paths()["include"],
+           os.path.join(CSRC, "marshal.c"), "-o", tmp]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"marshal.c failed to compile:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, MARSHAL)
+
+
 def build(verbose_ptxas: bool = False, force: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [os.path.join(ROOT, "include", "convrot.h")]
-    if (not force and os.path.exists(LIB)
-            and os.path.getmtime(LIB) > max(os.path.getmtime(d) for d in deps)):
+    newest = max(os.path.getmtime(d) for d in deps)
+    if not force and all(os.path.exists(f) and os.path.getmtime(f) > newest for f in (LIB, MARSHAL)):
         return LIB
     extra = ["-Xptxas", "-v"] if verbose_ptxas else []
-    with cf.ThreadPoolExecutor(len(SOURCES)) as ex:
+    with cf.ThreadPoolExecutor(len(SOURCES) + 1) as ex:
+        marshal = ex.submit(_compile_marshal)
         objs = list(ex.map(lambda s: _compile(s, extra), SOURCES))
+        marshal.result()
     tmp = LIB + ".tmp"
     cmd = [nvcc(), *ARCH, "-shared", "-cudart", "shared", *objs, "-o", tmp]
     r = subprocess.run(cmd, capture_output=True, text=True)

@@ -3,7 +3,7 @@
 // One to CONVROT_FEW_TOKENS token rows against a whole weight: each weight
 // code is read once and used M times, so the bytes of the weight bound it.
 //
-// A CTA owns 16 MT weight rows; its eight warps take the K units (64 bytes of
+// A CTA owns 16 weight rows; its eight warps take the K units (64 bytes of
 // every row) in turn.  The products run on the warp-level tensor instruction
 // (mma.sync m16n8k16, FP16 in, FP32 out) with the weight as its 16-row operand
 // and the tokens, eight to a tile, as the other one: at one to a few dozen
@@ -27,6 +27,11 @@ namespace crfused {
 
 constexpr int WARPS = 8;
 constexpr int EXACT_CODES = 1024;        // codes per exact FP32 partial sum
+constexpr int ROWS = 16;                 // weight rows per CTA
+// What keeps HBM busy is loads in flight: three CTAs per SM where the sums
+// leave the registers for it (two measured 20% slower with 8 tokens).
+template <int NT>
+constexpr int CTAS_PER_SM = NT <= 2 ? 3 : 2;
 
 // 16 bytes of a weight row: read once, kept out of L1.
 __device__ __forceinline__ uint4 load_weight(const char* p) {
@@ -71,14 +76,13 @@ __device__ __forceinline__ int ld_cluster(const int* p, uint32_t rank) {
   return v;
 }
 
-// NT tiles of eight tokens, MT tiles of 16 weight rows, U units in flight per
-// warp.  A cluster of `split` CTAs shares the K units of a row tile; each
+// NT tiles of eight tokens, U units in flight per warp.  A cluster of `split` CTAs shares the K units of a row tile; each
 // finishes its part of the tile's outputs from all of their sums.
-template <bool S8, int NT, int MT, int U>
-__global__ void __launch_bounds__(32 * WARPS, MT == 1 ? 3 : 1)
+template <bool S8, int NT, int U>
+__global__ void __launch_bounds__(32 * WARPS, CTAS_PER_SM<NT>)
 few_kernel(const char* __restrict__ a_q, int64_t a_pitch, const char* __restrict__ w_q, int64_t w_pitch, int units,
            int split, int out_dtype, const Epilogue e) {
-  constexpr int ROWS = 16 * MT, TOKENS = 8 * NT, PITCH = ROWS + 4;   // pad: no bank conflicts below
+  constexpr int TOKENS = 8 * NT, PITCH = ROWS + 4;   // pad: no bank conflicts below
   constexpr int STEPS = S8 ? 4 : 2, CODES = S8 ? 64 : 32;            // per unit of 64 bytes
   __shared__ __align__(16) int sums[TOKENS * PITCH];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
@@ -100,24 +104,24 @@ few_kernel(const char* __restrict__ a_q, int64_t a_pitch, const char* __restrict
                                                     (m * e.ld_res + n) * (out_dtype == CONVROT_FP32 ? 4 : 2)));
   }
   // rows and tokens past the matrix repeat the last one; their sums are not used
-  const char *wr[2 * MT], *ar[NT];
+  const char *wr[2], *ar[NT];
 #pragma unroll
-  for (int i = 0; i < 2 * MT; ++i) wr[i] = w_q + min(n0 + 8 * i + g, e.N - 1) * w_pitch + 16 * q;
+  for (int i = 0; i < 2; ++i) wr[i] = w_q + min(n0 + 8 * i + g, e.N - 1) * w_pitch + 16 * q;
 #pragma unroll
   for (int t = 0; t < NT; ++t) ar[t] = a_q + min(8 * t + g, e.M - 1) * a_pitch + 16 * q;
-  int total[MT][NT][4] = {};
+  int total[NT][4] = {};
   const int wstep = WARPS * split;                       // the tile's warps take the units in turn
   for (int first = part * WARPS + warp; first < units; first += wstep * (EXACT_CODES / CODES)) {
     const int end = min(units, first + wstep * (EXACT_CODES / CODES));
-    float acc[MT][NT][4] = {};
+    float acc[NT][4] = {};
     for (int u0 = first; u0 < end; u0 += wstep * U) {
-      uint4 wv[U][2 * MT], av[U][NT];
+      uint4 wv[U][2], av[U][NT];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int at = u0 + u * wstep;
         if (at < end) {
 #pragma unroll
-          for (int i = 0; i < 2 * MT; ++i) wv[u][i] = load_weight(wr[i] + static_cast<int64_t>(at) * 64);
+          for (int i = 0; i < 2; ++i) wv[u][i] = load_weight(wr[i] + static_cast<int64_t>(at) * 64);
 #pragma unroll
           for (int t = 0; t < NT; ++t) av[u][t] = __ldg(reinterpret_cast<const uint4*>(ar[t] + static_cast<int64_t>(at) * 64));
         }
@@ -130,32 +134,24 @@ few_kernel(const char* __restrict__ a_q, int64_t a_pitch, const char* __restrict
           uint32_t b[NT][2];
 #pragma unroll
           for (int t = 0; t < NT; ++t) step_words<S8>(av[u][t], s, b[t][0], b[t][1]);
+          uint32_t a0, a1, a2, a3;
+          step_words<S8>(wv[u][0], s, a0, a2);
+          step_words<S8>(wv[u][1], s, a1, a3);
 #pragma unroll
-          for (int i = 0; i < MT; ++i) {
-            uint32_t a0, a1, a2, a3;
-            step_words<S8>(wv[u][2 * i], s, a0, a2);
-            step_words<S8>(wv[u][2 * i + 1], s, a1, a3);
-#pragma unroll
-            for (int t = 0; t < NT; ++t) mma16816(acc[i][t], a0, a1, a2, a3, b[t][0], b[t][1]);
-          }
+          for (int t = 0; t < NT; ++t) mma16816(acc[t], a0, a1, a2, a3, b[t][0], b[t][1]);
         }
       }
     }
 #pragma unroll
-    for (int i = 0; i < MT; ++i)
+    for (int t = 0; t < NT; ++t)
 #pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) total[i][t][j] += __float2int_rn(acc[i][t][j]);     // exact
+      for (int j = 0; j < 4; ++j) total[t][j] += __float2int_rn(acc[t][j]);     // exact
   }
   __syncthreads();                                       // sums are zero
 #pragma unroll
-  for (int i = 0; i < MT; ++i)
+  for (int t = 0; t < NT; ++t)
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        atomicAdd(&sums[(8 * t + 2 * q + (j & 1)) * PITCH + 16 * i + g + 8 * (j >> 1)], total[i][t][j]);
+    for (int j = 0; j < 4; ++j) atomicAdd(&sums[(8 * t + 2 * q + (j & 1)) * PITCH + g + 8 * (j >> 1)], total[t][j]);
   if (split > 1) crgemm::cluster_sync();
   else __syncthreads();
   for (int i = mine; i < groups; i += 32 * WARPS * split) {
@@ -188,16 +184,16 @@ few_kernel(const char* __restrict__ a_q, int64_t a_pitch, const char* __restrict
   if (split > 1) crgemm::cluster_sync();                 // the peers have read this CTA's sums
 }
 
-template <bool S8, int NT, int MT, int U>
+template <bool S8, int NT, int U>
 static cudaError_t launch_few(const void* a_q, int64_t ld_aq, const void* w_q, int64_t ld_wq, int K_p, int out_dtype,
                               const Epilogue& e, cudaStream_t st) {
   constexpr int es = S8 ? 1 : 2;
-  const int tiles = (e.N + 16 * MT - 1) / (16 * MT), units = K_p * es / 64;
+  const int tiles = (e.N + ROWS - 1) / ROWS, units = K_p * es / 64;
   // Few row tiles: up to eight CTAs share one, as long as all fit the GPU at
-  // once (152 SMs, FIT each) and every warp keeps a full batch of loads.
-  constexpr int FIT = MT == 1 ? 3 : 1;
+  // once (152 SMs) and every warp keeps a full batch of loads.  One token,
+  // 300 x 20480 S8 codes: 17.3 us without, 6.2 us with it.
   int split = 1;
-  while (split < 8 && tiles * 2 * split <= 152 * FIT && units >= 2 * split * WARPS * U) split *= 2;
+  while (split < 8 && tiles * 2 * split <= 152 * CTAS_PER_SM<NT> && units >= 2 * split * WARPS * U) split *= 2;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -208,20 +204,23 @@ static cudaError_t launch_few(const void* a_q, int64_t ld_aq, const void* w_q, i
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = split > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, few_kernel<S8, NT, MT, U>, static_cast<const char*>(a_q), ld_aq * es,
+  return cudaLaunchKernelEx(&cfg, few_kernel<S8, NT, U>, static_cast<const char*>(a_q), ld_aq * es,
                             static_cast<const char*>(w_q), ld_wq * es, units, split, out_dtype, e);
 }
+
+// FP16 codes of 17 to 64 tokens: up to this weight size this kernel is the
+// faster one (32 tokens: 1000 x 2048 6.1 us against 11.6, 300 x 20480 10.7
+// against 32.5, 5376 x 5376 28.4 against 26.2; 64 tokens: 9.3 against 11.8,
+// 18.4 against 32.7, 49.5 against 26.7).
+constexpr int64_t kFewBytes = 16 << 20;
 
 template <bool S8>
 static cudaError_t launch_tokens(const void* a_q, int64_t ld_aq, const void* w_q, int64_t ld_wq, int K_p, int out_dtype,
                                  const Epilogue& e, cudaStream_t st) {
-  if (e.M <= 8) return launch_few<S8, 1, 1, 3>(a_q, ld_aq, w_q, ld_wq, K_p, out_dtype, e, st);
-  if (e.M <= 16) return launch_few<S8, 2, 1, 2>(a_q, ld_aq, w_q, ld_wq, K_p, out_dtype, e, st);
-  if constexpr (S8) {
-    if (e.M <= 32) return launch_few<S8, 4, 2, 2>(a_q, ld_aq, w_q, ld_wq, K_p, out_dtype, e, st);
-    return launch_few<S8, 8, 2, 1>(a_q, ld_aq, w_q, ld_wq, K_p, out_dtype, e, st);
-  }
-  return cudaErrorInvalidValue;                          // FP16 codes of more tokens go to gemm_many
+  if (e.M <= 8) return launch_few<S8, 1, 3>(a_q, ld_aq, w_q, ld_wq, K_p, out_dtype, e, st);
+  if (e.M <= 16) return launch_few<S8, 2, 2>(a_q, ld_aq, w_q, ld_wq, K_p, out_dtype, e, st);
+  if (e.M <= 32) return launch_few<S8, 4, 2>(a_q, ld_aq, w_q, ld_wq, K_p, out_dtype, e, st);
+  return launch_few<S8, 8, 1>(a_q, ld_aq, w_q, ld_wq, K_p, out_dtype, e, st);
 }
 
 int gemm_few(const void* a_q, int64_t ld_aq, const void* w_q, int64_t ld_wq, convrot_codes fmt, int K_p,
@@ -271,7 +270,9 @@ extern "C" int convrot_gemm_fused(const void* a_q, int64_t ld_aq, const float* a
   e.act = act;
   e.vec_out = !off(out, 4 * es) && ld_out % 4 == 0;
   e.vec_res = !off(residual, 4 * es) && ld_residual % 4 == 0;
-  if (fmt == CONVROT_CODES_S8 || M <= 16) return gemm_few(a_q, ld_aq, w_q, ld_wq, fmt, K_p, e, out_dtype, stream);
+  const int64_t weight_bytes = static_cast<int64_t>(N) * K_p * 2;
+  const bool few = M <= 16 || (M <= CONVROT_FEW_TOKENS && weight_bytes <= kFewBytes);
+  if (fmt == CONVROT_CODES_S8 || few) return gemm_few(a_q, ld_aq, w_q, ld_wq, fmt, K_p, e, out_dtype, stream);
   switch (out_dtype) {
     case CONVROT_BF16: return gemm_many<CONVROT_BF16>(a_q, ld_aq, w_q, ld_wq, K_p, e, stream);
     case CONVROT_FP16: return gemm_many<CONVROT_FP16>(a_q, ld_aq, w_q, ld_wq, K_p, e, stream);

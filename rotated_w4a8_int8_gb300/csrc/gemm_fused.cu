@@ -122,32 +122,53 @@ struct Box {
 };
 
 // Copies a box between shared memory and the matrix, W bytes per lane, rows in
-// turn; elements outside the matrix are skipped (zeros on the way in).
+// turn; elements outside the matrix are skipped (zeros on the way in).  Eight
+// rows' accesses go out together: one at a time, each waits out a latency.
 template <int OUT, bool SPLITK, typename W, bool IN>
 __device__ __forceinline__ void copy_box(const Epilogue& e, uint8_t* box, int lane, int m_base, int nb) {
   using B = Box<OUT, SPLITK>;
+  using T = typename OutT<OUT>::T;
   constexpr int PER_ROW = B::RB / sizeof(W), ROWS = 32 / PER_ROW;    // lanes per row, rows per step
   constexpr int EPL = sizeof(W) / B::ES;                              // elements per lane
-  const int n = nb + (lane % PER_ROW) * EPL;
-#pragma unroll 4
-  for (int r = lane / PER_ROW; r < 32; r += ROWS) {
-    W* s = reinterpret_cast<W*>(box + B::at(r, (lane % PER_ROW) * static_cast<int>(sizeof(W))));
-    const bool row = m_base + r < e.M;
-    char* g = IN ? const_cast<char*>(static_cast<const char*>(e.residual)) + ((m_base + r) * e.ld_res + n) * B::ES
-                 : static_cast<char*>(e.out) + ((m_base + r) * e.ld_out + n) * B::ES;
-    if (row && n + EPL <= e.N) {
-      if (IN) *s = *reinterpret_cast<const W*>(g);
-      else *reinterpret_cast<W*>(g) = *s;
-    } else {
-      using T = typename OutT<OUT>::T;
+  constexpr int STEPS = 32 / ROWS, BATCH = STEPS < 8 ? STEPS : 8;
+  const int n = nb + (lane % PER_ROW) * EPL, byte = (lane % PER_ROW) * static_cast<int>(sizeof(W));
+  const int64_t ld = (IN ? e.ld_res : e.ld_out) * B::ES;
+  const char* g0 = static_cast<const char*>(IN ? e.residual : e.out) + (m_base + lane / PER_ROW) * ld + n * B::ES;
+  const int rows = e.M - m_base - lane / PER_ROW;                     // rows of the matrix from this lane's first one on
+  const bool whole = n + EPL <= e.N;
+#pragma unroll 1
+  for (int s0 = 0; s0 < STEPS; s0 += BATCH) {
+    W v[BATCH];
 #pragma unroll
-      for (int j = 0; j < EPL; ++j) {
-        T* se = reinterpret_cast<T*>(s) + j;
-        if (row && n + j < e.N) {
-          if (IN) *se = reinterpret_cast<const T*>(g)[j];
-          else reinterpret_cast<T*>(g)[j] = *se;
-        } else if (IN) {
-          *se = T(0.f);
+    for (int i = 0; i < BATCH; ++i) {
+      const int r = (s0 + i) * ROWS;
+      if constexpr (IN) {
+        const W* g = reinterpret_cast<const W*>(g0 + r * ld);
+        v[i] = W{};
+        if (whole && r < rows) {
+          v[i] = *g;
+        } else if (r < rows) {
+#pragma unroll
+          for (int j = 0; j < EPL; ++j)
+            if (n + j < e.N) reinterpret_cast<T*>(&v[i])[j] = reinterpret_cast<const T*>(g)[j];
+        }
+      } else {
+        v[i] = *reinterpret_cast<const W*>(box + B::at(lane / PER_ROW + r, byte));
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < BATCH; ++i) {
+      const int r = (s0 + i) * ROWS;
+      if constexpr (IN) {
+        *reinterpret_cast<W*>(box + B::at(lane / PER_ROW + r, byte)) = v[i];
+      } else {
+        W* g = reinterpret_cast<W*>(const_cast<char*>(g0) + r * ld);
+        if (whole && r < rows) {
+          *g = v[i];
+        } else if (r < rows) {
+#pragma unroll
+          for (int j = 0; j < EPL; ++j)
+            if (n + j < e.N) reinterpret_cast<T*>(g)[j] = reinterpret_cast<const T*>(&v[i])[j];
         }
       }
     }
@@ -391,6 +412,11 @@ fused_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__
     uint32_t chunk = 0;
     bool ok = true;
     const uint32_t lacce0 = map_to_rank(acce0, leader);   // the even CTA's acc_empty barriers
+    // The first tile's pass begins with a rehearsal: one box of it, filled from
+    // nothing and sent nowhere, while the tensor core works on the tile.  It
+    // brings the output phase's instructions and the column terms into their
+    // caches, which a launch of few tiles otherwise waits for at its end.
+    bool rehearsal = true;
     for (int tile = cluster_id; tile < p.num_items && ok; tile += num_clusters) {
       int m2, nt;
       work_coords(p, tile, m2, nt);
@@ -409,7 +435,7 @@ fused_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__
       const int b_first = SPLITK ? static_cast<int>(pair) : 0;
       auto wanted = [&](int b) { return b < BOXES && m_base < p.e.M && n0 + b * B::CPB < p.e.N; };
       // the first boxes' residual comes while the tile is multiplied, the rest waits in L2
-      if (res_tma) {
+      if (res_tma && !rehearsal) {
 #pragma unroll
         for (int i = 0; i < B::BUFS; ++i)
           if (wanted(b_first + i * S)) request(b_first + i * S);
@@ -432,7 +458,7 @@ fused_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__
       int32_t acc[L::COLS];
 #pragma unroll
       for (int j = 0; j < L::COLS; ++j) acc[j] = 0;
-      for (int c = 0; c < nchunks; ++c, ++chunk) {
+      for (int c = rehearsal ? nchunks : 0; c < nchunks; ++c, ++chunk) {
         const uint32_t buf = chunk & 1u, use = chunk >> 1;
         int got = 1;
         if (lane == 0) got = mbar_wait(accf0 + 8 * buf, use & 1u, ERR_WAIT_ACC_FULL, abort_flag) ? 1 : 0;
@@ -463,7 +489,7 @@ fused_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__
         __syncwarp();
         if (lane == 0) mbar_arrive_cluster(lacce0 + 8 * buf);
       }
-      if constexpr (SPLITK) {
+      if (SPLITK && !rehearsal) {
         // one tile per cluster: the stages of every CTA are free once all have their sums
         cluster_sync();
         const int slots = (L::UNITS + S - 1) / S;          // units a pair owns, at most
@@ -501,7 +527,6 @@ fused_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__
         }
       }
       if (!ok) break;
-      if (m_base >= p.e.M) continue;
       if (!keep_bits) {
 #pragma unroll
         for (int j = 0; j < L::COLS; ++j) acc[j] = __float_as_int(static_cast<float>(acc[j]));
@@ -511,15 +536,15 @@ fused_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__
 #pragma unroll 1
       for (int b = 0; b < BOXES; ++b) {
         const int nb = n0 + b * B::CPB;
-        if ((!SPLITK || b % S == static_cast<int>(pair)) && nb < p.e.N) {
+        if ((!SPLITK || b % S == static_cast<int>(pair)) && m_base < p.e.M && nb < p.e.N) {
           const uint32_t buf = done % B::BUFS;
           uint8_t* box = wstage + buf * (32 * B::RB);
-          if (res_tma) {
+          if (res_tma && !rehearsal) {
             if (asked == done) request(b);
             // every lane waits: each reads what the load wrote
             const bool got = mbar_wait(resf + 8 * buf, (done / B::BUFS) & 1u, ERR_WAIT_FULL, abort_flag);
             if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
-          } else {
+          } else if (!rehearsal) {
             if (out_tma && lane == 0) bulk_wait_read<B::BUFS - 1>();    // this buffer's last store has read it
             __syncwarp();
             if (p.e.residual) {
@@ -527,26 +552,30 @@ fused_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__
               __syncwarp();
             }
           }
-          ++done;
           if (nb + B::CPB <= p.e.N) fill_box<OUT, ACT, SPLITK, true>(p.e, acc, box, lane, nb, sa);
           else fill_box<OUT, ACT, SPLITK, false>(p.e, acc, box, lane, nb, sa);
+          // this warp's accesses of the box before TMA reads or refills it
+          if (out_tma || res_tma) fence_proxy_async_smem();
+          __syncwarp();
+          if (rehearsal) break;
+          ++done;
           if (out_tma) {
-            fence_proxy_async_smem();
-            __syncwarp();
             if (lane == 0) {
               tma_store_2d(&tmap_out, smem_u32(box), nb, m_base);
               bulk_commit();
             }
           } else {
-            __syncwarp();
             copy_box_by<OUT, SPLITK, false>(p.out_piece, p.e, box, lane, m_base, nb);
-            // the copy's reads of the box before the next residual lands in it
             if (res_tma) fence_proxy_async_smem();
             __syncwarp();
           }
         }
 #pragma unroll
         for (int j = 0; j < L::COLS - B::CPB; ++j) acc[j] = acc[j + B::CPB];
+      }
+      if (rehearsal) {
+        rehearsal = false;
+        tile -= num_clusters;           // and now the tile itself
       }
     }
     // every TMA store of this warp must have read its box before the CTA exits,
@@ -685,8 +714,13 @@ struct Shape {
 
 template <int OUT, int ACT>
 static int pick_shape(const Params& p, Shape* best) {
-  // model of a tile's time in microseconds (a 64-deep step of a 256- and a 128-wide tile; joining a split tile)
-  constexpr double step256 = 0.33, step128 = 0.20, join = 2.0;
+  // Microseconds, fitted to runs at 100 to 1024 tokens (weights 512 x 512 to
+  // 21504 x 5376): a 64-deep step of a tile; what a tile's output phase
+  // takes at the launch's end beyond a 128-wide one's; joining a split tile.
+  // 256 x 5376 x 14336: 256-wide tiles whole 76 us, split in three 48 us;
+  // 512 x 2048 x 5376: 128-wide whole 30 us, split in two 21 us, 256-wide
+  // split in three 26 us; 1024 x 5376 x 5376: 256-wide 65 us, 128-wide 78 us.
+  constexpr double step256 = 0.29, step128 = 0.26, tail256 = 4.0, join256 = 5.5, join128 = 1.5;
   double least = 0;
   for (int bn : {256, 128}) {
     const int items = p.num_m2 * ((p.e.N + bn - 1) / bn);
@@ -701,7 +735,8 @@ static int pick_shape(const Params& p, Shape* best) {
       if (e != cudaSuccess) return convrot::record_cuda_error("fused GEMM set-up", e);
       if (split > 1 && items > resident) break;
       const int rounds = (items + resident - 1) / resident, steps = (p.k_steps + split - 1) / split;
-      const double t = rounds * steps * step + (split > 1 ? join : 0.0);
+      const double t = rounds * steps * step + (bn == 256 ? tail256 : 0.0) +
+                       (split == 1 ? 0.0 : bn == 256 ? join256 : join128);
       if (least == 0 || t < least) {
         least = t;
         *best = {bn, split};

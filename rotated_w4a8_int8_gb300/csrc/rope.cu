@@ -205,19 +205,38 @@ __device__ __forceinline__ void load8(const float* base, int n, int i, float (&v
 
 // T tokens per CTA (1, 2, 4 or 8), kWarps / T warps each; gridDim.y CTAs share a token's heads.
 template <int DT, bool INTERLEAVED, int G, int T>
-__global__ void __launch_bounds__(32 * kWarps, 6) rope_kernel(const Params p) {
+__global__ void __launch_bounds__(32 * kWarps, DT == CONVROT_FP32 ? 4 : 5) rope_kernel(const Params p) {
   extern __shared__ __align__(16) float smem[];
   float* cs = smem;                          // [T][2][P]: cosines, sines
   float* ws = smem + T * 2 * p.P;            // [2][D]: weights of q and k
   constexpr int HPW = 32 / G;
+  constexpr int WPT = kWarps / T;            // warps per token
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int m0 = blockIdx.x * T;
+  const int m0 = blockIdx.x * T, t = warp / WPT, m = m0 + t;
+  const int c = lane % G, hl = lane / G;
+  const bool piece = 16 * c < p.D;           // lanes past the head's pieces idle
+  const bool turns = 8 * c < p.P;            // this piece is rotated
+  // the piece's two runs: a rotated piece of the split layout lies in both halves
+  const int j0 = !turns || INTERLEAVED ? 16 * c : 8 * c;
+  const int j1 = !turns || INTERLEAVED ? 16 * c + 8 : 8 * c + p.P;
+  const int gq = (p.q.heads + HPW - 1) / HPW, gk = (p.k.heads + HPW - 1) / HPW;
+  const int groups = m < p.M ? gq + gk : 0, step = WPT * gridDim.y;
+  auto load = [&](int g, Piece<DT>& r) {
+    const Operand& o = g < gq ? p.q : p.k;
+    const int head = (g < gq ? g : g - gq) * HPW + hl;
+    r = {};
+    if (g < groups && piece && head < o.heads) load_piece<DT>(o.x, m * o.x_tok + head * o.x_head, j0, j1, r);
+  };
+  // the first heads are on their way while the turns are worked out
+  int g = blockIdx.y * WPT + warp % WPT;
+  Piece<DT> r;
+  load(g, r);
   for (int i = threadIdx.x; i < T * p.P; i += 32 * kWarps) {
-    const int t = i / p.P, j = i - t * p.P;
-    if (m0 + t < p.M) {
-      const float2 v = pair_turn(p, m0 + t, j);
-      cs[t * 2 * p.P + spread(j, p.P)] = v.x;
-      cs[t * 2 * p.P + p.P + spread(j, p.P)] = v.y;
+    const int u = i / p.P, j = i - u * p.P;
+    if (m0 + u < p.M) {
+      const float2 v = pair_turn(p, m0 + u, j);
+      cs[u * 2 * p.P + spread(j, p.P)] = v.x;
+      cs[u * 2 * p.P + p.P + spread(j, p.P)] = v.y;
     }
   }
   for (int i = threadIdx.x; i < 2 * p.D; i += 32 * kWarps) {
@@ -226,30 +245,18 @@ __global__ void __launch_bounds__(32 * kWarps, 6) rope_kernel(const Params p) {
     if (w) ws[(i < p.D ? 0 : p.D) + spread(j, p.D)] = __ldg(w + j);
   }
   __syncthreads();
-  constexpr int WPT = kWarps / T;            // warps per token
-  const int t = warp / WPT, m = m0 + t;
-  if (m >= p.M) return;
-  const int c = lane % G, hl = lane / G;
-  const bool piece = 16 * c < p.D;           // lanes past the head's pieces idle
-  const bool turns = 8 * c < p.P;            // this piece is rotated
-  // the piece's two runs: a rotated piece of the split layout lies in both halves
-  const int j0 = !turns || INTERLEAVED ? 16 * c : 8 * c;
-  const int j1 = !turns || INTERLEAVED ? 16 * c + 8 : 8 * c + p.P;
   const float* tcs = cs + t * 2 * p.P;
-  const int gq = (p.q.heads + HPW - 1) / HPW, gk = (p.k.heads + HPW - 1) / HPW;
-  const int step = WPT * gridDim.y;
-  for (int g = blockIdx.y * WPT + warp % WPT; g < gq + gk; g += step) {
+  for (; g < groups; g += step) {
     const bool is_q = g < gq;
     const Operand& o = is_q ? p.q : p.k;
     const int head = (is_q ? g : g - gq) * HPW + hl;
     const bool active = piece && head < o.heads;
-    Piece<DT> r = {};
-    if (active) load_piece<DT>(o.x, m * o.x_tok + head * o.x_head, j0, j1, r);
     float v[2][8];
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[h][e] = piece_elem<DT>(r, h, e);
+    load(g + step, r);
     if (o.weight) {
       float ss = 0.f;
 #pragma unroll
@@ -290,11 +297,14 @@ template <int DT, bool INTERLEAVED, int G>
 static cudaError_t launch_g(const Params& p, cudaStream_t st) {
   const int per_warp = 32 / G, groups = (p.q.heads + per_warp - 1) / per_warp + (p.k.heads + per_warp - 1) / per_warp;
   auto smem = [&](int T) { return static_cast<size_t>(T * 2 * p.P + 2 * p.D) * sizeof(float); };
-  if (p.M >= 4 * 2 * 152) {
+  constexpr int kFit = 6 * 152;              // CTAs that the GPU holds at once
+  if (p.M >= 4 * 2 * kFit) {
     rope_kernel<DT, INTERLEAVED, G, 4><<<(p.M + 3) / 4, 32 * kWarps, smem(4), st>>>(p);
+  } else if (p.M >= 2 * kFit) {
+    rope_kernel<DT, INTERLEAVED, G, 2><<<(p.M + 1) / 2, 32 * kWarps, smem(2), st>>>(p);
   } else {
     // few tokens: their heads over several CTAs, up to one warp per group of heads
-    int y = (4 * 152 + p.M - 1) / p.M;
+    int y = (kFit + p.M - 1) / p.M;
     const int most = (groups + kWarps - 1) / kWarps;
     if (y > most) y = most;
     rope_kernel<DT, INTERLEAVED, G, 1><<<dim3(p.M, y), 32 * kWarps, smem(1), st>>>(p);
