@@ -114,7 +114,7 @@ __device__ __forceinline__ float* row_slot(char* rows, int e) {
 // its squares are summed, and h * weight goes to shared memory (zeros at and
 // past K).  Returns this thread's share of the sum of squares.
 template <int DT, bool RES, int V>
-__device__ __forceinline__ float stage_row(const NormArgs& a, int row, int e0, int n, char* rows) {
+__device__ __forceinline__ float stage_row(const NormArgs& a, int row, int e0, int n, char* rows, int tid, int nthreads) {
   constexpr int64_t es = (DT == DT_FP32) ? 4 : 2;
   // accesses in flight per thread and operand (with a residual two measured
   // faster than four: 155.4 against 161.9 us; without one, slower)
@@ -124,11 +124,11 @@ __device__ __forceinline__ float stage_row(const NormArgs& a, int row, int e0, i
   char* h = a.h ? a.h + (row * a.ld_h + e0) * es : nullptr;
   const int left = a.K - e0;                 // elements of the row from e0 on
   float ss = 0.f;
-  for (int base = threadIdx.x * V; base < n; base += blockDim.x * V * BATCH) {
+  for (int base = tid * V; base < n; base += nthreads * V * BATCH) {
     Chunk<DT, V> cx[BATCH], cr[RES ? BATCH : 1];
 #pragma unroll
     for (int b = 0; b < BATCH; ++b) {
-      const int e = base + b * blockDim.x * V;
+      const int e = base + b * nthreads * V;
       if (e + V <= left) {
         cx[b].load(x + e * es);
         if constexpr (RES) cr[b].load(r + e * es);
@@ -136,7 +136,7 @@ __device__ __forceinline__ float stage_row(const NormArgs& a, int row, int e0, i
     }
 #pragma unroll
     for (int b = 0; b < BATCH; ++b) {
-      const int e = base + b * blockDim.x * V;
+      const int e = base + b * nthreads * V;
       if (e >= n) break;
       float v[V];
       if (e + V <= left) {
@@ -196,6 +196,18 @@ __device__ __forceinline__ float stage_row(const NormArgs& a, int row, int e0, i
   return ss;
 }
 
+// What the row's totals give: scale, multiplier of z and norm bound.  z / 16 is
+// the rotated row, and r its RMS factor.
+struct RowResult {
+  float scale, mult, norm;
+};
+
+__device__ __forceinline__ RowResult row_result(float amax, float ssh, float ssz, const NormArgs& a) {
+  const float pre = __frcp_rn(__fsqrt_rn(ssh * a.inv_k + a.eps)) * 0.0625f;
+  const RowQuant q(amax * pre);
+  return {q.s, q.r * pre, a.norm ? code_norm_bound(q, ssz, pre, a.half_sqrt_kp) : 0.f};
+}
+
 // Row reduction of (max|z|, sum h^2, sum z^2) over the CTA (SPLIT == 1) or
 // the two CTAs of a cluster, and the row's quantiser.  `red` (floats): [0, 16)
 // per-warp maxima, [16, 32) and [32, 48) per-warp sums, [48, 51) this CTA's
@@ -203,7 +215,7 @@ __device__ __forceinline__ float stage_row(const NormArgs& a, int row, int e0, i
 constexpr int kNormRedFloats = 56;
 
 template <int SPLIT>
-__device__ __forceinline__ void norm_reduce(float amax, float ssh, float ssz, const NormArgs& a, float* red) {
+__device__ __forceinline__ RowResult norm_reduce(float amax, float ssh, float ssz, const NormArgs& a, float* red) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nwarps = blockDim.x >> 5;
   amax = warp_max_nonneg(amax);
   ssh = warp_sum(ssh);
@@ -245,42 +257,57 @@ __device__ __forceinline__ void norm_reduce(float amax, float ssh, float ssz, co
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");   // done reading the peer
   }
   if (threadIdx.x == 0) {
-    // z / 16 is the rotated row, and r its RMS factor
-    const float pre = __frcp_rn(__fsqrt_rn(ssh * a.inv_k + a.eps)) * 0.0625f;
-    const RowQuant q(amax * pre);
-    red[51] = q.s;
-    red[52] = q.r * pre;
-    if (a.norm) red[53] = code_norm_bound(q, ssz, pre, a.half_sqrt_kp);
+    const RowResult r = row_result(amax, ssh, ssz, a);
+    red[51] = r.scale;
+    red[52] = r.mult;
+    red[53] = r.norm;
   }
   __syncthreads();
+  return {red[51], red[52], red[53]};
 }
 
-template <int DT, bool RES, int V, int NBMAX, int SPLIT>
-__global__ void __launch_bounds__(kMaxThreads) norm_quant_kernel(const NormArgs a) {
-  extern __shared__ __align__(16) char smem[];
-  constexpr int64_t es = (DT == DT_FP32) ? 4 : 2;
-  const int slot = threadIdx.x >> 3, lane8 = threadIdx.x & 7;
-  const int row = blockIdx.x / SPLIT, part = blockIdx.x % SPLIT;
-  const int nbl = (a.nblocks + SPLIT - 1) / SPLIT;
-  const int blk0 = part * nbl, nloc = min(nbl, a.nblocks - blk0);
-  float* red = reinterpret_cast<float*>(smem + nbl * kSlotBytes);
+// SPLIT == 0: rows of at most four blocks; 8, 16 or 32 lanes of a warp hold a
+// row, eight warps share a CTA, and no barrier is wider than the warp.
+// SPLIT == 1: a CTA per row.  SPLIT == 2: a cluster of two CTAs per row.
+// V: elements per access of the first pass.
+constexpr int kShortWarps = 8, kShortBlocks = 4;
 
-  const float ssh = stage_row<DT, RES, V>(a, row, blk0 * kBlock, nloc * kBlock, smem);
-  // this CTA's share of a later row, into L2 (see l2_prefetch)
-  if (const int later = row + a.pf_dist; later < a.M) {
-    const size_t rb = static_cast<size_t>(a.K) * es, share = (rb + SPLIT - 1) / SPLIT;
-    const size_t b0 = part * share, b1 = b0 + share < rb ? b0 + share : rb;
-    l2_prefetch(a.x + later * a.ld_x * es + b0, b1 - b0);
-    if constexpr (RES) l2_prefetch(a.res + later * a.ld_res * es + b0, b1 - b0);
+template <int DT, bool RES, int V, int NBMAX, int SPLIT>
+__global__ void __launch_bounds__(SPLIT == 0 ? 32 * kShortWarps : kMaxThreads) norm_quant_kernel(const NormArgs a) {
+  extern __shared__ __align__(16) char smem_all[];
+  constexpr int64_t es = (DT == DT_FP32) ? 4 : 2;
+  constexpr int PARTS = SPLIT == 2 ? 2 : 1;
+  const int nbl = (a.nblocks + PARTS - 1) / PARTS;
+  const int width = SPLIT == 0 ? 8 * (nbl == 3 ? 4 : nbl) : blockDim.x;         // threads of a row
+  const int tid = SPLIT == 0 ? threadIdx.x & (width - 1) : threadIdx.x;
+  const int local_row = SPLIT == 0 ? static_cast<int>(threadIdx.x) / width : 0;
+  const int row = SPLIT == 0 ? static_cast<int>(blockIdx.x) * (32 * kShortWarps / width) + local_row : blockIdx.x / PARTS;
+  const bool live = SPLIT != 0 || row < a.M;
+  const int slot = tid >> 3, lane8 = tid & 7, part = blockIdx.x % PARTS;
+  const int blk0 = part * nbl, nloc = min(nbl, a.nblocks - blk0);
+  char* smem = smem_all + local_row * nbl * kSlotBytes;
+  float* red = reinterpret_cast<float*>(smem_all + nbl * kSlotBytes);   // (SPLIT == 0: unused)
+
+  float ssh = 0.f;
+  if (live) ssh = stage_row<DT, RES, V>(a, row, blk0 * kBlock, nloc * kBlock, smem, tid, width);
+  if constexpr (SPLIT != 0) {
+    // this CTA's share of a later row, into L2 (see l2_prefetch)
+    if (const int later = row + a.pf_dist; later < a.M) {
+      const size_t rb = static_cast<size_t>(a.K) * es, share = (rb + PARTS - 1) / PARTS;
+      const size_t b0 = part * share, b1 = b0 + share < rb ? b0 + share : rb;
+      l2_prefetch(a.x + later * a.ld_x * es + b0, b1 - b0);
+      if constexpr (RES) l2_prefetch(a.res + later * a.ld_res * es + b0, b1 - b0);
+    }
   }
-  __syncthreads();
+  if constexpr (SPLIT != 0) __syncthreads();
+  else __syncwarp();
 
   BlockCols c[NBMAX];
   float amax = 0.f, ssz = 0.f;
 #pragma unroll
   for (int i = 0; i < NBMAX; ++i) {
     const int li = slot + a.S * i;
-    const bool active = (slot < a.S) && (li < nloc);
+    const bool active = live && (slot < a.S) && (li < nloc);
     char* mine = smem + (active ? li : 0) * kSlotBytes;
     float2 P[16];                                  // (element b, element 16 + b) of the thread's 32
     if (active) {
@@ -301,18 +328,27 @@ __global__ void __launch_bounds__(kMaxThreads) norm_quant_kernel(const NormArgs 
       if (a.norm) ssz = sumsq_cols(ssz, c[i]);
     }
   }
-  norm_reduce<SPLIT>(amax, ssh, ssz, a, red);
-  if (threadIdx.x == 0 && part == 0) {
-    a.scale[row] = red[51];
-    if (a.norm) a.norm[row] = red[53];
+  RowResult r;
+  if constexpr (SPLIT == 0) {
+    for (int o = width / 2; o > 0; o >>= 1) {
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+      ssh += __shfl_xor_sync(0xffffffffu, ssh, o);
+      ssz += __shfl_xor_sync(0xffffffffu, ssz, o);
+    }
+    r = row_result(amax, ssh, ssz, a);
+  } else {
+    r = norm_reduce<SPLIT>(amax, ssh, ssz, a, red);
   }
-  const float mult = red[52];
+  if (tid == 0 && part == 0 && live) {
+    a.scale[row] = r.scale;
+    if (a.norm) a.norm[row] = r.norm;
+  }
   char* qrow = static_cast<char*>(a.q) + row * a.ld_q * (a.f16_codes ? 2 : 1);
 #pragma unroll
   for (int i = 0; i < NBMAX; ++i) {
     const int li = slot + a.S * i;
-    if (slot < a.S && li < nloc) {
-      scale_cols(c[i], mult);
+    if (live && slot < a.S && li < nloc) {
+      scale_cols(c[i], r.mult);
       store_codes<false>(qrow, a.f16_codes, blk0 + li, lane8, c[i]);
     }
   }
@@ -321,6 +357,15 @@ __global__ void __launch_bounds__(kMaxThreads) norm_quant_kernel(const NormArgs 
 
 template <int DT, bool RES, int V>
 static cudaError_t launch_norm_cfg(const RowGeometry& g, const NormArgs& a, cudaStream_t st) {
+  // Short rows share CTAs once there are more of them than SMs; fewer rows
+  // get whole CTAs, and more threads than their blocks need (see below).
+  if (g.nblocks <= kShortBlocks && a.M > 152) {
+    const int per_cta = 32 * kShortWarps / (8 * (g.nblocks == 3 ? 4 : g.nblocks));
+    RowGeometry w = g;
+    w.threads = 32 * kShortWarps;
+    w.smem = static_cast<size_t>(per_cta) * g.nblocks * kSlotBytes;
+    return launch_rows(norm_quant_kernel<DT, RES, V, 1, 0>, w, (a.M + per_cta - 1) / per_cta, st, a);
+  }
   if (g.split == 1) return launch_rows(norm_quant_kernel<DT, RES, V, 1, 1>, g, a.M, st, a);
   if (g.nbmax == 1) return launch_rows(norm_quant_kernel<DT, RES, V, 1, 2>, g, a.M, st, a);
   return launch_rows(norm_quant_kernel<DT, RES, V, 2, 2>, g, a.M, st, a);
@@ -367,6 +412,7 @@ extern "C" int convrot_rms_norm_quant(const void* x, convrot_dtype dtype, int64_
   if (!row_geometry(K_p, kMaxSlots, &g)) return CONVROT_ERR_UNSUPPORTED;
   const int nbl = (g.nblocks + g.split - 1) / g.split;
   g.smem = static_cast<size_t>(nbl) * kSlotBytes + kNormRedFloats * sizeof(float);
+  if (M <= 2 * 152) g.threads = kMaxThreads;      // few rows: the first pass is spread wider (2 x 3077: 8.3 -> 4.3 us)
   NormArgs a = {};
   a.x = static_cast<const char*>(x);
   a.res = static_cast<const char*>(residual);
