@@ -9,12 +9,18 @@
 // and the tokens, eight to a tile, as the other one: at one to a few dozen
 // tokens a tcgen05 tile would be mostly padding.  Which k an operand's slot
 // holds does not matter as long as both operands agree, so a lane feeds the
-// instruction from 16 contiguous bytes of its rows: no shared memory, no
-// shuffles, and every load is a full 16 bytes.  One-byte codes become FP16 in
-// registers (1024 + 128 + code is a byte permute away, an exact subtraction
-// leaves the code).  Sums are exact integers: FP32 partial sums over at most
-// 1024 codes stay below 2^24, then go to int32 registers; the warps' sums meet
-// in shared memory by integer addition, whose order does not matter.
+// instruction from 16 contiguous bytes of its rows, without shuffles.  Up to
+// 16 tokens the pieces are loaded into registers, two or three units at a
+// time; beyond, the sums leave no registers for that, and every lane fetches
+// its pieces with asynchronous copies several units ahead into shared memory
+// of its own, which it alone reads back, without a barrier (S8 codes, 32 and
+// 64 tokens x 14336 x 5376: 42.4 -> 32.4 us and 78 -> 62 us; for 8 and 16
+// tokens in FP16-held codes the copies are slower, 27.7 -> 32.5 us and 31.3
+// -> 37.6 us).  One-byte codes become FP16 in registers (1024 + 128 + code is
+// a byte permute away, an exact subtraction leaves the code).  Sums are exact
+// integers: FP32 partial sums over at most 1024 codes stay below 2^24, then go
+// to int32 registers; the warps' sums meet in shared memory by integer
+// addition, whose order does not matter.
 #include <cstdint>
 #include <cuda_runtime.h>
 #include <cuda_fp16.h>
@@ -32,12 +38,35 @@ constexpr int ROWS = 16;                 // weight rows per CTA
 // leave the registers for it (two measured 20% slower with 8 tokens).
 template <int NT>
 constexpr int CTAS_PER_SM = NT <= 2 ? 3 : 2;
+template <int NT>
+constexpr bool RING = NT > 2;
+// Units in a warp's ring (one of them being read), as the SM's shared memory allows.
+template <int NT>
+constexpr int DEPTH = NT == 4 ? 4 : 2;
+template <int NT>
+constexpr int UNIT_BYTES = (2 + NT) * 512;       // per warp: 16 bytes per lane of two weight rows and NT tokens
+template <int NT>
+constexpr int FEW_SMEM = RING<NT> ? WARPS * DEPTH<NT> * UNIT_BYTES<NT> : 0;
 
 // 16 bytes of a weight row: read once, kept out of L1.
 __device__ __forceinline__ uint4 load_weight(const char* p) {
   uint4 v;
   asm("ld.global.nc.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
       : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+
+// An asynchronous copy of 16 bytes; `bytes` 0 fills with zeros and reads nothing.
+__device__ __forceinline__ void copy16(uint32_t dst, const char* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+__device__ __forceinline__ uint4 lds16(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
   return v;
 }
 
@@ -70,21 +99,119 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// One unit's products: acc += weights x tokens.
+template <bool S8, int NT>
+__device__ __forceinline__ void multiply(const uint4 (&wv)[2], const uint4 (&av)[NT], float (&acc)[NT][4]) {
+#pragma unroll
+  for (int s = 0; s < (S8 ? 4 : 2); ++s) {
+    uint32_t a0, a1, a2, a3;
+    step_words<S8>(wv[0], s, a0, a2);
+    step_words<S8>(wv[1], s, a1, a3);
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      uint32_t b0, b1;
+      step_words<S8>(av[t], s, b0, b1);
+      mma16816(acc[t], a0, a1, a2, a3, b0, b1);
+    }
+  }
+}
+
+// total += the exact FP32 partial sums.
+template <int NT>
+__device__ __forceinline__ void add_exact(const float (&acc)[NT][4], int (&total)[NT][4]) {
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) total[t][j] += __float2int_rn(acc[t][j]);
+}
+
+template <bool S8>
+constexpr int EXACT_UNITS = EXACT_CODES / (S8 ? 64 : 32);     // units of 64 bytes per exact partial sum
+
+// Sums of the units first, first + wstep, ... through loads into registers.
+template <bool S8, int NT>
+__device__ __forceinline__ void sum_loads(const char* const (&wr)[2], const char* const (&ar)[NT], int units, int first,
+                                          int wstep, int (&total)[NT][4]) {
+  constexpr int U = NT == 1 ? 3 : 2;                     // units in flight
+  for (; first < units; first += wstep * EXACT_UNITS<S8>) {
+    const int end = min(units, first + wstep * EXACT_UNITS<S8>);
+    float acc[NT][4] = {};
+    for (int u0 = first; u0 < end; u0 += wstep * U) {
+      uint4 wv[U][2], av[U][NT];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int at = u0 + u * wstep;
+        if (at < end) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) wv[u][i] = load_weight(wr[i] + static_cast<int64_t>(at) * 64);
+#pragma unroll
+          for (int t = 0; t < NT; ++t) av[u][t] = __ldg(reinterpret_cast<const uint4*>(ar[t] + static_cast<int64_t>(at) * 64));
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (u0 + u * wstep >= end) break;                // uniform in the warp
+        multiply<S8, NT>(wv[u], av[u], acc);
+      }
+    }
+    add_exact<NT>(acc, total);
+  }
+}
+
+// The same through the warp's ring of asynchronous copies; tokens[t] exists where 8 t < live.
+template <bool S8, int NT>
+__device__ __forceinline__ void sum_ring(const char* const (&wr)[2], const char* const (&ar)[NT], int units, int first,
+                                         int wstep, uint32_t ring, int live, int (&total)[NT][4]) {
+  int ahead = first;                                     // the next unit to ask for
+  uint32_t in = ring, from = ring;
+  auto next = [&](uint32_t at) { return at == ring + (DEPTH<NT> - 1) * UNIT_BYTES<NT> ? ring : at + UNIT_BYTES<NT>; };
+  auto ask = [&]() {
+    if (ahead < units) {
+      const int64_t at = static_cast<int64_t>(ahead) * 64;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) copy16(in + 512 * i, wr[i] + at, 16);
+#pragma unroll
+      for (int t = 0; t < NT; ++t) copy16(in + 512 * (2 + t), ar[t] + at, 8 * t < live ? 16 : 0);
+    }
+    copy_commit();                                       // (an empty group past the last unit keeps the count)
+    ahead += wstep;
+    in = next(in);
+  };
+#pragma unroll
+  for (int d = 0; d < DEPTH<NT> - 1; ++d) ask();
+  for (; first < units; first += wstep * EXACT_UNITS<S8>) {
+    const int end = min(units, first + wstep * EXACT_UNITS<S8>);
+    float acc[NT][4] = {};
+    for (int u = first; u < end; u += wstep) {
+      ask();
+      copy_wait<DEPTH<NT> - 1>();                        // this unit's copies have landed
+      uint4 wv[2], av[NT];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) wv[i] = lds16(from + 512 * i);
+#pragma unroll
+      for (int t = 0; t < NT; ++t) av[t] = lds16(from + 512 * (2 + t));
+      from = next(from);
+      multiply<S8, NT>(wv, av, acc);
+    }
+    add_exact<NT>(acc, total);
+  }
+}
+
 __device__ __forceinline__ int ld_cluster(const int* p, uint32_t rank) {
   int v;
   asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(crgemm::map_to_rank(crgemm::smem_u32(p), rank)) : "memory");
   return v;
 }
 
-// NT tiles of eight tokens, U units in flight per warp.  A cluster of `split` CTAs shares the K units of a row tile; each
+// NT tiles of eight tokens.  A cluster of `split` CTAs shares the K units of a row tile; each
 // finishes its part of the tile's outputs from all of their sums.
-template <bool S8, int NT, int U>
+template <bool S8, int NT>
 __global__ void __launch_bounds__(32 * WARPS, CTAS_PER_SM<NT>)
 few_kernel(const char* __restrict__ a_q, int64_t a_pitch, const char* __restrict__ w_q, int64_t w_pitch, int units,
            int split, int out_dtype, const Epilogue e) {
   constexpr int TOKENS = 8 * NT, PITCH = ROWS + 4;   // pad: no bank conflicts below
-  constexpr int STEPS = S8 ? 4 : 2, CODES = S8 ? 64 : 32;            // per unit of 64 bytes
   __shared__ __align__(16) int sums[TOKENS * PITCH];
+  extern __shared__ __align__(16) char ring_all[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
   for (int i = threadIdx.x; i < TOKENS * PITCH; i += 32 * WARPS) sums[i] = 0;
   const int part = blockIdx.x % split;
@@ -110,42 +237,12 @@ few_kernel(const char* __restrict__ a_q, int64_t a_pitch, const char* __restrict
 #pragma unroll
   for (int t = 0; t < NT; ++t) ar[t] = a_q + min(8 * t + g, e.M - 1) * a_pitch + 16 * q;
   int total[NT][4] = {};
-  const int wstep = WARPS * split;                       // the tile's warps take the units in turn
-  for (int first = part * WARPS + warp; first < units; first += wstep * (EXACT_CODES / CODES)) {
-    const int end = min(units, first + wstep * (EXACT_CODES / CODES));
-    float acc[NT][4] = {};
-    for (int u0 = first; u0 < end; u0 += wstep * U) {
-      uint4 wv[U][2], av[U][NT];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int at = u0 + u * wstep;
-        if (at < end) {
-#pragma unroll
-          for (int i = 0; i < 2; ++i) wv[u][i] = load_weight(wr[i] + static_cast<int64_t>(at) * 64);
-#pragma unroll
-          for (int t = 0; t < NT; ++t) av[u][t] = __ldg(reinterpret_cast<const uint4*>(ar[t] + static_cast<int64_t>(at) * 64));
-        }
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (u0 + u * wstep >= end) break;                // uniform in the warp
-#pragma unroll
-        for (int s = 0; s < STEPS; ++s) {
-          uint32_t b[NT][2];
-#pragma unroll
-          for (int t = 0; t < NT; ++t) step_words<S8>(av[u][t], s, b[t][0], b[t][1]);
-          uint32_t a0, a1, a2, a3;
-          step_words<S8>(wv[u][0], s, a0, a2);
-          step_words<S8>(wv[u][1], s, a1, a3);
-#pragma unroll
-          for (int t = 0; t < NT; ++t) mma16816(acc[t], a0, a1, a2, a3, b[t][0], b[t][1]);
-        }
-      }
-    }
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) total[t][j] += __float2int_rn(acc[t][j]);     // exact
+  const int wstep = WARPS * split, first = part * WARPS + warp;      // the tile's warps take the units in turn
+  if constexpr (RING<NT>) {
+    sum_ring<S8, NT>(wr, ar, units, first, wstep, crgemm::smem_u32(ring_all) + warp * (DEPTH<NT> * UNIT_BYTES<NT>) + 16 * lane,
+                     e.M - g, total);
+  } else {
+    sum_loads<S8, NT>(wr, ar, units, first, wstep, total);
   }
   __syncthreads();                                       // sums are zero
 #pragma unroll
@@ -184,43 +281,49 @@ few_kernel(const char* __restrict__ a_q, int64_t a_pitch, const char* __restrict
   if (split > 1) crgemm::cluster_sync();                 // the peers have read this CTA's sums
 }
 
-template <bool S8, int NT, int U>
+template <bool S8, int NT>
 static cudaError_t launch_few(const void* a_q, int64_t ld_aq, const void* w_q, int64_t ld_wq, int K_p, int out_dtype,
                               const Epilogue& e, cudaStream_t st) {
   constexpr int es = S8 ? 1 : 2;
   const int tiles = (e.N + ROWS - 1) / ROWS, units = K_p * es / 64;
   // Few row tiles: up to eight CTAs share one, as long as all fit the GPU at
-  // once (152 SMs) and every warp keeps a full batch of loads.  One token,
+  // once (152 SMs) and every warp keeps a few units.  One token,
   // 300 x 20480 S8 codes: 17.3 us without, 6.2 us with it.
   int split = 1;
-  while (split < 8 && tiles * 2 * split <= 152 * CTAS_PER_SM<NT> && units >= 2 * split * WARPS * U) split *= 2;
+  while (split < 8 && tiles * 2 * split <= 152 * CTAS_PER_SM<NT> && units >= 2 * split * WARPS * 3) split *= 2;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = split;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  auto k = few_kernel<S8, NT>;
+  if constexpr (RING<NT>) {
+    const cudaError_t set = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, FEW_SMEM<NT>);
+    if (set != cudaSuccess) return set;
+  }
+  cfg.dynamicSmemBytes = FEW_SMEM<NT>;
   cfg.gridDim = dim3(tiles * split);
   cfg.blockDim = dim3(32 * WARPS);
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = split > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, few_kernel<S8, NT, U>, static_cast<const char*>(a_q), ld_aq * es,
+  return cudaLaunchKernelEx(&cfg, k, static_cast<const char*>(a_q), ld_aq * es,
                             static_cast<const char*>(w_q), ld_wq * es, units, split, out_dtype, e);
 }
 
 // FP16 codes of 17 to 64 tokens: up to this weight size this kernel is the
-// faster one (32 tokens: 1000 x 2048 6.1 us against 11.6, 300 x 20480 10.7
-// against 32.5, 5376 x 5376 28.4 against 26.2; 64 tokens: 9.3 against 11.8,
-// 18.4 against 32.7, 49.5 against 26.7).
+// faster one (32 tokens: 1000 x 2048 5.1 us against 11.6, 300 x 20480 10.5
+// against 32.5; 64 tokens: 6.7 against 11.8, 15.4 against 32.7, and 5376 x
+// 5376 more than 40 against 25).
 constexpr int64_t kFewBytes = 16 << 20;
 
 template <bool S8>
 static cudaError_t launch_tokens(const void* a_q, int64_t ld_aq, const void* w_q, int64_t ld_wq, int K_p, int out_dtype,
                                  const Epilogue& e, cudaStream_t st) {
-  if (e.M <= 8) return launch_few<S8, 1, 3>(a_q, ld_aq, w_q, ld_wq, K_p, out_dtype, e, st);
-  if (e.M <= 16) return launch_few<S8, 2, 2>(a_q, ld_aq, w_q, ld_wq, K_p, out_dtype, e, st);
-  if (e.M <= 32) return launch_few<S8, 4, 2>(a_q, ld_aq, w_q, ld_wq, K_p, out_dtype, e, st);
-  return launch_few<S8, 8, 1>(a_q, ld_aq, w_q, ld_wq, K_p, out_dtype, e, st);
+  if (e.M <= 8) return launch_few<S8, 1>(a_q, ld_aq, w_q, ld_wq, K_p, out_dtype, e, st);
+  if (e.M <= 16) return launch_few<S8, 2>(a_q, ld_aq, w_q, ld_wq, K_p, out_dtype, e, st);
+  if (e.M <= 32) return launch_few<S8, 4>(a_q, ld_aq, w_q, ld_wq, K_p, out_dtype, e, st);
+  return launch_few<S8, 8>(a_q, ld_aq, w_q, ld_wq, K_p, out_dtype, e, st);
 }
 
 int gemm_few(const void* a_q, int64_t ld_aq, const void* w_q, int64_t ld_wq, convrot_codes fmt, int K_p,

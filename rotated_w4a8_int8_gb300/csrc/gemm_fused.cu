@@ -63,14 +63,15 @@ template <int BN>
 struct Tile {
   static constexpr int B_BYTES = (BN / 2) * BK * 2;
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
-  static constexpr int STAGES = BN == 256 ? 6 : 8;
+  static constexpr int STAGES = BN == 256 ? 6 : BN == 192 ? 6 : 8;
   static constexpr int COLS = BN / 4;                        // per epilogue warp
   static constexpr int UNITS = COLS / UNIT;
-  static constexpr int TMEM_COLS = 2 * BN;                   // two accumulator buffers
+  static constexpr int TMEM_COLS = BN == 128 ? 256 : 512;    // two accumulator buffers, a power of two
   static constexpr int SMEM = STAGES * STAGE_BYTES + STAGING + 1024 /*align*/ + 512 /*barriers*/;
   static constexpr uint32_t IDESC = (1u << 4)                // D FP32, A and B FP16, K-major, M = 256
                                     | (static_cast<uint32_t>(BN >> 3) << 17)
                                     | (static_cast<uint32_t>((2 * BM) >> 4) << 24);
+  static_assert(SMEM <= 232448, "shared memory");
   static_assert((2 * STAGES + 7 + 2 * NUM_EPI_WARPS) * 8 <= 512, "barrier area");
   // partial sums received by a CTA of a split tile: (S - 1) senders x owned units x 16 warps
   static_assert(2 * ((UNITS + 2) / 3) * STAGING <= STAGES * STAGE_BYTES, "split buffers");
@@ -633,6 +634,12 @@ static bool make_box_map(CUtensorMap* map, const void* base, int M, int N, int64
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Records a CUDA error and clears it, so that the caller's next CUDA call does not report it again.
+static int failed(const char* what, cudaError_t e) {
+  (void)cudaGetLastError();
+  return convrot::record_cuda_error(what, e);
+}
+
 constexpr int kMaxDevices = 64;
 
 // Clusters of 2 * split CTAs of this kernel that are resident at once.
@@ -692,7 +699,7 @@ static int launch(const void* a_q, int64_t ld_aq, const void* w_q, int64_t ld_wq
     return convrot::record_error("cuTensorMapEncodeTiled failed for an operand map");
   int resident = 0;
   cudaError_t e = resident_clusters<OUT, ACT, BN, SPLITK>(split, &resident);
-  if (e != cudaSuccess) return convrot::record_cuda_error("fused GEMM set-up", e);
+  if (e != cudaSuccess) return failed("fused GEMM set-up", e);
   const int clusters = SPLITK ? p.num_items : (p.num_items < resident ? p.num_items : resident);
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
@@ -706,7 +713,7 @@ static int launch(const void* a_q, int64_t ld_aq, const void* w_q, int64_t ld_wq
   cfg.numAttrs = 1;
   cfg.gridDim = dim3(clusters * 2 * split);
   e = cudaLaunchKernelEx(&cfg, fused_kernel<OUT, ACT, BN, SPLITK>, ma, mb, mo, mr, p);
-  return e == cudaSuccess ? CONVROT_OK : convrot::record_cuda_error("fused GEMM launch", e);
+  return e == cudaSuccess ? CONVROT_OK : failed("fused GEMM launch", e);
 }
 
 // Tile width and pairs per tile.
@@ -722,26 +729,29 @@ static int pick_shape(const Params& p, Shape* best) {
   // 256 x 5376 x 14336: 256-wide tiles whole 76 us, split in three 48 us;
   // 512 x 2048 x 5376: 128-wide whole 30 us, split in two 21 us, 256-wide
   // split in three 26 us; 1024 x 5376 x 5376: 256-wide 65 us, 128-wide 78 us.
-  constexpr double step256 = 0.29, step128 = 0.26, tail256 = 4.0, join256 = 5.5, join128 = 1.5;
+  struct Variant {
+    int bn;
+    double step, tail, join;
+  };
+  constexpr Variant variants[] = {{256, 0.29, 4.0, 5.5}, {192, 0.28, 2.0, 3.0}, {128, 0.26, 0.0, 1.5}};
   double least = 0;
-  for (int bn : {256, 128}) {
-    const int items = p.num_m2 * ((p.e.N + bn - 1) / bn);
-    const double step = bn == 256 ? step256 : step128;
-    for (int split = 1; split <= MAX_SPLIT; ++split) {
+  for (const Variant& v : variants) {
+    const int items = p.num_m2 * ((p.e.N + v.bn - 1) / v.bn);
+    for (int split = v.bn == 192 ? 2 : 1; split <= MAX_SPLIT; ++split) {     // (192: split tiles only)
       if (split > 1 && p.k_steps < 8 * split) break;
       int resident = 0;
-      cudaError_t e = bn == 256 ? (split == 1 ? resident_clusters<OUT, ACT, 256, false>(1, &resident)
-                                              : resident_clusters<OUT, ACT, 256, true>(split, &resident))
-                                : (split == 1 ? resident_clusters<OUT, ACT, 128, false>(1, &resident)
-                                              : resident_clusters<OUT, ACT, 128, true>(split, &resident));
-      if (e != cudaSuccess) return convrot::record_cuda_error("fused GEMM set-up", e);
+      cudaError_t e = v.bn == 256 ? (split == 1 ? resident_clusters<OUT, ACT, 256, false>(1, &resident)
+                                                : resident_clusters<OUT, ACT, 256, true>(split, &resident))
+                      : v.bn == 192 ? resident_clusters<OUT, ACT, 192, true>(split, &resident)
+                                    : (split == 1 ? resident_clusters<OUT, ACT, 128, false>(1, &resident)
+                                                  : resident_clusters<OUT, ACT, 128, true>(split, &resident));
+      if (e != cudaSuccess) return failed("fused GEMM set-up", e);
       if (split > 1 && items > resident) break;
       const int rounds = (items + resident - 1) / resident, steps = (p.k_steps + split - 1) / split;
-      const double t = rounds * steps * step + (bn == 256 ? tail256 : 0.0) +
-                       (split == 1 ? 0.0 : bn == 256 ? join256 : join128);
+      const double t = rounds * steps * v.step + v.tail + (split == 1 ? 0.0 : v.join);
       if (least == 0 || t < least) {
         least = t;
-        *best = {bn, split};
+        *best = {v.bn, split};
       }
     }
   }
@@ -757,6 +767,7 @@ static int launch_act(const void* a_q, int64_t ld_aq, const void* w_q, int64_t l
   if (s.bn == 256)
     return s.split == 1 ? launch<OUT, ACT, 256, false>(a_q, ld_aq, w_q, ld_wq, K_p, p, 1, st)
                         : launch<OUT, ACT, 256, true>(a_q, ld_aq, w_q, ld_wq, K_p, p, s.split, st);
+  if (s.bn == 192) return launch<OUT, ACT, 192, true>(a_q, ld_aq, w_q, ld_wq, K_p, p, s.split, st);
   return s.split == 1 ? launch<OUT, ACT, 128, false>(a_q, ld_aq, w_q, ld_wq, K_p, p, 1, st)
                       : launch<OUT, ACT, 128, true>(a_q, ld_aq, w_q, ld_wq, K_p, p, s.split, st);
 }
