@@ -28,6 +28,7 @@
 #include "../../include/convrot.h"
 #include "epilogue.cuh"
 #include "errors.h"
+#include "pdl.cuh"
 
 namespace crfused {
 
@@ -212,6 +213,7 @@ few_kernel(const char* __restrict__ a_q, int64_t a_pitch, const char* __restrict
   constexpr int TOKENS = 8 * NT, PITCH = ROWS + 4;   // pad: no bank conflicts below
   __shared__ __align__(16) int sums[TOKENS * PITCH];
   extern __shared__ __align__(16) char ring_all[];
+  convrot::after_previous_kernel();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
   for (int i = threadIdx.x; i < TOKENS * PITCH; i += 32 * WARPS) sums[i] = 0;
   const int part = blockIdx.x % split;
@@ -291,24 +293,13 @@ static cudaError_t launch_few(const void* a_q, int64_t ld_aq, const void* w_q, i
   // 300 x 20480 S8 codes: 17.3 us without, 6.2 us with it.
   int split = 1;
   while (split < 8 && tiles * 2 * split <= 152 * CTAS_PER_SM<NT> && units >= 2 * split * WARPS * 3) split *= 2;
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = split;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   auto k = few_kernel<S8, NT>;
   if constexpr (RING<NT>) {
     const cudaError_t set = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, FEW_SMEM<NT>);
     if (set != cudaSuccess) return set;
   }
-  cfg.dynamicSmemBytes = FEW_SMEM<NT>;
-  cfg.gridDim = dim3(tiles * split);
-  cfg.blockDim = dim3(32 * WARPS);
-  cfg.stream = st;
-  cfg.attrs = attr;
-  cfg.numAttrs = split > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, k, static_cast<const char*>(a_q), ld_aq * es,
-                            static_cast<const char*>(w_q), ld_wq * es, units, split, out_dtype, e);
+  return convrot::launch_after(k, dim3(tiles * split), 32 * WARPS, FEW_SMEM<NT>, split, st, static_cast<const char*>(a_q),
+                               ld_aq * es, static_cast<const char*>(w_q), ld_wq * es, units, split, out_dtype, e);
 }
 
 // FP16 codes of 17 to 64 tokens: up to this weight size this kernel is the

@@ -38,6 +38,7 @@
 #include "../../include/convrot.h"
 #include "errors.h"
 #include "epilogue.cuh"
+#include "pdl.cuh"
 #include "tcgen05.cuh"
 
 namespace crfused {
@@ -298,6 +299,7 @@ fused_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__
                  ::"r"(smem_u32(const_cast<uint32_t*>(tmem_slot))), "r"(L::TMEM_COLS) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
   }
+  convrot::after_previous_kernel();
   tc_fence_before();
   __syncthreads();
   cluster_sync();            // the peers' barriers are initialised before any load or commit targets them
@@ -701,18 +703,8 @@ static int launch(const void* a_q, int64_t ld_aq, const void* w_q, int64_t ld_wq
   cudaError_t e = resident_clusters<OUT, ACT, BN, SPLITK>(split, &resident);
   if (e != cudaSuccess) return failed("fused GEMM set-up", e);
   const int clusters = SPLITK ? p.num_items : (p.num_items < resident ? p.num_items : resident);
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2 * split;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cfg.blockDim = dim3(THREADS);
-  cfg.dynamicSmemBytes = Tile<BN>::SMEM;
-  cfg.stream = st;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  cfg.gridDim = dim3(clusters * 2 * split);
-  e = cudaLaunchKernelEx(&cfg, fused_kernel<OUT, ACT, BN, SPLITK>, ma, mb, mo, mr, p);
+  e = convrot::launch_after(fused_kernel<OUT, ACT, BN, SPLITK>, dim3(clusters * 2 * split), THREADS, Tile<BN>::SMEM, 2 * split,
+                            st, ma, mb, mo, mr, p);
   return e == cudaSuccess ? CONVROT_OK : failed("fused GEMM launch", e);
 }
 

@@ -32,6 +32,7 @@
 
 #include "../../include/convrot.h"
 #include "errors.h"
+#include "pdl.cuh"
 #include "row_input.cuh"
 
 namespace convrot {
@@ -275,6 +276,7 @@ constexpr int kShortWarps = 8, kShortBlocks = 4;
 template <int DT, bool RES, int V, int NBMAX, int SPLIT>
 __global__ void __launch_bounds__(SPLIT == 0 ? 32 * kShortWarps : kMaxThreads) norm_quant_kernel(const NormArgs a) {
   extern __shared__ __align__(16) char smem_all[];
+  after_previous_kernel();
   constexpr int64_t es = (DT == DT_FP32) ? 4 : 2;
   constexpr int PARTS = SPLIT == 2 ? 2 : 1;
   const int nbl = (a.nblocks + PARTS - 1) / PARTS;
@@ -355,6 +357,13 @@ __global__ void __launch_bounds__(SPLIT == 0 ? 32 * kShortWarps : kMaxThreads) n
   if constexpr (SPLIT == 2) cluster_exit_wait();
 }
 
+// launch_rows with launch_after.
+template <typename Kern>
+static cudaError_t launch_norm_rows(Kern k, const RowGeometry& g, int rows, cudaStream_t st, const NormArgs& a) {
+  const cudaError_t e = prep_smem(k, g.smem);
+  return e != cudaSuccess ? e : launch_after(k, dim3(static_cast<unsigned>(rows) * g.split), g.threads, g.smem, g.split, st, a);
+}
+
 template <int DT, bool RES, int V>
 static cudaError_t launch_norm_cfg(const RowGeometry& g, const NormArgs& a, cudaStream_t st) {
   // Short rows share CTAs once there are more of them than SMs; fewer rows
@@ -364,11 +373,11 @@ static cudaError_t launch_norm_cfg(const RowGeometry& g, const NormArgs& a, cuda
     RowGeometry w = g;
     w.threads = 32 * kShortWarps;
     w.smem = static_cast<size_t>(per_cta) * g.nblocks * kSlotBytes;
-    return launch_rows(norm_quant_kernel<DT, RES, V, 1, 0>, w, (a.M + per_cta - 1) / per_cta, st, a);
+    return launch_norm_rows(norm_quant_kernel<DT, RES, V, 1, 0>, w, (a.M + per_cta - 1) / per_cta, st, a);
   }
-  if (g.split == 1) return launch_rows(norm_quant_kernel<DT, RES, V, 1, 1>, g, a.M, st, a);
-  if (g.nbmax == 1) return launch_rows(norm_quant_kernel<DT, RES, V, 1, 2>, g, a.M, st, a);
-  return launch_rows(norm_quant_kernel<DT, RES, V, 2, 2>, g, a.M, st, a);
+  if (g.split == 1) return launch_norm_rows(norm_quant_kernel<DT, RES, V, 1, 1>, g, a.M, st, a);
+  if (g.nbmax == 1) return launch_norm_rows(norm_quant_kernel<DT, RES, V, 1, 2>, g, a.M, st, a);
+  return launch_norm_rows(norm_quant_kernel<DT, RES, V, 2, 2>, g, a.M, st, a);
 }
 
 template <int DT, int V>

@@ -23,6 +23,7 @@
 
 #include "../../include/convrot.h"
 #include "errors.h"
+#include "pdl.cuh"
 
 namespace crrope {
 
@@ -89,6 +90,7 @@ __global__ void __launch_bounds__(32 * kAnyWarps) rope_any_kernel(const Params p
   using E = Elem<DT>;
   using T = typename E::T;
   __shared__ float2 turn[CONVROT_MAX_HEAD / 2];
+  convrot::after_previous_kernel();
   const int m = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   for (int i = threadIdx.x; i < p.P; i += blockDim.x) turn[i] = pair_turn(p, m, i);
   __syncthreads();
@@ -207,6 +209,7 @@ __device__ __forceinline__ void load8(const float* base, int n, int i, float (&v
 template <int DT, bool INTERLEAVED, int G, int T>
 __global__ void __launch_bounds__(32 * kWarps, DT == CONVROT_FP32 ? 4 : 5) rope_kernel(const Params p) {
   extern __shared__ __align__(16) float smem[];
+  convrot::after_previous_kernel();
   float* cs = smem;                          // [T][2][P]: cosines, sines
   float* ws = smem + T * 2 * p.P;            // [2][D]: weights of q and k
   constexpr int HPW = 32 / G;
@@ -299,15 +302,15 @@ static cudaError_t launch_g(const Params& p, cudaStream_t st) {
   auto smem = [&](int T) { return static_cast<size_t>(T * 2 * p.P + 2 * p.D) * sizeof(float); };
   constexpr int kFit = 6 * 152;              // CTAs that the GPU holds at once
   if (p.M >= 4 * 2 * kFit) {
-    rope_kernel<DT, INTERLEAVED, G, 4><<<(p.M + 3) / 4, 32 * kWarps, smem(4), st>>>(p);
+    return convrot::launch_after(rope_kernel<DT, INTERLEAVED, G, 4>, dim3((p.M + 3) / 4), 32 * kWarps, smem(4), 1, st, p);
   } else if (p.M >= 2 * kFit) {
-    rope_kernel<DT, INTERLEAVED, G, 2><<<(p.M + 1) / 2, 32 * kWarps, smem(2), st>>>(p);
+    return convrot::launch_after(rope_kernel<DT, INTERLEAVED, G, 2>, dim3((p.M + 1) / 2), 32 * kWarps, smem(2), 1, st, p);
   } else {
     // few tokens: their heads over several CTAs, up to one warp per group of heads
     int y = (kFit + p.M - 1) / p.M;
     const int most = (groups + kWarps - 1) / kWarps;
     if (y > most) y = most;
-    rope_kernel<DT, INTERLEAVED, G, 1><<<dim3(p.M, y), 32 * kWarps, smem(1), st>>>(p);
+    return convrot::launch_after(rope_kernel<DT, INTERLEAVED, G, 1>, dim3(p.M, y), 32 * kWarps, smem(1), 1, st, p);
   }
   return cudaGetLastError();
 }
@@ -320,8 +323,7 @@ static cudaError_t launch_layout(const Params& p, bool vec, cudaStream_t st) {
     if (pieces <= 8) return launch_g<DT, INTERLEAVED, 8>(p, st);
     if (pieces <= 16) return launch_g<DT, INTERLEAVED, 16>(p, st);
   }
-  rope_any_kernel<DT, INTERLEAVED><<<p.M, 32 * kAnyWarps, 0, st>>>(p);
-  return cudaGetLastError();
+  return convrot::launch_after(rope_any_kernel<DT, INTERLEAVED>, dim3(p.M), 32 * kAnyWarps, 0, 1, st, p);
 }
 
 template <int DT>
