@@ -131,82 +131,100 @@ __global__ void __launch_bounds__(32 * kAnyWarps) rope_any_kernel(const Params p
   }
 }
 
-// Head widths in whole 16-element pieces, on 16-byte boundaries.  A lane holds
-// one piece: 8 pairs, as two runs of 8 elements (pairs i .. i+7 at i and at
-// i + P, or 16 neighbouring elements), G = D / 16 rounded up to a power of two
-// lanes hold a head, and a warp 32 / G heads of one token at a time.  The
-// turns of the CTA's tokens and the norm's weights sit in shared memory, in
-// runs of four with the second runs of four behind the first ones, so that
-// the 16-byte reads of a head's lanes are free of bank conflicts and shared
-// by the warp's heads.
+// Head widths in whole pieces of 2 R elements (R = 8 or 4), on boundaries of R
+// elements.  A lane holds one piece: R pairs, as two runs of R elements (pairs
+// i .. at i and at i + P, or 2 R neighbouring elements), G = D / 2R rounded up
+// to a power of two lanes hold a head, and a warp 32 / G heads of one token at
+// a time.  The turns of the CTA's tokens and the norm's weights sit in shared
+// memory, for R = 8 in runs of four with the second runs of four behind the
+// first ones, so that the 16-byte reads of a head's lanes are free of bank
+// conflicts and shared by the warp's heads.
 constexpr int kWarps = 8;
 
-__device__ __forceinline__ int spread(int i, int n) { return ((i >> 2) & 1) * (n / 2) + (i >> 3) * 4 + (i & 3); }
+template <int R>
+__device__ __forceinline__ int spread(int i, int n) {
+  return R == 8 ? ((i >> 2) & 1) * (n / 2) + (i >> 3) * 4 + (i & 3) : i;
+}
 
-template <int DT>
+template <int DT, int R>
 struct Piece {
-  static constexpr int W = DT == CONVROT_FP32 ? 8 : 4;     // words of one run of 8 elements
+  static constexpr int W = DT == CONVROT_FP32 ? R : R / 2;     // words of one run
   uint32_t w[2][W];
 };
 
-template <int DT>
-__device__ __forceinline__ void load_piece(const void* x, int64_t off, int j0, int j1, Piece<DT>& r) {
-  using T = typename Elem<DT>::T;
-  const T* p = static_cast<const T*>(x) + off;
+// One run's words to or from memory, 16 or 8 bytes at a time.
+template <int W>
+__device__ __forceinline__ void load_run(const void* p, uint32_t (&w)[W]) {
+  if constexpr (W == 2) {
+    const uint2 v = *static_cast<const uint2*>(p);
+    w[0] = v.x; w[1] = v.y;
+  } else {
 #pragma unroll
-  for (int h = 0; h < 2; ++h)
-#pragma unroll
-    for (int u = 0; u < Piece<DT>::W / 4; ++u) {
-      const uint4 v = *(reinterpret_cast<const uint4*>(p + (h ? j1 : j0)) + u);
-      r.w[h][4 * u] = v.x; r.w[h][4 * u + 1] = v.y; r.w[h][4 * u + 2] = v.z; r.w[h][4 * u + 3] = v.w;
+    for (int u = 0; u < W; u += 4) {
+      const uint4 v = *(static_cast<const uint4*>(p) + u / 4);
+      w[u] = v.x; w[u + 1] = v.y; w[u + 2] = v.z; w[u + 3] = v.w;
     }
+  }
+}
+template <int W>
+__device__ __forceinline__ void store_run(void* p, const uint32_t (&w)[W]) {
+  if constexpr (W == 2) {
+    *static_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+  } else {
+#pragma unroll
+    for (int u = 0; u < W; u += 4) *(static_cast<uint4*>(p) + u / 4) = make_uint4(w[u], w[u + 1], w[u + 2], w[u + 3]);
+  }
 }
 
-template <int DT>
-__device__ __forceinline__ float piece_elem(const Piece<DT>& r, int h, int e) {
+template <int DT, int R>
+__device__ __forceinline__ void load_piece(const void* x, int64_t off, int j0, int j1, Piece<DT, R>& r) {
+  const typename Elem<DT>::T* p = static_cast<const typename Elem<DT>::T*>(x) + off;
+  load_run(p + j0, r.w[0]);
+  load_run(p + j1, r.w[1]);
+}
+
+template <int DT, int R>
+__device__ __forceinline__ float piece_elem(const Piece<DT, R>& r, int h, int e) {
   if constexpr (DT == CONVROT_FP32) return __uint_as_float(r.w[h][e]);
   else if constexpr (DT == CONVROT_BF16) return __uint_as_float((e & 1) ? (r.w[h][e >> 1] & 0xffff0000u) : (r.w[h][e >> 1] << 16));
   else return __half2float(__ushort_as_half(static_cast<unsigned short>((e & 1) ? (r.w[h][e >> 1] >> 16) : (r.w[h][e >> 1] & 0xffffu))));
 }
 
-template <int DT>
-__device__ __forceinline__ void store_piece(void* y, int64_t off, int j0, int j1, const float (&v)[2][8]) {
-  using T = typename Elem<DT>::T;
-  T* p = static_cast<T*>(y) + off;
+template <int DT, int R>
+__device__ __forceinline__ void store_piece(void* y, int64_t off, int j0, int j1, const float (&v)[2][R]) {
+  typename Elem<DT>::T* p = static_cast<typename Elem<DT>::T*>(y) + off;
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    uint4* d = reinterpret_cast<uint4*>(p + (h ? j1 : j0));
-    if constexpr (DT == CONVROT_FP32) {
+    uint32_t w[Piece<DT, R>::W];
 #pragma unroll
-      for (int u = 0; u < 2; ++u)
-        d[u] = make_uint4(__float_as_uint(v[h][4 * u]), __float_as_uint(v[h][4 * u + 1]),
-                          __float_as_uint(v[h][4 * u + 2]), __float_as_uint(v[h][4 * u + 3]));
-    } else {
-      uint32_t w[4];
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        if constexpr (DT == CONVROT_BF16) {
-          const __nv_bfloat162 t = __floats2bfloat162_rn(v[h][2 * u], v[h][2 * u + 1]);
-          w[u] = *reinterpret_cast<const uint32_t*>(&t);
-        } else {
-          const __half2 t = __floats2half2_rn(v[h][2 * u], v[h][2 * u + 1]);
-          w[u] = *reinterpret_cast<const uint32_t*>(&t);
-        }
+    for (int u = 0; u < Piece<DT, R>::W; ++u) {
+      if constexpr (DT == CONVROT_FP32) {
+        w[u] = __float_as_uint(v[h][u]);
+      } else if constexpr (DT == CONVROT_BF16) {
+        const __nv_bfloat162 t = __floats2bfloat162_rn(v[h][2 * u], v[h][2 * u + 1]);
+        w[u] = *reinterpret_cast<const uint32_t*>(&t);
+      } else {
+        const __half2 t = __floats2half2_rn(v[h][2 * u], v[h][2 * u + 1]);
+        w[u] = *reinterpret_cast<const uint32_t*>(&t);
       }
-      d[0] = make_uint4(w[0], w[1], w[2], w[3]);
     }
+    store_run(p + (h ? j1 : j0), w);
   }
 }
 
-__device__ __forceinline__ void load8(const float* base, int n, int i, float (&v)[8]) {   // i a multiple of 8
-  const float4 a = *reinterpret_cast<const float4*>(base + i / 2);
-  const float4 b = *reinterpret_cast<const float4*>(base + n / 2 + i / 2);
+// R values from i on (a multiple of R) of an array of n in shared memory.
+template <int R>
+__device__ __forceinline__ void load_values(const float* base, int n, int i, float (&v)[R]) {
+  const float4 a = *reinterpret_cast<const float4*>(base + (R == 8 ? i / 2 : i));
   v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  if constexpr (R == 8) {
+    const float4 b = *reinterpret_cast<const float4*>(base + n / 2 + i / 2);
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  }
 }
 
-// T tokens per CTA (1, 2, 4 or 8), kWarps / T warps each; gridDim.y CTAs share a token's heads.
-template <int DT, bool INTERLEAVED, int G, int T>
+// T tokens per CTA (1, 2 or 4), kWarps / T warps each; gridDim.y CTAs share a token's heads.
+template <int DT, bool INTERLEAVED, int R, int G, int T>
 __global__ void __launch_bounds__(32 * kWarps, DT == CONVROT_FP32 ? 4 : 5) rope_kernel(const Params p) {
   extern __shared__ __align__(16) float smem[];
   convrot::after_previous_kernel();
@@ -217,35 +235,35 @@ __global__ void __launch_bounds__(32 * kWarps, DT == CONVROT_FP32 ? 4 : 5) rope_
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int m0 = blockIdx.x * T, t = warp / WPT, m = m0 + t;
   const int c = lane % G, hl = lane / G;
-  const bool piece = 16 * c < p.D;           // lanes past the head's pieces idle
-  const bool turns = 8 * c < p.P;            // this piece is rotated
+  const bool piece = 2 * R * c < p.D;           // lanes past the head's pieces idle
+  const bool turns = R * c < p.P;            // this piece is rotated
   // the piece's two runs: a rotated piece of the split layout lies in both halves
-  const int j0 = !turns || INTERLEAVED ? 16 * c : 8 * c;
-  const int j1 = !turns || INTERLEAVED ? 16 * c + 8 : 8 * c + p.P;
+  const int j0 = !turns || INTERLEAVED ? 2 * R * c : R * c;
+  const int j1 = !turns || INTERLEAVED ? 2 * R * c + R : R * c + p.P;
   const int gq = (p.q.heads + HPW - 1) / HPW, gk = (p.k.heads + HPW - 1) / HPW;
   const int groups = m < p.M ? gq + gk : 0, step = WPT * gridDim.y;
-  auto load = [&](int g, Piece<DT>& r) {
+  auto load = [&](int g, Piece<DT, R>& r) {
     const Operand& o = g < gq ? p.q : p.k;
     const int head = (g < gq ? g : g - gq) * HPW + hl;
     r = {};
-    if (g < groups && piece && head < o.heads) load_piece<DT>(o.x, m * o.x_tok + head * o.x_head, j0, j1, r);
+    if (g < groups && piece && head < o.heads) load_piece<DT, R>(o.x, m * o.x_tok + head * o.x_head, j0, j1, r);
   };
   // the first heads are on their way while the turns are worked out
   int g = blockIdx.y * WPT + warp % WPT;
-  Piece<DT> r;
+  Piece<DT, R> r;
   load(g, r);
   for (int i = threadIdx.x; i < T * p.P; i += 32 * kWarps) {
     const int u = i / p.P, j = i - u * p.P;
     if (m0 + u < p.M) {
       const float2 v = pair_turn(p, m0 + u, j);
-      cs[u * 2 * p.P + spread(j, p.P)] = v.x;
-      cs[u * 2 * p.P + p.P + spread(j, p.P)] = v.y;
+      cs[u * 2 * p.P + spread<R>(j, p.P)] = v.x;
+      cs[u * 2 * p.P + p.P + spread<R>(j, p.P)] = v.y;
     }
   }
   for (int i = threadIdx.x; i < 2 * p.D; i += 32 * kWarps) {
     const float* w = i < p.D ? p.q.weight : p.k.weight;
     const int j = i < p.D ? i : i - p.D;
-    if (w) ws[(i < p.D ? 0 : p.D) + spread(j, p.D)] = __ldg(w + j);
+    if (w) ws[(i < p.D ? 0 : p.D) + spread<R>(j, p.D)] = __ldg(w + j);
   }
   __syncthreads();
   const float* tcs = cs + t * 2 * p.P;
@@ -254,81 +272,85 @@ __global__ void __launch_bounds__(32 * kWarps, DT == CONVROT_FP32 ? 4 : 5) rope_
     const Operand& o = is_q ? p.q : p.k;
     const int head = (is_q ? g : g - gq) * HPW + hl;
     const bool active = piece && head < o.heads;
-    float v[2][8];
+    float v[2][R];
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[h][e] = piece_elem<DT>(r, h, e);
+      for (int e = 0; e < R; ++e) v[h][e] = piece_elem<DT, R>(r, h, e);
     load(g + step, r);
     if (o.weight) {
       float ss = 0.f;
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) ss = fmaf(v[h][e], v[h][e], ss);
+        for (int e = 0; e < R; ++e) ss = fmaf(v[h][e], v[h][e], ss);
 #pragma unroll
       for (int s = G / 2; s > 0; s >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, s);
       const float f = rsqrtf(ss / static_cast<float>(p.D) + p.eps);
       if (piece) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          float w[8];
-          load8(ws + (is_q ? 0 : p.D), p.D, h ? j1 : j0, w);
+          float w[R];
+          load_values<R>(ws + (is_q ? 0 : p.D), p.D, h ? j1 : j0, w);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) v[h][e] *= f * w[e];
+          for (int e = 0; e < R; ++e) v[h][e] *= f * w[e];
         }
       }
     }
     if (turns) {
-      float co[8], si[8];
-      load8(tcs, p.P, 8 * c, co);
-      load8(tcs + p.P, p.P, 8 * c, si);
+      float co[R], si[R];
+      load_values<R>(tcs, p.P, R * c, co);
+      load_values<R>(tcs + p.P, p.P, R * c, si);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        float& a = INTERLEAVED ? v[e >> 2][2 * (e & 3)] : v[0][e];
-        float& b = INTERLEAVED ? v[e >> 2][2 * (e & 3) + 1] : v[1][e];
+      for (int e = 0; e < R; ++e) {
+        float& a = INTERLEAVED ? v[2 * e / R][2 * e % R] : v[0][e];
+        float& b = INTERLEAVED ? v[2 * e / R][2 * e % R + 1] : v[1][e];
         const float ta = a * co[e] - b * si[e], tb = b * co[e] + a * si[e];
         a = ta;
         b = tb;
       }
     }
-    if (active) store_piece<DT>(o.y, m * o.y_tok + head * o.y_head, j0, j1, v);
+    if (active) store_piece<DT, R>(o.y, m * o.y_tok + head * o.y_head, j0, j1, v);
   }
 }
 
-template <int DT, bool INTERLEAVED, int G>
+template <int DT, bool INTERLEAVED, int R, int G>
 static cudaError_t launch_g(const Params& p, cudaStream_t st) {
   const int per_warp = 32 / G, groups = (p.q.heads + per_warp - 1) / per_warp + (p.k.heads + per_warp - 1) / per_warp;
   auto smem = [&](int T) { return static_cast<size_t>(T * 2 * p.P + 2 * p.D) * sizeof(float); };
   constexpr int kFit = 6 * 152;              // CTAs that the GPU holds at once
   if (p.M >= 4 * 2 * kFit) {
-    return convrot::launch_after(rope_kernel<DT, INTERLEAVED, G, 4>, dim3((p.M + 3) / 4), 32 * kWarps, smem(4), 1, st, p);
+    return convrot::launch_after(rope_kernel<DT, INTERLEAVED, R, G, 4>, dim3((p.M + 3) / 4), 32 * kWarps, smem(4), 1, st, p);
   } else if (p.M >= 2 * kFit) {
-    return convrot::launch_after(rope_kernel<DT, INTERLEAVED, G, 2>, dim3((p.M + 1) / 2), 32 * kWarps, smem(2), 1, st, p);
+    return convrot::launch_after(rope_kernel<DT, INTERLEAVED, R, G, 2>, dim3((p.M + 1) / 2), 32 * kWarps, smem(2), 1, st, p);
   } else {
     // few tokens: their heads over several CTAs, up to one warp per group of heads
     int y = (kFit + p.M - 1) / p.M;
     const int most = (groups + kWarps - 1) / kWarps;
     if (y > most) y = most;
-    return convrot::launch_after(rope_kernel<DT, INTERLEAVED, G, 1>, dim3(p.M, y), 32 * kWarps, smem(1), 1, st, p);
+    return convrot::launch_after(rope_kernel<DT, INTERLEAVED, R, G, 1>, dim3(p.M, y), 32 * kWarps, smem(1), 1, st, p);
   }
   return cudaGetLastError();
 }
 
 template <int DT, bool INTERLEAVED>
-static cudaError_t launch_layout(const Params& p, bool vec, cudaStream_t st) {
-  if (vec) {
-    const int pieces = p.D / 16;
-    if (pieces <= 4) return launch_g<DT, INTERLEAVED, 4>(p, st);
-    if (pieces <= 8) return launch_g<DT, INTERLEAVED, 8>(p, st);
-    if (pieces <= 16) return launch_g<DT, INTERLEAVED, 16>(p, st);
+static cudaError_t launch_layout(const Params& p, int run, cudaStream_t st) {
+  if (run == 8) {
+    if (p.D <= 64) return launch_g<DT, INTERLEAVED, 8, 4>(p, st);
+    if (p.D <= 128) return launch_g<DT, INTERLEAVED, 8, 8>(p, st);
+    return launch_g<DT, INTERLEAVED, 8, 16>(p, st);
+  }
+  if (run == 4) {
+    if (p.D <= 64) return launch_g<DT, INTERLEAVED, 4, 8>(p, st);
+    if (p.D <= 128) return launch_g<DT, INTERLEAVED, 4, 16>(p, st);
+    return launch_g<DT, INTERLEAVED, 4, 32>(p, st);
   }
   return convrot::launch_after(rope_any_kernel<DT, INTERLEAVED>, dim3(p.M), 32 * kAnyWarps, 0, 1, st, p);
 }
 
 template <int DT>
-static cudaError_t launch(const Params& p, bool interleaved, bool vec, cudaStream_t st) {
-  return interleaved ? launch_layout<DT, true>(p, vec, st) : launch_layout<DT, false>(p, vec, st);
+static cudaError_t launch(const Params& p, bool interleaved, int run, cudaStream_t st) {
+  return interleaved ? launch_layout<DT, true>(p, run, st) : launch_layout<DT, false>(p, run, st);
 }
 
 }  // namespace crrope
@@ -402,20 +424,27 @@ extern "C" int convrot_qk_norm_rope(const void* q, int64_t q_tok, int64_t q_head
   p.ld_pos = ld_pos;
   p.inv_freq = inv_freq;
   p.eps = eps;
-  // vector path: whole 16-element pieces on 16-byte boundaries
-  const int64_t e16 = 16 / static_cast<int64_t>(es);
-  auto on16 = [&](const void* t, int64_t tok, int64_t head, int heads) {
-    return reinterpret_cast<uintptr_t>(t) % 16 == 0 && (M == 1 || tok % e16 == 0) && (heads <= 1 || head % e16 == 0);
+  // runs of 8 or 4 elements: whole pieces, on their boundaries (at most 16 bytes)
+  auto fits = [&](int run) {
+    const int64_t bytes = run * static_cast<int64_t>(es) < 16 ? run * static_cast<int64_t>(es) : 16;
+    const int64_t elems = bytes / static_cast<int64_t>(es);
+    if (D % (2 * run) != 0 || pairs % run != 0 || D > 256) return false;
+    for (const Operand* o : {&p.q, &p.k}) {
+      if (o->heads == 0) continue;
+      for (int side = 0; side < 2; ++side) {
+        const int64_t tok = side ? o->y_tok : o->x_tok, head = side ? o->y_head : o->x_head;
+        if (reinterpret_cast<uintptr_t>(side ? o->y : o->x) % bytes || (M > 1 && tok % elems) || (o->heads > 1 && head % elems))
+          return false;
+      }
+    }
+    return true;
   };
-  bool vec = D % 16 == 0 && pairs % 8 == 0;
-  for (const Operand* o : {&p.q, &p.k})
-    if (o->heads > 0)
-      vec = vec && on16(o->x, o->x_tok, o->x_head, o->heads) && on16(o->y, o->y_tok, o->y_head, o->heads);
+  const int run = fits(8) ? 8 : fits(4) ? 4 : 0;
   cudaError_t e;
   switch (dtype) {
-    case CONVROT_BF16: e = launch<CONVROT_BF16>(p, interleaved != 0, vec, stream); break;
-    case CONVROT_FP16: e = launch<CONVROT_FP16>(p, interleaved != 0, vec, stream); break;
-    default: e = launch<CONVROT_FP32>(p, interleaved != 0, vec, stream); break;
+    case CONVROT_BF16: e = launch<CONVROT_BF16>(p, interleaved != 0, run, stream); break;
+    case CONVROT_FP16: e = launch<CONVROT_FP16>(p, interleaved != 0, run, stream); break;
+    default: e = launch<CONVROT_FP32>(p, interleaved != 0, run, stream); break;
   }
   return e == cudaSuccess ? CONVROT_OK : convrot::record_cuda_error("qk_norm_rope launch", e);
 }
