@@ -171,6 +171,18 @@ def test_strides_and_neighbours(cr, M, out, off, pitch, roff, rpitch):
         assert torch.all(ob == 9)
 
 
+@pytest.mark.parametrize("M,fmt,pitch", [(3, torch.int8, 2 ** 30 + 8), (3, torch.float16, 2 ** 30 + 3),
+                                         (70, torch.float16, 2 ** 25 + 8), (70, torch.float16, 2 ** 25 + 5)])
+def test_offsets_past_32_bits(cr, M, fmt, pitch):
+    # output and residual (the same matrix) span more than 2^31 elements; aligned rows and odd ones
+    N, Kp = 130, 512
+    p = problem(M, N, Kp, "bf16", 51)
+    big = torch.empty((M - 1) * pitch + N, dtype=torch.bfloat16, device=DEV)
+    y = big.as_strided((M, N), (pitch, 1))
+    y.copy_(p["residual"])
+    assert torch.equal(run(cr, p, "bf16", fmt, y=y, residual=y).cpu(), exact_f32(p, "bf16"))
+
+
 def test_many_tiles_and_full_waves(cr):
     # more tiles than CTA pairs, a ragged last strip and column
     p = problem(2305, 2600, 512, "bf16", 31)

@@ -203,6 +203,22 @@ def test_other_stream_and_graph(cr):
     assert torch.equal(q, q2) and torch.equal(s, s2)
 
 
+def test_offsets_past_32_bits(cr):
+    # two rows more than 2^31 elements apart
+    K, pitch = 1000, 2 ** 31 + 24
+    x, r, w = make(2, K, "bf16", 9, True)
+    h_ref, q_ref, s_ref = reference(x, r, w, 1e-6)
+    big = torch.empty(pitch + K, dtype=torch.bfloat16, device=DEV)
+    xv = big.as_strided((2, K), (pitch, 1))
+    xv.copy_(x)
+    q = torch.empty(2, 1024, dtype=torch.float16, device=DEV)
+    s = torch.empty(2, device=DEV)
+    cr.rms_norm_quant(xv, K, q, s, residual=r.to(DEV), h=xv, weight=w.to(DEV))
+    torch.cuda.synchronize()
+    check(q, s, q_ref, s_ref)
+    assert torch.equal(xv.cpu(), h_ref)
+
+
 def test_empty_call(cr):
     x = torch.empty(0, 300, device=DEV)
     cr.rms_norm_quant(x, 300, torch.empty(0, 512, dtype=torch.int8, device=DEV), torch.empty(0, device=DEV))

@@ -126,6 +126,21 @@ def test_strides_and_alignment(cr, off, head, tok):
     assert torch.all(out == 3)
 
 
+def test_offsets_past_32_bits(cr):
+    M, H, D, pairs, tok = 2, 3, 128, [64], 2 ** 31 + 512
+    g = torch.Generator().manual_seed(8)
+    x = torch.randn(M, H, D, generator=g).to(torch.bfloat16)
+    buf = torch.empty(tok + H * D, dtype=torch.bfloat16, device=DEV)
+    q = buf.as_strided((M, H, D), (tok, D, 1))
+    q.copy_(x)
+    pos = torch.tensor([[3], [11]], dtype=torch.int32)
+    fd = torch.tensor(cr.rope_inv_freq(pairs), dtype=torch.float64, device=DEV)
+    w = 1 + 0.3 * torch.randn(D, generator=g)
+    cr.qk_norm_rope(q, None, pos.to(DEV), fd, pairs, q, None, q_weight=w.to(DEV))
+    torch.cuda.synchronize()
+    check(q, reference(x, w, pos, pairs, 10000.0, 1e-6, False), "bf16")
+
+
 def test_large_and_negative_positions(cr):
     # FP32 products of position and frequency would be off by up to 60 radians here
     D, pairs = 64, [16, 16]
