@@ -11,12 +11,25 @@
 // only in the quantiser.  One read of the row, one reduction.
 //
 // Bound by HBM: per element the row, the residual, h and an FP16-held code,
-// 8 bytes with 16-bit storage.  The row's elements are read and h is written
-// in whole coalesced accesses and handed to the rotation through shared
-// memory; a thread's own 32 elements (two sectors of a row per thread) read
-// and written directly took 257 us where this takes 155 us (19989 x 5376,
-// BF16, residual: 82% of the copy bandwidth), and it keeps rows of any
-// alignment coalesced.
+// 8 bytes with 16-bit storage.  Two ways into the rotation:
+//
+// - direct (read_block, rotate_direct, store_direct), where rows, weights and
+//   codes lie on whole vectors: eight lanes read neighbouring bytes of a
+//   block, transform over the five element bits that this leaves in a lane,
+//   exchange once through shared memory for the other three and write eight
+//   codes at a time.  19989 x 5376 BF16 with residual 129 us (98% of the copy
+//   bandwidth), without 103; 4097 x 5000 FP32 30 us (60%: without weights 26,
+//   and the layer's quant_act, which has neither weights nor a sum of squares,
+//   also takes 30).
+// - staged (stage_row, rotate_block), for any alignment and for rows of more
+//   than 32768: coalesced accesses that hand the row to the rotation through
+//   shared memory.  153, 127 and 34 us for the same.
+//
+// What the weights cost decides between layouts: at 4 bytes per element they
+// are twice a 16-bit row, and lanes whose weights are 64 or 128 bytes apart
+// read them at a half or a quarter of the L1 rate (19989 x 5376 BF16 with
+// residual: 137 and 224 us).  CTAs that stay, with the weights in registers
+// and rows fetched by asynchronous copies, need 128 registers: 146 us.
 //
 // The sum and the norm's statistics are FP32; h is rounded to the storage
 // type before anything else uses it, so that the codes are those of the
@@ -197,6 +210,183 @@ __device__ __forceinline__ float stage_row(const NormArgs& a, int row, int e0, i
   return ss;
 }
 
+// Eight elements of a row, aligned to the whole.  Rows are read once: they
+// take no L1 lines from the weights.
+template <int DT>
+struct Eight {
+  static constexpr int W = DT == DT_FP32 ? 8 : 4;
+  uint32_t w[W];
+
+  __device__ __forceinline__ void load(const char* p) {
+    if constexpr (W == 8)
+      asm volatile("ld.global.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                   : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+                   : "l"(p));
+    else
+      asm volatile("ld.global.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                   : "l"(p));
+  }
+  __device__ __forceinline__ void store(char* p) const {
+    if constexpr (W == 8)
+      asm volatile("st.global.v8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::"r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
+                   "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]), "l"(p)
+                   : "memory");
+    else
+      *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+};
+
+// The direct way from a row to its rotation, for rows, weights and codes on
+// whole vectors.  Lane l of a block's eight reads
+// elements 64 c + 8 l + b (c < 4, b < 8): eight lanes read neighbouring bytes
+// of x, residual, h and weight.  Element bits 0-2 and 6-7 are thereby its
+// own, and it transforms over them (P[8 c' + b] holds chunks c' and c' + 2;
+// the packed transform covers b and c', a scalar stage the pair); bits 3-5
+// follow after one exchange through shared memory.
+template <int DT, bool RES>
+__device__ __forceinline__ float read_block(const NormArgs& a, int row, int blk, int lane8, float2 (&P)[16]) {
+  constexpr int64_t es = (DT == DT_FP32) ? 4 : 2;
+  const int e0 = blk * kBlock + 8 * lane8;
+  const char* x = a.x + (row * a.ld_x + e0) * es;
+  const char* r = RES ? a.res + (row * a.ld_res + e0) * es : nullptr;
+  char* h = a.h ? a.h + (row * a.ld_h + e0) * es : nullptr;
+  Eight<DT> cx[4], cr[RES ? 4 : 1];
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    if (e0 + 64 * c + 8 <= a.K) {
+      cx[c].load(x + 64 * c * es);
+      if constexpr (RES) cr[c].load(r + 64 * c * es);
+    }
+  }
+  constexpr int kAhead = 2;                  // chunks that the weights are loaded ahead
+  float w[4][8];
+  auto weights = [&](int c) {
+    const int e = e0 + 64 * c;
+    if (a.weight && e + 8 <= a.K)
+      asm volatile("ld.global.nc.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                   : "=f"(w[c][0]), "=f"(w[c][1]), "=f"(w[c][2]), "=f"(w[c][3]), "=f"(w[c][4]), "=f"(w[c][5]),
+                     "=f"(w[c][6]), "=f"(w[c][7])
+                   : "l"(a.weight + e));
+    else
+#pragma unroll
+      for (int b = 0; b < 8; ++b) w[c][b] = a.weight && e + b < a.K ? __ldg(a.weight + e + b) : 1.f;
+  };
+#pragma unroll
+  for (int c = 0; c < kAhead; ++c) weights(c);
+  float ss = 0.f;
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    if (c + kAhead < 4) weights(c + kAhead);
+    float v[8];
+    if (e0 + 64 * c + 8 <= a.K) {
+      Chunk<DT, 8> t;
+#pragma unroll
+      for (int i = 0; i < Eight<DT>::W; ++i) t.w[i] = cx[c].w[i];
+      if constexpr (RES) {
+        Chunk<DT, 8> u;
+#pragma unroll
+        for (int i = 0; i < Eight<DT>::W; ++i) u.w[i] = cr[c].w[i];
+        t.add(u);
+#pragma unroll
+        for (int i = 0; i < Eight<DT>::W; ++i) cx[c].w[i] = t.w[i];
+      }
+      if (h) cx[c].store(h + 64 * c * es);
+#pragma unroll
+      for (int b = 0; b < 8; ++b) v[b] = t.get(b);
+    } else {
+      // the row's end: element by element, zeros past it
+#pragma unroll
+      for (int b = 0; b < 8; ++b) {
+        v[b] = 0.f;
+        if (e0 + 64 * c + b < a.K) {
+          Chunk<DT, 1> c1, r1;
+          c1.load(x + (64 * c + b) * es);
+          if constexpr (RES) {
+            r1.load(r + (64 * c + b) * es);
+            c1.add(r1);
+          }
+          if (h) c1.store(h + (64 * c + b) * es);
+          v[b] = c1.get(0);
+        }
+      }
+    }
+#pragma unroll
+    for (int b = 0; b < 8; ++b) ss = fmaf(v[b], v[b], ss);
+#pragma unroll
+    for (int b = 0; b < 8; ++b) {
+      const float y = v[b] * w[c][b];
+      if (c < 2) P[8 * c + b].x = y;
+      else P[8 * (c - 2) + b].y = y;
+    }
+  }
+  return ss;
+}
+
+// The block's transform z: U[l], V[l] of lane 2 c + h hold elements
+// 64 c + 8 l + 4 h + (0, 1) and (2, 3).  Reached by every lane of the warp.
+__device__ __forceinline__ void rotate_direct(float2 (&P)[16], BlockCols& out, char* slot_smem, int lane8, bool active) {
+  float4* s = reinterpret_cast<float4*>(slot_smem);
+  if (active) {
+    fwht16x2(P);
+    // chunk c, lane l, half h (four elements) at 18 c + (2 l + h) ^ (l / 4):
+    // neither the writes nor the reads meet bank conflicts
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float2 *p = P + 8 * c + 4 * h;
+        const int at = (2 * lane8 + h) ^ (lane8 >> 2);
+        s[18 * c + at] = make_float4(p[0].x + p[0].y, p[1].x + p[1].y, p[2].x + p[2].y, p[3].x + p[3].y);
+        s[18 * (c + 2) + at] = make_float4(p[0].x - p[0].y, p[1].x - p[1].y, p[2].x - p[2].y, p[3].x - p[3].y);
+      }
+  }
+  __syncwarp();
+  if (active) {
+    const float4* from = s + 18 * (lane8 >> 1);
+#pragma unroll
+    for (int l = 0; l < 8; ++l) {
+      const float4 f = from[(2 * l + (lane8 & 1)) ^ (l >> 2)];
+      out.U[l] = make_float2(f.x, f.y);
+      out.V[l] = make_float2(f.z, f.w);
+    }
+    fwht8x2(out.U);
+    fwht8x2(out.V);
+  }
+  __syncwarp();
+}
+
+// Codes of rotate_direct's block (already multiplied, so only the rounding is
+// left).  Two neighbouring lanes exchange halves, so that each writes eight
+// codes at a time.  Reached by every lane of the warp.
+__device__ __forceinline__ void store_direct(char* q_row, bool f16_codes, int blk, int lane8, const BlockCols& c, bool active) {
+  const int h = lane8 & 1, e = blk * kBlock + 64 * (lane8 >> 1) + 8 * h;
+  auto pair = [](float2 v) {
+    const __half2 t = __floats2half2_rn(rint_f<false>(v.x), rint_f<false>(v.y));
+    return *reinterpret_cast<const uint32_t*>(&t);
+  };
+  if (f16_codes) {
+    char* to = q_row + 2 * e;
+#pragma unroll
+    for (int l = 0; l < 8; l += 2) {
+      const uint32_t u0 = pair(c.U[l]), v0 = pair(c.V[l]), u1 = pair(c.U[l + 1]), v1 = pair(c.V[l + 1]);
+      const uint32_t ru = __shfl_xor_sync(0xffffffffu, h ? u0 : u1, 1), rv = __shfl_xor_sync(0xffffffffu, h ? v0 : v1, 1);
+      if (active) *reinterpret_cast<uint4*>(to + 16 * l) = h ? make_uint4(ru, rv, u1, v1) : make_uint4(u0, v0, ru, rv);
+    }
+  } else {
+    char* to = q_row + e;
+    auto four = [](float2 u, float2 v) {
+      return code_byte<false>(u.x) | code_byte<false>(u.y) << 8 | code_byte<false>(v.x) << 16 | code_byte<false>(v.y) << 24;
+    };
+#pragma unroll
+    for (int l = 0; l < 8; l += 2) {
+      const uint32_t w0 = four(c.U[l], c.V[l]), w1 = four(c.U[l + 1], c.V[l + 1]);
+      const uint32_t r = __shfl_xor_sync(0xffffffffu, h ? w0 : w1, 1);
+      if (active) *reinterpret_cast<uint2*>(to + 8 * l) = h ? make_uint2(r, w1) : make_uint2(w0, r);
+    }
+  }
+}
+
 // What the row's totals give: scale, multiplier of z and norm bound.  z / 16 is
 // the rotated row, and r its RMS factor.
 struct RowResult {
@@ -270,11 +460,13 @@ __device__ __forceinline__ RowResult norm_reduce(float amax, float ssh, float ss
 // SPLIT == 0: rows of at most four blocks; 8, 16 or 32 lanes of a warp hold a
 // row, eight warps share a CTA, and no barrier is wider than the warp.
 // SPLIT == 1: a CTA per row.  SPLIT == 2: a cluster of two CTAs per row.
-// V: elements per access of the first pass.
+// V: elements per access of the first pass, or kDirect.
+
+constexpr int kDirect = 16;
 constexpr int kShortWarps = 8, kShortBlocks = 4;
 
 template <int DT, bool RES, int V, int NBMAX, int SPLIT>
-__global__ void __launch_bounds__(SPLIT == 0 ? 32 * kShortWarps : kMaxThreads) norm_quant_kernel(const NormArgs a) {
+__device__ __forceinline__ void norm_row(const NormArgs& a) {
   extern __shared__ __align__(16) char smem_all[];
   after_previous_kernel();
   constexpr int64_t es = (DT == DT_FP32) ? 4 : 2;
@@ -291,7 +483,7 @@ __global__ void __launch_bounds__(SPLIT == 0 ? 32 * kShortWarps : kMaxThreads) n
   float* red = reinterpret_cast<float*>(smem_all + nbl * kSlotBytes);   // (SPLIT == 0: unused)
 
   float ssh = 0.f;
-  if (live) ssh = stage_row<DT, RES, V>(a, row, blk0 * kBlock, nloc * kBlock, smem, tid, width);
+  if (V != kDirect && live) ssh = stage_row<DT, RES, V>(a, row, blk0 * kBlock, nloc * kBlock, smem, tid, width);
   if constexpr (SPLIT != 0) {
     // this CTA's share of a later row, into L2 (see l2_prefetch)
     if (const int later = row + a.pf_dist; later < a.M) {
@@ -301,8 +493,10 @@ __global__ void __launch_bounds__(SPLIT == 0 ? 32 * kShortWarps : kMaxThreads) n
       if constexpr (RES) l2_prefetch(a.res + later * a.ld_res * es + b0, b1 - b0);
     }
   }
-  if constexpr (SPLIT != 0) __syncthreads();
-  else __syncwarp();
+  if constexpr (V != kDirect) {
+    if constexpr (SPLIT != 0) __syncthreads();
+    else __syncwarp();
+  }
 
   BlockCols c[NBMAX];
   float amax = 0.f, ssz = 0.f;
@@ -312,7 +506,9 @@ __global__ void __launch_bounds__(SPLIT == 0 ? 32 * kShortWarps : kMaxThreads) n
     const bool active = live && (slot < a.S) && (li < nloc);
     char* mine = smem + (active ? li : 0) * kSlotBytes;
     float2 P[16];                                  // (element b, element 16 + b) of the thread's 32
-    if (active) {
+    if constexpr (V == kDirect) {
+      if (active) ssh += read_block<DT, RES>(a, row, blk0 + li, lane8, P);
+    } else if (active) {
       const float4* line = reinterpret_cast<const float4*>(mine) + 8 * lane8;
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
@@ -323,8 +519,9 @@ __global__ void __launch_bounds__(SPLIT == 0 ? 32 * kShortWarps : kMaxThreads) n
         P[4 * u + 3] = make_float2(lo.w, hi.w);
       }
     }
-    __syncwarp();                                  // the block is read before its region becomes the transpose buffer
-    rotate_block(P, c[i], mine, lane8, active);
+    if constexpr (V != kDirect) __syncwarp();      // the block is read before its region becomes the transpose buffer
+    if constexpr (V == kDirect) rotate_direct(P, c[i], mine, lane8, active);
+    else rotate_block(P, c[i], mine, lane8, active);
     if (active) {
       amax = absmax_cols(amax, c[i]);
       if (a.norm) ssz = sumsq_cols(ssz, c[i]);
@@ -349,12 +546,36 @@ __global__ void __launch_bounds__(SPLIT == 0 ? 32 * kShortWarps : kMaxThreads) n
 #pragma unroll
   for (int i = 0; i < NBMAX; ++i) {
     const int li = slot + a.S * i;
-    if (live && slot < a.S && li < nloc) {
+    const bool active = live && slot < a.S && li < nloc;
+    if constexpr (V == kDirect) {
+      scale_cols(c[i], r.mult);
+      store_direct(qrow, a.f16_codes, blk0 + li, lane8, c[i], active);
+    } else if (active) {
       scale_cols(c[i], r.mult);
       store_codes<false>(qrow, a.f16_codes, blk0 + li, lane8, c[i]);
     }
   }
   if constexpr (SPLIT == 2) cluster_exit_wait();
+}
+
+template <int DT, bool RES, int V, int NBMAX, int SPLIT>
+__global__ void __launch_bounds__(SPLIT == 0 ? 32 * kShortWarps : kMaxThreads) norm_quant_kernel(const NormArgs a) {
+  norm_row<DT, RES, V, NBMAX, SPLIT>(a);
+}
+
+// The direct way.  80 registers keep four CTAs of a 5376-wide row on an SM,
+// 64 five; FP32 rows with a residual spill below 104 (8192 x 5376: 92 us, with
+// 80 registers 141).
+template <int DT, bool RES, int NBMAX, int SPLIT>
+__global__ void __maxnreg__(DT == DT_FP32 ? (RES ? 104 : 80) : RES ? 80 : 64) norm_direct_kernel(const NormArgs a) {
+  norm_row<DT, RES, kDirect, NBMAX, SPLIT>(a);
+}
+
+// The kernel of a variant.
+template <int DT, bool RES, int V, int NBMAX, int SPLIT>
+static auto norm_kernel() {
+  if constexpr (V == kDirect) return norm_direct_kernel<DT, RES, NBMAX, SPLIT>;
+  else return norm_quant_kernel<DT, RES, V, NBMAX, SPLIT>;
 }
 
 // launch_rows with launch_after.
@@ -373,11 +594,11 @@ static cudaError_t launch_norm_cfg(const RowGeometry& g, const NormArgs& a, cuda
     RowGeometry w = g;
     w.threads = 32 * kShortWarps;
     w.smem = static_cast<size_t>(per_cta) * g.nblocks * kSlotBytes;
-    return launch_norm_rows(norm_quant_kernel<DT, RES, V, 1, 0>, w, (a.M + per_cta - 1) / per_cta, st, a);
+    return launch_norm_rows(norm_kernel<DT, RES, V, 1, 0>(), w, (a.M + per_cta - 1) / per_cta, st, a);
   }
-  if (g.split == 1) return launch_norm_rows(norm_quant_kernel<DT, RES, V, 1, 1>, g, a.M, st, a);
-  if (g.nbmax == 1) return launch_norm_rows(norm_quant_kernel<DT, RES, V, 1, 2>, g, a.M, st, a);
-  return launch_norm_rows(norm_quant_kernel<DT, RES, V, 2, 2>, g, a.M, st, a);
+  if (g.split == 1) return launch_norm_rows(norm_kernel<DT, RES, V, 1, 1>(), g, a.M, st, a);
+  if (V == kDirect || g.nbmax == 1) return launch_norm_rows(norm_kernel<DT, RES, V, 1, 2>(), g, a.M, st, a);
+  if constexpr (V != kDirect) return launch_norm_rows(norm_kernel<DT, RES, V, 2, 2>(), g, a.M, st, a);
 }
 
 template <int DT, int V>
@@ -385,9 +606,11 @@ static cudaError_t launch_norm(const RowGeometry& g, const NormArgs& a, cudaStre
   return a.res ? launch_norm_cfg<DT, true, V>(g, a, st) : launch_norm_cfg<DT, false, V>(g, a, st);
 }
 
-// `align`: the bytes that every row of x, residual and h starts on.
+// `align`: the bytes that every row of x, residual and h starts on.  `direct`:
+// these rows, the weights and the codes lie on whole runs of eight elements.
 template <int DT>
-static cudaError_t launch_norm_dt(const RowGeometry& g, const NormArgs& a, int align, cudaStream_t st) {
+static cudaError_t launch_norm_dt(const RowGeometry& g, const NormArgs& a, int align, bool direct, cudaStream_t st) {
+  if (direct) return launch_norm<DT, kDirect>(g, a, st);
   if constexpr (DT == DT_FP32) {
     return align >= 16 ? launch_norm<DT, 4>(g, a, st) : launch_norm<DT, 1>(g, a, st);
   } else {
@@ -421,7 +644,6 @@ extern "C" int convrot_rms_norm_quant(const void* x, convrot_dtype dtype, int64_
   if (!row_geometry(K_p, kMaxSlots, &g)) return CONVROT_ERR_UNSUPPORTED;
   const int nbl = (g.nblocks + g.split - 1) / g.split;
   g.smem = static_cast<size_t>(nbl) * kSlotBytes + kNormRedFloats * sizeof(float);
-  if (M <= 2 * 152) g.threads = kMaxThreads;      // few rows: the first pass is spread wider (2 x 3077: 8.3 -> 4.3 us)
   NormArgs a = {};
   a.x = static_cast<const char*>(x);
   a.res = static_cast<const char*>(residual);
@@ -438,7 +660,6 @@ extern "C" int convrot_rms_norm_quant(const void* x, convrot_dtype dtype, int64_
   a.K = K;
   a.nblocks = g.nblocks;
   a.S = g.S;
-  a.pf_dist = prefetch_distance(static_cast<size_t>(K) * es);
   a.f16_codes = fmt == CONVROT_CODES_F16;
   a.eps = eps;
   a.inv_k = 1.0f / static_cast<float>(K);
@@ -448,11 +669,18 @@ extern "C" int convrot_rms_norm_quant(const void* x, convrot_dtype dtype, int64_
   };
   auto all_on = [&](int64_t n) { return rows_on(x, ld_x, n) && rows_on(residual, ld_residual, n) && rows_on(h, ld_h, n); };
   const int align = all_on(16) ? 16 : all_on(4) ? 4 : 2;
+  const int code_run = fmt == CONVROT_CODES_F16 ? 16 : 8;                  // bytes of eight codes
+  const bool direct = all_on(8 * static_cast<int64_t>(es)) && !off(weight, 32) && !off(a_q, code_run) &&
+                      ld_aq * (code_run / 8) % code_run == 0 && g.nbmax == 1;
+  // staged: few rows spread the first pass wider (2 x 3077: 8.3 -> 4.3 us)
+  if (M <= 2 * 152 && !direct) g.threads = kMaxThreads;
+  // direct: half the distance measured 0-3% faster, the whole 0-3% in the staged kernels
+  a.pf_dist = prefetch_distance(static_cast<size_t>(K) * es) / (direct ? 2 : 1);
   cudaError_t e;
   switch (dtype) {
-    case CONVROT_BF16: e = launch_norm_dt<DT_BF16>(g, a, align, stream); break;
-    case CONVROT_FP16: e = launch_norm_dt<DT_FP16>(g, a, align, stream); break;
-    default: e = launch_norm_dt<DT_FP32>(g, a, align, stream); break;
+    case CONVROT_BF16: e = launch_norm_dt<DT_BF16>(g, a, align, direct, stream); break;
+    case CONVROT_FP16: e = launch_norm_dt<DT_FP16>(g, a, align, direct, stream); break;
+    default: e = launch_norm_dt<DT_FP32>(g, a, align, direct, stream); break;
   }
   return e == cudaSuccess ? CONVROT_OK : convrot::record_cuda_error("rms_norm_quant launch", e);
 }
