@@ -112,6 +112,61 @@ def test_strided_rows_and_neighbours(cr, dtype, off, pitch):
     assert torch.all(hb == 5)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("K", [590, 5001, 20483, 33025])
+@pytest.mark.parametrize("starts,pads", [((0, 1, 3), (0, 0, 0)), ((5, 5, 5), (1, 9, 17)), ((2, 2, 2), (0, 3, 0)),
+                                         ((8, 0, 16), (8, 16, 0))])
+def test_operands_that_lie_differently(cr, dtype, K, starts, pads):
+    # x, residual and h each with its own start and pitch; one-byte codes from an odd multiple of two
+    M, Kp = 6, cr.padded_k(K)
+    x, r, w = make(M, K, dtype, K + starts[1] + pads[1], True)
+    h_ref, q_ref, s_ref = reference(x, r, w, 1e-6)
+
+    def wide(t, start, pad):
+        b = torch.full((start + M * (K + pad) + 8,), 5.0, dtype=t.dtype, device=DEV)
+        v = b[start:start + M * (K + pad)].view(M, K + pad)[:, :K]
+        v.copy_(t)
+        return b, v
+    (_, xv), (_, rv), (hb, hv) = (wide(t, a, b) for t, a, b in zip((x, r, torch.full_like(x, 5.0)), starts, pads))
+    qb = torch.full((M, Kp + 10), 77, dtype=torch.int8, device=DEV)
+    s = torch.empty(M, device=DEV)
+    cr.rms_norm_quant(xv, K, qb[:, 2:2 + Kp], s, residual=rv, h=hv, weight=w.to(DEV))
+    torch.cuda.synchronize()
+    check(qb[:, 2:2 + Kp], s, q_ref, s_ref)
+    assert torch.equal(hv.cpu(), h_ref)
+    assert torch.all(qb[:, :2] == 77) and torch.all(qb[:, 2 + Kp:] == 77)
+    hv.fill_(5.0)
+    assert torch.all(hb == 5)
+
+
+@pytest.mark.parametrize("K", [1001, 5377, 20483, 40001])
+def test_in_place_odd_widths(cr, K):
+    # vectors that two rows, or two CTAs of a row, share
+    M = 50
+    x, r, w = make(M, K, "bf16", K, True)
+    h_ref, q_ref, s_ref = reference(x, r, w, 1e-6)
+    xd = x.to(DEV)
+    q = torch.empty(M, cr.padded_k(K), dtype=torch.float16, device=DEV)
+    s = torch.empty(M, device=DEV)
+    cr.rms_norm_quant(xd, K, q, s, residual=r.to(DEV), h=xd, weight=w.to(DEV))
+    torch.cuda.synchronize()
+    check(q, s, q_ref, s_ref)
+    assert torch.equal(xd.cpu(), h_ref)
+
+
+@pytest.mark.parametrize("M,K", [(700, 512), (700, 768), (700, 1024), (700, 333), (400, 40000)])
+def test_many_rows(cr, M, K):
+    x, r, w = make(M, K, "bf16", M + K, True)
+    h_ref, q_ref, s_ref = reference(x, r, w, 1e-6)
+    q = torch.empty(M, cr.padded_k(K), dtype=torch.float16, device=DEV)
+    s = torch.empty(M, device=DEV)
+    h = torch.empty_like(x, device=DEV)
+    cr.rms_norm_quant(x.to(DEV), K, q, s, residual=r.to(DEV), h=h, weight=w.to(DEV))
+    torch.cuda.synchronize()
+    check(q, s, q_ref, s_ref)
+    assert torch.equal(h.cpu(), h_ref)
+
+
 @pytest.mark.parametrize("K", [1000, 5376, 20480])
 @pytest.mark.parametrize("which", ["x", "residual"])
 def test_in_place(cr, which, K):
