@@ -62,13 +62,25 @@ struct Params {
   float eps;
 };
 
+// t modulo 1 as a 64-bit fraction, from the bits of t (its FP64 arithmetic,
+// floor and conversion would take longer than sine and cosine).
+__device__ __forceinline__ unsigned long long turn_fraction(double t) {
+  const long long b = __double_as_longlong(t);
+  const int up = static_cast<int>((b >> 52) & 0x7ff) - 1011;            // |t| = m * 2^(up - 64)
+  const unsigned long long m = (b & 0xfffffffffffffll) | 0x10000000000000ll;
+  unsigned long long f = 0;
+  if (up >= 0 && up < 64) f = m << up;
+  else if (up < 0 && up > -54) f = (m + (1ull << (-up - 1))) >> -up;
+  return b < 0 ? 0ull - f : f;
+}
+
 __device__ __forceinline__ float2 pair_turn(const Params& p, int m, int i) {
   int a = 0;
 #pragma unroll
   for (int j = 0; j < CONVROT_MAX_AXES - 1; ++j)
     if (j < p.naxes - 1 && i >= p.cut[j]) a = j + 1;
   const double t = __ldg(p.inv_freq + i) * 0.15915494309189533577;     // turns per unit of position
-  const unsigned long long f = __double2ull_rn((t - floor(t)) * 18446744073709551616.0);
+  const unsigned long long f = turn_fraction(t);
   const long long at = __ldg(p.pos + static_cast<int64_t>(m) * p.ld_pos + a);
   const unsigned long long phase = static_cast<unsigned long long>(at) * f;
   float s, c;
