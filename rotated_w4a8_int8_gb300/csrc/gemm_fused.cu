@@ -274,6 +274,14 @@ fused_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__
   const uint32_t leader = rank & ~1u;                     // the pair's even CTA: issues the MMAs
   const bool is_leader = half == 0;
   const int S = SPLITK ? p.split : 1;
+  const int cluster_id = blockIdx.x / (2 * S), num_clusters = gridDim.x / (2 * S);
+
+  // this pair's K steps, in equal chunks of at most KCHUNK_STEPS
+  const int per_pair = SPLITK ? (p.k_steps + S - 1) / S : p.k_steps;
+  const int k_first = SPLITK ? static_cast<int>(pair) * per_pair : 0;
+  const int k_count = SPLITK ? min(per_pair, p.k_steps - k_first) : p.k_steps;
+  const int nchunks = (k_count + KCHUNK_STEPS - 1) / KCHUNK_STEPS;
+  const int csteps = (k_count + nchunks - 1) / nchunks;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
@@ -293,6 +301,16 @@ fused_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__
   if (warp == 0 && lane == 0) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmap_a)) : "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmap_b)) : "memory");
+    if (cluster_id < p.num_items) {
+      // The first tile's weights start for L2 while the previous kernel ends (a
+      // hint, which need not wait for that one's writes): 256 x 5376 x 5376
+      // 25.6 -> 24.3 us with 8 steps, 25.2 with 16.
+      int m2, nt;
+      work_coords(p, cluster_id, m2, nt);
+      for (int ks = 0; ks < min(k_count, 8); ++ks)
+        asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(&tmap_b),
+                     "r"((k_first + ks) * BK), "r"(nt * BN + static_cast<int>(half) * (BN / 2)) : "memory");
+    }
   }
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;"
@@ -305,15 +323,7 @@ fused_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__
   cluster_sync();            // the peers' barriers are initialised before any load or commit targets them
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
-  const int cluster_id = blockIdx.x / (2 * S), num_clusters = gridDim.x / (2 * S);
   const uint16_t pair_mask = static_cast<uint16_t>(3u << (2 * pair));
-
-  // this pair's K steps, in equal chunks of at most KCHUNK_STEPS
-  const int per_pair = SPLITK ? (p.k_steps + S - 1) / S : p.k_steps;
-  const int k_first = SPLITK ? static_cast<int>(pair) * per_pair : 0;
-  const int k_count = SPLITK ? min(per_pair, p.k_steps - k_first) : p.k_steps;
-  const int nchunks = (k_count + KCHUNK_STEPS - 1) / KCHUNK_STEPS;
-  const int csteps = (k_count + nchunks - 1) / nchunks;
 
   if (warp == 0) {
     // ---------------------------------------------------------------- TMA producer (both CTAs)
