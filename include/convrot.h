@@ -245,7 +245,9 @@ int convrot_gemm(const void* a_q, int64_t ld_aq, const float* a_scale,
  * codes and scale 0.  A row that holds an Inf or NaN, or whose sum of squares
  * leaves FP32's range (values beyond about 1e17), gets unspecified codes and
  * scale (h is written all the same).  x, residual and h need only element
- * alignment; where all their rows start on 16 bytes the vectorised path runs.
+ * alignment; fastest where their rows, weight and a_q's rows start on whole
+ * runs of eight elements, slowest where x, residual and h lie differently
+ * within 16 bytes.
  */
 int convrot_rms_norm_quant(const void* x, convrot_dtype dtype, int64_t ld_x,
                            const void* residual, int64_t ld_residual,
