@@ -28,7 +28,7 @@ static PyObject *dt_bf16, *dt_fp16, *dt_fp32, *dt_fp64, *dt_int8, *dt_int32;
 static PyObject *s_shape, *s_stride, *s_dtype, *s_is_cuda, *s_data_ptr, *s_numel, *s_is_contiguous, *s_get_device,
     *s_cuda_stream;
 
-enum { MAX_AXES = 4 };
+enum { MAX_AXES = 4, BLOCK = 256 };           /* CONVROT_MAX_AXES, CONVROT_BLOCK */
 
 /* ---- integers of Python objects; -1 with an exception set on failure */
 static int to_ll(PyObject* o, long long* v) {
@@ -221,6 +221,9 @@ static int rows_of(PyObject* t, int* rows) {
   return 0;
 }
 
+/* Codes in a row of K elements: whole rotation blocks, all of which are written. */
+static long long padded(long long K) { return (K + BLOCK - 1) / BLOCK * BLOCK; }
+
 /* (x, K, a_q, a_scale, residual, h, weight, eps, a_norm, stream) -> status */
 static PyObject* rms_norm_quant(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   (void)self;
@@ -232,7 +235,7 @@ static PyObject* rms_norm_quant(PyObject* self, PyObject* const* a, Py_ssize_t n
   void *w, *s, *nb, *st;
   if (want(n, 10) || to_int(a[1], &K) || rows_of(a[0], &M) || (dtype = storage_code(fn, "x", a[0], &dt)) < 0 ||
       (fmt = codes_code(fn, "a_q", a[2], &cdt)) < 0 || matrix(fn, "x", a[0], M, K, dt, &x) ||
-      matrix(fn, "a_q", a[2], M, K, cdt, &q) || vector(fn, "a_scale", a[3], M, dt_fp32, &s) ||
+      matrix(fn, "a_q", a[2], M, padded(K), cdt, &q) || vector(fn, "a_scale", a[3], M, dt_fp32, &s) ||
       matrix(fn, "residual", a[4], M, K, dt, &r) || matrix(fn, "h", a[5], M, K, dt, &h) ||
       vector(fn, "weight", a[6], K, dt_fp32, &w) || to_float(a[7], &eps) ||
       vector(fn, "a_norm", a[8], M, dt_fp32, &nb) || stream_of(a[0], a[9], &st))
