@@ -3,8 +3,9 @@
 Argument marshalling only: every step of the layer runs in the CUDA kernels
 behind the C ABI declared in include/convrot.h.  Tensors are torch CUDA
 tensors (PyTorch supplies device memory and streams); each function passes
-their device pointers and the current stream to the library.  There is no
-CPU fallback: if the library is missing or a call fails, an exception says
+their device pointers and the current stream to the library.  They have to lie
+on the current device (rms_norm_quant, qk_norm_rope and gemm_fused raise
+ValueError otherwise).  There is no CPU fallback: if the library is missing or a call fails, an exception says
 so.
 """
 from __future__ import annotations
@@ -162,7 +163,8 @@ def _operators():
             return torch.cuda.current_stream(device).cuda_stream
         m.bind(*(ctypes.cast(f, ctypes.c_void_p).value
                  for f in (lib.convrot_rms_norm_quant, lib.convrot_qk_norm_rope, lib.convrot_gemm_fused)),
-               _refuse, getattr(torch._C, "_cuda_getCurrentRawStream", current), torch.bfloat16, torch.float16,
+               _refuse, getattr(torch._C, "_cuda_getCurrentRawStream", current),
+               getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device), torch.bfloat16, torch.float16,
                torch.float32, torch.float64, torch.int8, torch.int32)
         _block_ops = m
     return _block_ops

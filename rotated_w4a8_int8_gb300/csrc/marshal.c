@@ -23,7 +23,7 @@ typedef int (*gemm_fn)(const void*, int64_t, const float*, const void*, int64_t,
 static norm_fn call_norm;
 static rope_fn call_rope;
 static gemm_fn call_gemm;
-static PyObject *refuse, *raw_stream;                         /* Python callables */
+static PyObject *refuse, *raw_stream, *current_device;        /* Python callables */
 static PyObject *dt_bf16, *dt_fp16, *dt_fp32, *dt_fp64, *dt_int8, *dt_int32;
 static PyObject *s_shape, *s_stride, *s_dtype, *s_is_cuda, *s_data_ptr, *s_numel, *s_is_contiguous, *s_get_device,
     *s_cuda_stream;
@@ -176,12 +176,36 @@ static int codes_code(const char* fn, const char* name, PyObject* t, PyObject** 
   return refusal(fn, name, t, PyUnicode_FromString("int8 or float16 codes"));
 }
 
-/* The given stream (a handle or an object with cuda_stream), or the current one of t's device. */
-static int stream_of(PyObject* t, PyObject* stream, void** out) {
+/*
+ * The device that holds every tensor of a call (None aside), which has to be
+ * the calling thread's current one: the C ABI launches there, and the stream
+ * is one of its streams.  `names` are the tensors' names; -1 refused.
+ */
+static int device_of(const char* fn, PyObject* const* t, const char* const* names, int n, int* device) {
+  long long first = 0, d, current;
+  for (int i = 0; i < n; ++i) {
+    if (t[i] == Py_None) continue;
+    if (method_ll(t[i], s_get_device, &d)) return -1;
+    if (i == 0) first = d;                       /* the first one is always given */
+    if (d != first) return refusal(fn, names[i], t[i], PyUnicode_FromFormat("on cuda:%lld like %s", first, names[0]));
+  }
+  PyObject* r = PyObject_CallNoArgs(current_device);
+  if (!r) return -1;
+  const int bad = to_ll(r, &current);
+  Py_DECREF(r);
+  if (bad) return -1;
+  if (first != current)
+    return refusal(fn, names[0], t[0], PyUnicode_FromFormat("on the current device (cuda:%lld)", current));
+  *device = (int)first;
+  return 0;
+}
+
+/* The given stream (a handle or an object with cuda_stream), or the current one of the device. */
+static int stream_of(int device, PyObject* stream, void** out) {
   long long v;
   PyObject* r;
   if (stream == Py_None) {
-    PyObject* dev = PyObject_CallMethodNoArgs(t, s_get_device);
+    PyObject* dev = PyLong_FromLong(device);
     if (!dev) return -1;
     r = PyObject_CallOneArg(raw_stream, dev);
     Py_DECREF(dev);
@@ -228,7 +252,7 @@ static long long padded(long long K) { return (K + BLOCK - 1) / BLOCK * BLOCK; }
 static PyObject* rms_norm_quant(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   (void)self;
   const char* fn = "rms_norm_quant";
-  int M, K, dtype, fmt;
+  int M, K, dtype, fmt, dev;
   float eps;
   PyObject *dt, *cdt;
   matrix_t x, r, h, q;
@@ -238,8 +262,11 @@ static PyObject* rms_norm_quant(PyObject* self, PyObject* const* a, Py_ssize_t n
       matrix(fn, "a_q", a[2], M, padded(K), cdt, &q) || vector(fn, "a_scale", a[3], M, dt_fp32, &s) ||
       matrix(fn, "residual", a[4], M, K, dt, &r) || matrix(fn, "h", a[5], M, K, dt, &h) ||
       vector(fn, "weight", a[6], K, dt_fp32, &w) || to_float(a[7], &eps) ||
-      vector(fn, "a_norm", a[8], M, dt_fp32, &nb) || stream_of(a[0], a[9], &st))
+      vector(fn, "a_norm", a[8], M, dt_fp32, &nb))
     return NULL;
+  PyObject* const used[] = {a[0], a[2], a[3], a[4], a[5], a[6], a[8]};
+  static const char* const names[] = {"x", "a_q", "a_scale", "residual", "h", "weight", "a_norm"};
+  if (device_of(fn, used, names, 7, &dev) || stream_of(dev, a[9], &st)) return NULL;
   return PyLong_FromLong(call_norm(x.ptr, dtype, x.ld, r.ptr, r.ld, h.ptr, h.ld, w, eps, M, K, q.ptr, fmt, q.ld, s, nb, st));
 }
 
@@ -279,7 +306,7 @@ static PyObject* qk_norm_rope(PyObject* self, PyObject* const* a, Py_ssize_t n) 
   (void)self;
   const char* fn = "qk_norm_rope";
   if (want(n, 12)) return NULL;
-  int pairs[MAX_AXES], axes, dtype;
+  int pairs[MAX_AXES], axes, dtype, dev;
   long long shape[3], sum = 0;
   float eps;
   PyObject* dt;
@@ -314,8 +341,11 @@ static PyObject* qk_norm_rope(PyObject* self, PyObject* const* a, Py_ssize_t n) 
       heads(fn, "q_out", a[5], shape[0], shape[2], dt, &q, &qo) || heads(fn, "k_out", a[6], shape[0], shape[2], dt, &k, &ko) ||
       matrix(fn, "pos", a[2], shape[0], axes, dt_int32, &pos) || vector(fn, "inv_freq", a[3], sum, dt_fp64, &f) ||
       vector(fn, "q_weight", a[7], shape[2], dt_fp32, &qw) || vector(fn, "k_weight", a[8], shape[2], dt_fp32, &kw) ||
-      to_float(a[9], &eps) || stream_of(a[0], a[11], &st))
+      to_float(a[9], &eps))
     return NULL;
+  PyObject* const used[] = {a[0], a[1], a[2], a[3], a[5], a[6], a[7], a[8]};
+  static const char* const names[] = {"q", "k", "pos", "inv_freq", "q_out", "k_out", "q_weight", "k_weight"};
+  if (device_of(fn, used, names, 8, &dev) || stream_of(dev, a[11], &st)) return NULL;
   return PyLong_FromLong(call_rope(q.ptr, q.tok, q.head, qo.ptr, qo.tok, qo.head, q.heads, qw, k.ptr, k.tok, k.head, ko.ptr,
                                    ko.tok, ko.head, k.heads, kw, dtype, (int)shape[0], (int)shape[2], pos.ptr, pos.ld, pairs,
                                    axes, f, eps, interleaved, st));
@@ -327,7 +357,7 @@ static PyObject* gemm_fused(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   const char* fn = "gemm_fused";
   if (want(n, 11)) return NULL;
   long long sa[2], sw[2], kp;
-  int act, fmt, dtype;
+  int act, fmt, dtype, dev;
   PyObject *cdt, *odt;
   matrix_t aq, wq, out, res;
   void *as, *ws, *b, *g, *st;
@@ -347,25 +377,27 @@ static PyObject* gemm_fused(PyObject* self, PyObject* const* a, Py_ssize_t n) {
       matrix(fn, "a_q", a[0], sa[0], kp, cdt, &aq) || vector(fn, "a_scale", a[1], sa[0], dt_fp32, &as) ||
       matrix(fn, "w_q", a[2], sw[0], kp, cdt, &wq) || vector(fn, "w_scale", a[3], sw[0], dt_fp32, &ws) ||
       matrix(fn, "out", a[4], sa[0], sw[0], odt, &out) || vector(fn, "bias", a[6], sw[0], dt_fp32, &b) ||
-      vector(fn, "gate", a[8], sw[0], dt_fp32, &g) || matrix(fn, "residual", a[9], sa[0], sw[0], odt, &res) ||
-      stream_of(a[4], a[10], &st))
+      vector(fn, "gate", a[8], sw[0], dt_fp32, &g) || matrix(fn, "residual", a[9], sa[0], sw[0], odt, &res))
     return NULL;
+  PyObject* const used[] = {a[0], a[1], a[2], a[3], a[4], a[6], a[8], a[9]};
+  static const char* const names[] = {"a_q", "a_scale", "w_q", "w_scale", "out", "bias", "gate", "residual"};
+  if (device_of(fn, used, names, 8, &dev) || stream_of(dev, a[10], &st)) return NULL;
   return PyLong_FromLong(call_gemm(aq.ptr, aq.ld, as, wq.ptr, wq.ld, ws, fmt, b, act, g, res.ptr, res.ld, (int)sa[0],
                                    (int)sw[0], (int)kp, out.ptr, dtype, out.ld, st));
 }
 
-/* (norm, rope, gemm addresses, refuse, raw_stream, bf16, fp16, fp32, fp64, int8, int32): once, at load. */
+/* (norm, rope, gemm addresses, refuse, raw_stream, current_device, bf16, fp16, fp32, fp64, int8, int32): once, at load. */
 static PyObject* bind(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   (void)self;
   long long p[3];
-  if (want(n, 11)) return NULL;
+  if (want(n, 12)) return NULL;
   for (int i = 0; i < 3; ++i)
     if (to_ll(a[i], &p[i])) return NULL;
   call_norm = (norm_fn)(uintptr_t)p[0];
   call_rope = (rope_fn)(uintptr_t)p[1];
   call_gemm = (gemm_fn)(uintptr_t)p[2];
-  PyObject** kept[] = {&refuse, &raw_stream, &dt_bf16, &dt_fp16, &dt_fp32, &dt_fp64, &dt_int8, &dt_int32};
-  for (int i = 0; i < 8; ++i) Py_XSETREF(*kept[i], Py_NewRef(a[3 + i]));
+  PyObject** kept[] = {&refuse, &raw_stream, &current_device, &dt_bf16, &dt_fp16, &dt_fp32, &dt_fp64, &dt_int8, &dt_int32};
+  for (int i = 0; i < 9; ++i) Py_XSETREF(*kept[i], Py_NewRef(a[3 + i]));
   Py_RETURN_NONE;
 }
 
