@@ -29,6 +29,7 @@
 // every pair sends its int32 sums of the boxes it does not own into the
 // owners' shared memory (box b belongs to pair b mod S) and finishes its own
 // boxes.  Integer sums: the result does not depend on S.
+#include <atomic>
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -660,11 +661,11 @@ constexpr int kMaxDevices = 64;
 // Clusters of 2 * split CTAs of this kernel that are resident at once.
 template <int OUT, int ACT, int BN, bool SPLITK>
 static cudaError_t resident_clusters(int split, int* out) {
-  static int known[kMaxDevices][MAX_SPLIT + 1] = {};
+  static std::atomic<int> known[kMaxDevices][MAX_SPLIT + 1] = {};    // 0: not set up (two threads may both do it)
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  int n = dev < kMaxDevices ? known[dev][split] : 0;
+  int n = dev < kMaxDevices ? known[dev][split].load() : 0;
   if (n == 0) {
     auto k = fused_kernel<OUT, ACT, BN, SPLITK>;
     if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, Tile<BN>::SMEM)) != cudaSuccess) return e;
