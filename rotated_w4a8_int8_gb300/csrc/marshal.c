@@ -252,7 +252,7 @@ static long long padded(long long K) { return (K + BLOCK - 1) / BLOCK * BLOCK; }
 static PyObject* rms_norm_quant(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   (void)self;
   const char* fn = "rms_norm_quant";
-  int M, K, dtype, fmt, dev;
+  int M, K, dtype, fmt, dev, status;
   float eps;
   PyObject *dt, *cdt;
   matrix_t x, r, h, q;
@@ -267,7 +267,10 @@ static PyObject* rms_norm_quant(PyObject* self, PyObject* const* a, Py_ssize_t n
   PyObject* const used[] = {a[0], a[2], a[3], a[4], a[5], a[6], a[8]};
   static const char* const names[] = {"x", "a_q", "a_scale", "residual", "h", "weight", "a_norm"};
   if (device_of(fn, used, names, 7, &dev) || stream_of(dev, a[9], &st)) return NULL;
-  return PyLong_FromLong(call_norm(x.ptr, dtype, x.ld, r.ptr, r.ld, h.ptr, h.ld, w, eps, M, K, q.ptr, fmt, q.ld, s, nb, st));
+  Py_BEGIN_ALLOW_THREADS                         /* a launch waits while the launch queue is full */
+  status = call_norm(x.ptr, dtype, x.ld, r.ptr, r.ld, h.ptr, h.ld, w, eps, M, K, q.ptr, fmt, q.ld, s, nb, st);
+  Py_END_ALLOW_THREADS
+  return PyLong_FromLong(status);
 }
 
 typedef struct {
@@ -306,7 +309,7 @@ static PyObject* qk_norm_rope(PyObject* self, PyObject* const* a, Py_ssize_t n) 
   (void)self;
   const char* fn = "qk_norm_rope";
   if (want(n, 12)) return NULL;
-  int pairs[MAX_AXES], axes, dtype, dev;
+  int pairs[MAX_AXES], axes, dtype, dev, status;
   long long shape[3], sum = 0;
   float eps;
   PyObject* dt;
@@ -346,9 +349,12 @@ static PyObject* qk_norm_rope(PyObject* self, PyObject* const* a, Py_ssize_t n) 
   PyObject* const used[] = {a[0], a[1], a[2], a[3], a[5], a[6], a[7], a[8]};
   static const char* const names[] = {"q", "k", "pos", "inv_freq", "q_out", "k_out", "q_weight", "k_weight"};
   if (device_of(fn, used, names, 8, &dev) || stream_of(dev, a[11], &st)) return NULL;
-  return PyLong_FromLong(call_rope(q.ptr, q.tok, q.head, qo.ptr, qo.tok, qo.head, q.heads, qw, k.ptr, k.tok, k.head, ko.ptr,
-                                   ko.tok, ko.head, k.heads, kw, dtype, (int)shape[0], (int)shape[2], pos.ptr, pos.ld, pairs,
-                                   axes, f, eps, interleaved, st));
+  Py_BEGIN_ALLOW_THREADS                         /* a launch waits while the launch queue is full */
+  status = call_rope(q.ptr, q.tok, q.head, qo.ptr, qo.tok, qo.head, q.heads, qw, k.ptr, k.tok, k.head, ko.ptr,
+                     ko.tok, ko.head, k.heads, kw, dtype, (int)shape[0], (int)shape[2], pos.ptr, pos.ld, pairs,
+                     axes, f, eps, interleaved, st);
+  Py_END_ALLOW_THREADS
+  return PyLong_FromLong(status);
 }
 
 /* (a_q, a_scale, w_q, w_scale, out, K_p or None, bias, act, gate, residual, stream) -> status */
@@ -357,7 +363,7 @@ static PyObject* gemm_fused(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   const char* fn = "gemm_fused";
   if (want(n, 11)) return NULL;
   long long sa[2], sw[2], kp;
-  int act, fmt, dtype, dev;
+  int act, fmt, dtype, dev, status;
   PyObject *cdt, *odt;
   matrix_t aq, wq, out, res;
   void *as, *ws, *b, *g, *st;
@@ -382,8 +388,11 @@ static PyObject* gemm_fused(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   PyObject* const used[] = {a[0], a[1], a[2], a[3], a[4], a[6], a[8], a[9]};
   static const char* const names[] = {"a_q", "a_scale", "w_q", "w_scale", "out", "bias", "gate", "residual"};
   if (device_of(fn, used, names, 8, &dev) || stream_of(dev, a[10], &st)) return NULL;
-  return PyLong_FromLong(call_gemm(aq.ptr, aq.ld, as, wq.ptr, wq.ld, ws, fmt, b, act, g, res.ptr, res.ld, (int)sa[0],
-                                   (int)sw[0], (int)kp, out.ptr, dtype, out.ld, st));
+  Py_BEGIN_ALLOW_THREADS                         /* a launch waits while the launch queue is full */
+  status = call_gemm(aq.ptr, aq.ld, as, wq.ptr, wq.ld, ws, fmt, b, act, g, res.ptr, res.ld, (int)sa[0],
+                     (int)sw[0], (int)kp, out.ptr, dtype, out.ld, st);
+  Py_END_ALLOW_THREADS
+  return PyLong_FromLong(status);
 }
 
 /* (norm, rope, gemm addresses, refuse, raw_stream, current_device, bf16, fp16, fp32, fp64, int8, int32): once, at load. */

@@ -1,7 +1,10 @@
 """The binding of rms_norm_quant, qk_norm_rope and gemm_fused (csrc/marshal.c), with a C ABI that only counts its
-calls: what it checks of memory written past a tensor's logical columns, and of devices."""
+calls: what it checks of memory written past a tensor's logical columns, and of devices, and that other Python threads run
+while a call waits."""
 import ctypes
 import subprocess
+import threading
+import time
 
 import pytest
 import torch
@@ -89,6 +92,29 @@ def test_tensors_lie_on_the_current_device(marshal, tmp_path, call, names):
     with pytest.raises(ValueError, match=f"{names[0]} must be on the current device"):
         call(marshal, [1] * len(names))
     assert calls.value == 1
+
+
+# a launch that waits, 2 s at most, for something that a Python thread does
+WAITING_ABI = """
+#include <unistd.h>
+volatile int flag;
+int wait_for_flag() { for (int i = 0; i < 2000 && !flag; ++i) usleep(1000); return flag ? 0 : 7; }
+"""
+
+
+@pytest.mark.parametrize("call,names", CALLS)
+def test_other_threads_run_while_a_call_waits(marshal, tmp_path, call, names):
+    abi = compiled(tmp_path, WAITING_ABI)
+    flag = ctypes.c_int.in_dll(abi, "flag")
+    bind(marshal, abi.wait_for_flag, 0)
+
+    def later():
+        time.sleep(0.05)
+        flag.value = 1
+    t = threading.Thread(target=later)
+    t.start()
+    assert call(marshal, [0] * len(names)) == 0
+    t.join()
 
 
 @pytest.mark.parametrize("K,shape,strides", [
