@@ -9,6 +9,7 @@
 #include <cuda_fp16.h>
 
 #include "../../include/convrot.h"
+#include "pdl.cuh"
 #include "tcgen05.cuh"
 
 namespace crfused {
@@ -100,11 +101,11 @@ struct ColumnTerms {
 // on the activation, a box's loads together exceed the registers)
 __device__ __forceinline__ void load4(const float* p, int n, int N, float (&v)[4]) {
   if (n + 4 <= N) {
-    asm volatile("ld.global.nc.v4.f32 {%0, %1, %2, %3}, [%4];"
+    asm volatile("ld.global.v4.f32 {%0, %1, %2, %3}, [%4];"
                  : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]) : "l"(p + n));
   } else {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = n + j < N ? __ldg(p + n + j) : 0.f;
+    for (int j = 0; j < 4; ++j) v[j] = n + j < N ? convrot::load_global(p + n + j) : 0.f;
   }
 }
 

@@ -52,7 +52,7 @@ constexpr int FEW_SMEM = RING<NT> ? WARPS * DEPTH<NT> * UNIT_BYTES<NT> : 0;
 // 16 bytes of a weight row: read once, kept out of L1.
 __device__ __forceinline__ uint4 load_weight(const char* p) {
   uint4 v;
-  asm("ld.global.nc.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
+  asm volatile("ld.global.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
       : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
   return v;
 }
@@ -146,7 +146,7 @@ __device__ __forceinline__ void sum_loads(const char* const (&wr)[2], const char
 #pragma unroll
           for (int i = 0; i < 2; ++i) wv[u][i] = load_weight(wr[i] + static_cast<int64_t>(at) * 64);
 #pragma unroll
-          for (int t = 0; t < NT; ++t) av[u][t] = __ldg(reinterpret_cast<const uint4*>(ar[t] + static_cast<int64_t>(at) * 64));
+          for (int t = 0; t < NT; ++t) av[u][t] = convrot::load_global(reinterpret_cast<const uint4*>(ar[t] + static_cast<int64_t>(at) * 64));
         }
       }
 #pragma unroll
@@ -208,7 +208,7 @@ __device__ __forceinline__ int ld_cluster(const int* p, uint32_t rank) {
 // finishes its part of the tile's outputs from all of their sums.
 template <bool S8, int NT>
 __global__ void __launch_bounds__(32 * WARPS, CTAS_PER_SM<NT>)
-few_kernel(const char* __restrict__ a_q, int64_t a_pitch, const char* __restrict__ w_q, int64_t w_pitch, int units,
+few_kernel(const char* a_q, int64_t a_pitch, const char* w_q, int64_t w_pitch, int units,
            int split, int out_dtype, const Epilogue e) {
   constexpr int TOKENS = 8 * NT, PITCH = ROWS + 4;   // pad: no bank conflicts below
   __shared__ __align__(16) int sums[TOKENS * PITCH];
@@ -278,7 +278,7 @@ few_kernel(const char* __restrict__ a_q, int64_t a_pitch, const char* __restrict
     const float4 f = make_float4(static_cast<float>(v.x), static_cast<float>(v.y), static_cast<float>(v.z),
                                  static_cast<float>(v.w));
     const ColumnTerms t = load_columns(e, n);
-    const float sa = __ldg(e.a_scale + m);
+    const float sa = convrot::load_global(e.a_scale + m);
     float y[4] = {f.x, f.y, f.z, f.w};
     with_act(e.act, [&](auto act) { activate4<decltype(act)::value>(e, t, y, sa); });
     auto finish = [&](auto kind) {

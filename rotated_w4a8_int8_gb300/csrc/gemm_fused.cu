@@ -216,9 +216,9 @@ __device__ __forceinline__ void fill_box(const Epilogue& e, const int32_t (&acc)
       const int j = q * V + 4 * h;
       float ts[4], tb[4], tg[4];
       if constexpr (WHOLE) {
-        const float4 a = __ldg(reinterpret_cast<const float4*>(sw + j));
-        const float4 b = __ldg(reinterpret_cast<const float4*>(bias + (j / 4) * bstep));
-        const float4 g = __ldg(reinterpret_cast<const float4*>(gate + (j / 4) * gstep));
+        const float4 a = convrot::load_global(reinterpret_cast<const float4*>(sw + j));
+        const float4 b = convrot::load_global(reinterpret_cast<const float4*>(bias + (j / 4) * bstep));
+        const float4 g = convrot::load_global(reinterpret_cast<const float4*>(gate + (j / 4) * gstep));
         ts[0] = a.x; ts[1] = a.y; ts[2] = a.z; ts[3] = a.w;
         tb[0] = b.x; tb[1] = b.y; tb[2] = b.z; tb[3] = b.w;
         tg[0] = g.x; tg[1] = g.y; tg[2] = g.z; tg[3] = g.w;
@@ -226,9 +226,9 @@ __device__ __forceinline__ void fill_box(const Epilogue& e, const int32_t (&acc)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const bool in = nb + j + i < e.N;
-          ts[i] = in ? __ldg(sw + j + i) : 0.f;
-          tb[i] = in ? __ldg(bias + (j / 4) * bstep + i) : 0.f;
-          tg[i] = in ? __ldg(gate + (j / 4) * gstep + i) : 0.f;
+          ts[i] = in ? convrot::load_global(sw + j + i) : 0.f;
+          tb[i] = in ? convrot::load_global(bias + (j / 4) * bstep + i) : 0.f;
+          tg[i] = in ? convrot::load_global(gate + (j / 4) * gstep + i) : 0.f;
         }
       }
       ResidualWords<OUT> r;
@@ -465,7 +465,7 @@ fused_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__
         for (; r < end; r += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(r));
       }
       // what the output phase reads, asked for while the tile is multiplied
-      const float sa = m_base + lane < p.e.M ? __ldg(p.e.a_scale + m_base + lane) : 0.f;
+      const float sa = m_base + lane < p.e.M ? convrot::load_global(p.e.a_scale + m_base + lane) : 0.f;
       for (int j = lane; j < L::COLS && n0 + j < p.e.N; j += 32) {
         warm_l1(p.e.w_scale + n0 + j);
         if (p.e.bias) warm_l1(p.e.bias + n0 + j);

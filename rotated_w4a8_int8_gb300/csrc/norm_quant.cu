@@ -260,19 +260,19 @@ __device__ __forceinline__ float read_block(const NormArgs& a, int row, int blk,
     const int e = e0 + 64 * c;
     if (a.weight && e + 8 <= a.K) {
       if constexpr (DIRECT) {
-        asm volatile("ld.global.nc.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+        asm volatile("ld.global.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                      : "=f"(w[c][0]), "=f"(w[c][1]), "=f"(w[c][2]), "=f"(w[c][3]), "=f"(w[c][4]), "=f"(w[c][5]),
                        "=f"(w[c][6]), "=f"(w[c][7])
                      : "l"(a.weight + e));
       } else {
-        const float4 lo = __ldg(reinterpret_cast<const float4*>(a.weight + e));
-        const float4 hi = __ldg(reinterpret_cast<const float4*>(a.weight + e + 4));
+        const float4 lo = load_global(reinterpret_cast<const float4*>(a.weight + e));
+        const float4 hi = load_global(reinterpret_cast<const float4*>(a.weight + e + 4));
         w[c][0] = lo.x; w[c][1] = lo.y; w[c][2] = lo.z; w[c][3] = lo.w;
         w[c][4] = hi.x; w[c][5] = hi.y; w[c][6] = hi.z; w[c][7] = hi.w;
       }
     } else {
 #pragma unroll
-      for (int b = 0; b < 8; ++b) w[c][b] = a.weight && e + b < a.K ? __ldg(a.weight + e + b) : 1.f;
+      for (int b = 0; b < 8; ++b) w[c][b] = a.weight && e + b < a.K ? load_global(a.weight + e + b) : 1.f;
     }
   };
 #pragma unroll

@@ -79,9 +79,9 @@ __device__ __forceinline__ float2 pair_turn(const Params& p, int m, int i) {
 #pragma unroll
   for (int j = 0; j < CONVROT_MAX_AXES - 1; ++j)
     if (j < p.naxes - 1 && i >= p.cut[j]) a = j + 1;
-  const double t = __ldg(p.inv_freq + i) * 0.15915494309189533577;     // turns per unit of position
+  const double t = convrot::load_global(p.inv_freq + i) * 0.15915494309189533577;     // turns per unit of position
   const unsigned long long f = turn_fraction(t);
-  const long long at = __ldg(p.pos + static_cast<int64_t>(m) * p.ld_pos + a);
+  const long long at = convrot::load_global(p.pos + static_cast<int64_t>(m) * p.ld_pos + a);
   const unsigned long long phase = static_cast<unsigned long long>(at) * f;
   float s, c;
   sincospif(static_cast<float>(static_cast<int32_t>(phase >> 32)) * 4.656612873077393e-10f, &s, &c);   // 2^-31
@@ -128,8 +128,8 @@ __global__ void __launch_bounds__(32 * kAnyWarps) rope_any_kernel(const Params p
       const int j0 = INTERLEAVED ? 2 * i : i, j1 = INTERLEAVED ? 2 * i + 1 : i + p.P;
       float a = E::load(x[j0]), b = E::load(x[j1]);
       if (w) {
-        a = a * r * __ldg(w + j0);
-        b = b * r * __ldg(w + j1);
+        a = a * r * convrot::load_global(w + j0);
+        b = b * r * convrot::load_global(w + j1);
       }
       const float2 cs = turn[i];
       y[j0] = E::store(a * cs.x - b * cs.y);
@@ -137,7 +137,7 @@ __global__ void __launch_bounds__(32 * kAnyWarps) rope_any_kernel(const Params p
     }
     for (int j = 2 * p.P + lane; j < p.D; j += 32) {
       float a = E::load(x[j]);
-      if (w) a = a * r * __ldg(w + j);
+      if (w) a = a * r * convrot::load_global(w + j);
       y[j] = E::store(a);
     }
   }
@@ -275,7 +275,7 @@ __global__ void __launch_bounds__(32 * kWarps, DT == CONVROT_FP32 ? 4 : 5) rope_
   for (int i = threadIdx.x; i < 2 * p.D; i += 32 * kWarps) {
     const float* w = i < p.D ? p.q.weight : p.k.weight;
     const int j = i < p.D ? i : i - p.D;
-    if (w) ws[(i < p.D ? 0 : p.D) + spread<R>(j, p.D)] = __ldg(w + j);
+    if (w) ws[(i < p.D ? 0 : p.D) + spread<R>(j, p.D)] = convrot::load_global(w + j);
   }
   __syncthreads();
   const float* tcs = cs + t * 2 * p.P;
