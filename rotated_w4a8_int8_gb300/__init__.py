@@ -163,7 +163,7 @@ def _operators():
             return torch.cuda.current_stream(device).cuda_stream
         m.bind(*(ctypes.cast(f, ctypes.c_void_p).value
                  for f in (lib.convrot_rms_norm_quant, lib.convrot_qk_norm_rope, lib.convrot_gemm_fused)),
-               _refuse, getattr(torch._C, "_cuda_getCurrentRawStream", current),
+               torch.cuda.device_count(), _refuse, getattr(torch._C, "_cuda_getCurrentRawStream", current),
                getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device), torch.bfloat16, torch.float16,
                torch.float32, torch.float64, torch.int8, torch.int32)
         _block_ops = m

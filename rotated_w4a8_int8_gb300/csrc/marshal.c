@@ -23,6 +23,7 @@ typedef int (*gemm_fn)(const void*, int64_t, const float*, const void*, int64_t,
 static norm_fn call_norm;
 static rope_fn call_rope;
 static gemm_fn call_gemm;
+static int gpus;                                              /* GPUs that torch sees */
 static PyObject *refuse, *raw_stream, *current_device;        /* Python callables */
 static PyObject *dt_bf16, *dt_fp16, *dt_fp32, *dt_fp64, *dt_int8, *dt_int32;
 static PyObject *s_shape, *s_stride, *s_dtype, *s_is_cuda, *s_data_ptr, *s_numel, *s_is_contiguous, *s_get_device,
@@ -179,10 +180,13 @@ static int codes_code(const char* fn, const char* name, PyObject* t, PyObject** 
 /*
  * The device that holds every tensor of a call (None aside), which has to be
  * the calling thread's current one: the C ABI launches there, and the stream
- * is one of its streams.  `names` are the tensors' names; -1 refused.
+ * is one of its streams.  `names` are the tensors' names; -1 refused.  With
+ * one GPU there is nothing to ask (0.8 us of a one-token call's 6).
  */
 static int device_of(const char* fn, PyObject* const* t, const char* const* names, int n, int* device) {
   long long first = 0, d, current;
+  *device = 0;
+  if (gpus == 1) return 0;
   for (int i = 0; i < n; ++i) {
     if (t[i] == Py_None) continue;
     if (method_ll(t[i], s_get_device, &d)) return -1;
@@ -395,18 +399,19 @@ static PyObject* gemm_fused(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   return PyLong_FromLong(status);
 }
 
-/* (norm, rope, gemm addresses, refuse, raw_stream, current_device, bf16, fp16, fp32, fp64, int8, int32): once, at load. */
+/* (norm, rope, gemm addresses, GPUs, refuse, raw_stream, current_device, bf16, fp16, fp32, fp64, int8, int32): once, at load. */
 static PyObject* bind(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   (void)self;
   long long p[3];
-  if (want(n, 12)) return NULL;
+  if (want(n, 13)) return NULL;
   for (int i = 0; i < 3; ++i)
     if (to_ll(a[i], &p[i])) return NULL;
+  if (to_int(a[3], &gpus)) return NULL;
   call_norm = (norm_fn)(uintptr_t)p[0];
   call_rope = (rope_fn)(uintptr_t)p[1];
   call_gemm = (gemm_fn)(uintptr_t)p[2];
   PyObject** kept[] = {&refuse, &raw_stream, &current_device, &dt_bf16, &dt_fp16, &dt_fp32, &dt_fp64, &dt_int8, &dt_int32};
-  for (int i = 0; i < 9; ++i) Py_XSETREF(*kept[i], Py_NewRef(a[3 + i]));
+  for (int i = 0; i < 9; ++i) Py_XSETREF(*kept[i], Py_NewRef(a[4 + i]));
   Py_RETURN_NONE;
 }
 

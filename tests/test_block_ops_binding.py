@@ -32,10 +32,10 @@ def compiled(tmp_path, source):
     return ctypes.CDLL(str(so))
 
 
-def bind(m, entry, device):
-    """Binds the marshalling module to `entry` for all three calls; `device` is the current one."""
+def bind(m, entry, device, gpus=2):
+    """Binds the marshalling module to `entry` for all three calls; `device` is the current one of `gpus`."""
     address = ctypes.cast(entry, ctypes.c_void_p).value
-    m.bind(address, address, address, cr._refuse, lambda d: 100 + d, lambda: device, torch.bfloat16, torch.float16,
+    m.bind(address, address, address, gpus, cr._refuse, lambda d: 100 + d, lambda: device, torch.bfloat16, torch.float16,
            torch.float32, torch.float64, torch.int8, torch.int32)
 
 
@@ -92,6 +92,8 @@ def test_tensors_lie_on_the_current_device(marshal, tmp_path, call, names):
     with pytest.raises(ValueError, match=f"{names[0]} must be on the current device"):
         call(marshal, [1] * len(names))
     assert calls.value == 1
+    bind(marshal, abi.count, None, gpus=1)           # with one GPU neither tensors nor the runtime are asked
+    assert call(marshal, [None] * len(names)) == 0 and calls.value == 2
 
 
 # a launch that waits, 2 s at most, for something that a Python thread does
