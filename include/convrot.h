@@ -291,6 +291,7 @@ int convrot_rope_inv_freq(const int* axis_pairs, int naxes, double theta,
  *   pos     [M][ld_pos] int32 (4-byte aligned), ld_pos >= naxes.
  *   axis_pairs  HOST array [naxes] of pairs per axis (each >= 0).
  *   inv_freq  [P] FP64, device (8-byte aligned): radians per unit of position.
+ *           One that is Inf or NaN makes its pair NaN.
  *   eps     > 0 and finite where a weight is given.
  */
 int convrot_qk_norm_rope(const void* q, int64_t q_tok, int64_t q_head,

@@ -85,6 +85,7 @@ __device__ __forceinline__ float2 pair_turn(const Params& p, int m, int i) {
   const unsigned long long phase = static_cast<unsigned long long>(at) * f;
   float s, c;
   sincospif(static_cast<float>(static_cast<int32_t>(phase >> 32)) * 4.656612873077393e-10f, &s, &c);   // 2^-31
+  if ((__double2hiint(t) & 0x7ff00000) == 0x7ff00000) s = c = __int_as_float(0x7fffffff);    // Inf or NaN: no angle
   return make_float2(c, s);
 }
 
