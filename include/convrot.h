@@ -313,6 +313,10 @@ int convrot_qk_norm_rope(const void* q, int64_t q_tok, int64_t q_head,
  *
  * in FP32, rounded once to out_dtype; acc is the exact int32 sum over K_p.
  * Without activation, gate and residual it equals convrot_gemm bit for bit.
+ * The activations' FP32 functions are good to about 1e-6 of their value for
+ * FP32 outputs, in the far tails too (GELU_TANH: to that and the rounding of
+ * its cubic argument v, |v| 2.4e-7), and to 3e-5 for BF16 and FP16 outputs,
+ * which are rounded more coarsely.
  *
  *   a_q, w_q  [M][ld_aq] and [N][ld_wq] codes, both in `fmt`.
  *           CONVROT_CODES_F16: any M.  CONVROT_CODES_S8 (weights resident at

@@ -28,42 +28,99 @@ struct Epilogue {
   int vec_res, vec_out;    // four neighbouring columns start on a whole vector
 };
 
-// 1 / (1 + e^-x) on the hardware base-2 exponential and reciprocal: relative
-// error below |x| 2^-23 + 2^-21.  Where e^-x overflows the reciprocal of
-// infinity is the limit 0.
-__device__ __forceinline__ float sigmoid(float x) {
-  float e, r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * -1.4426950408889634f));
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+// The activations' functions come in two forms.  FULL, for FP32 outputs: within
+// a few units of 2^-23 of the value anywhere in the range.  The other, for
+// outputs that are rounded to 16 bits: the hardware's base-2 exponential and
+// reciprocal, within 3e-5 of the value wherever that is a normal FP32 number
+// (the exponent's rounding, up to 127 x 2^-23; 2e-6 for |x| < 5), far below half
+// a unit of BF16 or FP16 (at least 2^-9 and 2^-12 of the value).  FULL costs
+// 4097 x 21500, K = 5120, FP32 out: SiLU 557 -> 574 us, GELU 558 -> 622, its tanh
+// form 558 -> 592 (the library's expf, division and normcdff: 613, 693, 632).
+
+__device__ __forceinline__ float rcp_approx(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
+__device__ __forceinline__ float exp2_approx(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+// 1 / d for 1 <= d < 2^100: the hardware's reciprocal and one Newton step.
+__device__ __forceinline__ float reciprocal(float d) {
+  const float r = rcp_approx(d);
+  return fmaf(r, fmaf(-d, r, 1.0f), r);
+}
 
-// GELU with the normal distribution's cumulative function from Abramowitz and
-// Stegun 7.1.26 (|error| <= 1.5e-7 in erf): for z = |x| / sqrt 2, t = 1 / (1 + p z),
-// erfc(z) = (a1 t + ... + a5 t^5) e^(-z^2).  Twelve operations and two
-// hardware functions where erff takes twice as many.
+// 1 / (1 + e^-v).  FULL: e / (1 + e) for v < 0, with e = e^-|v|, so that nothing
+// overflows.
+template <bool FULL>
+__device__ __forceinline__ float sigmoid(float v) {
+  if constexpr (FULL) {
+    const float e = expf(-fabsf(v)), r = reciprocal(1.0f + e);
+    return v < 0.f ? e * r : r;
+  } else {
+    return rcp_approx(1.0f + exp2_approx(v * -1.4426950408889634f));
+  }
+}
+
+// x sigmoid(x).  Not FULL: numerator and divisor times 2^-8, since below -87.3
+// the divisor 1 + e^-x passes 2^126, where its reciprocal is flushed to zero, while
+// the value is still a normal number (the tanh form of GELU is none there).
+template <bool FULL>
+__device__ __forceinline__ float silu(float x) {
+  if constexpr (FULL) return x * sigmoid<true>(x);
+  else return (x * 0.00390625f) * rcp_approx(exp2_approx(fmaf(x, -1.4426950408889634f, -8.0f)) + 0.00390625f);
+}
+
+// GELU: x times the normal distribution's cumulative function.  Beyond |x| the
+// distribution has the mass e^(-x^2/2) R(|x|), R falling slowly from 1/2 as
+// 1 / |x|: a polynomial of t = 1 / (1 + p |x|) without constant term, fitted for
+// the least largest relative error over 0 <= |x| <= 20 (fits of erf's absolute
+// error leave 5e-5 of the value at -3 and 2e-3 at -5).  FULL: nine terms (3e-7
+// evaluated in FP32), and the rounding of x^2 made good in the exponential;
+// otherwise seven (1e-6).
+template <bool FULL>
 __device__ __forceinline__ float gelu(float x) {
-  const float z = fabsf(x) * 0.70710678118654752f;
-  float t, e;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(t) : "f"(fmaf(0.3275911f, z, 1.0f)));
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(z * z * -1.4426950408889634f));
-  float q = fmaf(1.061405429f, t, -1.453152027f);
-  q = fmaf(q, t, 1.421413741f);
-  q = fmaf(q, t, -0.284496736f);
-  q = fmaf(q, t, 0.254829592f);
-  const float tail = 0.5f * q * t * e;               // the distribution's mass beyond |x|
+  float tail;
+  if constexpr (FULL) {
+    const float a = fminf(fabsf(x), 100.0f), h = a * a;
+    const float t = reciprocal(fmaf(0.35800001f, a, 1.0f));
+    float e = expf(-0.5f * h);
+    e = fmaf(e, -0.5f * fmaf(a, a, -h), e);
+    float q = fmaf(-0.0303161647f, t, 0.141607985f);
+    q = fmaf(q, t, -0.231846973f);
+    q = fmaf(q, t, 0.118834712f);
+    q = fmaf(q, t, -0.005121578f);
+    q = fmaf(q, t, 0.0978900045f);
+    q = fmaf(q, t, 0.123223044f);
+    q = fmaf(q, t, 0.142910033f);
+    q = fmaf(q, t, 0.142818913f);
+    tail = q * t * e;
+  } else {
+    const float t = rcp_approx(fmaf(0.26804f, fabsf(x), 1.0f));
+    const float e = exp2_approx(x * x * -0.72134752044448170f);
+    float q = fmaf(-0.0635638461f, t, 0.172559708f);
+    q = fmaf(q, t, -0.039989192f);
+    q = fmaf(q, t, 0.126776755f);
+    q = fmaf(q, t, 0.0891763493f);
+    q = fmaf(q, t, 0.10816849f);
+    q = fmaf(q, t, 0.106871277f);
+    tail = q * t * e;
+  }
   return x * (x < 0.f ? tail : 1.0f - tail);
 }
 
 // The activations, in FP32.  The tanh form of GELU is a sigmoid of twice its
 // cubic argument: x/2 (1 + tanh u) = x sigmoid(2u).
-template <int ACT>
+template <int ACT, bool FULL>
 __device__ __forceinline__ float activate(float x) {
   if constexpr (ACT == CONVROT_ACT_RELU) return x < 0.f ? 0.f : x;          // NaN stays NaN
-  else if constexpr (ACT == CONVROT_ACT_SILU) return x * sigmoid(x);
-  else if constexpr (ACT == CONVROT_ACT_GELU) return gelu(x);
+  else if constexpr (ACT == CONVROT_ACT_SILU) return silu<FULL>(x);
+  else if constexpr (ACT == CONVROT_ACT_GELU) return gelu<FULL>(x);
   else if constexpr (ACT == CONVROT_ACT_GELU_TANH)
-    return x * sigmoid(1.5957691216057307f * x * fmaf(0.044715f * x, x, 1.0f));
+    return x * sigmoid<FULL>(1.5957691216057307f * x * fmaf(0.044715f * x, x, 1.0f));
   else return x;
 }
 
@@ -169,7 +226,7 @@ __device__ __forceinline__ float residual_value(const ResidualWords<OUT>& r, int
 
 // The four columns' values before the residual: `y` holds fp32(acc).  The
 // dequantising products and the bias are rounded as convrot_gemm rounds them.
-template <int ACT>
+template <int ACT, bool FULL>
 __device__ __forceinline__ void activate4(const Epilogue& e, const ColumnTerms& t, float (&y)[4], float sa) {
 #pragma unroll
   for (int j = 0; j < 4; ++j) y[j] = __fmul_rn(__fmul_rn(y[j], sa), t.sw[j]);
@@ -178,7 +235,7 @@ __device__ __forceinline__ void activate4(const Epilogue& e, const ColumnTerms& 
     for (int j = 0; j < 4; ++j) y[j] = __fadd_rn(y[j], t.bias[j]);
   }
 #pragma unroll
-  for (int j = 0; j < 4; ++j) y[j] = activate<ACT>(y[j]);
+  for (int j = 0; j < 4; ++j) y[j] = activate<ACT, FULL>(y[j]);
   if (e.gate) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) y[j] = __fmul_rn(y[j], t.gate[j]);

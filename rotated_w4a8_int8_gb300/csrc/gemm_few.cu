@@ -280,7 +280,10 @@ few_kernel(const char* a_q, int64_t a_pitch, const char* w_q, int64_t w_pitch, i
     const ColumnTerms t = load_columns(e, n);
     const float sa = convrot::load_global(e.a_scale + m);
     float y[4] = {f.x, f.y, f.z, f.w};
-    with_act(e.act, [&](auto act) { activate4<decltype(act)::value>(e, t, y, sa); });
+    with_act(e.act, [&](auto act) {
+      if (out_dtype == CONVROT_FP32) activate4<decltype(act)::value, true>(e, t, y, sa);
+      else activate4<decltype(act)::value, false>(e, t, y, sa);
+    });
     auto finish = [&](auto kind) {
       constexpr int OUT = decltype(kind)::value;
       ResidualWords<OUT> res = {};

@@ -238,7 +238,7 @@ __device__ __forceinline__ void fill_box(const Epilogue& e, const int32_t (&acc)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         y[i] = __fadd_rn(__fmul_rn(__fmul_rn(__int_as_float(acc[j + i]), sa), ts[i]), tb[i]);
-        y[i] = __fadd_rn(__fmul_rn(activate<ACT>(y[i]), tg[i]), residual_value<OUT>(r, i));
+        y[i] = __fadd_rn(__fmul_rn(activate<ACT, OUT == CONVROT_FP32>(y[i]), tg[i]), residual_value<OUT>(r, i));
       }
       if constexpr (OUT == CONVROT_FP32) {
 #pragma unroll
