@@ -157,7 +157,8 @@ def _operators():
         try:
             from . import _marshal as m
         except ImportError as e:
-            raise ImportError("the marshalling module is not built: run __graft_entry__.build() first") from e
+            raise ImportError("the marshalling module is not built for this interpreter (it needs Python's headers): "
+                              "run __graft_entry__.build() first") from e
 
         def current(device: int) -> int:
             return torch.cuda.current_stream(device).cuda_stream

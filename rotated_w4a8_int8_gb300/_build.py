@@ -17,7 +17,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libconvrot.so")
-MARSHAL = os.path.join(HERE, "_marshal.so")
+# the binding's compiled module, named for this interpreter: another version does not load it
+MARSHAL = os.path.join(HERE, "_marshal" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
 # (source, object, defines): quant.cu is compiled twice, once without and once
 # with the kernels that write code-norm bounds; gemm_fused.cu once per output type
 SOURCES = [("api.cu", "api", []), ("quant.cu", "quant", []),
@@ -50,14 +51,27 @@ def _compile(unit, extra: list[str]) -> str:
     return obj
 
 
-def _compile_marshal(_=None) -> None:
+def _python_include() -> str | None:
+    """Where Python.h lies, or None: the library (C ABI) does not need it."""
+    paths = sysconfig.get_paths()
+    for name in ("include", "platinclude"):
+        if os.path.exists(os.path.join(paths[name], "Python.h")):
+            return paths[name]
+    return None
+
+
+def _compile_marshal() -> None:
     """The CPython extension that marshals the block operators' arguments."""
+    include = _python_include()
+    if include is None:
+        sys.stderr.write("Python.h not found: libconvrot.so is built without the Python calls of rms_norm_quant, "
+                         "qk_norm_rope and gemm_fused\n")
+        return
     cc = shutil.which("gcc") or shutil.which("cc")
     if cc is None:
         raise RuntimeError("no C compiler found for the marshalling module")
     tmp = MARSHAL + ".tmp"
-    cmd = [cc, "-O2", "-std=c11", "-shared", "-fPIC", "-I", sysconfig.get_paths()["include"],
-           os.path.join(CSRC, "marshal.c"), "-o", tmp]
+    cmd = [cc, "-O2", "-std=c11", "-shared", "-fPIC", "-I", include, os.path.join(CSRC, "marshal.c"), "-o", tmp]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"marshal.c failed to compile:\n{r.stdout}\n{r.stderr}")
@@ -68,7 +82,12 @@ def build(verbose_ptxas: bool = False, force: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [os.path.join(ROOT, "include", "convrot.h")]
     newest = max(os.path.getmtime(d) for d in deps)
-    if not force and all(os.path.exists(f) and os.path.getmtime(f) > newest for f in (LIB, MARSHAL)):
+
+    def current(f: str) -> bool:
+        return not force and os.path.exists(f) and os.path.getmtime(f) > newest
+    if current(LIB):
+        if _python_include() and not current(MARSHAL):
+            _compile_marshal()
         return LIB
     extra = ["-Xptxas", "-v"] if verbose_ptxas else []
     with cf.ThreadPoolExecutor(len(SOURCES) + 1) as ex:
