@@ -345,6 +345,26 @@ int convrot_gemm_fused(const void* a_q, int64_t ld_aq, const float* a_scale,
                        cudaStream_t stream);
 
 /*
+ * Self-test of the many-token kernel behind convrot_gemm_fused: the same call
+ * on FP16-held codes with its output tile (tile: 128 or 256 columns wide, or
+ * 192 in slices) and the CTA pairs that share one (slices: 1 to 4 parts of K,
+ * each of at least 512) given instead of chosen, whatever M.  The result does
+ * not depend on them.  With `starve` nonzero the kernel's producer loads
+ * nothing: its waits run out after about two seconds, the output is undefined,
+ * and convrot_device_error reports CONVROT_ERR_DEVICE_TIMEOUT.  The context
+ * stays usable.
+ */
+int convrot_gemm_fused_selftest(const void* a_q, int64_t ld_aq,
+                                const float* a_scale, const void* w_q,
+                                int64_t ld_wq, const float* w_scale,
+                                const float* bias, convrot_act act,
+                                const float* gate, const void* residual,
+                                int64_t ld_residual, int M, int N, int K_p,
+                                void* out, convrot_dtype out_dtype,
+                                int64_t ld_out, int tile, int slices,
+                                int starve, cudaStream_t stream);
+
+/*
  * W8A8 with resident weights: widens S8 codes (CONVROT_CODES_S8, e.g. weight
  * codes prepared once and kept at one byte each) into the FP16-held codes
  * that convrot_gemm reads.  Source: the NVFP4 loader entry's W8A8 comparison,

@@ -19,7 +19,7 @@ __all__ = [
     "device_error", "ConvRotError", "BF16", "FP16",
     "FP32", "CODES_S8",
     "CODES_F16", "LIB_PATH", "EXPORTS",
-    "rms_norm_quant", "rope_inv_freq", "qk_norm_rope", "gemm_fused",
+    "rms_norm_quant", "rope_inv_freq", "qk_norm_rope", "gemm_fused", "gemm_fused_selftest",
     "ACT_NONE", "ACT_RELU", "ACT_SILU", "ACT_GELU", "ACT_GELU_TANH", "FEW_TOKENS",
 ]
 
@@ -32,7 +32,7 @@ EXPORTS = ("convrot_padded_k", "convrot_status_string", "convrot_prepare_weight"
            "convrot_quant_act", "convrot_gemm", "convrot_gemm_i32", "convrot_device_error",
            "convrot_last_error", "convrot_gemm_timeout_selftest", "convrot_widen_codes", "convrot_int8_mma_probe",
            "convrot_decode_gemm_probe", "convrot_rms_norm_quant", "convrot_rope_inv_freq", "convrot_qk_norm_rope",
-           "convrot_gemm_fused")
+           "convrot_gemm_fused", "convrot_gemm_fused_selftest")
 
 _lib = None
 _block_ops = None
@@ -86,6 +86,9 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.convrot_gemm_fused.argtypes = [vp, i64, vp, vp, i64, vp, i32, vp, i32, vp, vp, i64, i32, i32, i32, vp, i32,
                                        i64, vp]
     lib.convrot_gemm_fused.restype = i32
+    lib.convrot_gemm_fused_selftest.argtypes = [vp, i64, vp, vp, i64, vp, vp, i32, vp, vp, i64, i32, i32, i32, vp, i32, i64,
+                                                i32, i32, i32, vp]
+    lib.convrot_gemm_fused_selftest.restype = i32
     lib.convrot_last_error.argtypes = []
     lib.convrot_last_error.restype = ctypes.c_char_p
     lib.convrot_device_error.argtypes = [vp, ctypes.POINTER(i32)]
@@ -251,6 +254,17 @@ def gemm_fused(a_q, a_scale, w_q, w_scale, out, K_p: int | None = None, bias=Non
                                                    stream)
     if status:
         _check("convrot_gemm_fused", status)
+
+
+def gemm_fused_selftest(a_q, a_scale, w_q, w_scale, out, tile: int, slices: int, starve: bool = False, bias=None,
+                        act: int = ACT_NONE, gate=None, residual=None, stream=None) -> None:
+    """convrot_gemm_fused_selftest: gemm_fused on float16 codes with the many-token kernel's tile width (128, 192 or
+    256) and K slices (1 to 4) given; starve: its producer is off (a wait runs out)."""
+    M, N = a_q.shape[0], w_q.shape[0]
+    _check("convrot_gemm_fused_selftest", load_library().convrot_gemm_fused_selftest(
+        _ptr(a_q), _ld(a_q), _ptr(a_scale), _ptr(w_q), _ld(w_q), _ptr(w_scale), _ptr(bias), int(act), _ptr(gate),
+        _ptr(residual), 0 if residual is None else _ld(residual), M, N, int(a_q.shape[1]), _ptr(out), _dtype_code(out),
+        _ld(out), int(tile), int(slices), int(bool(starve)), _stream(stream)))
 
 
 def widen_codes(src, dst, cols: int | None = None, stream=None) -> None:

@@ -263,17 +263,26 @@ __device__ __forceinline__ void finish4(const Epilogue& e, float (&y)[4], const 
   }
 }
 
+// Tile width and K slices of the many-token kernel, 0: its own choice; starve: its
+// producer loads nothing, so that every wait for operands runs out.
+struct Variant {
+  int tile, slices, starve;
+};
+
 // The two kernels.  gemm_many: FP16-held codes, any number of tokens (one
 // object per output type, each with its own device error word).  gemm_few:
 // either form of the codes, at most CONVROT_FEW_TOKENS tokens.
 template <int OUT>
 int gemm_many(const void* a_q, int64_t ld_aq, const void* w_q, int64_t ld_wq, int K_p, const Epilogue& ep,
-              cudaStream_t st);
+              const Variant& variant, cudaStream_t st);
 template <int OUT>
 cudaError_t take_fused_error_word(int* v);
-template <> int gemm_many<CONVROT_BF16>(const void*, int64_t, const void*, int64_t, int, const Epilogue&, cudaStream_t);
-template <> int gemm_many<CONVROT_FP16>(const void*, int64_t, const void*, int64_t, int, const Epilogue&, cudaStream_t);
-template <> int gemm_many<CONVROT_FP32>(const void*, int64_t, const void*, int64_t, int, const Epilogue&, cudaStream_t);
+template <> int gemm_many<CONVROT_BF16>(const void*, int64_t, const void*, int64_t, int, const Epilogue&, const Variant&,
+                                        cudaStream_t);
+template <> int gemm_many<CONVROT_FP16>(const void*, int64_t, const void*, int64_t, int, const Epilogue&, const Variant&,
+                                        cudaStream_t);
+template <> int gemm_many<CONVROT_FP32>(const void*, int64_t, const void*, int64_t, int, const Epilogue&, const Variant&,
+                                        cudaStream_t);
 template <> cudaError_t take_fused_error_word<CONVROT_BF16>(int*);
 template <> cudaError_t take_fused_error_word<CONVROT_FP16>(int*);
 template <> cudaError_t take_fused_error_word<CONVROT_FP32>(int*);

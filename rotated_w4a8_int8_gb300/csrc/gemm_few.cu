@@ -342,11 +342,10 @@ int gemm_few(const void* a_q, int64_t ld_aq, const void* w_q, int64_t ld_wq, con
 
 using namespace crfused;
 
-extern "C" int convrot_gemm_fused(const void* a_q, int64_t ld_aq, const float* a_scale, const void* w_q,
-                                  int64_t ld_wq, const float* w_scale, convrot_codes fmt, const float* bias,
-                                  convrot_act act, const float* gate, const void* residual, int64_t ld_residual,
-                                  int M, int N, int K_p, void* out, convrot_dtype out_dtype, int64_t ld_out,
-                                  cudaStream_t stream) {
+static int fused_call(const void* a_q, int64_t ld_aq, const float* a_scale, const void* w_q, int64_t ld_wq,
+                      const float* w_scale, convrot_codes fmt, const float* bias, convrot_act act, const float* gate,
+                      const void* residual, int64_t ld_residual, int M, int N, int K_p, void* out,
+                      convrot_dtype out_dtype, int64_t ld_out, const Variant& variant, cudaStream_t stream) {
   if (out_dtype != CONVROT_BF16 && out_dtype != CONVROT_FP16 && out_dtype != CONVROT_FP32)
     return CONVROT_ERR_UNSUPPORTED;
   if (fmt != CONVROT_CODES_S8 && fmt != CONVROT_CODES_F16) return CONVROT_ERR_UNSUPPORTED;
@@ -379,13 +378,33 @@ extern "C" int convrot_gemm_fused(const void* a_q, int64_t ld_aq, const float* a
   e.vec_out = !off(out, 4 * es) && ld_out % 4 == 0;
   e.vec_res = !off(residual, 4 * es) && ld_residual % 4 == 0;
   const int64_t weight_bytes = static_cast<int64_t>(N) * K_p * 2;
-  const bool few = M <= 16 || (M <= CONVROT_FEW_TOKENS && weight_bytes <= kFewBytes);
+  const bool few = !variant.tile && (M <= 16 || (M <= CONVROT_FEW_TOKENS && weight_bytes <= kFewBytes));
   if (fmt == CONVROT_CODES_S8 || few) return gemm_few(a_q, ld_aq, w_q, ld_wq, fmt, K_p, e, out_dtype, stream);
   switch (out_dtype) {
-    case CONVROT_BF16: return gemm_many<CONVROT_BF16>(a_q, ld_aq, w_q, ld_wq, K_p, e, stream);
-    case CONVROT_FP16: return gemm_many<CONVROT_FP16>(a_q, ld_aq, w_q, ld_wq, K_p, e, stream);
-    default: return gemm_many<CONVROT_FP32>(a_q, ld_aq, w_q, ld_wq, K_p, e, stream);
+    case CONVROT_BF16: return gemm_many<CONVROT_BF16>(a_q, ld_aq, w_q, ld_wq, K_p, e, variant, stream);
+    case CONVROT_FP16: return gemm_many<CONVROT_FP16>(a_q, ld_aq, w_q, ld_wq, K_p, e, variant, stream);
+    default: return gemm_many<CONVROT_FP32>(a_q, ld_aq, w_q, ld_wq, K_p, e, variant, stream);
   }
+}
+
+extern "C" int convrot_gemm_fused(const void* a_q, int64_t ld_aq, const float* a_scale, const void* w_q,
+                                  int64_t ld_wq, const float* w_scale, convrot_codes fmt, const float* bias,
+                                  convrot_act act, const float* gate, const void* residual, int64_t ld_residual,
+                                  int M, int N, int K_p, void* out, convrot_dtype out_dtype, int64_t ld_out,
+                                  cudaStream_t stream) {
+  return fused_call(a_q, ld_aq, a_scale, w_q, ld_wq, w_scale, fmt, bias, act, gate, residual, ld_residual, M, N, K_p,
+                    out, out_dtype, ld_out, Variant{}, stream);
+}
+
+extern "C" int convrot_gemm_fused_selftest(const void* a_q, int64_t ld_aq, const float* a_scale, const void* w_q,
+                                           int64_t ld_wq, const float* w_scale, const float* bias, convrot_act act,
+                                           const float* gate, const void* residual, int64_t ld_residual, int M, int N,
+                                           int K_p, void* out, convrot_dtype out_dtype, int64_t ld_out, int tile,
+                                           int slices, int starve, cudaStream_t stream) {
+  const bool known = tile == 128 || tile == 256 || (tile == 192 && slices > 1);
+  if (!known || slices < 1 || slices > 4 || (slices > 1 && K_p < 512 * slices)) return CONVROT_ERR_INVALID_ARG;
+  return fused_call(a_q, ld_aq, a_scale, w_q, ld_wq, w_scale, CONVROT_CODES_F16, bias, act, gate, residual,
+                    ld_residual, M, N, K_p, out, out_dtype, ld_out, Variant{tile, slices, starve != 0}, stream);
 }
 
 namespace convrot {

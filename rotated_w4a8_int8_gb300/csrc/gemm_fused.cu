@@ -83,7 +83,7 @@ struct Tile {
 
 struct Params {
   Epilogue e;
-  int k_steps, num_m2, num_n, num_items, split;
+  int k_steps, num_m2, num_n, num_items, split, starve;
   int out_piece, res_piece;     // 16: boxes by TMA; else bytes per lane of the warp's copy (8, 4 or 2)
 };
 
@@ -337,7 +337,7 @@ fused_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__
       bool ok = true;
       uint32_t issued_mask = 0, issued_phase = 0;   // even CTA: last outstanding stage phase
       const uint32_t lfull0 = map_to_rank(full0, leader);
-      for (int tile = cluster_id; tile < p.num_items && ok; tile += num_clusters) {
+      for (int tile = p.starve ? p.num_items : cluster_id; tile < p.num_items && ok; tile += num_clusters) {
         int m2, nt;
         work_coords(p, tile, m2, nt);
         const int m_row = (2 * m2 + static_cast<int>(half)) * BM;
@@ -716,6 +716,7 @@ static int launch(const void* a_q, int64_t ld_aq, const void* w_q, int64_t ld_wq
   int resident = 0;
   cudaError_t e = resident_clusters<OUT, ACT, BN, SPLITK>(split, &resident);
   if (e != cudaSuccess) return failed("fused GEMM set-up", e);
+  if (resident <= 0) return CONVROT_ERR_UNSUPPORTED;
   const int clusters = SPLITK ? p.num_items : (p.num_items < resident ? p.num_items : resident);
   e = convrot::launch_after(fused_kernel<OUT, ACT, BN, SPLITK>, dim3(clusters * 2 * split), THREADS, Tile<BN>::SMEM, 2 * split,
                             st, ma, mb, mo, mr, p);
@@ -766,10 +767,14 @@ static int pick_shape(const Params& p, Shape* best) {
 
 template <int OUT, int ACT>
 static int launch_act(const void* a_q, int64_t ld_aq, const void* w_q, int64_t ld_wq, int K_p, Params p,
-                      cudaStream_t st) {
+                      const Variant& variant, cudaStream_t st) {
   Shape s = {256, 1};
-  const int r = pick_shape<OUT, ACT>(p, &s);
-  if (r != CONVROT_OK) return r;
+  if (variant.tile) {
+    s = {variant.tile, variant.slices};
+  } else {
+    const int r = pick_shape<OUT, ACT>(p, &s);
+    if (r != CONVROT_OK) return r;
+  }
   if (s.bn == 256)
     return s.split == 1 ? launch<OUT, ACT, 256, false>(a_q, ld_aq, w_q, ld_wq, K_p, p, 1, st)
                         : launch<OUT, ACT, 256, true>(a_q, ld_aq, w_q, ld_wq, K_p, p, s.split, st);
@@ -787,18 +792,19 @@ static int launch_act(const void* a_q, int64_t ld_aq, const void* w_q, int64_t l
 
 template <>
 int gemm_many<CONVROT_FUSED_OUT>(const void* a_q, int64_t ld_aq, const void* w_q, int64_t ld_wq, int K_p,
-                                 const Epilogue& ep, cudaStream_t st) {
+                                 const Epilogue& ep, const Variant& variant, cudaStream_t st) {
   constexpr int OUT = CONVROT_FUSED_OUT;
   Params p = {};
   p.e = ep;
   p.k_steps = K_p / BK;
   p.num_m2 = (ep.M + 2 * BM - 1) / (2 * BM);
+  p.starve = variant.starve;
   switch (ep.act) {
-    case CONVROT_ACT_RELU: return launch_act<OUT, CONVROT_ACT_RELU>(a_q, ld_aq, w_q, ld_wq, K_p, p, st);
-    case CONVROT_ACT_SILU: return launch_act<OUT, CONVROT_ACT_SILU>(a_q, ld_aq, w_q, ld_wq, K_p, p, st);
-    case CONVROT_ACT_GELU: return launch_act<OUT, CONVROT_ACT_GELU>(a_q, ld_aq, w_q, ld_wq, K_p, p, st);
-    case CONVROT_ACT_GELU_TANH: return launch_act<OUT, CONVROT_ACT_GELU_TANH>(a_q, ld_aq, w_q, ld_wq, K_p, p, st);
-    default: return launch_act<OUT, CONVROT_ACT_NONE>(a_q, ld_aq, w_q, ld_wq, K_p, p, st);
+    case CONVROT_ACT_RELU: return launch_act<OUT, CONVROT_ACT_RELU>(a_q, ld_aq, w_q, ld_wq, K_p, p, variant, st);
+    case CONVROT_ACT_SILU: return launch_act<OUT, CONVROT_ACT_SILU>(a_q, ld_aq, w_q, ld_wq, K_p, p, variant, st);
+    case CONVROT_ACT_GELU: return launch_act<OUT, CONVROT_ACT_GELU>(a_q, ld_aq, w_q, ld_wq, K_p, p, variant, st);
+    case CONVROT_ACT_GELU_TANH: return launch_act<OUT, CONVROT_ACT_GELU_TANH>(a_q, ld_aq, w_q, ld_wq, K_p, p, variant, st);
+    default: return launch_act<OUT, CONVROT_ACT_NONE>(a_q, ld_aq, w_q, ld_wq, K_p, p, variant, st);
   }
 }
 
