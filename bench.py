@@ -44,20 +44,36 @@ METRIC = "ms/layer and effective INT8 TOPS at M=19989 (QKV, FFN-down); % of INT8
 PAGES_QKV_MS = 25.08
 FALLBACK_PEAKS = {"hbm_gbs": 6800.0, "bf16_tflops": 1900.0, "bf16_tflops_sustained": 1700.0}
 # DRAM traffic (read + write bytes) of one full-size QKV GEMM launch, from an ncu capture of
-# this kernel; valid only while code_sha16(gemm.cu) equals this (the hash ignores comments;
-# otherwise the bench line reports traffic as null).
-GEMM_TRAFFIC = {"sha256_16": "b760061e254b6c7f", "bytes": 2730000000 + 930500000}
+# this kernel; valid only while code_sha16 of gemm_sources() equals this (the hash ignores
+# comments; otherwise the bench line reports traffic as null).
+GEMM_TRAFFIC = {"sha256_16": "80156c16e0db3b0f", "bytes": 2719698432 + 937778944}
 
 
-def code_sha16(path: str) -> str:
-    """First 16 hex digits of the SHA-256 of a C++ source with its comments and
+def gemm_sources(path: str | None = None) -> list[str]:
+    """gemm.cu and the device headers (.cuh) that it includes: what its kernel is made of."""
+    import re
+    path = path or os.path.join(ROOT, "rotated_w4a8_int8_gb300", "csrc", "gemm.cu")
+    found = [path]
+    for p in found:
+        with open(p) as f:
+            for name in re.findall(r'^#include "([^"]+\.cuh)"', f.read(), flags=re.M):
+                q = os.path.join(os.path.dirname(p), name)
+                if q not in found:
+                    found.append(q)
+    return found
+
+
+def code_sha16(*paths: str) -> str:
+    """First 16 hex digits of the SHA-256 of C++ sources with their comments and
     blank lines removed: it changes when the code changes, not the comments."""
     import re
-    with open(path) as f:
-        src = f.read()
-    src = re.sub(r"/\*.*?\*/", "", src, flags=re.S)
-    src = re.sub(r"//[^\n]*", "", src)
-    lines = [ln.rstrip() for ln in src.splitlines() if ln.strip()]
+    lines = []
+    for path in paths:
+        with open(path) as f:
+            src = f.read()
+        src = re.sub(r"/\*.*?\*/", "", src, flags=re.S)
+        src = re.sub(r"//[^\n]*", "", src)
+        lines += [ln.rstrip() for ln in src.splitlines() if ln.strip()]
     return hashlib.sha256("\n".join(lines).encode()).hexdigest()[:16]
 
 
@@ -957,8 +973,7 @@ def main():
     a_ms = statistics.mean(r["act_ms"])
     w_ms = statistics.mean(r["weight_ms"])
     achieved = sz["gemm_flops"] / (g_ms / 1e3) / 1e12
-    gemm_src = os.path.join(ROOT, "rotated_w4a8_int8_gb300", "csrc", "gemm.cu")
-    traffic = GEMM_TRAFFIC["bytes"] if GEMM_TRAFFIC["sha256_16"] == code_sha16(gemm_src) else None
+    traffic = GEMM_TRAFFIC["bytes"] if GEMM_TRAFFIC["sha256_16"] == code_sha16(*gemm_sources()) else None
 
     def quant_kernel(us, alg, moved):
         gbs = alg / (us / 1e6) / 1e9
