@@ -10,6 +10,7 @@ namespace convrot {
 int record_cuda_error(const char* what, cudaError_t e) {
   std::snprintf(g_last_error, sizeof(g_last_error), "%s: %s (%s)", what, cudaGetErrorString(e),
                 cudaGetErrorName(e));
+  (void)cudaGetLastError();      // reported here: the caller's next CUDA call must not find it again
   return CONVROT_ERR_CUDA;
 }
 int record_error(const char* what) {

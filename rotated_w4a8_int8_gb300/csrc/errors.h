@@ -3,7 +3,7 @@
 #include <cuda_runtime_api.h>
 
 namespace convrot {
-// Records "<what>: <CUDA error text>" and returns CONVROT_ERR_CUDA.
+// Records "<what>: <CUDA error text>", clears it from the runtime and returns CONVROT_ERR_CUDA.
 int record_cuda_error(const char* what, cudaError_t e);
 // Records `what` verbatim and returns CONVROT_ERR_CUDA.
 int record_error(const char* what);

@@ -650,12 +650,6 @@ static bool make_box_map(CUtensorMap* map, const void* base, int M, int N, int64
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Records a CUDA error and clears it, so that the caller's next CUDA call does not report it again.
-static int failed(const char* what, cudaError_t e) {
-  (void)cudaGetLastError();
-  return convrot::record_cuda_error(what, e);
-}
-
 constexpr int kMaxDevices = 64;
 
 // Clusters of 2 * split CTAs of this kernel that are resident at once.
@@ -715,12 +709,12 @@ static int launch(const void* a_q, int64_t ld_aq, const void* w_q, int64_t ld_wq
     return convrot::record_error("cuTensorMapEncodeTiled failed for an operand map");
   int resident = 0;
   cudaError_t e = resident_clusters<OUT, ACT, BN, SPLITK>(split, &resident);
-  if (e != cudaSuccess) return failed("fused GEMM set-up", e);
+  if (e != cudaSuccess) return convrot::record_cuda_error("fused GEMM set-up", e);
   if (resident <= 0) return CONVROT_ERR_UNSUPPORTED;
   const int clusters = SPLITK ? p.num_items : (p.num_items < resident ? p.num_items : resident);
   e = convrot::launch_after(fused_kernel<OUT, ACT, BN, SPLITK>, dim3(clusters * 2 * split), THREADS, Tile<BN>::SMEM, 2 * split,
                             st, ma, mb, mo, mr, p);
-  return e == cudaSuccess ? CONVROT_OK : failed("fused GEMM launch", e);
+  return e == cudaSuccess ? CONVROT_OK : convrot::record_cuda_error("fused GEMM launch", e);
 }
 
 // Tile width and pairs per tile.
@@ -752,7 +746,7 @@ static int pick_shape(const Params& p, Shape* best) {
                       : v.bn == 192 ? resident_clusters<OUT, ACT, 192, true>(split, &resident)
                                     : (split == 1 ? resident_clusters<OUT, ACT, 128, false>(1, &resident)
                                                   : resident_clusters<OUT, ACT, 128, true>(split, &resident));
-      if (e != cudaSuccess) return failed("fused GEMM set-up", e);
+      if (e != cudaSuccess) return convrot::record_cuda_error("fused GEMM set-up", e);
       if (split > 1 && items > resident) break;
       const int rounds = (items + resident - 1) / resident, steps = (p.k_steps + split - 1) / split;
       const double t = rounds * steps * v.step + v.tail + (split == 1 ? 0.0 : v.join);
