@@ -33,9 +33,10 @@ struct Epilogue {
 // outputs that are rounded to 16 bits: the hardware's base-2 exponential and
 // reciprocal, within 3e-5 of the value wherever that is a normal FP32 number
 // (the exponent's rounding, up to 127 x 2^-23; 2e-6 for |x| < 5), far below half
-// a unit of BF16 or FP16 (at least 2^-9 and 2^-12 of the value).  FULL costs
-// 4097 x 21500, K = 5120, FP32 out: SiLU 557 -> 574 us, GELU 558 -> 622, its tanh
-// form 558 -> 592 (the library's expf, division and normcdff: 613, 693, 632).
+// a unit of BF16 or FP16 (at least 2^-9 and 2^-12 of the value).  4097 x 21500,
+// K = 5120, FP32 out, FULL against the other form: SiLU 548 us for 550 to 557, tanh
+// GELU 578 for 558, GELU 619 for 558 (with an IEEE division and normcdff 613, 632
+// and 693).
 
 __device__ __forceinline__ float rcp_approx(float x) {
   float r;
@@ -47,31 +48,21 @@ __device__ __forceinline__ float exp2_approx(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
-// 1 / d for 1 <= d < 2^100: the hardware's reciprocal and one Newton step.
-__device__ __forceinline__ float reciprocal(float d) {
-  const float r = rcp_approx(d);
-  return fmaf(r, fmaf(-d, r, 1.0f), r);
-}
-
-// 1 / (1 + e^-v).  FULL: e / (1 + e) for v < 0, with e = e^-|v|, so that nothing
-// overflows.
+// 1 / (1 + e^-v).  FULL: 2 units of 2^-23 from expf, 1/2 from the sum and 1 from
+// the reciprocal.
 template <bool FULL>
 __device__ __forceinline__ float sigmoid(float v) {
-  if constexpr (FULL) {
-    const float e = expf(-fabsf(v)), r = reciprocal(1.0f + e);
-    return v < 0.f ? e * r : r;
-  } else {
-    return rcp_approx(1.0f + exp2_approx(v * -1.4426950408889634f));
-  }
+  return rcp_approx(1.0f + (FULL ? expf(-v) : exp2_approx(v * -1.4426950408889634f)));
 }
 
-// x sigmoid(x).  Not FULL: numerator and divisor times 2^-8, since below -87.3
-// the divisor 1 + e^-x passes 2^126, where its reciprocal is flushed to zero, while
-// the value is still a normal number (the tanh form of GELU is none there).
+// x sigmoid(x), with numerator and divisor times 2^-8: below -87.3 the divisor
+// 1 + e^-x passes 2^126, where its reciprocal is flushed to zero, while the value
+// is still a normal number (the tanh form of GELU is none there).
 template <bool FULL>
 __device__ __forceinline__ float silu(float x) {
-  if constexpr (FULL) return x * sigmoid<true>(x);
-  else return (x * 0.00390625f) * rcp_approx(exp2_approx(fmaf(x, -1.4426950408889634f, -8.0f)) + 0.00390625f);
+  constexpr float k = 0.00390625f;
+  const float d = FULL ? fmaf(expf(-x), k, k) : exp2_approx(fmaf(x, -1.4426950408889634f, -8.0f)) + k;
+  return (x * k) * rcp_approx(d);
 }
 
 // GELU: x times the normal distribution's cumulative function.  Beyond |x| the
@@ -86,7 +77,7 @@ __device__ __forceinline__ float gelu(float x) {
   float tail;
   if constexpr (FULL) {
     const float a = fminf(fabsf(x), 100.0f), h = a * a;
-    const float t = reciprocal(fmaf(0.35800001f, a, 1.0f));
+    const float t = rcp_approx(fmaf(0.35800001f, a, 1.0f));
     float e = expf(-0.5f * h);
     e = fmaf(e, -0.5f * fmaf(a, a, -h), e);
     float q = fmaf(-0.0303161647f, t, 0.141607985f);
