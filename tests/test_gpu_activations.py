@@ -1,8 +1,9 @@
 """gemm_fused's activations over their whole range, tails included: products of zero codes leave act(bias).
 
-Tolerances, relative to the value.  FP32 outputs: SiLU's exponential (2 units of 2^-23), sum, division and two products
-(half a unit each) stay below 2^-21; GELU's distribution function (5 units) and product below 2^-20; the tanh form's
-cubic argument v is rounded four times, which its exponential turns into |v| 2^-22 of the value, beside SiLU's 2^-21.
+Tolerances, relative to the value, in units of 2^-23.  FP32 outputs: SiLU's exponential (2), sum (1/2), reciprocal (1) and
+product (1/2) are 4, 2^-21; GELU's polynomial (2 1/2), its variable's reciprocal (1), exponential and its correction
+(2 1/2) and three products (1 1/2) are less than 8, 2^-20; the tanh form's cubic argument v is rounded four times, which
+its exponential turns into |v| 2^-22 of the value, beside SiLU's 2^-21.
 16-bit outputs: 3e-5 of the value, as the header states, and half a unit of the type.  Values below 2^-120 leave the
 normal numbers within the functions: 2^-120 is allowed as an absolute error.
 """
