@@ -60,6 +60,8 @@ extern "C" {
 #define CONVROT_MAX_HEAD 1024      /* largest head width (qk_norm_rope)     */
 #define CONVROT_MAX_AXES 4         /* most position axes (qk_norm_rope)     */
 #define CONVROT_FEW_TOKENS 64      /* most rows with S8 codes (gemm_fused)  */
+#define CONVROT_MAX_ATT_HEAD 128   /* largest head width (attention)        */
+#define CONVROT_MAX_SEQUENCES 65535 /* most sequences of a call (attention) */
 
 typedef enum {
     CONVROT_OK = 0,
@@ -216,7 +218,9 @@ int convrot_gemm(const void* a_q, int64_t ld_aq, const float* a_scale,
  * The operators around the layer's linear products in a video DiT block: the
  * norm before one (convrot_rms_norm_quant), the per-head norm and rotary
  * positions of q and k after the qkv product (convrot_qk_norm_rope), and the
- * product with its bias, activation, gate and residual (convrot_gemm_fused).
+ * product with its bias, activation, gate and residual (convrot_gemm_fused);
+ * and its attention, to rows (convrot_attention) or to a cache in pages
+ * (convrot_paged_attention, convrot_cache_write).
  * The conventions at the top of this file hold for them; like the layer's
  * calls they only enqueue kernels and can be captured in a CUDA graph (after
  * one eager call of the same kind on the device).
@@ -365,6 +369,126 @@ int convrot_gemm_fused_selftest(const void* a_q, int64_t ld_aq,
                                 int starve, cudaStream_t stream);
 
 /*
+ * Attention of packed sequences: a block's tokens to the states of an encoder,
+ * which are of another length (cross attention), or to their own (self
+ * attention).  For row i of a sequence and head h, with the keys and values of
+ * head h / (heads_q / heads_k):
+ *
+ *     out_i = sum_j p_j v_j,   p = softmax over j < n(i) of scale * q_i . k_j
+ *     n(i) = k_len, or with `causal` min(k_len, k_len - q_len + i + 1)
+ *
+ * (causal: the last row sees every key).  A row that sees no key (n(i) <= 0)
+ * becomes zeros.
+ *
+ *   q, out  [rows][heads_q][D], k and v [keys][heads_k][D] in `dtype` (BF16 or
+ *           FP16), a head's D values contiguous; row and head strides in
+ *           elements, so they can be views of the packed qkv output.
+ *           heads_q is a multiple of heads_k.  out overlaps no input, and its
+ *           heads and rows do not overlap.
+ *   D       a multiple of 8, 8 .. CONVROT_MAX_ATT_HEAD.
+ *   seqs    NULL: one sequence of all rows and all keys.  Otherwise device
+ *           int32 [B][4] (16-byte aligned; B <= CONVROT_MAX_SEQUENCES), for every
+ *           sequence q_start, q_len,
+ *           k_start, k_len: rows q_start .. q_start + q_len - 1 attend to keys
+ *           k_start .. k_start + k_len - 1.  Lengths may be 0.  The rows of the
+ *           sequences are disjoint, in any order; keys may be shared.  Rows in
+ *           no sequence are left as they were, and keys in none are not used,
+ *           whatever they hold (Inf or NaN too).  A sequence that reaches past
+ *           its tensors is skipped and reported by convrot_device_error.
+ *   scale   > 0 and finite.
+ *
+ * Scores, maximum, sum and outputs are FP32; the weights p are rounded to
+ * `dtype` for their product with v, and the result once.  An Inf or NaN in v
+ * (or in a row of scores) shows in the rows that see that key; with `causal` it
+ * may also show in earlier rows of the same sequence.  The result does not
+ * depend on other sequences of the call, nor on the run; it may change in its
+ * last bits with the sizes of the call (how the keys are split).
+ * Alignment: every pointer 16-byte aligned, row and head strides multiples of 8
+ * elements and not below D (where that dimension is more than one long).
+ */
+int convrot_attention(const void* q, int64_t q_row, int64_t q_head,
+                      const void* k, int64_t k_row, int64_t k_head,
+                      const void* v, int64_t v_row, int64_t v_head,
+                      void* out, int64_t out_row, int64_t out_head,
+                      convrot_dtype dtype, int rows, int keys, int heads_q,
+                      int heads_k, int D, const int32_t* seqs, int B,
+                      float scale, int causal, cudaStream_t stream);
+
+/*
+ * The same attention where keys and values lie in the pages of a cache: a chunk
+ * of new tokens, or single ones, after what came before.  The keys of sequence
+ * b lie at positions k_start .. k_start + k_len - 1 of its row of the page
+ * table (a k_start above 0 leaves out what came before a window): position j is
+ * row j % page_size of page pages[b][j / page_size].
+ *
+ *   k_cache, v_cache  [num_pages][page_size][heads_k][D] in `dtype`, with page,
+ *           row and head strides in elements; the new tokens' own keys are in it
+ *           (convrot_cache_write).
+ *   page_size  a power of two, 16 .. 65536.
+ *   pages   device int32 [B][ld_pages], pages_per_seq entries of each row are
+ *           used, ld_pages >= pages_per_seq.  Entries that hold none of a
+ *           sequence's positions are not read.  Sequences may share pages.  An
+ *           entry that is needed and names no page is reported by
+ *           convrot_device_error (the sequence's outputs are then undefined).
+ *   seqs    as above, B of them, not NULL.
+ */
+int convrot_paged_attention(const void* q, int64_t q_row, int64_t q_head,
+                            const void* k_cache, int64_t k_page, int64_t k_row, int64_t k_head,
+                            const void* v_cache, int64_t v_page, int64_t v_row, int64_t v_head,
+                            void* out, int64_t out_row, int64_t out_head,
+                            convrot_dtype dtype, int rows, int heads_q,
+                            int heads_k, int D, int num_pages, int page_size,
+                            const int32_t* pages, int64_t ld_pages,
+                            int pages_per_seq, const int32_t* seqs, int B,
+                            float scale, int causal, cudaStream_t stream);
+
+/*
+ * Keys and values of new tokens into the pages of a cache: row q_start + i of k
+ * and v (i < q_len) goes to position k_start + k_len - q_len + i of sequence b,
+ * so that a convrot_paged_attention call with the same seqs finds them as the
+ * last q_len of its k_len keys.  q_len <= k_len.  Everything else in the cache
+ * is left as it was.
+ *
+ *   k, v    [rows][heads_k][D] in `dtype` (BF16 or FP16), row and head strides
+ *           in elements (views of the packed qkv output).
+ *   k_cache, v_cache, pages, seqs   as above; the caches overlap no input, their
+ *           heads, rows and pages do not overlap, and no two tokens of a call go
+ *           to the same place (a page that is written belongs to one sequence).
+ *           A token whose page entry names no page is left out and reported by
+ *           convrot_device_error, as is a sequence with q_len > k_len.
+ * Alignment as for convrot_attention.
+ */
+int convrot_cache_write(const void* k, int64_t k_row, int64_t k_head,
+                        const void* v, int64_t v_row, int64_t v_head,
+                        void* k_cache, int64_t kc_page, int64_t kc_row, int64_t kc_head,
+                        void* v_cache, int64_t vc_page, int64_t vc_row, int64_t vc_head,
+                        convrot_dtype dtype, int rows, int heads_k, int D,
+                        int num_pages, int page_size, const int32_t* pages,
+                        int64_t ld_pages, int pages_per_seq,
+                        const int32_t* seqs, int B, cudaStream_t stream);
+
+/*
+ * Self-test of the kernels behind convrot_attention and convrot_paged_attention:
+ * the same call (`paged` 0: k and v are rows, num_pages counts them, the page
+ * strides and page_size are not used, pages is NULL) with the kernel given
+ * instead of chosen: 1 few rows, 2 many rows, whole items, 3 many rows, shared
+ * keys; and with the CTAs that share a sequence's keys (slices 1 to 8; 1 for
+ * kernel 2).  The results agree up to roundings.  With `starve` nonzero the
+ * many-row kernels load no keys: their waits run out after about two seconds,
+ * the output is undefined, and convrot_device_error reports it.
+ */
+int convrot_attention_selftest(const void* q, int64_t q_row, int64_t q_head,
+                               const void* k, int64_t k_page, int64_t k_row, int64_t k_head,
+                               const void* v, int64_t v_page, int64_t v_row, int64_t v_head,
+                               void* out, int64_t out_row, int64_t out_head,
+                               convrot_dtype dtype, int rows, int heads_q,
+                               int heads_k, int D, int num_pages, int page_size,
+                               int paged, const int32_t* pages, int64_t ld_pages,
+                               int pages_per_seq, const int32_t* seqs, int B,
+                               float scale, int causal, int kernel, int slices,
+                               int starve, cudaStream_t stream);
+
+/*
  * W8A8 with resident weights: widens S8 codes (CONVROT_CODES_S8, e.g. weight
  * codes prepared once and kept at one byte each) into the FP16-held codes
  * that convrot_gemm reads.  Source: the NVFP4 loader entry's W8A8 comparison,
@@ -460,7 +584,11 @@ const char* convrot_last_error(void);
  * a device word and return early (their outputs are then incomplete).  This
  * call synchronises `stream`, copies the word to *code (0 = no failure),
  * clears it and returns CONVROT_ERR_DEVICE_TIMEOUT if it was set,
- * CONVROT_OK otherwise.  `code` may be NULL.
+ * CONVROT_OK otherwise.  `code` may be NULL.  Two codes are no
+ * failed waits but the attention operators' findings in their device-side
+ * arguments (same status): 16, a sequence that reaches past its tensors; 17, a
+ * page entry that names no page.  A call with such arguments touches no memory
+ * outside its tensors.
  */
 int convrot_device_error(cudaStream_t stream, int* code);
 

@@ -4,8 +4,8 @@ Argument marshalling only: every step of the layer runs in the CUDA kernels
 behind the C ABI declared in include/convrot.h.  Tensors are torch CUDA
 tensors (PyTorch supplies device memory and streams); each function passes
 their device pointers and the current stream to the library.  They have to lie
-on the current device (rms_norm_quant, qk_norm_rope and gemm_fused raise
-ValueError otherwise).  There is no CPU fallback: if the library is missing or a call fails, an exception says
+on the current device (the block operators, from rms_norm_quant to cache_write,
+raise ValueError otherwise).  There is no CPU fallback: if the library is missing or a call fails, an exception says
 so.
 """
 from __future__ import annotations
@@ -20,6 +20,7 @@ __all__ = [
     "FP32", "CODES_S8",
     "CODES_F16", "LIB_PATH", "EXPORTS",
     "rms_norm_quant", "rope_inv_freq", "qk_norm_rope", "gemm_fused", "gemm_fused_selftest",
+    "attention", "paged_attention", "cache_write", "attention_selftest", "KERNEL_FEW", "KERNEL_WHOLE", "KERNEL_SHARED",
     "ACT_NONE", "ACT_RELU", "ACT_SILU", "ACT_GELU", "ACT_GELU_TANH", "FEW_TOKENS",
 ]
 
@@ -27,12 +28,14 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libconvrot.
 BF16, FP16, FP32 = 0, 1, 2
 CODES_S8, CODES_F16 = 0, 1
 ACT_NONE, ACT_RELU, ACT_SILU, ACT_GELU, ACT_GELU_TANH = 0, 1, 2, 3, 4
+KERNEL_FEW, KERNEL_WHOLE, KERNEL_SHARED = 1, 2, 3       # attention_selftest
 FEW_TOKENS = 64          # most token rows gemm_fused takes with int8 codes
 EXPORTS = ("convrot_padded_k", "convrot_status_string", "convrot_prepare_weight",
            "convrot_quant_act", "convrot_gemm", "convrot_gemm_i32", "convrot_device_error",
            "convrot_last_error", "convrot_gemm_timeout_selftest", "convrot_widen_codes", "convrot_int8_mma_probe",
            "convrot_decode_gemm_probe", "convrot_rms_norm_quant", "convrot_rope_inv_freq", "convrot_qk_norm_rope",
-           "convrot_gemm_fused", "convrot_gemm_fused_selftest")
+           "convrot_gemm_fused", "convrot_gemm_fused_selftest", "convrot_attention", "convrot_paged_attention",
+           "convrot_cache_write", "convrot_attention_selftest")
 
 _lib = None
 _block_ops = None
@@ -89,6 +92,17 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.convrot_gemm_fused_selftest.argtypes = [vp, i64, vp, vp, i64, vp, vp, i32, vp, vp, i64, i32, i32, i32, vp, i32, i64,
                                                 i32, i32, i32, vp]
     lib.convrot_gemm_fused_selftest.restype = i32
+    row = [vp, i64, i64]
+    pages = [vp, i64, i64, i64]
+    lib.convrot_attention.argtypes = row * 4 + [i32] * 6 + [vp, i32, ctypes.c_float, i32, vp]
+    lib.convrot_attention.restype = i32
+    lib.convrot_paged_attention.argtypes = row + pages * 2 + row + [i32] * 7 + [vp, i64, i32, vp, i32, ctypes.c_float, i32, vp]
+    lib.convrot_paged_attention.restype = i32
+    lib.convrot_cache_write.argtypes = row * 2 + pages * 2 + [i32] * 6 + [vp, i64, i32, vp, i32, vp]
+    lib.convrot_cache_write.restype = i32
+    lib.convrot_attention_selftest.argtypes = (row + pages * 2 + row + [i32] * 8 + [vp, i64, i32, vp, i32, ctypes.c_float] +
+                                               [i32] * 4 + [vp])
+    lib.convrot_attention_selftest.restype = i32
     lib.convrot_last_error.argtypes = []
     lib.convrot_last_error.restype = ctypes.c_char_p
     lib.convrot_device_error.argtypes = [vp, ctypes.POINTER(i32)]
@@ -170,6 +184,8 @@ def _operators():
                torch.cuda.device_count(), _refuse, getattr(torch._C, "_cuda_getCurrentRawStream", current),
                getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device), torch.bfloat16, torch.float16,
                torch.float32, torch.float64, torch.int8, torch.int32)
+        m.bind_attention(*(ctypes.cast(f, ctypes.c_void_p).value
+                           for f in (lib.convrot_attention, lib.convrot_paged_attention, lib.convrot_cache_write)))
         _block_ops = m
     return _block_ops
 
@@ -265,6 +281,50 @@ def gemm_fused_selftest(a_q, a_scale, w_q, w_scale, out, tile: int, slices: int,
         _ptr(a_q), _ld(a_q), _ptr(a_scale), _ptr(w_q), _ld(w_q), _ptr(w_scale), _ptr(bias), int(act), _ptr(gate),
         _ptr(residual), 0 if residual is None else _ld(residual), M, N, int(a_q.shape[1]), _ptr(out), _dtype_code(out),
         _ld(out), int(tile), int(slices), int(bool(starve)), _stream(stream)))
+
+
+def attention(q, k, v, out, seqs=None, scale: float | None = None, causal: bool = False, stream=None) -> None:
+    """convrot_attention: q and out bf16/fp16 [rows, heads_q, D] views, k and v the same type [keys, heads_k, D] (values
+    of a head contiguous; heads_q a multiple of heads_k), seqs None (one sequence of all rows and keys) or int32 [B, 4]
+    of q_start, q_len, k_start, k_len, scale None (D ** -0.5) or a factor on the scores."""
+    status = (_block_ops or _operators()).attention(q, k, v, out, seqs, scale, causal, stream)
+    if status:
+        _check("convrot_attention", status)
+
+
+def paged_attention(q, k_cache, v_cache, pages, seqs, out, scale: float | None = None, causal: bool = False,
+                    stream=None) -> None:
+    """convrot_paged_attention: q and out as for attention, k_cache and v_cache [pages, page_size, heads_k, D], pages
+    int32 [B, pages per sequence], seqs int32 [B, 4] of q_start, q_len, k_start, k_len (positions in the table's
+    pages)."""
+    status = (_block_ops or _operators()).paged_attention(q, k_cache, v_cache, pages, seqs, out, scale, causal, stream)
+    if status:
+        _check("convrot_paged_attention", status)
+
+
+def cache_write(k, v, k_cache, v_cache, pages, seqs, stream=None) -> None:
+    """convrot_cache_write: k and v [rows, heads_k, D] of new tokens into the caches' pages, as the last q_len of the
+    k_len keys of their sequences; the other arguments as for paged_attention."""
+    status = (_block_ops or _operators()).cache_write(k, v, k_cache, v_cache, pages, seqs, stream)
+    if status:
+        _check("convrot_cache_write", status)
+
+
+def attention_selftest(q, k, v, out, kernel: int, slices: int = 1, pages=None, seqs=None, scale: float | None = None,
+                       causal: bool = False, starve: bool = False, stream=None) -> None:
+    """convrot_attention_selftest: attention (pages None) or paged_attention with the kernel (KERNEL_*) and the CTAs that
+    share a sequence's keys (1 to 8; 1 for KERNEL_WHOLE) given; starve: the many-row kernels' loads are off (a wait runs
+    out)."""
+    paged = pages is not None
+    caches = [(t.data_ptr(), *([t.stride(0), t.stride(1), t.stride(2)] if paged else [0, t.stride(0), t.stride(1)]))
+              for t in (k, v)]
+    scale = q.shape[2] ** -0.5 if scale is None else scale
+    dims = [k.shape[0], k.shape[1], pages.shape[1]] if paged else [k.shape[0], 0, 0]
+    _check("convrot_attention_selftest", load_library().convrot_attention_selftest(
+        _ptr(q), q.stride(0), q.stride(1), *caches[0], *caches[1], _ptr(out), out.stride(0), out.stride(1), _dtype_code(q),
+        q.shape[0], q.shape[1], k.shape[-2], q.shape[2], *dims[:2], int(paged), _ptr(pages), pages.stride(0) if paged else 0,
+        dims[2], _ptr(seqs), 1 if seqs is None else seqs.shape[0], float(scale), int(causal), int(kernel), int(slices),
+        int(starve), _stream(stream)))
 
 
 def widen_codes(src, dst, cols: int | None = None, stream=None) -> None:

@@ -1,0 +1,902 @@
+// convrot_attention and convrot_paged_attention, many rows: softmax(scale q k^T) v
+// on tcgen05, one pass over the keys.
+//
+//   s_j = scale q . k_j,  p_j = exp(s_j - m),  out = sum_j p_j v_j / sum_j p_j
+//
+// with a running reference m per row.  A CTA holds two slots of 128 rows.  Per
+// slot and tile of 128 keys the tensor core multiplies S = Q K^T (FP32, tensor
+// memory), 128 threads, one per row, turn S into weights P in the operands'
+// type (over S's own columns), and the tensor core adds P V to the slot's O
+// (FP32, tensor memory; P is read from tensor memory, V as it lies).  While one
+// slot's rows are turned, the other slot's products run, so both units are busy.
+//
+// m follows a row's maximum only once that has grown by more than 2^kLag: O and
+// the sum are then scaled (rarely after the first tile), otherwise m stays and
+// weights above one are kept as they are.  The sum adds the FP32 weights; P is
+// rounded to the operands' type for the product (half a step of that type each,
+// at random: the result's error grows by about its own rounding's).
+//
+// Rows of a slot: `pack` heads that share a K head for each of `tps` tokens (one
+// head for many tokens).  Masks are applied where a tile crosses a row's last
+// key, as selections, so what lies behind has no say; rows of V outside the
+// sequence are zeroed in shared memory (0 x NaN).
+//
+// Whole items (SPLIT false): the slots are neighbouring tiles of rows and share
+// every K and V tile; CTAs stay and take items in turn, the loads and products
+// of the next item running into the output phase of the last.  Few rows (SPLIT
+// true): both slots hold the same rows and take the key tiles in turn, and a
+// cluster of up to eight CTAs shares the keys; sums and outputs are joined
+// through distributed shared memory in a fixed order.
+#include <atomic>
+#include <cstdint>
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "../../include/convrot.h"
+#include "attention.cuh"
+#include "attention_many.cuh"
+#include "errors.h"
+#include "pdl.cuh"
+#include "tcgen05.cuh"
+
+namespace cratt {
+
+using namespace crgemm;
+
+constexpr int THREADS = 320;              // warps 0-7: rows (two slots), 8: loads, 9: products
+constexpr int MAX_SPLIT = 8;
+
+template <int DP, bool SPLIT>
+struct Layout {
+  static constexpr int TILE = KEYS * DP * 2;                 // bytes of a Q, K or V tile
+  static constexpr int BOX = KEYS * 128;                     // a 64-wide column block of it
+  static constexpr int QTILES = SPLIT ? 1 : 2;
+  static constexpr int STAGES = DP == 128 ? 5 : 8;
+  static constexpr int S_COL = 0, O_COL = 256;               // tensor memory: S of both slots, O of both slots
+  static constexpr int PITCH = DP + 4;                       // floats per row of a joined partial
+  // barriers and small things, then the tiles
+  static constexpr int ITEM = 256, STATS = 512, SUMS = STATS + 2 * 128 * 8, AUX = SPLIT ? 3072 : 1024;
+  static constexpr int SMEM = (QTILES + STAGES) * TILE + AUX + 1024;
+  static_assert(SMEM <= 232448, "shared memory");
+  static_assert((2 * STAGES + 10) * 8 + 8 <= ITEM && SUMS + 512 <= 3072, "barrier area");
+  // partials that a CTA receives: 2 slots of every CTA x its share of the 128 rows
+  static constexpr int PARTS = 2 * MAX_SPLIT * ((128 + MAX_SPLIT - 1) / MAX_SPLIT) + 2 * MAX_SPLIT;
+  static_assert(!SPLIT || PARTS * PITCH * 4 <= (QTILES + STAGES) * TILE, "joined partials");
+};
+
+// What every role needs of an item; positions count from the first tile's first key.
+struct Item {
+  int q_row, tokens;       // first row of q, rows of this item; q_row < 0: no more items
+  int head0, head_kv;
+  int base, lo, hi;        // position of key 0 of the first tile; keys lo .. hi - 1 are the sequence's
+  int see0;                // causal: the first row sees keys below see0, the next one one more
+  int seq;
+
+  // first key that token t does not see (at most lo: it sees none)
+  __device__ __forceinline__ int limit(int t, int causal) const { return causal ? min(hi, see0 + t) : hi; }
+  // tiles up to the last key that token t sees
+  __device__ __forceinline__ int tiles(int t, int causal) const {
+    const int l = limit(t, causal);
+    return l > lo ? (l + KEYS - 1) / KEYS : 0;
+  }
+};
+static_assert(sizeof(Item) <= 256, "item area");
+
+// ------------------------------------------------------------------ PTX
+__device__ __forceinline__ void load_box_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];"
+      ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z) : "memory");
+}
+__device__ __forceinline__ void load_box_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z, int w) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], [%2];"
+      ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+__device__ __forceinline__ void commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+// D (+)= A B^T, A in shared memory
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+      ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate) : "memory");
+}
+// the same, A in tensor memory (two 16-bit values per column)
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+      ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(accumulate) : "memory");
+}
+// 32 lanes x 32 columns from or to tensor memory
+__device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31},"
+      " [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+        "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
+        "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+        "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(addr));
+}
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
+      ::"r"(addr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* r) {
+  tmem_st16(addr, r);
+  tmem_st16(addr + 16, r + 16);
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+// two FP32 values at once
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 ra, rb, rc;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\tmov.b64 rc, {%6, %7};\n\t"
+      "fma.rn.f32x2 ra, ra, rb, rc;\n\tmov.b64 {%0, %1}, ra;\n\t}"
+      : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 ra, rb;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+      "add.rn.f32x2 ra, ra, rb;\n\tmov.b64 {%0, %1}, ra;\n\t}"
+      : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void st_cluster_f32x4(uint32_t addr, float a, float b, float c, float d) {
+  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(a), "f"(b), "f"(c), "f"(d) : "memory");
+}
+
+// V [128 keys][DP] as it lies (columns contiguous): 64-wide column blocks BOX
+// bytes apart, groups of 8 keys 1024 bytes apart, 128-byte swizzling.
+__device__ __forceinline__ uint64_t v_desc(uint32_t saddr, uint32_t box) {
+  uint64_t d = smem_desc_sw128(saddr) & ~(static_cast<uint64_t>(0x3FFF) << 16);
+  return d | static_cast<uint64_t>(box >> 4) << 16;
+}
+
+// ------------------------------------------------------------------ items
+struct Work {
+  int pack, tps;             // heads per tile, tokens per tile of 128 rows
+  int item_tokens;           // tokens per item: tps, or 2 tps
+};
+
+// Tiles of all sequences (a warp together).
+__device__ __forceinline__ int64_t count_tiles(const Problem& p, const Work& w, int lane, int* error) {
+  if (p.B == 1) return (load_sequence(p, 0, error).q_len + static_cast<int64_t>(w.item_tokens) - 1) / w.item_tokens;
+  int64_t n = 0;
+  for (int b = lane; b < p.B; b += 32)
+    n += (load_sequence(p, b, error).q_len + static_cast<int64_t>(w.item_tokens) - 1) / w.item_tokens;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+  return n;
+}
+
+// The sequence that holds tile `tile` and the tile's first token in it (a warp
+// together; the tile is one of count_tiles' ones).  Causal sequences go from
+// their last tile, the longest one, to the first.
+__device__ __forceinline__ void find_tile(const Problem& p, const Work& w, int64_t tile, int lane, int* error, Sequence& s,
+                                          int& b, int& token) {
+  for (int b0 = 0;; b0 += 32) {
+    Sequence mine = {0, 0, 0, 0};
+    if (b0 + lane < p.B) mine = load_sequence(p, b0 + lane, error);
+    const int64_t n = (mine.q_len + static_cast<int64_t>(w.item_tokens) - 1) / w.item_tokens;
+    int64_t upto = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += v;
+    }
+    const unsigned past = __ballot_sync(0xffffffffu, upto > tile);
+    if (past == 0 && b0 + 32 < p.B) {
+      tile -= __shfl_sync(0xffffffffu, upto, 31);
+      continue;
+    }
+    const int src = past ? __ffs(past) - 1 : 0;
+    s.q_start = __shfl_sync(0xffffffffu, mine.q_start, src);
+    s.q_len = __shfl_sync(0xffffffffu, mine.q_len, src);
+    s.k_start = __shfl_sync(0xffffffffu, mine.k_start, src);
+    s.k_len = __shfl_sync(0xffffffffu, mine.k_len, src);
+    const int64_t count = __shfl_sync(0xffffffffu, n, src);
+    int64_t at = tile - (__shfl_sync(0xffffffffu, upto, src) - count);
+    if (p.causal) at = count - 1 - at;
+    b = b0 + src;
+    token = static_cast<int>(at * w.item_tokens);
+    return;
+  }
+}
+
+// ------------------------------------------------------------------ kernel
+template <int DT, int DP, bool PAGED, bool SPLIT>
+__global__ void __launch_bounds__(THREADS, 1)
+attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+                 const __grid_constant__ CUtensorMap map_v, const __grid_constant__ Problem p, const Work w, const int slices) {
+  using L = Layout<DP, SPLIT>;
+  constexpr int STAGES = L::STAGES;
+  // FP32 accumulators; operands BF16 or FP16; M = 128, N = 128 keys or DP columns; V is not transposed (bit 16)
+  constexpr uint32_t KIND = (1u << 4) | (DT == CONVROT_BF16 ? (1u << 7) | (1u << 10) : 0u) | (static_cast<uint32_t>(128 >> 4) << 24);
+  constexpr uint32_t IDESC_S = KIND | (static_cast<uint32_t>(KEYS >> 3) << 17);
+  constexpr uint32_t IDESC_O = KIND | (static_cast<uint32_t>(DP >> 3) << 17) | (1u << 16);
+
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* aux = smem_raw + (1024 - (smem_u32(smem_raw) & 1023)) % 1024;
+  uint8_t* tiles = aux + L::AUX;
+  const uint32_t bars = smem_u32(aux);
+  const uint32_t full0 = bars, empty0 = bars + 8 * STAGES, s_full0 = empty0 + 8 * STAGES, p_full0 = s_full0 + 16,
+                 o_full0 = p_full0 + 16, q_full = o_full0 + 16, q_empty = q_full + 8, v_raw = q_full + 16, drain = q_full + 24;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(aux + (2 * STAGES + 10) * 8);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(aux + (2 * STAGES + 10) * 8 + 4);
+  Item* item = reinterpret_cast<Item*>(aux + L::ITEM);
+  const uint32_t q_tiles = smem_u32(tiles), stages = q_tiles + L::QTILES * L::TILE;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < STAGES; ++i) {
+      mbar_init(full0 + 8 * i, 1);
+      mbar_init(empty0 + 8 * i, 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(s_full0 + 8 * s, 1);
+      mbar_init(p_full0 + 8 * s, 4);
+      mbar_init(o_full0 + 8 * s, 1);
+    }
+    mbar_init(q_full, 1);
+    mbar_init(q_empty, 9);                 // the last scores' commit, and every row warp has read the item
+    mbar_init(v_raw, 1);
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 9) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(tmem_slot)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const int rank = SPLIT ? static_cast<int>(blockIdx.x % slices) : 0;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+
+  // key tiles of a SPLIT CTA: its part of those that the item's last row sees
+  auto part = [&](const Item& it, int& t0, int& t1) {
+    const int64_t n = it.tiles(it.tokens - 1, p.causal);
+    t0 = static_cast<int>(n * rank / slices);
+    t1 = static_cast<int>(n * (rank + 1) / slices);
+  };
+  // key tiles of a slot's rows otherwise
+  auto slot_tiles = [&](const Item& it, int s) {
+    const int last = min(it.tokens, (s + 1) * w.tps) - 1;
+    return last >= s * w.tps ? it.tiles(last, p.causal) : 0;
+  };
+
+  if (warp == 8) {
+    // ---------------------------------------------------------------- loads
+    const int64_t num_tiles = count_tiles(p, w, lane, &g_error);
+    const int64_t num_items = num_tiles * (p.heads_q / w.pack);
+    const int group = p.heads_q / p.heads_k;
+    const int box_rows = PAGED ? min(1 << p.page_log2, KEYS) : KEYS;
+    uint32_t stage = 0, phase = 0, raw_phase = 0;
+    uint32_t issued = 0, issued_phase = 0;       // outstanding loads, for an abort
+    bool ok = true, q_out = false, raw_out = false;
+    uint32_t n_items = 0;
+    for (int64_t i = SPLIT ? blockIdx.x / slices : blockIdx.x;; i += gridDim.x, ++n_items) {
+      const bool more = i < num_items && !(SPLIT && n_items > 0);
+      Item it = {};
+      it.q_row = -1;
+      if (more) {
+        Sequence s;
+        int token;
+        const int unit = static_cast<int>(i / num_tiles);
+        find_tile(p, w, i % num_tiles, lane, &g_error, s, it.seq, token);
+        it.q_row = s.q_start + token;
+        it.tokens = min(w.item_tokens, s.q_len - token);
+        it.head0 = unit * w.pack;
+        it.head_kv = it.head0 / group;
+        it.base = PAGED ? s.k_start / box_rows * box_rows : s.k_start;
+        it.lo = s.k_start - it.base;
+        it.hi = it.lo + s.k_len;
+        it.see0 = it.hi - s.q_len + token + 1;
+      }
+      if (n_items > 0) {
+        ok = mbar_wait(q_empty, (n_items - 1) & 1u, ERR_WAIT_EMPTY, abort_flag);
+        if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+        q_out = false;
+      }
+      if (SPLIT && n_items > 0) break;
+      if (lane == 0) {
+        *item = it;
+        if (!more) {
+          mbar_arrive_local(q_full);
+        } else {
+          const int slots = !SPLIT && it.tokens > w.tps ? 2 : 1;
+          mbar_arrive_expect_tx(q_full, slots * w.pack * w.tps * DP * 2);
+          for (int s = 0; s < slots; ++s)
+            for (int c = 0; c < DP / 64; ++c)
+              load_box_3d(q_tiles + s * L::TILE + c * L::BOX, &map_q, q_full, 64 * c, it.head0, it.q_row + s * w.tps);
+        }
+      }
+      __syncwarp();
+      if (!more) break;
+      q_out = true;
+      int t0 = 0, t1;
+      if (SPLIT) part(it, t0, t1);
+      else t1 = max(slot_tiles(it, 0), slot_tiles(it, 1));
+      // lanes 0 .. boxes-1 hold the pages of the next K tile's boxes
+      const int boxes = KEYS / box_rows;
+      auto page_of = [&](int t) {
+        const int64_t pos = static_cast<int64_t>(it.base) + static_cast<int64_t>(t) * KEYS + lane % boxes * box_rows;
+        int page = -1;
+        if (pos < static_cast<int64_t>(it.base) + it.hi)
+          page = convrot::load_global(p.pages + it.seq * p.ld_pages + (pos >> p.page_log2));
+        return page;
+      };
+      int page_next = PAGED && t0 < t1 ? page_of(t0) : 0;
+      // K or V tile t into the next stage
+      auto load = [&](bool is_v, int t) {
+        bool got = mbar_wait(empty0 + 8 * stage, phase ^ 1u, ERR_WAIT_EMPTY, abort_flag);
+        if (!__all_sync(0xffffffffu, got)) return false;
+        // a V tile with rows outside the sequence is zeroed there before anyone is told of it
+        const int first = t == 0 ? it.lo : 0, end = min(KEYS, it.hi - t * KEYS);
+        const bool ragged = is_v && (first > 0 || end < KEYS);
+        const uint32_t bar = ragged ? v_raw : full0 + 8 * stage, dst = stages + stage * L::TILE;
+        const CUtensorMap* map = is_v ? &map_v : &map_k;
+        if (!PAGED) {
+          if (lane == 0) {
+            mbar_arrive_expect_tx(bar, L::TILE);
+            for (int c = 0; c < DP / 64; ++c)
+              load_box_3d(dst + c * L::BOX, map, bar, 64 * c, it.head_kv, it.base + t * KEYS);
+          }
+        } else {
+          const int wanted = (end + box_rows - 1) / box_rows;
+          int page = is_v ? page_of(t) : page_next;
+          if (lane == 0) mbar_arrive_expect_tx(bar, wanted * box_rows * DP * 2);
+          __syncwarp();
+          const int i0 = lane % boxes;
+          if (lane < boxes * (DP / 64) && i0 < wanted) {
+            if (page < 0 || page >= p.num_pages) {
+              atomicCAS(&g_error, 0, ERR_PAGE);
+              page = p.num_pages;                  // past the last one: reads as zeros
+            }
+            const int pos = it.base + t * KEYS + i0 * box_rows, c = lane / boxes;
+            load_box_4d(dst + c * L::BOX + i0 * box_rows * 128, map, bar, 64 * c, it.head_kv,
+                        pos & ((1 << p.page_log2) - 1), page);
+          }
+          if (!is_v && t + 1 < t1) page_next = page_of(t + 1);
+        }
+        if (ragged) {
+          raw_out = true;
+          got = mbar_wait(v_raw, raw_phase, ERR_WAIT_FULL, abort_flag);
+          if (!__all_sync(0xffffffffu, got)) return false;
+          raw_out = false;
+          raw_phase ^= 1u;
+          uint8_t* tile = tiles + (L::QTILES + stage) * L::TILE;
+          const int out = first + KEYS - end;
+          for (int j = lane; j < out * 8 * (DP / 64); j += 32) {
+            const int r = j / 8 % out, row = r < first ? r : end + r - first;
+            *reinterpret_cast<uint4*>(tile + j / (8 * out) * L::BOX + row * 128 + j % 8 * 16) = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_local(full0 + 8 * stage);
+        } else {
+          issued |= 1u << stage;
+          issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
+        }
+        if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+        return true;
+      };
+      // in the order in which the products use them
+      constexpr int AHEAD = SPLIT ? 2 : 1;
+      if (p.starve) break;
+      for (int t = t0; ok && t < min(t1, t0 + AHEAD); ++t) ok = load(false, t);
+      for (int t = t0; ok && t < t1; ++t) {
+        ok = load(true, t);
+        if (ok && t + AHEAD < t1) ok = load(false, t + AHEAD);
+      }
+      if (!ok) break;
+    }
+    if (ok) {
+      // the products' last commits arrive on the empty barriers: wait for them before leaving
+      for (int i = 0; i < STAGES; ++i) {
+        if (!mbar_wait(empty0 + 8 * stage, phase ^ 1u, ERR_WAIT_EMPTY, abort_flag)) break;
+        if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+      }
+    } else {
+      // let every load still in flight land before the CTA can exit
+      const uint64_t t_start = globaltimer();
+      auto land = [&](uint32_t bar, uint32_t parity) {
+        while (!mbar_try_wait(bar, parity) && globaltimer() - t_start < kWaitLimitNs) {}
+      };
+      for (int i = 0; i < STAGES; ++i)
+        if (issued >> i & 1u) land(full0 + 8 * i, issued_phase >> i & 1u);
+      if (raw_out) land(v_raw, raw_phase);
+      if (q_out) land(q_full, n_items & 1u);
+    }
+    __syncwarp();
+    if (SPLIT) {
+      cluster_sync();
+      cluster_sync();
+    }
+  } else if (warp == 9) {
+    // ---------------------------------------------------------------- products
+    if (lane == 0) {
+      uint32_t stage = 0, phase = 0, p_phase[2] = {0, 0};
+      bool ok = true, any = false;
+      auto next_full = [&]() { return ok = ok && mbar_wait(full0 + 8 * stage, phase, ERR_WAIT_FULL, abort_flag); };
+      auto release = [&]() {
+        commit(empty0 + 8 * stage);
+        if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+      };
+      auto scores = [&](int s) {                  // S of slot s = its Q times the stage's K
+        tc_fence_after();
+        const uint64_t a = smem_desc_sw128(q_tiles + (SPLIT ? 0 : s) * L::TILE), b = smem_desc_sw128(stages + stage * L::TILE);
+#pragma unroll
+        for (int kk = 0; kk < DP / 16; ++kk) {
+          const uint64_t at = (kk / 4) * (L::BOX >> 4) + (kk % 4) * 2;
+          mma_ss(tmem + L::S_COL + s * KEYS, a + at, b + at, IDESC_S, kk > 0);
+        }
+        commit(s_full0 + 8 * s);
+        any = true;
+      };
+      auto outputs = [&](int s, bool accumulate) {   // O of slot s += its P times the stage's V
+        ok = ok && mbar_wait(p_full0 + 8 * s, p_phase[s], ERR_WAIT_ACC_FULL, abort_flag);
+        if (!ok) return;
+        p_phase[s] ^= 1u;
+        tc_fence_after();
+        const uint64_t b = v_desc(stages + stage * L::TILE, L::BOX);
+#pragma unroll
+        for (int kk = 0; kk < KEYS / 16; ++kk)
+          mma_ts(tmem + L::O_COL + s * DP, tmem + L::S_COL + s * KEYS + kk * 8, b + kk * (2048 >> 4), IDESC_O,
+                 accumulate || kk > 0);
+      };
+      for (uint32_t n_items = 0; ok; ++n_items) {
+        ok = mbar_wait(q_full, n_items & 1u, ERR_WAIT_FULL, abort_flag);
+        if (!ok) break;
+        const Item it = *item;
+        if (it.q_row < 0) break;
+        if (SPLIT) {
+          int t0, t1;
+          part(it, t0, t1);
+          const int n = t1 - t0;
+          for (int j = 0; j < min(n, 2) && next_full(); ++j) {
+            scores(j);
+            release();
+          }
+          for (int j = 0; ok && j < n; ++j) {
+            const int s = j & 1;
+            if (!next_full()) break;
+            outputs(s, j >= 2);
+            if (!ok) break;
+            if (j + 2 >= n) commit(o_full0 + 8 * s);
+            release();
+            if (j + 2 < n && next_full()) {
+              scores(s);
+              release();
+            }
+          }
+          if (ok) commit(q_empty);
+          break;
+        }
+        const int n0 = slot_tiles(it, 0), n1 = slot_tiles(it, 1), n = max(n0, n1);
+        if (n > 0 && next_full()) {
+          if (n0 > 0) scores(0);
+          if (n1 > 0) scores(1);
+          release();
+        }
+        if (ok && n <= 1) commit(q_empty);
+        for (int j = 0; ok && j < n; ++j) {
+          if (!next_full()) break;
+          // both slots' outputs use this stage, both slots' next scores the one after it
+          const uint32_t v_stage = stage, v_phase = phase;
+          const uint32_t k_stage = stage + 1 == STAGES ? 0 : stage + 1, k_phase = stage + 1 == STAGES ? phase ^ 1u : phase;
+          const bool more = j + 1 < n;
+          bool k_here = false;
+          for (int s = 0; ok && s < 2; ++s) {
+            const int ns = s ? n1 : n0;
+            stage = v_stage;
+            phase = v_phase;
+            if (j < ns) {
+              outputs(s, j > 0);
+              if (!ok) break;
+              if (j + 1 == ns) commit(o_full0 + 8 * s);
+            }
+            if (s == 1) commit(empty0 + 8 * v_stage);
+            stage = k_stage;
+            phase = k_phase;
+            if (j + 1 < ns) {
+              if (!k_here && !next_full()) break;
+              k_here = true;
+              scores(s);
+            }
+          }
+          if (!ok) break;
+          if (more) {
+            release();
+            if (j + 2 == n) commit(q_empty);
+          }
+        }
+      }
+      if (!ok && any) {
+        // wait for the tensor core to finish everything issued before its memory is freed
+        commit(drain);
+        const uint64_t t0 = globaltimer();
+        while (!mbar_try_wait(drain, 0) && globaltimer() - t0 < kWaitLimitNs) {}
+      }
+    }
+    __syncwarp();
+    if (SPLIT) {
+      cluster_sync();
+      cluster_sync();
+    }
+  } else {
+    // ---------------------------------------------------------------- rows
+    const int slot = warp >> 2, row = (warp & 3) * 32 + lane;
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t s_addr = tmem + lanes + L::S_COL + slot * KEYS, o_addr = tmem + lanes + L::O_COL + slot * DP;
+    const int my_token = row / w.pack + (SPLIT ? 0 : slot * w.tps), my_head = row % w.pack;
+    const bool held = row < w.pack * w.tps;
+    const float2 c2 = make_float2(p.scale_log2, p.scale_log2);
+    uint32_t s_phase = 0, o_phase = 0;
+    bool ok = true;
+    for (uint32_t n_items = 0; ok; ++n_items) {
+      ok = __all_sync(0xffffffffu, mbar_wait(q_full, n_items & 1u, ERR_WAIT_FULL, abort_flag));
+      Item it = {};
+      it.q_row = -1;
+      if (ok) it = *item;
+      __syncwarp();
+      if (lane == 0) mbar_arrive_local(q_empty);
+      int t0 = 0, t1 = 0, step = 1;
+      if (it.q_row >= 0) {
+        if (SPLIT) {
+          part(it, t0, t1);
+          t0 += slot;
+          step = 2;
+        } else {
+          t1 = slot_tiles(it, slot);
+        }
+      } else if (!SPLIT) {
+        break;
+      }
+      const int limit = it.limit(my_token, p.causal);
+      // tiles that some row of the slot sees in part
+      const int whole = it.limit(SPLIT ? 0 : slot * w.tps, p.causal) / KEYS;
+      float m = -INFINITY, l0 = 0.f, l1 = 0.f;             // reference and sum (in two parts) of this row
+      const bool any = t0 < t1;
+      for (int t = t0; t < t1; t += step) {
+        ok = __all_sync(0xffffffffu, mbar_wait(s_full0 + 8 * slot, s_phase, ERR_WAIT_ACC_FULL, abort_flag));
+        if (!ok) break;
+        s_phase ^= 1u;
+        tc_fence_after();
+        float x[KEYS];
+#pragma unroll
+        for (int c = 0; c < KEYS / 32; ++c) tmem_ld32(s_addr + 32 * c, reinterpret_cast<uint32_t*>(x) + 32 * c);
+        tmem_ld_wait();
+        if (t >= whole || (t == 0 && it.lo > 0)) {
+          const int end = limit - t * KEYS, first = t == 0 ? it.lo : 0;
+#pragma unroll
+          for (int j = 0; j < KEYS; ++j)
+            if (j >= end || j < first) x[j] = -INFINITY;
+        }
+        float top[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) top[i] = max3(x[i], x[4 + i], x[8 + i]);
+#pragma unroll
+        for (int j = 12; j < 124; j += 8)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) top[i] = max3(top[i], x[j + i], x[j + 4 + i]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) top[i] = fmaxf(top[i], x[124 + i]);
+        const float now = fmaxf(fmaxf(m, fmaxf(top[0], top[1])), fmaxf(top[2], top[3]));
+        if (t == t0) {
+          m = now;                                        // nothing summed yet
+        } else if (__any_sync(0xffffffffu, (now - m) * p.scale_log2 > kLag)) {
+          const float f = now == m ? 1.f : exp2_approx((m - now) * p.scale_log2);
+          m = now;
+          l0 *= f;
+          l1 *= f;
+#pragma unroll 1
+          for (int c = 0; c < DP / 32; ++c) {
+            uint32_t o[32];
+            tmem_ld32(o_addr + 32 * c, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+            tmem_st32(o_addr + 32 * c, o);
+          }
+        }
+        // a row that has seen no key yet keeps -inf, its weights are exp2(-inf) = 0
+        const float ref = kLift<DT> - (m == -INFINITY ? 0.f : m * p.scale_log2);
+        const float2 r2 = make_float2(ref, ref);
+        float2 sum = make_float2(l0, l1);
+#pragma unroll
+        for (int c = 0; c < KEYS / 32; ++c) {
+          uint32_t packed[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            float2 e = fma2(make_float2(x[32 * c + 2 * j], x[32 * c + 2 * j + 1]), c2, r2);
+            e.x = exp2_approx(e.x);
+            e.y = exp2_approx(e.y);
+            sum = add2(sum, e);
+            packed[j] = pack2<DT>(e.x, e.y);
+          }
+          tmem_st16(s_addr + 16 * c, packed);
+        }
+        l0 = sum.x;
+        l1 = sum.y;
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_local(p_full0 + 8 * slot);
+      }
+      if (ok && any) {
+        ok = __all_sync(0xffffffffu, mbar_wait(o_full0 + 8 * slot, o_phase, ERR_WAIT_ACC_FULL, abort_flag));
+        o_phase ^= 1u;
+        tc_fence_after();
+      }
+      const float l = l0 + l1;
+      const bool mine = ok && it.q_row >= 0 && held && my_token < it.tokens;
+      char* const out_row = static_cast<char*>(p.out) +
+                            2 * ((static_cast<int64_t>(it.q_row) + my_token) * p.out_tok + (it.head0 + my_head) * p.out_head);
+      if constexpr (!SPLIT) {
+        if (!ok) break;
+        const float f = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll 1
+        for (int c = 0; c < DP / 32; ++c) {
+          uint32_t o[32];
+          if (any) {
+            tmem_ld32(o_addr + 32 * c, o);
+            tmem_ld_wait();
+          }
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            uint32_t v[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float a = __uint_as_float(o[8 * g + 2 * j]) * f, b = __uint_as_float(o[8 * g + 2 * j + 1]) * f;
+              v[j] = !any || l == 0.f ? 0u : pack2<DT>(a, b);
+            }
+            if (mine && 32 * c + 8 * g < p.D) store_global(out_row + 64 * c + 16 * g, make_uint4(v[0], v[1], v[2], v[3]));
+          }
+        }
+        tc_fence_before();          // these reads before the next item's products, which wait for this warp's weights
+      } else {
+        // Join: every slot of the cluster's CTAs holds a part of the keys for the same rows.
+        float2* stats = reinterpret_cast<float2*>(aux + L::STATS);
+        float* inverse = reinterpret_cast<float*>(aux + L::SUMS);
+        stats[slot * 128 + row] = make_float2(any ? m : -INFINITY, any ? l : 0.f);
+        cluster_sync();              // statistics are there, and all tiles have been used
+        float top = -INFINITY, total = 0.f;
+        for (int i = 0; i < 2 * slices; ++i) {
+          const uint32_t a = map_to_rank(smem_u32(stats + (i & 1) * 128 + row), i >> 1);
+          const float mi = ld_cluster_f32(a), li = ld_cluster_f32(a + 4), high = fmaxf(top, mi);
+          if (high == -INFINITY) {                        // no key so far (or nothing but NaN)
+            total += li;
+            continue;
+          }
+          total = total * exp2_approx((top - high) * p.scale_log2) + li * exp2_approx((mi - high) * p.scale_log2);
+          top = high;
+        }
+        const float f = m == -INFINITY ? 0.f : exp2_approx((m - top) * p.scale_log2);
+        if (slot == 0) inverse[row] = total == 0.f ? 0.f : 1.f / total;
+        const int rows = (128 + slices - 1) / slices, source = 2 * rank + slot;
+        const uint32_t to = map_to_rank(smem_u32(tiles) + ((source * rows + row / slices) * L::PITCH) * 4, row % slices);
+#pragma unroll 1
+        for (int c = 0; c < DP / 32; ++c) {
+          uint32_t o[32];
+          if (ok && any) {
+            tmem_ld32(o_addr + 32 * c, o);
+            tmem_ld_wait();
+          }
+          if (mine) {
+#pragma unroll
+            for (int j = 0; j < 32; j += 4) {
+              const float z = any ? f : 0.f;
+              auto at = [&](int i) { return any ? __uint_as_float(o[i]) * z : 0.f; };
+              st_cluster_f32x4(to + (32 * c + j) * 4, at(j), at(j + 1), at(j + 2), at(j + 3));
+            }
+          }
+        }
+        cluster_sync();              // and the partial outputs
+        if (ok && it.q_row >= 0) {
+          const float* partial = reinterpret_cast<const float*>(tiles);
+          for (int i = threadIdx.x; i < rows * (DP / 8); i += 256) {
+            const int local = i / (DP / 8), col = i % (DP / 8) * 8, r = local * slices + rank;
+            const int token = r / w.pack, head = it.head0 + r % w.pack;
+            if (r >= w.pack * w.tps || token >= it.tokens || col >= p.D) continue;      // (rows past 128 too)
+            float y[8] = {};
+            for (int from = 0; from < 2 * slices; ++from) {
+              const float* src = partial + (from * rows + local) * L::PITCH + col;
+#pragma unroll
+              for (int j = 0; j < 8; ++j) y[j] += src[j];
+            }
+            const float z = inverse[r];                     // 0: a row that sees no key
+            if (z == 0.f) {
+#pragma unroll
+              for (int j = 0; j < 8; ++j) y[j] = 0.f;
+            }
+            char* dst = static_cast<char*>(p.out) +
+                        2 * ((static_cast<int64_t>(it.q_row) + token) * p.out_tok + head * p.out_head + col);
+            store_global(dst, make_uint4(pack2<DT>(y[0] * z, y[1] * z), pack2<DT>(y[2] * z, y[3] * z),
+                                         pack2<DT>(y[4] * z, y[5] * z), pack2<DT>(y[6] * z, y[7] * z)));
+          }
+        }
+        break;
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (SPLIT) cluster_sync();
+  tc_fence_after();
+  if (warp == 9) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+}
+
+// ------------------------------------------------------------------ host side
+// Boxes of 64 columns x heads x rows (x pages): strides of dimensions with one element do not count.
+template <int DT>
+static bool make_map(CUtensorMap* map, const void* base, int D, const int64_t (&dims)[3], const int64_t (&strides)[3], int rank,
+                     int box_heads, int box_rows) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t size[4] = {static_cast<cuuint64_t>(D)}, pitch[3];
+  for (int i = 0; i < rank - 1; ++i) {
+    size[i + 1] = static_cast<cuuint64_t>(dims[i] > 0 ? dims[i] : 1);
+    pitch[i] = static_cast<cuuint64_t>(dims[i] > 1 ? strides[i] : D) * 2;
+  }
+  cuuint32_t box[4] = {64, static_cast<cuuint32_t>(box_heads), static_cast<cuuint32_t>(box_rows), 1}, one[4] = {1, 1, 1, 1};
+  return fn(map, DT == CONVROT_FP16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+            static_cast<cuuint32_t>(rank), const_cast<void*>(base), size, pitch, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+constexpr int kMaxDevices = 64;
+
+// Clusters of `slices` CTAs of this kernel that are resident at once (0: none of this size).
+template <int DT, int DP, bool PAGED, bool SPLIT>
+static cudaError_t resident_clusters(int slices, int* out) {
+  static std::atomic<int> known[kMaxDevices][MAX_SPLIT + 1] = {};    // 0: not set up (two threads may both do it)
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  int n = dev < kMaxDevices ? known[dev][slices].load() : 0;
+  if (n == 0) {
+    auto k = attention_kernel<DT, DP, PAGED, SPLIT>;
+    constexpr int smem = Layout<DP, SPLIT>::SMEM;
+    if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return e;
+    int sms = 0;
+    if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
+    n = sms;
+    if (slices > 1) {
+      cudaLaunchConfig_t cfg = {};
+      cudaLaunchAttribute attr[1];
+      attr[0].id = cudaLaunchAttributeClusterDimension;
+      attr[0].val.clusterDim.x = slices;
+      attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+      cfg.blockDim = dim3(THREADS);
+      cfg.dynamicSmemBytes = smem;
+      cfg.gridDim = dim3(sms / slices * slices);
+      cfg.attrs = attr;
+      cfg.numAttrs = 1;
+      e = cudaOccupancyMaxActiveClusters(&n, k, &cfg);
+      if (e != cudaSuccess || n <= 0) {
+        (void)cudaGetLastError();
+        n = -1;
+      }
+    }
+    if (dev < kMaxDevices) known[dev][slices] = n;
+  }
+  *out = n > 0 ? n : 0;
+  return cudaSuccess;
+}
+
+template <int DT, int DP, bool PAGED, bool SPLIT>
+static int launch(const Problem& p, const Work& w, int slices, int64_t items, cudaStream_t st) {
+  using L = Layout<DP, SPLIT>;
+  static_assert(L::SMEM >= L::AUX + (L::QTILES + L::STAGES) * L::TILE + 1023, "shared memory");
+  CUtensorMap mq, mk, mv;
+  const int64_t q_dims[3] = {p.heads_q, p.rows, 1}, q_strides[3] = {p.q_head, p.q_tok, 0};
+  bool made = make_map<DT>(&mq, p.q, p.D, q_dims, q_strides, 3, w.pack, w.tps);
+  for (int i = 0; i < 2 && made; ++i) {
+    const void* base = i ? p.v : p.k;
+    const int64_t row = i ? p.v_row : p.k_row, head = i ? p.v_head : p.k_head, page = i ? p.v_page : p.k_page;
+    if (PAGED) {
+      const int size = 1 << p.page_log2;
+      const int64_t dims[3] = {p.heads_k, size, p.num_pages}, strides[3] = {head, row, page};
+      made = make_map<DT>(i ? &mv : &mk, base, p.D, dims, strides, 4, 1, size < KEYS ? size : KEYS);
+    } else {
+      const int64_t dims[3] = {p.heads_k, p.keys, 1}, strides[3] = {head, row, 0};
+      made = make_map<DT>(i ? &mv : &mk, base ? base : p.q, p.D, dims, strides, 3, 1, KEYS);
+    }
+  }
+  if (!made) return convrot::record_error("cuTensorMapEncodeTiled failed for q, k or v");
+  int resident = 0;
+  cudaError_t e = resident_clusters<DT, DP, PAGED, SPLIT>(slices, &resident);
+  if (e != cudaSuccess) return convrot::record_cuda_error("attention set-up", e);
+  if (resident <= 0) return CONVROT_ERR_UNSUPPORTED;
+  const int64_t clusters = SPLIT ? items : items < resident ? items : resident;
+  if (clusters * slices > INT32_MAX) return CONVROT_ERR_UNSUPPORTED;
+  e = convrot::launch_after(attention_kernel<DT, DP, PAGED, SPLIT>, dim3(static_cast<unsigned>(clusters * slices)), THREADS,
+                            L::SMEM, slices, st, mq, mk, mv, p, w, slices);
+  return e == cudaSuccess ? CONVROT_OK : convrot::record_cuda_error("attention launch", e);
+}
+
+// Items of `tokens` tokens each that the sequences can have at most.
+static int64_t most_items(const Problem& p, int tokens) {
+  const int64_t rows = p.rows, B = p.B;
+  return B == 1 ? (rows + tokens - 1) / tokens : (rows + B * (tokens - 1)) / tokens;
+}
+
+template <int DT, int DP, bool PAGED>
+static int choose(const Problem& p, const Variant& variant, cudaStream_t st) {
+  const int group = p.heads_q / p.heads_k;
+  // Lengths are on the device: every sequence is taken for an average one, with
+  // the whole table in use.
+  const double q = static_cast<double>(p.rows) / p.B, k = p.seqs && !p.pages ? static_cast<double>(p.keys) / p.B : p.keys;
+  const double key_tiles = k > KEYS ? k / KEYS : 1;
+  Work best = {1, KEYS, 2 * KEYS};
+  int slices = 0;                            // 0: whole items
+  double least = 0;
+  auto consider = [&](int pack, int n, int resident) {
+    const Work w = {pack, KEYS / pack, (n ? 1 : 2) * (KEYS / pack)};
+    const double per = q / w.item_tokens, items = p.B * (per > 1 ? per : 1) * (p.heads_q / pack);
+    const double rounds = items > resident ? items / resident : 1;
+    // Microseconds.
+    const double t = n ? rounds * (key_tiles / n * 0.6 + 5.0 + (n > 1 ? 2.0 : 0.0)) : rounds * (key_tiles * 1.15 + 3.0);
+    if (least == 0 || t < least) {
+      least = t;
+      best = w;
+      slices = n;
+    }
+  };
+  for (int pack : {1, group}) {
+    if (pack > KEYS) break;
+    for (int n = 0; n <= MAX_SPLIT; ++n) {             // 0: whole items
+      if (variant.kernel == WHOLE && n != 0) break;
+      if (variant.kernel == SHARED && n != variant.slices) continue;
+      int resident = 0;
+      const cudaError_t e = n ? resident_clusters<DT, DP, PAGED, true>(n, &resident)
+                              : resident_clusters<DT, DP, PAGED, false>(1, &resident);
+      if (e != cudaSuccess) return convrot::record_cuda_error("attention set-up", e);
+      if (resident > 0) consider(pack, n, resident);
+    }
+    if (group == 1) break;
+  }
+  const int64_t items = most_items(p, best.item_tokens) * (p.heads_q / best.pack);
+  return slices ? launch<DT, DP, PAGED, true>(p, best, slices, items, st) : launch<DT, DP, PAGED, false>(p, best, 1, items, st);
+}
+
+// This file is compiled once per type of q, k and v (CONVROT_ATTENTION_TYPE).
+#ifndef CONVROT_ATTENTION_TYPE
+#error "compile with -DCONVROT_ATTENTION_TYPE=<convrot_dtype>"
+#endif
+
+template <>
+int attention_many<CONVROT_ATTENTION_TYPE>(const Problem& p, const Variant& variant, cudaStream_t st) {
+  constexpr int DT = CONVROT_ATTENTION_TYPE;
+  if (p.pages) return p.D <= 64 ? choose<DT, 64, true>(p, variant, st) : choose<DT, 128, true>(p, variant, st);
+  return p.D <= 64 ? choose<DT, 64, false>(p, variant, st) : choose<DT, 128, false>(p, variant, st);
+}
+
+template <>
+cudaError_t take_attention_error<CONVROT_ATTENTION_TYPE>(int* v) { return crgemm::take_error_word(v); }
+
+}  // namespace cratt

@@ -1,0 +1,92 @@
+// Shared by the attention kernels: the problem of one call, the sequences that
+// it is made of, and the key ranges that a row sees.
+#pragma once
+
+#include <cstdint>
+#include <cuda_runtime.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "../../include/convrot.h"
+#include "pdl.cuh"
+
+namespace cratt {
+
+constexpr int KEYS = 128;                 // keys of a tile of the many-row kernel
+constexpr int MAX_D = CONVROT_MAX_ATT_HEAD;
+
+// Codes in the device error word (beside the waits' own): an entry of `seqs`
+// reaches past its tensors, or a needed entry of `pages` names no page.
+enum : int { ERR_SEQUENCE = 16, ERR_PAGE = 17 };
+
+// Keys and values: rows (pages == nullptr: row, head strides) or pages (page,
+// row, head strides), all in elements.
+struct Problem {
+  const void *q, *k, *v;
+  void* out;
+  int64_t q_tok, q_head, out_tok, out_head;
+  int64_t k_page, k_row, k_head, v_page, v_row, v_head;
+  const int4* seqs;                       // nullptr: one sequence, all rows and keys
+  const int32_t* pages;
+  int64_t ld_pages;
+  int rows, keys;                         // rows of q; rows of k, or positions that a row of the table holds
+  int heads_q, heads_k, D, B;
+  int page_log2, num_pages;
+  float scale_log2;                       // scale * log2(e)
+  int causal;
+  int starve;                             // self-test: no key tile is loaded
+};
+
+// One sequence: rows and keys as in seqs; all zero (no rows) if out of range.
+struct Sequence {
+  int q_start, q_len, k_start, k_len;
+};
+
+__device__ __forceinline__ Sequence load_sequence(const Problem& p, int b, int* error) {
+  if (!p.seqs) return {0, p.rows, 0, p.keys};
+  int4 s;
+  asm volatile("ld.global.v4.s32 {%0, %1, %2, %3}, [%4];" : "=r"(s.x), "=r"(s.y), "=r"(s.z), "=r"(s.w) : "l"(p.seqs + b));
+  if (s.x < 0 || s.y < 0 || s.z < 0 || s.w < 0 || s.x > p.rows || s.y > p.rows - s.x || s.z > p.keys || s.w > p.keys - s.z) {
+    atomicCAS(error, 0, ERR_SEQUENCE);
+    return {0, 0, 0, 0};
+  }
+  return {s.x, s.y, s.z, s.w};
+}
+
+// Keys that token i of the sequence sees: the first n of them (none if n <= 0).
+__device__ __forceinline__ int seen(const Problem& p, const Sequence& s, int i) {
+  return p.causal ? min(s.k_len, s.k_len - s.q_len + i + 1) : s.k_len;
+}
+
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Weights are held in the operands' type for the second product, as powers of
+// two around the running maximum: at most 2^kLag above it (the maximum is only
+// followed once it has grown by more).  FP16's narrow range gets them 2^6 higher
+// (at most 2^14), which puts its subnormals below 2^-20 of the largest weight;
+// the factor leaves with the sum.
+constexpr float kLag = 8.f;
+template <int DT>
+constexpr float kLift = DT == CONVROT_FP16 ? 6.f : 0.f;
+
+template <int DT>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi);
+template <> __device__ __forceinline__ uint32_t pack2<CONVROT_BF16>(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+template <> __device__ __forceinline__ uint32_t pack2<CONVROT_FP16>(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// 16 bytes of outputs.
+__device__ __forceinline__ void store_global(void* p, uint4 v) {
+  asm volatile("st.global.v4.b32 [%0], {%1, %2, %3, %4};" ::"l"(p), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
+}  // namespace cratt

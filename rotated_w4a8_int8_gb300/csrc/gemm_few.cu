@@ -413,7 +413,9 @@ cudaError_t take_fused_error_word(int* v) {
   cudaError_t e = crfused::take_fused_error_word<CONVROT_BF16>(&each[0]);
   if (e == cudaSuccess) e = crfused::take_fused_error_word<CONVROT_FP16>(&each[1]);
   if (e == cudaSuccess) e = crfused::take_fused_error_word<CONVROT_FP32>(&each[2]);
-  *v = each[0] ? each[0] : each[1] ? each[1] : each[2];
+  int attention = 0;
+  if (e == cudaSuccess) e = take_attention_error_word(&attention);
+  *v = each[0] ? each[0] : each[1] ? each[1] : each[2] ? each[2] : attention;
   return e;
 }
 }  // namespace convrot

@@ -1,6 +1,7 @@
 /*
  * Argument marshalling of the block operators' Python entry points
- * (rms_norm_quant, qk_norm_rope, gemm_fused) on the CPython C API: takes
+ * (rms_norm_quant, qk_norm_rope, gemm_fused, attention, paged_attention,
+ * cache_write) on the CPython C API: takes
  * pointers, shapes and pitches of torch tensors through their Python
  * attributes, refuses what does not fit, and calls the C ABI.  A call of these
  * operators on one token costs the host more than the GPU: checked and
@@ -19,10 +20,21 @@ typedef int (*rope_fn)(const void*, int64_t, int64_t, void*, int64_t, int64_t, i
                        const int*, int, const double*, float, int, void*);
 typedef int (*gemm_fn)(const void*, int64_t, const float*, const void*, int64_t, const float*, int, const float*, int,
                        const float*, const void*, int64_t, int, int, int, void*, int, int64_t, void*);
+typedef int (*attention_fn)(const void*, int64_t, int64_t, const void*, int64_t, int64_t, const void*, int64_t, int64_t,
+                            void*, int64_t, int64_t, int, int, int, int, int, int, const int32_t*, int, float, int, void*);
+typedef int (*paged_fn)(const void*, int64_t, int64_t, const void*, int64_t, int64_t, int64_t, const void*, int64_t,
+                        int64_t, int64_t, void*, int64_t, int64_t, int, int, int, int, int, int, int, const int32_t*, int64_t,
+                        int, const int32_t*, int, float, int, void*);
+typedef int (*write_fn)(const void*, int64_t, int64_t, const void*, int64_t, int64_t, void*, int64_t, int64_t, int64_t,
+                        void*, int64_t, int64_t, int64_t, int, int, int, int, int, int, const int32_t*, int64_t, int,
+                        const int32_t*, int, void*);
 
 static norm_fn call_norm;
 static rope_fn call_rope;
 static gemm_fn call_gemm;
+static attention_fn call_attention;
+static paged_fn call_paged;
+static write_fn call_write;
 static int gpus;                                              /* GPUs that torch sees */
 static PyObject *refuse, *raw_stream, *current_device;        /* Python callables */
 static PyObject *dt_bf16, *dt_fp16, *dt_fp32, *dt_fp64, *dt_int8, *dt_int32;
@@ -399,6 +411,200 @@ static PyObject* gemm_fused(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   return PyLong_FromLong(status);
 }
 
+/* The type of q, k and v: bfloat16 or float16. */
+static int head_type(const char* fn, const char* name, PyObject* t, PyObject** dtype) {
+  *dtype = dtype_of(t);
+  if (*dtype && *dtype == dt_bf16) return 0;
+  if (*dtype && *dtype == dt_fp16) return 1;
+  return refusal(fn, name, t, PyUnicode_FromString("bfloat16 or float16"));
+}
+
+/* Rows and head width of q or k [rows, heads, D]. */
+static int rows_and_width(const char* fn, const char* name, PyObject* t, int* rows, int* D) {
+  long long shape[3];
+  const int d = shape_of(t, shape, 3);
+  if (d < 0) return -1;
+  if (d != 3 || shape[0] != (int)shape[0] || shape[2] != (int)shape[2])
+    return refusal(fn, name, t, PyUnicode_FromString("[rows, heads, head width]"));
+  *rows = (int)shape[0];
+  *D = (int)shape[2];
+  return 0;
+}
+
+/* seqs int32 [B, 4], contiguous: the pointer (NULL: None) and B. */
+static int sequences(const char* fn, PyObject* t, int needed, void** out, int* B) {
+  *out = NULL;
+  *B = 1;
+  if (t == Py_None && !needed) return 0;
+  long long shape[2];
+  const int d = t == Py_None ? 0 : shape_of(t, shape, 2);
+  if (d < 0) return -1;
+  if (d != 2 || shape[1] != 4 || shape[0] != (int)shape[0]) {
+    if (t == Py_None) {
+      PyErr_Format(PyExc_ValueError, "%s: seqs is needed", fn);
+      return -1;
+    }
+    return refusal(fn, "seqs", t, PyUnicode_FromString("int32 [sequences, 4]"));
+  }
+  *B = (int)shape[0];
+  return vector(fn, "seqs", t, 4 * shape[0], dt_int32, out);
+}
+
+typedef struct {
+  void* ptr;
+  int64_t page, row, head;
+  int pages, size, heads;
+} cache_t;
+
+/* [pages, page size, heads, D] of `dtype` on the device, a head's values contiguous; `like` gives the other sizes. */
+static int cache(const char* fn, const char* name, PyObject* t, long long D, PyObject* dtype, const cache_t* like,
+                 cache_t* out) {
+  long long shape[4], stride[4], p;
+  const int d = shape_of(t, shape, 4);
+  if (d < 0) return -1;
+  if (d == 4 && shape[3] == D && shape[0] == (int)shape[0] && shape[1] == (int)shape[1] && shape[2] == (int)shape[2] &&
+      (!like || (shape[0] == like->pages && shape[1] == like->size && shape[2] == like->heads)) && dtype_of(t) == dtype &&
+      is_cuda(t) == 1) {
+    if (ints(PyObject_CallMethodNoArgs(t, s_stride), stride, 4) != 4) return -1;
+    if (stride[3] == 1 || D <= 1) {
+      if (method_ll(t, s_data_ptr, &p)) return -1;
+      out->ptr = (void*)(uintptr_t)p;
+      out->page = stride[0];
+      out->row = stride[1];
+      out->head = stride[2];
+      out->pages = (int)shape[0];
+      out->size = (int)shape[1];
+      out->heads = (int)shape[2];
+      return 0;
+    }
+  }
+  return refusal(fn, name, t, PyUnicode_FromFormat("a %S CUDA tensor [pages, page size, heads, %lld], contiguous heads, k's "
+                                                   "and v's of the same sizes", dtype, D));
+}
+
+/* pages int32 [B, >= 0]: the table and its width. */
+static int page_table(const char* fn, PyObject* t, int B, matrix_t* out, int* per_seq) {
+  long long shape[2];
+  const int d = shape_of(t, shape, 2);
+  if (d < 0) return -1;
+  if (d != 2 || shape[1] != (int)shape[1])
+    return refusal(fn, "pages", t, PyUnicode_FromString("int32 [sequences, pages per sequence]"));
+  *per_seq = (int)shape[1];
+  return matrix(fn, "pages", t, B, shape[1], dt_int32, out);
+}
+
+/* The factor on the scores; None is D ** -0.5 (Newton's iteration, no libm). */
+static int to_scale(PyObject* o, int D, float* v) {
+  if (o != Py_None) return to_float(o, v);
+  double root = D > 0 ? D : 1;
+  for (int i = 0; i < 40; ++i) root = 0.5 * (root + (D > 0 ? D : 1) / root);
+  *v = (float)(1 / root);
+  return 0;
+}
+
+/* (q, k, v, out, seqs, scale, causal, stream) -> status */
+static PyObject* attention(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  (void)self;
+  const char* fn = "attention";
+  int rows, keys, D, width, dtype, B, dev, status;
+  float scale;
+  PyObject* dt;
+  heads_t q, k, v, out;
+  void *seqs, *st;
+  if (want(n, 8)) return NULL;
+  const int causal = PyObject_IsTrue(a[6]);
+  if (causal < 0 || rows_and_width(fn, "q", a[0], &rows, &D) || rows_and_width(fn, "k", a[1], &keys, &width) ||
+      (dtype = head_type(fn, "q", a[0], &dt)) < 0 || heads(fn, "q", a[0], rows, D, dt, NULL, &q) ||
+      heads(fn, "k", a[1], keys, D, dt, NULL, &k) || heads(fn, "v", a[2], keys, D, dt, &k, &v) ||
+      heads(fn, "out", a[3], rows, D, dt, &q, &out) || sequences(fn, a[4], 0, &seqs, &B) || to_scale(a[5], D, &scale))
+    return NULL;
+  if (a[2] == Py_None || a[3] == Py_None) {
+    PyErr_Format(PyExc_ValueError, "%s: v and out are needed", fn);
+    return NULL;
+  }
+  static const char* const names[] = {"q", "k", "v", "out", "seqs"};
+  if (device_of(fn, a, names, 5, &dev) || stream_of(dev, a[7], &st)) return NULL;
+  Py_BEGIN_ALLOW_THREADS                         /* a launch waits while the launch queue is full */
+  status = call_attention(q.ptr, q.tok, q.head, k.ptr, k.tok, k.head, v.ptr, v.tok, v.head, out.ptr, out.tok, out.head,
+                          dtype, rows, keys, q.heads, k.heads, D, seqs, B, scale, causal, st);
+  Py_END_ALLOW_THREADS
+  return PyLong_FromLong(status);
+}
+
+/* (q, k_cache, v_cache, pages, seqs, out, scale, causal, stream) -> status */
+static PyObject* paged_attention(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  (void)self;
+  const char* fn = "paged_attention";
+  int rows, D, dtype, B, per_seq, dev, status;
+  float scale;
+  PyObject* dt;
+  heads_t q, out;
+  cache_t k, v;
+  matrix_t pages;
+  void *seqs, *st;
+  if (want(n, 9)) return NULL;
+  const int causal = PyObject_IsTrue(a[7]);
+  if (causal < 0 || rows_and_width(fn, "q", a[0], &rows, &D) || (dtype = head_type(fn, "q", a[0], &dt)) < 0 ||
+      heads(fn, "q", a[0], rows, D, dt, NULL, &q) || cache(fn, "k_cache", a[1], D, dt, NULL, &k) ||
+      cache(fn, "v_cache", a[2], D, dt, &k, &v) || sequences(fn, a[4], 1, &seqs, &B) ||
+      page_table(fn, a[3], B, &pages, &per_seq) || heads(fn, "out", a[5], rows, D, dt, &q, &out) || to_scale(a[6], D, &scale))
+    return NULL;
+  if (a[5] == Py_None) {
+    PyErr_Format(PyExc_ValueError, "%s: out is needed", fn);
+    return NULL;
+  }
+  static const char* const names[] = {"q", "k_cache", "v_cache", "pages", "seqs", "out"};
+  if (device_of(fn, a, names, 6, &dev) || stream_of(dev, a[8], &st)) return NULL;
+  Py_BEGIN_ALLOW_THREADS                         /* a launch waits while the launch queue is full */
+  status = call_paged(q.ptr, q.tok, q.head, k.ptr, k.page, k.row, k.head, v.ptr, v.page, v.row, v.head, out.ptr, out.tok,
+                      out.head, dtype, rows, q.heads, k.heads, D, k.pages, k.size, pages.ptr, pages.ld, per_seq, seqs, B,
+                      scale, causal, st);
+  Py_END_ALLOW_THREADS
+  return PyLong_FromLong(status);
+}
+
+/* (k, v, k_cache, v_cache, pages, seqs, stream) -> status */
+static PyObject* cache_write(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  (void)self;
+  const char* fn = "cache_write";
+  int rows, D, dtype, B, per_seq, dev, status;
+  PyObject* dt;
+  heads_t k, v;
+  cache_t kc, vc;
+  matrix_t pages;
+  void *seqs, *st;
+  if (want(n, 7)) return NULL;
+  if (rows_and_width(fn, "k", a[0], &rows, &D) || (dtype = head_type(fn, "k", a[0], &dt)) < 0 ||
+      heads(fn, "k", a[0], rows, D, dt, NULL, &k) || heads(fn, "v", a[1], rows, D, dt, &k, &v) ||
+      cache(fn, "k_cache", a[2], D, dt, NULL, &kc) || cache(fn, "v_cache", a[3], D, dt, &kc, &vc) ||
+      sequences(fn, a[5], 1, &seqs, &B) || page_table(fn, a[4], B, &pages, &per_seq))
+    return NULL;
+  if (a[1] == Py_None || kc.heads != k.heads) {
+    PyErr_Format(PyExc_ValueError, "%s: v is needed, and k_cache with k's %d heads", fn, k.heads);
+    return NULL;
+  }
+  static const char* const names[] = {"k", "v", "k_cache", "v_cache", "pages", "seqs"};
+  if (device_of(fn, a, names, 6, &dev) || stream_of(dev, a[6], &st)) return NULL;
+  Py_BEGIN_ALLOW_THREADS                         /* a launch waits while the launch queue is full */
+  status = call_write(k.ptr, k.tok, k.head, v.ptr, v.tok, v.head, kc.ptr, kc.page, kc.row, kc.head, vc.ptr, vc.page, vc.row,
+                      vc.head, dtype, rows, k.heads, D, kc.pages, kc.size, pages.ptr, pages.ld, per_seq, seqs, B, st);
+  Py_END_ALLOW_THREADS
+  return PyLong_FromLong(status);
+}
+
+/* (attention, paged attention, cache write addresses): once, at load, after bind. */
+static PyObject* bind_attention(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  (void)self;
+  long long p[3];
+  if (want(n, 3)) return NULL;
+  for (int i = 0; i < 3; ++i)
+    if (to_ll(a[i], &p[i])) return NULL;
+  call_attention = (attention_fn)(uintptr_t)p[0];
+  call_paged = (paged_fn)(uintptr_t)p[1];
+  call_write = (write_fn)(uintptr_t)p[2];
+  Py_RETURN_NONE;
+}
+
 /* (norm, rope, gemm addresses, GPUs, refuse, raw_stream, current_device, bf16, fp16, fp32, fp64, int8, int32): once, at load. */
 static PyObject* bind(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   (void)self;
@@ -419,6 +625,10 @@ static PyMethodDef methods[] = {{"bind", (PyCFunction)(void (*)(void))bind, METH
                                 {"rms_norm_quant", (PyCFunction)(void (*)(void))rms_norm_quant, METH_FASTCALL, NULL},
                                 {"qk_norm_rope", (PyCFunction)(void (*)(void))qk_norm_rope, METH_FASTCALL, NULL},
                                 {"gemm_fused", (PyCFunction)(void (*)(void))gemm_fused, METH_FASTCALL, NULL},
+                                {"bind_attention", (PyCFunction)(void (*)(void))bind_attention, METH_FASTCALL, NULL},
+                                {"attention", (PyCFunction)(void (*)(void))attention, METH_FASTCALL, NULL},
+                                {"paged_attention", (PyCFunction)(void (*)(void))paged_attention, METH_FASTCALL, NULL},
+                                {"cache_write", (PyCFunction)(void (*)(void))cache_write, METH_FASTCALL, NULL},
                                 {NULL, NULL, 0, NULL}};
 
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", NULL, -1, methods, NULL, NULL, NULL, NULL};
