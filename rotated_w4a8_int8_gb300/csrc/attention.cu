@@ -43,7 +43,11 @@ namespace cratt {
 
 using namespace crgemm;
 
-constexpr int THREADS = 320;              // warps 0-7: rows (two slots), 8: loads, 9: products
+constexpr int THREADS = 384;              // warps 0-7: rows (two slots), 8: loads, 9: products (10 and 11 give registers)
+// Registers of a thread: a row's 128 scores need more than an equal share of the
+// SM's (168, with which they spilled).  2 x 128 x 208 + 128 x 80 <= 384 x 168.
+constexpr int ROW_REGISTERS = 208, OTHER_REGISTERS = 80;
+static_assert(256 * ROW_REGISTERS + 128 * OTHER_REGISTERS <= THREADS * 168, "registers");
 constexpr int MAX_SPLIT = 8;
 
 template <int DP, bool SPLIT>
@@ -58,7 +62,7 @@ struct Layout {
   static constexpr int ITEM = 256, STATS = 512, SUMS = STATS + 2 * 128 * 8, AUX = SPLIT ? 3072 : 1024;
   static constexpr int SMEM = (QTILES + STAGES) * TILE + AUX + 1024;
   static_assert(SMEM <= 232448, "shared memory");
-  static_assert((2 * STAGES + 10) * 8 + 8 <= ITEM && SUMS + 512 <= 3072, "barrier area");
+  static_assert((2 * STAGES + 12) * 8 + 8 <= ITEM && SUMS + 512 <= 3072, "barrier area");
   // partials that a CTA receives: 2 slots of every CTA x its share of the 128 rows
   static constexpr int PARTS = 2 * MAX_SPLIT * ((128 + MAX_SPLIT - 1) / MAX_SPLIT) + 2 * MAX_SPLIT;
   static_assert(!SPLIT || PARTS * PITCH * 4 <= (QTILES + STAGES) * TILE, "joined partials");
@@ -239,9 +243,9 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
   uint8_t* tiles = aux + L::AUX;
   const uint32_t bars = smem_u32(aux);
   const uint32_t full0 = bars, empty0 = bars + 8 * STAGES, s_full0 = empty0 + 8 * STAGES, p_full0 = s_full0 + 16,
-                 o_full0 = p_full0 + 16, q_full = o_full0 + 16, q_empty = q_full + 8, v_raw = q_full + 16, drain = q_full + 24;
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(aux + (2 * STAGES + 10) * 8);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(aux + (2 * STAGES + 10) * 8 + 4);
+                 o_full0 = p_full0 + 32, q_full = o_full0 + 16, q_empty = q_full + 8, v_raw = q_full + 16, drain = q_full + 24;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(aux + (2 * STAGES + 12) * 8);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(aux + (2 * STAGES + 12) * 8 + 4);
   Item* item = reinterpret_cast<Item*>(aux + L::ITEM);
   const uint32_t q_tiles = smem_u32(tiles), stages = q_tiles + L::QTILES * L::TILE;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -254,7 +258,8 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(s_full0 + 8 * s, 1);
-      mbar_init(p_full0 + 8 * s, 4);
+      mbar_init(p_full0 + 16 * s, 4);
+      mbar_init(p_full0 + 16 * s + 8, 4);
       mbar_init(o_full0 + 8 * s, 1);
     }
     mbar_init(q_full, 1);
@@ -287,6 +292,8 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
     return last >= s * w.tps ? it.tiles(last, p.causal) : 0;
   };
 
+  if (warp >= 8) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(OTHER_REGISTERS));
   if (warp == 8) {
     // ---------------------------------------------------------------- loads
     const int64_t num_tiles = count_tiles(p, w, lane, &g_error);
@@ -457,15 +464,18 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
         any = true;
       };
       auto outputs = [&](int s, bool accumulate) {   // O of slot s += its P times the stage's V
-        ok = ok && mbar_wait(p_full0 + 8 * s, p_phase[s], ERR_WAIT_ACC_FULL, abort_flag);
-        if (!ok) return;
-        p_phase[s] ^= 1u;
-        tc_fence_after();
         const uint64_t b = v_desc(stages + stage * L::TILE, L::BOX);
 #pragma unroll
-        for (int kk = 0; kk < KEYS / 16; ++kk)
-          mma_ts(tmem + L::O_COL + s * DP, tmem + L::S_COL + s * KEYS + kk * 8, b + kk * (2048 >> 4), IDESC_O,
-                 accumulate || kk > 0);
+        for (int half = 0; half < 2; ++half) {       // each as soon as its weights are there
+          ok = ok && mbar_wait(p_full0 + 16 * s + 8 * half, p_phase[s], ERR_WAIT_ACC_FULL, abort_flag);
+          if (!ok) return;
+          tc_fence_after();
+#pragma unroll
+          for (int kk = half * KEYS / 32; kk < (half + 1) * KEYS / 32; ++kk)
+            mma_ts(tmem + L::O_COL + s * DP, tmem + L::S_COL + s * KEYS + kk * 8, b + kk * (2048 >> 4), IDESC_O,
+                   accumulate || kk > 0);
+        }
+        p_phase[s] ^= 1u;
       };
       for (uint32_t n_items = 0; ok; ++n_items) {
         ok = mbar_wait(q_full, n_items & 1u, ERR_WAIT_FULL, abort_flag);
@@ -547,6 +557,13 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
       cluster_sync();
     }
   } else {
+    if (SPLIT) {
+      cluster_sync();
+      cluster_sync();
+    }
+  }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(ROW_REGISTERS));
     // ---------------------------------------------------------------- rows
     const int slot = warp >> 2, row = (warp & 3) * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
@@ -638,13 +655,15 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
             packed[j] = pack2<DT>(e.x, e.y);
           }
           tmem_st16(s_addr + 16 * c, packed);
+          if (c % (KEYS / 64) == KEYS / 64 - 1) {
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_local(p_full0 + 16 * slot + 8 * (c / (KEYS / 64)));
+          }
         }
         l0 = sum.x;
         l1 = sum.y;
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_local(p_full0 + 8 * slot);
       }
       if (ok && any) {
         ok = __all_sync(0xffffffffu, mbar_wait(o_full0 + 8 * slot, o_phase, ERR_WAIT_ACC_FULL, abort_flag));
