@@ -43,7 +43,7 @@ namespace cratt {
 
 using namespace crgemm;
 
-constexpr int THREADS = 384;              // warps 0-7: rows (two slots), 8: loads, 9: products (10 and 11 give registers)
+constexpr int THREADS = 384;              // warps 0-7: rows (two slots), 8: loads, 9: products, 10: ragged V tiles (11 gives registers)
 // Registers of a thread: a row's 128 scores need more than an equal share of the
 // SM's (168, with which they spilled).  2 x 128 x 208 + 128 x 80 <= 384 x 168.
 constexpr int ROW_REGISTERS = 208, OTHER_REGISTERS = 80;
@@ -55,14 +55,15 @@ struct Layout {
   static constexpr int TILE = KEYS * DP * 2;                 // bytes of a Q, K or V tile
   static constexpr int BOX = KEYS * 128;                     // a 64-wide column block of it
   static constexpr int QTILES = SPLIT ? 1 : 2;
-  static constexpr int STAGES = DP == 128 ? 5 : 8;
+  static constexpr int STAGES = DP == 128 ? (SPLIT ? 5 : 4) : 8;
+  static constexpr int STAGING = SPLIT ? 0 : 8 * 4096;       // 32 rows x 64 columns of output per warp
   static constexpr int S_COL = 0, O_COL = 256;               // tensor memory: S of both slots, O of both slots
   static constexpr int PITCH = DP + 4;                       // floats per row of a joined partial
   // barriers and small things, then the tiles
   static constexpr int ITEM = 256, STATS = 512, SUMS = STATS + 2 * 128 * 8, AUX = SPLIT ? 3072 : 1024;
-  static constexpr int SMEM = (QTILES + STAGES) * TILE + AUX + 1024;
+  static constexpr int SMEM = (QTILES + STAGES) * TILE + STAGING + AUX + 1024;
   static_assert(SMEM <= 232448, "shared memory");
-  static_assert((2 * STAGES + 12) * 8 + 8 <= ITEM && SUMS + 512 <= 3072, "barrier area");
+  static_assert((2 * STAGES + 13) * 8 + 8 <= ITEM && SUMS + 512 <= 3072, "barrier area");
   // partials that a CTA receives: 2 slots of every CTA x its share of the 128 rows
   static constexpr int PARTS = 2 * MAX_SPLIT * ((128 + MAX_SPLIT - 1) / MAX_SPLIT) + 2 * MAX_SPLIT;
   static_assert(!SPLIT || PARTS * PITCH * 4 <= (QTILES + STAGES) * TILE, "joined partials");
@@ -84,7 +85,12 @@ struct Item {
     return l > lo ? (l + KEYS - 1) / KEYS : 0;
   }
 };
-static_assert(sizeof(Item) <= 256, "item area");
+static_assert(sizeof(Item) <= 128, "item area");
+
+// A V tile that holds rows outside its sequence: rows before `first` and from `end` on are to be zero.
+struct Ragged {
+  int stage, first, end;   // stage < 0: no more
+};
 
 // ------------------------------------------------------------------ PTX
 __device__ __forceinline__ void load_box_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z) {
@@ -97,22 +103,38 @@ __device__ __forceinline__ void load_box_4d(uint32_t dst, const CUtensorMap* map
       "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], [%2];"
       ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
-__device__ __forceinline__ void commit(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+// The products' warp runs as one, its values in uniform registers, and one lane
+// (`leader`) issues: with the whole loop inside `if (lane == 0)` every operand of
+// every instruction had to be moved there first, and 8 + 8 alternating products
+// took 98 clocks each where the tensor core takes 64 (so: 72).
+__device__ __forceinline__ uint32_t elect_leader() {
+  uint32_t e;
+  asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(e));
+  return e;
 }
-// D (+)= A B^T, A in shared memory
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+__device__ __forceinline__ void commit(uint32_t bar, uint32_t leader) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
-      ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate) : "memory");
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}"
+      ::"r"(bar), "r"(leader) : "memory");
+}
+// D (+)= A B^T, A in shared memory; descriptors as their two halves
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t high, uint32_t idesc, uint32_t accumulate,
+                                       uint32_t leader) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 da, db;\n\tsetp.ne.b32 p, %5, 0;\n\tsetp.ne.b32 q, %6, 0;\n\t"
+      "mov.b64 da, {%1, %3};\n\tmov.b64 db, {%2, %3};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, p;\n\t}"
+      ::"r"(d), "r"(a), "r"(b), "r"(high), "r"(idesc), "r"(accumulate), "r"(leader) : "memory");
 }
 // the same, A in tensor memory (two 16-bit values per column)
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t high, uint32_t idesc, uint32_t accumulate,
+                                       uint32_t leader) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
-      ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(accumulate) : "memory");
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 db;\n\tsetp.ne.b32 p, %5, 0;\n\tsetp.ne.b32 q, %6, 0;\n\t"
+      "mov.b64 db, {%2, %3};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %4, p;\n\t}"
+      ::"r"(d), "r"(a), "r"(b), "r"(high), "r"(idesc), "r"(accumulate), "r"(leader) : "memory");
 }
 // 32 lanes x 32 columns from or to tensor memory
 __device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t* r) {
@@ -168,12 +190,12 @@ __device__ __forceinline__ void st_cluster_f32x4(uint32_t addr, float a, float b
   asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(a), "f"(b), "f"(c), "f"(d) : "memory");
 }
 
-// V [128 keys][DP] as it lies (columns contiguous): 64-wide column blocks BOX
-// bytes apart, groups of 8 keys 1024 bytes apart, 128-byte swizzling.
-__device__ __forceinline__ uint64_t v_desc(uint32_t saddr, uint32_t box) {
-  uint64_t d = smem_desc_sw128(saddr) & ~(static_cast<uint64_t>(0x3FFF) << 16);
-  return d | static_cast<uint64_t>(box >> 4) << 16;
-}
+// Shared-memory descriptors, 128-byte swizzling.  Q and K: rows of 128 bytes, groups
+// of 8 rows 1024 bytes apart.  V [128 keys][DP] as it lies (columns contiguous):
+// 64-wide column blocks `block` bytes apart (the low half's second field), groups
+// of 8 keys 1024 bytes apart.
+constexpr uint32_t DESC_HIGH = (1024 >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_low(uint32_t saddr, uint32_t block = 16) { return ((saddr & 0x3FFFFu) >> 4) | (block >> 4) << 16; }
 
 // ------------------------------------------------------------------ items
 struct Work {
@@ -243,12 +265,13 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
   uint8_t* tiles = aux + L::AUX;
   const uint32_t bars = smem_u32(aux);
   const uint32_t full0 = bars, empty0 = bars + 8 * STAGES, s_full0 = empty0 + 8 * STAGES, p_full0 = s_full0 + 16,
-                 o_full0 = p_full0 + 32, q_full = o_full0 + 16, q_empty = q_full + 8, v_raw = q_full + 16, drain = q_full + 24;
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(aux + (2 * STAGES + 12) * 8);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(aux + (2 * STAGES + 12) * 8 + 4);
+                 o_full0 = p_full0 + 32, q_full = o_full0 + 16, q_empty = q_full + 8, v_raw = q_full + 16, drain = q_full + 24, raw_free = q_full + 32;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(aux + (2 * STAGES + 13) * 8);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(aux + (2 * STAGES + 13) * 8 + 4);
   Item* item = reinterpret_cast<Item*>(aux + L::ITEM);
+  Ragged* ragged = reinterpret_cast<Ragged*>(aux + L::ITEM + 128);
   const uint32_t q_tiles = smem_u32(tiles), stages = q_tiles + L::QTILES * L::TILE;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (threadIdx.x == 0) {
@@ -266,6 +289,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
     mbar_init(q_empty, 9);                 // the last scores' commit, and every row warp has read the item
     mbar_init(v_raw, 1);
     mbar_init(drain, 1);
+    mbar_init(raw_free, 1);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -276,7 +300,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
   const int rank = SPLIT ? static_cast<int>(blockIdx.x % slices) : 0;
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
@@ -300,52 +324,40 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
     const int64_t num_items = num_tiles * (p.heads_q / w.pack);
     const int group = p.heads_q / p.heads_k;
     const int box_rows = PAGED ? min(1 << p.page_log2, KEYS) : KEYS;
-    uint32_t stage = 0, phase = 0, raw_phase = 0;
+    uint32_t stage = 0, phase = 0;
     uint32_t issued = 0, issued_phase = 0;       // outstanding loads, for an abort
-    bool ok = true, q_out = false, raw_out = false;
-    uint32_t n_items = 0;
-    for (int64_t i = SPLIT ? blockIdx.x / slices : blockIdx.x;; i += gridDim.x, ++n_items) {
-      const bool more = i < num_items && !(SPLIT && n_items > 0);
+    uint32_t n_items = 0, n_ragged = 0;
+    bool ok = true, q_out = false;
+    auto find = [&](int64_t i) {
       Item it = {};
       it.q_row = -1;
-      if (more) {
-        Sequence s;
-        int token;
-        const int unit = static_cast<int>(i / num_tiles);
-        find_tile(p, w, i % num_tiles, lane, &g_error, s, it.seq, token);
-        it.q_row = s.q_start + token;
-        it.tokens = min(w.item_tokens, s.q_len - token);
-        it.head0 = unit * w.pack;
-        it.head_kv = it.head0 / group;
-        it.base = PAGED ? s.k_start / box_rows * box_rows : s.k_start;
-        it.lo = s.k_start - it.base;
-        it.hi = it.lo + s.k_len;
-        it.see0 = it.hi - s.q_len + token + 1;
+      if (i >= num_items) return it;
+      Sequence s;
+      int token;
+      const int unit = static_cast<int>(i / num_tiles);
+      find_tile(p, w, i % num_tiles, lane, &g_error, s, it.seq, token);
+      it.q_row = s.q_start + token;
+      it.tokens = min(w.item_tokens, s.q_len - token);
+      it.head0 = unit * w.pack;
+      it.head_kv = it.head0 / group;
+      it.base = PAGED ? s.k_start / box_rows * box_rows : s.k_start;
+      it.lo = s.k_start - it.base;
+      it.hi = it.lo + s.k_len;
+      it.see0 = it.hi - s.q_len + token + 1;
+      return it;
+    };
+    auto wait_all = [&](uint32_t bar, uint32_t parity) {
+      return __all_sync(0xffffffffu, mbar_wait(bar, parity, ERR_WAIT_EMPTY, abort_flag)) != 0;
+    };
+    int64_t i = SPLIT ? blockIdx.x / slices : blockIdx.x;
+    Item it = find(i), next = {};
+    next.q_row = -1;
+    for (;; ++n_items) {
+      int t0 = 0, t1 = 0;
+      if (it.q_row >= 0) {
+        if (SPLIT) part(it, t0, t1);
+        else t1 = max(slot_tiles(it, 0), slot_tiles(it, 1));
       }
-      if (n_items > 0) {
-        ok = mbar_wait(q_empty, (n_items - 1) & 1u, ERR_WAIT_EMPTY, abort_flag);
-        if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-        q_out = false;
-      }
-      if (SPLIT && n_items > 0) break;
-      if (lane == 0) {
-        *item = it;
-        if (!more) {
-          mbar_arrive_local(q_full);
-        } else {
-          const int slots = !SPLIT && it.tokens > w.tps ? 2 : 1;
-          mbar_arrive_expect_tx(q_full, slots * w.pack * w.tps * DP * 2);
-          for (int s = 0; s < slots; ++s)
-            for (int c = 0; c < DP / 64; ++c)
-              load_box_3d(q_tiles + s * L::TILE + c * L::BOX, &map_q, q_full, 64 * c, it.head0, it.q_row + s * w.tps);
-        }
-      }
-      __syncwarp();
-      if (!more) break;
-      q_out = true;
-      int t0 = 0, t1;
-      if (SPLIT) part(it, t0, t1);
-      else t1 = max(slot_tiles(it, 0), slot_tiles(it, 1));
       // lanes 0 .. boxes-1 hold the pages of the next K tile's boxes
       const int boxes = KEYS / box_rows;
       auto page_of = [&](int t) {
@@ -358,12 +370,16 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
       int page_next = PAGED && t0 < t1 ? page_of(t0) : 0;
       // K or V tile t into the next stage
       auto load = [&](bool is_v, int t) {
-        bool got = mbar_wait(empty0 + 8 * stage, phase ^ 1u, ERR_WAIT_EMPTY, abort_flag);
-        if (!__all_sync(0xffffffffu, got)) return false;
-        // a V tile with rows outside the sequence is zeroed there before anyone is told of it
+        if (!wait_all(empty0 + 8 * stage, phase ^ 1u)) return false;
+        // a V tile with rows outside the sequence goes through the warp that zeroes them
         const int first = t == 0 ? it.lo : 0, end = min(KEYS, it.hi - t * KEYS);
-        const bool ragged = is_v && (first > 0 || end < KEYS);
-        const uint32_t bar = ragged ? v_raw : full0 + 8 * stage, dst = stages + stage * L::TILE;
+        const bool raw = is_v && (first > 0 || end < KEYS);
+        if (raw) {
+          if (n_ragged > 0 && !wait_all(raw_free, (n_ragged - 1) & 1u)) return false;
+          if (lane == 0) *ragged = {static_cast<int>(stage), first, end};
+          ++n_ragged;
+        }
+        const uint32_t bar = raw ? v_raw : full0 + 8 * stage, dst = stages + stage * L::TILE;
         const CUtensorMap* map = is_v ? &map_v : &map_k;
         if (!PAGED) {
           if (lane == 0) {
@@ -371,6 +387,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
             for (int c = 0; c < DP / 64; ++c)
               load_box_3d(dst + c * L::BOX, map, bar, 64 * c, it.head_kv, it.base + t * KEYS);
           }
+          __syncwarp();
         } else {
           const int wanted = (end + box_rows - 1) / box_rows;
           int page = is_v ? page_of(t) : page_next;
@@ -388,41 +405,55 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
           }
           if (!is_v && t + 1 < t1) page_next = page_of(t + 1);
         }
-        if (ragged) {
-          raw_out = true;
-          got = mbar_wait(v_raw, raw_phase, ERR_WAIT_FULL, abort_flag);
-          if (!__all_sync(0xffffffffu, got)) return false;
-          raw_out = false;
-          raw_phase ^= 1u;
-          uint8_t* tile = tiles + (L::QTILES + stage) * L::TILE;
-          const int out = first + KEYS - end;
-          for (int j = lane; j < out * 8 * (DP / 64); j += 32) {
-            const int r = j / 8 % out, row = r < first ? r : end + r - first;
-            *reinterpret_cast<uint4*>(tile + j / (8 * out) * L::BOX + row * 128 + j % 8 * 16) = make_uint4(0, 0, 0, 0);
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_local(full0 + 8 * stage);
-        } else {
+        if (!raw) {
           issued |= 1u << stage;
           issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
         }
         if (++stage == STAGES) { stage = 0; phase ^= 1u; }
         return true;
       };
-      // in the order in which the products use them
-      constexpr int AHEAD = SPLIT ? 2 : 1;
+      // in the order in which the products use them, the first keys even before the last item's Q is done with
+      if (t0 < t1 && !p.starve && !(ok = load(false, t0))) break;
+      if (n_items > 0) {
+        if (!(ok = wait_all(q_empty, (n_items - 1) & 1u))) break;
+        q_out = false;
+      }
+      if (lane == 0) {
+        *item = it;
+        if (it.q_row < 0) {
+          mbar_arrive_local(q_full);
+        } else {
+          const int slots = !SPLIT && it.tokens > w.tps ? 2 : 1;
+          mbar_arrive_expect_tx(q_full, slots * w.pack * w.tps * DP * 2);
+          for (int s = 0; s < slots; ++s)
+            for (int c = 0; c < DP / 64; ++c)
+              load_box_3d(q_tiles + s * L::TILE + c * L::BOX, &map_q, q_full, 64 * c, it.head0, it.q_row + s * w.tps);
+        }
+      }
+      __syncwarp();
+      if (it.q_row < 0) break;
+      q_out = true;
       if (p.starve) break;
-      for (int t = t0; ok && t < min(t1, t0 + AHEAD); ++t) ok = load(false, t);
+      if (SPLIT && t0 + 1 < t1) ok = load(false, t0 + 1);
+      constexpr int AHEAD = SPLIT ? 2 : 1;
       for (int t = t0; ok && t < t1; ++t) {
         ok = load(true, t);
         if (ok && t + AHEAD < t1) ok = load(false, t + AHEAD);
+        if (!SPLIT && t == t0) next = find(i + gridDim.x);        // while this item's first tiles are on their way
       }
       if (!ok) break;
+      if (!SPLIT && t0 >= t1) next = find(i + gridDim.x);
+      it = next;                                                   // (SPLIT: there is one item)
+      i += gridDim.x;
     }
     if (ok) {
+      if (n_ragged > 0) ok = wait_all(raw_free, (n_ragged - 1) & 1u);
+      if (ok && lane == 0) {
+        ragged->stage = -1;
+        mbar_arrive_local(v_raw);
+      }
       // the products' last commits arrive on the empty barriers: wait for them before leaving
-      for (int i = 0; i < STAGES; ++i) {
+      for (int j = 0; j < STAGES; ++j) {
         if (!mbar_wait(empty0 + 8 * stage, phase ^ 1u, ERR_WAIT_EMPTY, abort_flag)) break;
         if (++stage == STAGES) { stage = 0; phase ^= 1u; }
       }
@@ -432,9 +463,9 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
       auto land = [&](uint32_t bar, uint32_t parity) {
         while (!mbar_try_wait(bar, parity) && globaltimer() - t_start < kWaitLimitNs) {}
       };
-      for (int i = 0; i < STAGES; ++i)
-        if (issued >> i & 1u) land(full0 + 8 * i, issued_phase >> i & 1u);
-      if (raw_out) land(v_raw, raw_phase);
+      for (int j = 0; j < STAGES; ++j)
+        if (issued >> j & 1u) land(full0 + 8 * j, issued_phase >> j & 1u);
+      if (n_ragged > 0) land(v_raw, (n_ragged - 1) & 1u);
       if (q_out) land(q_full, n_items & 1u);
     }
     __syncwarp();
@@ -444,112 +475,117 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
     }
   } else if (warp == 9) {
     // ---------------------------------------------------------------- products
-    if (lane == 0) {
-      uint32_t stage = 0, phase = 0, p_phase[2] = {0, 0};
-      bool ok = true, any = false;
-      auto next_full = [&]() { return ok = ok && mbar_wait(full0 + 8 * stage, phase, ERR_WAIT_FULL, abort_flag); };
-      auto release = [&]() {
-        commit(empty0 + 8 * stage);
-        if (++stage == STAGES) { stage = 0; phase ^= 1u; }
-      };
-      auto scores = [&](int s) {                  // S of slot s = its Q times the stage's K
+    const uint32_t leader = elect_leader();
+    uint32_t stage = 0, phase = 0, p_phase[2] = {0, 0};
+    bool ok = true, any = false;
+    auto wait_all = [&](uint32_t bar, uint32_t parity, int code) {
+      return __all_sync(0xffffffffu, mbar_wait(bar, parity, code, abort_flag)) != 0;
+    };
+    auto next_full = [&]() { return ok = ok && wait_all(full0 + 8 * stage, phase, ERR_WAIT_FULL); };
+    auto release = [&]() {
+      commit(empty0 + 8 * stage, leader);
+      if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+    };
+    auto scores = [&](int s) {                  // S of slot s = its Q times the stage's K
+      tc_fence_after();
+      const uint32_t a = desc_low(q_tiles + (SPLIT ? 0 : s) * L::TILE), b = desc_low(stages + stage * L::TILE);
+#pragma unroll
+      for (int kk = 0; kk < DP / 16; ++kk) {
+        const uint32_t at = (kk / 4) * (L::BOX >> 4) + (kk % 4) * 2;
+        mma_ss(tmem + L::S_COL + s * KEYS, a + at, b + at, DESC_HIGH, IDESC_S, kk > 0, leader);
+      }
+      commit(s_full0 + 8 * s, leader);
+      any = true;
+    };
+    auto outputs = [&](int s, bool accumulate) {   // O of slot s += its P times the stage's V
+      const uint32_t b = desc_low(stages + stage * L::TILE, L::BOX);
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {       // each as soon as its weights are there
+        ok = ok && wait_all(p_full0 + 16 * s + 8 * half, p_phase[s], ERR_WAIT_ACC_FULL);
+        if (!ok) return;
         tc_fence_after();
-        const uint64_t a = smem_desc_sw128(q_tiles + (SPLIT ? 0 : s) * L::TILE), b = smem_desc_sw128(stages + stage * L::TILE);
 #pragma unroll
-        for (int kk = 0; kk < DP / 16; ++kk) {
-          const uint64_t at = (kk / 4) * (L::BOX >> 4) + (kk % 4) * 2;
-          mma_ss(tmem + L::S_COL + s * KEYS, a + at, b + at, IDESC_S, kk > 0);
-        }
-        commit(s_full0 + 8 * s);
-        any = true;
-      };
-      auto outputs = [&](int s, bool accumulate) {   // O of slot s += its P times the stage's V
-        const uint64_t b = v_desc(stages + stage * L::TILE, L::BOX);
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {       // each as soon as its weights are there
-          ok = ok && mbar_wait(p_full0 + 16 * s + 8 * half, p_phase[s], ERR_WAIT_ACC_FULL, abort_flag);
-          if (!ok) return;
-          tc_fence_after();
-#pragma unroll
-          for (int kk = half * KEYS / 32; kk < (half + 1) * KEYS / 32; ++kk)
-            mma_ts(tmem + L::O_COL + s * DP, tmem + L::S_COL + s * KEYS + kk * 8, b + kk * (2048 >> 4), IDESC_O,
-                   accumulate || kk > 0);
-        }
-        p_phase[s] ^= 1u;
-      };
-      for (uint32_t n_items = 0; ok; ++n_items) {
-        ok = mbar_wait(q_full, n_items & 1u, ERR_WAIT_FULL, abort_flag);
-        if (!ok) break;
-        const Item it = *item;
-        if (it.q_row < 0) break;
-        if (SPLIT) {
-          int t0, t1;
-          part(it, t0, t1);
-          const int n = t1 - t0;
-          for (int j = 0; j < min(n, 2) && next_full(); ++j) {
-            scores(j);
-            release();
-          }
-          for (int j = 0; ok && j < n; ++j) {
-            const int s = j & 1;
-            if (!next_full()) break;
-            outputs(s, j >= 2);
-            if (!ok) break;
-            if (j + 2 >= n) commit(o_full0 + 8 * s);
-            release();
-            if (j + 2 < n && next_full()) {
-              scores(s);
-              release();
-            }
-          }
-          if (ok) commit(q_empty);
-          break;
-        }
-        const int n0 = slot_tiles(it, 0), n1 = slot_tiles(it, 1), n = max(n0, n1);
-        if (n > 0 && next_full()) {
-          if (n0 > 0) scores(0);
-          if (n1 > 0) scores(1);
+        for (int kk = half * KEYS / 32; kk < (half + 1) * KEYS / 32; ++kk)
+          mma_ts(tmem + L::O_COL + s * DP, tmem + L::S_COL + s * KEYS + kk * 8, b + kk * (2048 >> 4), DESC_HIGH, IDESC_O,
+                 accumulate || kk > 0, leader);
+      }
+      p_phase[s] ^= 1u;
+    };
+    for (uint32_t n_items = 0; ok; ++n_items) {
+      ok = wait_all(q_full, n_items & 1u, ERR_WAIT_FULL);
+      if (!ok) break;
+      const Item it = *item;
+      if (it.q_row < 0) break;
+      if (SPLIT) {
+        int t0, t1;
+        part(it, t0, t1);
+        const int n = t1 - t0;
+        for (int j = 0; j < min(n, 2) && next_full(); ++j) {
+          scores(j);
           release();
         }
-        if (ok && n <= 1) commit(q_empty);
         for (int j = 0; ok && j < n; ++j) {
+          const int s = j & 1;
           if (!next_full()) break;
-          // both slots' outputs use this stage, both slots' next scores the one after it
-          const uint32_t v_stage = stage, v_phase = phase;
-          const uint32_t k_stage = stage + 1 == STAGES ? 0 : stage + 1, k_phase = stage + 1 == STAGES ? phase ^ 1u : phase;
-          const bool more = j + 1 < n;
-          bool k_here = false;
-          for (int s = 0; ok && s < 2; ++s) {
-            const int ns = s ? n1 : n0;
-            stage = v_stage;
-            phase = v_phase;
-            if (j < ns) {
-              outputs(s, j > 0);
-              if (!ok) break;
-              if (j + 1 == ns) commit(o_full0 + 8 * s);
-            }
-            if (s == 1) commit(empty0 + 8 * v_stage);
-            stage = k_stage;
-            phase = k_phase;
-            if (j + 1 < ns) {
-              if (!k_here && !next_full()) break;
-              k_here = true;
-              scores(s);
-            }
-          }
+          outputs(s, j >= 2);
           if (!ok) break;
-          if (more) {
+          if (j + 2 >= n) commit(o_full0 + 8 * s, leader);
+          release();
+          if (j + 2 < n && next_full()) {
+            scores(s);
             release();
-            if (j + 2 == n) commit(q_empty);
           }
         }
+        if (ok) commit(q_empty, leader);
+        break;
       }
-      if (!ok && any) {
-        // wait for the tensor core to finish everything issued before its memory is freed
-        commit(drain);
-        const uint64_t t0 = globaltimer();
-        while (!mbar_try_wait(drain, 0) && globaltimer() - t0 < kWaitLimitNs) {}
+      const int n0 = slot_tiles(it, 0), n1 = slot_tiles(it, 1), n = max(n0, n1);
+      __syncwarp();                               // every lane has read the item before the next one may come
+      if (n > 0 && next_full()) {
+        if (n0 > 0) scores(0);
+        if (n1 > 0) scores(1);
+        release();
       }
+      if (ok && n <= 1) commit(q_empty, leader);
+      for (int j = 0; ok && j < n; ++j) {
+        if (!next_full()) break;
+        // both slots' outputs use this stage, both slots' next scores the one after it
+        const uint32_t v_stage = stage;
+        const bool wraps = stage + 1 == STAGES;
+        const uint32_t k_stage = wraps ? 0 : stage + 1, k_phase = wraps ? phase ^ 1u : phase;
+        const bool more = j + 1 < n;
+        bool k_here = false;
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          const int ns = s ? n1 : n0;
+          if (ok && j < ns) {
+            stage = v_stage;
+            outputs(s, j > 0);
+            if (ok && j + 1 == ns) commit(o_full0 + 8 * s, leader);
+          }
+          if (ok && s == 1) commit(empty0 + 8 * v_stage, leader);
+          stage = k_stage;
+          if (ok && j + 1 < ns) {
+            if (!k_here) {
+              phase = k_phase;
+              k_here = next_full();
+            }
+            if (ok) scores(s);
+          }
+        }
+        phase = k_phase;
+        if (!ok) break;
+        if (more) {
+          release();
+          if (j + 2 == n) commit(q_empty, leader);
+        }
+      }
+    }
+    if (!ok && any) {
+      // wait for the tensor core to finish everything issued before its memory is freed
+      commit(drain, leader);
+      const uint64_t t0 = globaltimer();
+      while (!mbar_try_wait(drain, 0) && globaltimer() - t0 < kWaitLimitNs) {}
     }
     __syncwarp();
     if (SPLIT) {
@@ -557,6 +593,27 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
       cluster_sync();
     }
   } else {
+    if (warp == 10) {
+      // -------------------------------------------------------------- ragged V tiles
+      for (uint32_t n = 0;; ++n) {
+        if (!__all_sync(0xffffffffu, mbar_wait(v_raw, n & 1u, ERR_WAIT_FULL, abort_flag))) break;
+        const Ragged r = *ragged;
+        if (r.stage < 0) break;
+        uint8_t* tile = tiles + (L::QTILES + r.stage) * L::TILE;
+        const int out = r.first + KEYS - r.end;
+        for (int j = lane; j < out * 8 * (DP / 64); j += 32) {
+          const int k = j / 8 % out, row = k < r.first ? k : r.end + k - r.first;
+          *reinterpret_cast<uint4*>(tile + j / (8 * out) * L::BOX + row * 128 + j % 8 * 16) = make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive_local(full0 + 8 * r.stage);
+          mbar_arrive_local(raw_free);
+        }
+      }
+    }
+    __syncwarp();
     if (SPLIT) {
       cluster_sync();
       cluster_sync();
@@ -676,24 +733,41 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                             2 * ((static_cast<int64_t>(it.q_row) + my_token) * p.out_tok + (it.head0 + my_head) * p.out_head);
       if constexpr (!SPLIT) {
         if (!ok) break;
+        // Through shared memory (16-byte pieces swizzled by the row), so that a store of the warp covers four rows of
+        // 128 bytes; from the threads' own rows it covered 32 of 16.
         const float f = l == 0.f ? 0.f : 1.f / l;
+        const unsigned rows = __ballot_sync(0xffffffffu, mine);
+        uint4* box = reinterpret_cast<uint4*>(tiles + (L::QTILES + STAGES) * L::TILE + warp * 4096);
 #pragma unroll 1
-        for (int c = 0; c < DP / 32; ++c) {
-          uint32_t o[32];
-          if (any) {
-            tmem_ld32(o_addr + 32 * c, o);
-            tmem_ld_wait();
-          }
+        for (int half = 0; half < DP / 64; ++half) {
 #pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            uint32_t v[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const float a = __uint_as_float(o[8 * g + 2 * j]) * f, b = __uint_as_float(o[8 * g + 2 * j + 1]) * f;
-              v[j] = !any || l == 0.f ? 0u : pack2<DT>(a, b);
+          for (int c = 0; c < 2; ++c) {
+            uint32_t o[32];
+            if (any) {
+              tmem_ld32(o_addr + 64 * half + 32 * c, o);
+              tmem_ld_wait();
             }
-            if (mine && 32 * c + 8 * g < p.D) store_global(out_row + 64 * c + 16 * g, make_uint4(v[0], v[1], v[2], v[3]));
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+              uint32_t v[4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const float a = __uint_as_float(o[8 * g + 2 * j]) * f, b = __uint_as_float(o[8 * g + 2 * j + 1]) * f;
+                v[j] = !any || l == 0.f ? 0u : pack2<DT>(a, b);
+              }
+              box[8 * lane + ((4 * c + g) ^ (lane & 7))] = make_uint4(v[0], v[1], v[2], v[3]);
+            }
           }
+          __syncwarp();
+          const int piece = lane & 7;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int r = 4 * i + (lane >> 3);
+            char* dst = reinterpret_cast<char*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(out_row), r));
+            if ((rows >> r & 1u) && 64 * half + 8 * piece < p.D)
+              store_global(dst + 128 * half + 16 * piece, box[8 * r + (piece ^ (r & 7))]);
+          }
+          __syncwarp();
         }
         tc_fence_before();          // these reads before the next item's products, which wait for this warp's weights
       } else {
