@@ -310,7 +310,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
     t0 = static_cast<int>(n * rank / slices);
     t1 = static_cast<int>(n * (rank + 1) / slices);
   };
-  // key tiles of a slot's rows otherwise
+  // key tiles of a slot's rows (not SPLIT)
   auto slot_tiles = [&](const Item& it, int s) {
     const int last = min(it.tokens, (s + 1) * w.tps) - 1;
     return last >= s * w.tps ? it.tiles(last, p.causal) : 0;
@@ -486,7 +486,9 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
       commit(empty0 + 8 * stage, leader);
       if (++stage == STAGES) { stage = 0; phase ^= 1u; }
     };
-    auto scores = [&](int s) {                  // S of slot s = its Q times the stage's K
+    // Every product is whole: cutting the last tile's to its keys saves tensor time there, but the choice in this
+    // warp's path cost all others 3 to 7%.
+    auto scores = [&](int s) {                     // S of slot s = its Q times the stage's K
       tc_fence_after();
       const uint32_t a = desc_low(q_tiles + (SPLIT ? 0 : s) * L::TILE), b = desc_low(stages + stage * L::TILE);
 #pragma unroll
@@ -663,11 +665,18 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
 #pragma unroll
         for (int c = 0; c < KEYS / 32; ++c) tmem_ld32(s_addr + 32 * c, reinterpret_cast<uint32_t*>(x) + 32 * c);
         tmem_ld_wait();
-        if (t >= whole || (t == 0 && it.lo > 0)) {
-          const int end = limit - t * KEYS, first = t == 0 ? it.lo : 0;
+        if (t >= whole) {
+          const int end = limit - t * KEYS;
 #pragma unroll
-          for (int j = 0; j < KEYS; ++j)
-            if (j >= end || j < first) x[j] = -INFINITY;
+          for (int c = 0; c < KEYS / 32; ++c)
+            if (end < 32 * (c + 1)) {
+#pragma unroll
+              for (int j = 32 * c; j < 32 * (c + 1); ++j) x[j] = j < end ? x[j] : -INFINITY;
+            }
+        }
+        if (t == 0 && it.lo > 0) {
+#pragma unroll
+          for (int j = 0; j < KEYS; ++j) x[j] = j >= it.lo ? x[j] : -INFINITY;
         }
         float top[4];
 #pragma unroll
@@ -700,8 +709,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
         const float ref = kLift<DT> - (m == -INFINITY ? 0.f : m * p.scale_log2);
         const float2 r2 = make_float2(ref, ref);
         float2 sum = make_float2(l0, l1);
-#pragma unroll
-        for (int c = 0; c < KEYS / 32; ++c) {
+        auto weights = [&](int c) {                        // of 32 keys
           uint32_t packed[16];
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
@@ -712,13 +720,19 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
             packed[j] = pack2<DT>(e.x, e.y);
           }
           tmem_st16(s_addr + 16 * c, packed);
-          if (c % (KEYS / 64) == KEYS / 64 - 1) {
-            tmem_st_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_local(p_full0 + 16 * slot + 8 * (c / (KEYS / 64)));
-          }
-        }
+        };
+        auto hand_over = [&](int half) {
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_local(p_full0 + 16 * slot + 8 * half);
+        };
+        weights(0);
+        weights(1);
+        hand_over(0);
+        weights(2);
+        weights(3);
+        hand_over(1);
         l0 = sum.x;
         l1 = sum.y;
       }
