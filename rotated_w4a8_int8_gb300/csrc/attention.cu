@@ -76,6 +76,7 @@ struct Item {
   int base, lo, hi;        // position of key 0 of the first tile; keys lo .. hi - 1 are the sequence's
   int see0;                // causal: the first row sees keys below see0, the next one one more
   int seq;
+  int t0, t1[2];           // key tiles of this CTA: t0 .. t1 - 1 for each slot (SPLIT: for both, in turn)
 
   // first key that token t does not see (at most lo: it sees none)
   __device__ __forceinline__ int limit(int t, int causal) const { return causal ? min(hi, see0 + t) : hi; }
@@ -97,6 +98,14 @@ __device__ __forceinline__ void load_box_3d(uint32_t dst, const CUtensorMap* map
   asm volatile(
       "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];"
       ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z) : "memory");
+}
+__device__ __forceinline__ void store_box_3d(const CUtensorMap* map, uint32_t src, int x, int y, int z) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];"
+               ::"l"(reinterpret_cast<uint64_t>(map)), "r"(src), "r"(x), "r"(y), "r"(z) : "memory");
+}
+__device__ __forceinline__ void prefetch_box_3d(const CUtensorMap* map, int x, int y, int z) {
+  asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];"
+               ::"l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z) : "memory");
 }
 __device__ __forceinline__ void load_box_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z, int w) {
   asm volatile(
@@ -252,7 +261,8 @@ __device__ __forceinline__ void find_tile(const Problem& p, const Work& w, int64
 template <int DT, int DP, bool PAGED, bool SPLIT>
 __global__ void __launch_bounds__(THREADS, 1)
 attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
-                 const __grid_constant__ CUtensorMap map_v, const __grid_constant__ Problem p, const Work w, const int slices) {
+                 const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_out,
+                 const __grid_constant__ Problem p, const Work w, const int slices) {
   using L = Layout<DP, SPLIT>;
   constexpr int STAGES = L::STAGES;
   // FP32 accumulators; operands BF16 or FP16; M = 128, N = 128 keys or DP columns; V is not transposed (bit 16)
@@ -304,18 +314,6 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
   const int rank = SPLIT ? static_cast<int>(blockIdx.x % slices) : 0;
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
-  // key tiles of a SPLIT CTA: its part of those that the item's last row sees
-  auto part = [&](const Item& it, int& t0, int& t1) {
-    const int64_t n = it.tiles(it.tokens - 1, p.causal);
-    t0 = static_cast<int>(n * rank / slices);
-    t1 = static_cast<int>(n * (rank + 1) / slices);
-  };
-  // key tiles of a slot's rows (not SPLIT)
-  auto slot_tiles = [&](const Item& it, int s) {
-    const int last = min(it.tokens, (s + 1) * w.tps) - 1;
-    return last >= s * w.tps ? it.tiles(last, p.causal) : 0;
-  };
-
   if (warp >= 8) {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(OTHER_REGISTERS));
   if (warp == 8) {
@@ -344,6 +342,14 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
       it.lo = s.k_start - it.base;
       it.hi = it.lo + s.k_len;
       it.see0 = it.hi - s.q_len + token + 1;
+      if (SPLIT) {                              // a part of the tiles that the item's last row sees
+        const int64_t n = it.tiles(it.tokens - 1, p.causal);
+        it.t0 = static_cast<int>(n * rank / slices);
+        it.t1[0] = it.t1[1] = static_cast<int>(n * (rank + 1) / slices);
+      } else {
+        it.t1[0] = it.tiles(min(it.tokens, w.tps) - 1, p.causal);
+        it.t1[1] = it.tokens > w.tps ? it.tiles(it.tokens - 1, p.causal) : 0;
+      }
       return it;
     };
     auto wait_all = [&](uint32_t bar, uint32_t parity) {
@@ -352,12 +358,16 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
     int64_t i = SPLIT ? blockIdx.x / slices : blockIdx.x;
     Item it = find(i), next = {};
     next.q_row = -1;
+    // the next item, its Q on the way to L2
+    auto find_next = [&]() {
+      next = find(i + gridDim.x);
+      if (next.q_row >= 0 && lane == 0)
+        for (int s = 0; s < (next.tokens > w.tps ? 2 : 1); ++s)
+          for (int c = 0; c < DP / 64; ++c) prefetch_box_3d(&map_q, 64 * c, next.head0, next.q_row + s * w.tps);
+      __syncwarp();
+    };
     for (;; ++n_items) {
-      int t0 = 0, t1 = 0;
-      if (it.q_row >= 0) {
-        if (SPLIT) part(it, t0, t1);
-        else t1 = max(slot_tiles(it, 0), slot_tiles(it, 1));
-      }
+      const int t0 = it.t0, t1 = max(it.t1[0], it.t1[1]);
       // lanes 0 .. boxes-1 hold the pages of the next K tile's boxes
       const int boxes = KEYS / box_rows;
       auto page_of = [&](int t) {
@@ -439,10 +449,10 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
       for (int t = t0; ok && t < t1; ++t) {
         ok = load(true, t);
         if (ok && t + AHEAD < t1) ok = load(false, t + AHEAD);
-        if (!SPLIT && t == t0) next = find(i + gridDim.x);        // while this item's first tiles are on their way
+        if (!SPLIT && t == t0) find_next();        // while this item's first tiles are on their way
       }
       if (!ok) break;
-      if (!SPLIT && t0 >= t1) next = find(i + gridDim.x);
+      if (!SPLIT && t0 >= t1) find_next();
       it = next;                                                   // (SPLIT: there is one item)
       i += gridDim.x;
     }
@@ -516,12 +526,9 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
     for (uint32_t n_items = 0; ok; ++n_items) {
       ok = wait_all(q_full, n_items & 1u, ERR_WAIT_FULL);
       if (!ok) break;
-      const Item it = *item;
-      if (it.q_row < 0) break;
+      if (item->q_row < 0) break;
       if (SPLIT) {
-        int t0, t1;
-        part(it, t0, t1);
-        const int n = t1 - t0;
+        const int n = item->t1[0] - item->t0;
         for (int j = 0; j < min(n, 2) && next_full(); ++j) {
           scores(j);
           release();
@@ -541,8 +548,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
         if (ok) commit(q_empty, leader);
         break;
       }
-      const int n0 = slot_tiles(it, 0), n1 = slot_tiles(it, 1), n = max(n0, n1);
-      __syncwarp();                               // every lane has read the item before the next one may come
+      const int n0 = __shfl_sync(0xffffffffu, item->t1[0], 0), n1 = __shfl_sync(0xffffffffu, item->t1[1], 0), n = max(n0, n1);
       if (n > 0 && next_full()) {
         if (n0 > 0) scores(0);
         if (n1 > 0) scores(1);
@@ -639,18 +645,9 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
       if (ok) it = *item;
       __syncwarp();
       if (lane == 0) mbar_arrive_local(q_empty);
-      int t0 = 0, t1 = 0, step = 1;
-      if (it.q_row >= 0) {
-        if (SPLIT) {
-          part(it, t0, t1);
-          t0 += slot;
-          step = 2;
-        } else {
-          t1 = slot_tiles(it, slot);
-        }
-      } else if (!SPLIT) {
-        break;
-      }
+      if (!SPLIT && it.q_row < 0) break;
+      constexpr int step = SPLIT ? 2 : 1;
+      const int t0 = it.t0 + (SPLIT ? slot : 0), t1 = slot ? it.t1[1] : it.t1[0];
       const int limit = it.limit(my_token, p.causal);
       // tiles that some row of the slot sees in part
       const int whole = it.limit(SPLIT ? 0 : slot * w.tps, p.causal) / KEYS;
@@ -747,41 +744,49 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                             2 * ((static_cast<int64_t>(it.q_row) + my_token) * p.out_tok + (it.head0 + my_head) * p.out_head);
       if constexpr (!SPLIT) {
         if (!ok) break;
-        // Through shared memory (16-byte pieces swizzled by the row), so that a store of the warp covers four rows of
-        // 128 bytes; from the threads' own rows it covered 32 of 16.
+        // Through shared memory, 32 rows x 64 columns at a time (16-byte pieces swizzled by the row): by a TMA store
+        // where the warp's rows are all the item's, else copied, four rows of 128 bytes at a time.  (From the threads'
+        // own rows a store covered 32 rows of 16 bytes; copies alone took the warp 3300 clocks, the row's scores wait.)
         const float f = l == 0.f ? 0.f : 1.f / l;
         const unsigned rows = __ballot_sync(0xffffffffu, mine);
+        const bool whole_box = rows == 0xffffffffu && w.pack == 1;
         uint4* box = reinterpret_cast<uint4*>(tiles + (L::QTILES + STAGES) * L::TILE + warp * 4096);
 #pragma unroll 1
         for (int half = 0; half < DP / 64; ++half) {
+          uint32_t o[64], v[32];
+          tmem_ld32(o_addr + 64 * half, o);                // (without a key: whatever is there, not used)
+          tmem_ld32(o_addr + 64 * half + 32, o + 32);
+          tmem_ld_wait();
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            uint32_t o[32];
-            if (any) {
-              tmem_ld32(o_addr + 64 * half + 32 * c, o);
-              tmem_ld_wait();
-            }
-#pragma unroll
-            for (int g = 0; g < 4; ++g) {
-              uint32_t v[4];
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const float a = __uint_as_float(o[8 * g + 2 * j]) * f, b = __uint_as_float(o[8 * g + 2 * j + 1]) * f;
-                v[j] = !any || l == 0.f ? 0u : pack2<DT>(a, b);
-              }
-              box[8 * lane + ((4 * c + g) ^ (lane & 7))] = make_uint4(v[0], v[1], v[2], v[3]);
-            }
+          for (int j = 0; j < 32; ++j) {
+            const uint32_t two = pack2<DT>(__uint_as_float(o[2 * j]) * f, __uint_as_float(o[2 * j + 1]) * f);
+            v[j] = l == 0.f ? 0u : two;
           }
+          if (lane == 0) bulk_wait_read<0>();              // the box's last store has read it
           __syncwarp();
-          const int piece = lane & 7;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int r = 4 * i + (lane >> 3);
-            char* dst = reinterpret_cast<char*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(out_row), r));
-            if ((rows >> r & 1u) && 64 * half + 8 * piece < p.D)
-              store_global(dst + 128 * half + 16 * piece, box[8 * r + (piece ^ (r & 7))]);
+          for (int g = 0; g < 8; ++g)
+            box[8 * lane + (g ^ (lane & 7))] = make_uint4(v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]);
+          if (whole_box) {
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              store_box_3d(&map_out, smem_u32(box), 64 * half, it.head0, it.q_row + my_token);
+              bulk_commit();
+            }
+          } else {
+            __syncwarp();
+            const int piece = lane & 7;
+#pragma unroll 1
+            for (int i = 0; i < 8; ++i) {
+              const int r = 4 * i + (lane >> 3);
+              char* dst = reinterpret_cast<char*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(out_row), r));
+              if ((rows >> r & 1u) && 64 * half + 8 * piece < p.D)
+                store_global(dst + 128 * half + 16 * piece, box[8 * r + (piece ^ (r & 7))]);
+            }
+            fence_proxy_async_smem();                      // (a later store may read this box)
+            __syncwarp();
           }
-          __syncwarp();
         }
         tc_fence_before();          // these reads before the next item's products, which wait for this warp's weights
       } else {
@@ -848,6 +853,8 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
         break;
       }
     }
+    if (!SPLIT && lane == 0) bulk_wait_read<0>();          // no box is left unread
+    __syncwarp();
   }
 
   tc_fence_before();
@@ -919,9 +926,11 @@ template <int DT, int DP, bool PAGED, bool SPLIT>
 static int launch(const Problem& p, const Work& w, int slices, int64_t items, cudaStream_t st) {
   using L = Layout<DP, SPLIT>;
   static_assert(L::SMEM >= L::AUX + (L::QTILES + L::STAGES) * L::TILE + 1023, "shared memory");
-  CUtensorMap mq, mk, mv;
+  CUtensorMap mq, mk, mv, mo;
   const int64_t q_dims[3] = {p.heads_q, p.rows, 1}, q_strides[3] = {p.q_head, p.q_tok, 0};
   bool made = make_map<DT>(&mq, p.q, p.D, q_dims, q_strides, 3, w.pack, w.tps);
+  const int64_t out_strides[3] = {p.out_head, p.out_tok, 0};
+  made = made && make_map<DT>(&mo, p.out, p.D, q_dims, out_strides, 3, 1, 32);
   for (int i = 0; i < 2 && made; ++i) {
     const void* base = i ? p.v : p.k;
     const int64_t row = i ? p.v_row : p.k_row, head = i ? p.v_head : p.k_head, page = i ? p.v_page : p.k_page;
@@ -934,7 +943,7 @@ static int launch(const Problem& p, const Work& w, int slices, int64_t items, cu
       made = make_map<DT>(i ? &mv : &mk, base ? base : p.q, p.D, dims, strides, 3, 1, KEYS);
     }
   }
-  if (!made) return convrot::record_error("cuTensorMapEncodeTiled failed for q, k or v");
+  if (!made) return convrot::record_error("cuTensorMapEncodeTiled failed for q, k, v or out");
   int resident = 0;
   cudaError_t e = resident_clusters<DT, DP, PAGED, SPLIT>(slices, &resident);
   if (e != cudaSuccess) return convrot::record_cuda_error("attention set-up", e);
@@ -942,7 +951,7 @@ static int launch(const Problem& p, const Work& w, int slices, int64_t items, cu
   const int64_t clusters = SPLIT ? items : items < resident ? items : resident;
   if (clusters * slices > INT32_MAX) return CONVROT_ERR_UNSUPPORTED;
   e = convrot::launch_after(attention_kernel<DT, DP, PAGED, SPLIT>, dim3(static_cast<unsigned>(clusters * slices)), THREADS,
-                            L::SMEM, slices, st, mq, mk, mv, p, w, slices);
+                            L::SMEM, slices, st, mq, mk, mv, mo, p, w, slices);
   return e == cudaSuccess ? CONVROT_OK : convrot::record_cuda_error("attention launch", e);
 }
 
