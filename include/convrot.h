@@ -471,10 +471,10 @@ int convrot_cache_write(const void* k, int64_t k_row, int64_t k_head,
  * Self-test of the kernels behind convrot_attention and convrot_paged_attention:
  * the same call (`paged` 0: k and v are rows, num_pages counts them, the page
  * strides and page_size are not used, pages is NULL) with the kernel given
- * instead of chosen: 1 few rows, 2 many rows, whole items, 3 many rows, shared
- * keys; and with the CTAs that share a sequence's keys (slices 1 to 8; 1 for
- * kernel 2).  The results agree up to roundings.  With `starve` nonzero the
- * many-row kernels load no keys: their waits run out after about two seconds,
+ * instead of chosen: 1 few rows, 2 many rows, 3 many rows with shared keys; and
+ * with the CTAs that share a sequence's keys (slices: 1 to 16 for kernel 1, 1
+ * for 2, 1 to 8 for 3).  The results agree up to roundings.  With `starve`
+ * nonzero no keys are loaded: the kernels' waits run out after about two seconds,
  * the output is undefined, and convrot_device_error reports it.
  */
 int convrot_attention_selftest(const void* q, int64_t q_row, int64_t q_head,

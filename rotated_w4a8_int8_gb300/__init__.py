@@ -313,8 +313,8 @@ def cache_write(k, v, k_cache, v_cache, pages, seqs, stream=None) -> None:
 def attention_selftest(q, k, v, out, kernel: int, slices: int = 1, pages=None, seqs=None, scale: float | None = None,
                        causal: bool = False, starve: bool = False, stream=None) -> None:
     """convrot_attention_selftest: attention (pages None) or paged_attention with the kernel (KERNEL_*) and the CTAs that
-    share a sequence's keys (1 to 8; 1 for KERNEL_WHOLE) given; starve: the many-row kernels' loads are off (a wait runs
-    out)."""
+    share a sequence's keys (1 to 16, 1 for KERNEL_WHOLE, 1 to 8 for KERNEL_SHARED) given; starve: no keys are loaded (a wait
+    runs out)."""
     paged = pages is not None
     caches = [(t.data_ptr(), *([t.stride(0), t.stride(1), t.stride(2)] if paged else [0, t.stride(0), t.stride(1)]))
               for t in (k, v)]

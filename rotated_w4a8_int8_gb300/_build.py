@@ -26,7 +26,7 @@ SOURCES = [("api.cu", "api", []), ("quant.cu", "quant", []),
            ("quant.cu", "quant_norm", ["-DCONVROT_QUANT_NORM=1"]), ("gemm.cu", "gemm", []),
            ("int8_probe.cu", "int8_probe", []), ("decode_gemm_probe.cu", "decode_gemm_probe", []),
            ("norm_quant.cu", "norm_quant", []), ("rope.cu", "rope", []), ("gemm_few.cu", "gemm_few", []),
-           ("attention_few.cu", "attention_few", []), ("cache.cu", "cache", []),
+           ("attention_api.cu", "attention_api", []), ("attention_few.cu", "attention_few", []), ("cache.cu", "cache", []),
            *(("attention.cu", f"attention_{name}", [f"-DCONVROT_ATTENTION_TYPE=CONVROT_{name.upper()}"])
              for name in ("bf16", "fp16")),
            *(("gemm_fused.cu", f"gemm_fused_{name}", [f"-DCONVROT_FUSED_OUT=CONVROT_{name.upper()}"])

@@ -28,13 +28,15 @@
 // cluster of up to eight CTAs shares the keys; sums and outputs are joined
 // through distributed shared memory in a fixed order.
 #include <atomic>
+#include <cmath>
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_runtime.h>
 
 #include "../../include/convrot.h"
 #include "attention.cuh"
-#include "attention_many.cuh"
+#include "attention_kernels.cuh"
+#include "attention_map.cuh"
 #include "errors.h"
 #include "pdl.cuh"
 #include "tcgen05.cuh"
@@ -48,7 +50,7 @@ constexpr int THREADS = 384;              // warps 0-7: rows (two slots), 8: loa
 // SM's (168, with which they spilled).  2 x 128 x 208 + 128 x 80 <= 384 x 168.
 constexpr int ROW_REGISTERS = 208, OTHER_REGISTERS = 80;
 static_assert(256 * ROW_REGISTERS + 128 * OTHER_REGISTERS <= THREADS * 168, "registers");
-constexpr int MAX_SPLIT = 8;
+constexpr int MAX_SPLIT = MOST_SLICES;
 
 template <int DP, bool SPLIT>
 struct Layout {
@@ -94,11 +96,6 @@ struct Ragged {
 };
 
 // ------------------------------------------------------------------ PTX
-__device__ __forceinline__ void load_box_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];"
-      ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z) : "memory");
-}
 __device__ __forceinline__ void store_box_3d(const CUtensorMap* map, uint32_t src, int x, int y, int z) {
   asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];"
                ::"l"(reinterpret_cast<uint64_t>(map)), "r"(src), "r"(x), "r"(y), "r"(z) : "memory");
@@ -106,11 +103,6 @@ __device__ __forceinline__ void store_box_3d(const CUtensorMap* map, uint32_t sr
 __device__ __forceinline__ void prefetch_box_3d(const CUtensorMap* map, int x, int y, int z) {
   asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];"
                ::"l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z) : "memory");
-}
-__device__ __forceinline__ void load_box_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z, int w) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], [%2];"
-      ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
 // The products' warp runs as one, its values in uniform registers, and one lane
 // (`leader`) issues: with the whole loop inside `if (lane == 0)` every operand of
@@ -608,11 +600,11 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
         const Ragged r = *ragged;
         if (r.stage < 0) break;
         uint8_t* tile = tiles + (L::QTILES + r.stage) * L::TILE;
-        const int out = r.first + KEYS - r.end;
-        for (int j = lane; j < out * 8 * (DP / 64); j += 32) {
-          const int k = j / 8 % out, row = k < r.first ? k : r.end + k - r.first;
-          *reinterpret_cast<uint4*>(tile + j / (8 * out) * L::BOX + row * 128 + j % 8 * 16) = make_uint4(0, 0, 0, 0);
-        }
+        constexpr int PIECES = DP / 8;                     // 16-byte pieces of a row; a lane zeroes one of every 32 / PIECES rows
+        uint8_t* at = tile + lane % PIECES / 8 * L::BOX + lane % 8 * 16;
+        for (int row = lane / PIECES; row < r.first; row += 32 / PIECES) *reinterpret_cast<uint4*>(at + row * 128) = make_uint4(0, 0, 0, 0);
+#pragma unroll 4
+        for (int row = r.end + lane / PIECES; row < KEYS; row += 32 / PIECES) *reinterpret_cast<uint4*>(at + row * 128) = make_uint4(0, 0, 0, 0);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
@@ -865,23 +857,6 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
 }
 
 // ------------------------------------------------------------------ host side
-// Boxes of 64 columns x heads x rows (x pages): strides of dimensions with one element do not count.
-template <int DT>
-static bool make_map(CUtensorMap* map, const void* base, int D, const int64_t (&dims)[3], const int64_t (&strides)[3], int rank,
-                     int box_heads, int box_rows) {
-  EncodeTiledFn fn = encode_fn();
-  if (!fn) return false;
-  cuuint64_t size[4] = {static_cast<cuuint64_t>(D)}, pitch[3];
-  for (int i = 0; i < rank - 1; ++i) {
-    size[i + 1] = static_cast<cuuint64_t>(dims[i] > 0 ? dims[i] : 1);
-    pitch[i] = static_cast<cuuint64_t>(dims[i] > 1 ? strides[i] : D) * 2;
-  }
-  cuuint32_t box[4] = {64, static_cast<cuuint32_t>(box_heads), static_cast<cuuint32_t>(box_rows), 1}, one[4] = {1, 1, 1, 1};
-  return fn(map, DT == CONVROT_FP16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
-            static_cast<cuuint32_t>(rank), const_cast<void*>(base), size, pitch, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 constexpr int kMaxDevices = 64;
 
 // Clusters of `slices` CTAs of this kernel that are resident at once (0: none of this size).
@@ -931,18 +906,7 @@ static int launch(const Problem& p, const Work& w, int slices, int64_t items, cu
   bool made = make_map<DT>(&mq, p.q, p.D, q_dims, q_strides, 3, w.pack, w.tps);
   const int64_t out_strides[3] = {p.out_head, p.out_tok, 0};
   made = made && make_map<DT>(&mo, p.out, p.D, q_dims, out_strides, 3, 1, 32);
-  for (int i = 0; i < 2 && made; ++i) {
-    const void* base = i ? p.v : p.k;
-    const int64_t row = i ? p.v_row : p.k_row, head = i ? p.v_head : p.k_head, page = i ? p.v_page : p.k_page;
-    if (PAGED) {
-      const int size = 1 << p.page_log2;
-      const int64_t dims[3] = {p.heads_k, size, p.num_pages}, strides[3] = {head, row, page};
-      made = make_map<DT>(i ? &mv : &mk, base, p.D, dims, strides, 4, 1, size < KEYS ? size : KEYS);
-    } else {
-      const int64_t dims[3] = {p.heads_k, p.keys, 1}, strides[3] = {head, row, 0};
-      made = make_map<DT>(i ? &mv : &mk, base ? base : p.q, p.D, dims, strides, 3, 1, KEYS);
-    }
-  }
+  made = made && make_key_maps<DT, PAGED>(&mk, &mv, p, KEYS);
   if (!made) return convrot::record_error("cuTensorMapEncodeTiled failed for q, k, v or out");
   int resident = 0;
   cudaError_t e = resident_clusters<DT, DP, PAGED, SPLIT>(slices, &resident);
@@ -971,12 +935,17 @@ static int choose(const Problem& p, const Variant& variant, cudaStream_t st) {
   Work best = {1, KEYS, 2 * KEYS};
   int slices = 0;                            // 0: whole items
   double least = 0;
+  // Microseconds, fitted to runs of 1 to 700 rows per sequence over 64 to 16384
+  // keys: rounds of items or clusters; a tile of keys for both slots, or for one of
+  // a cluster's CTAs; what a round takes besides, more the more CTAs join.  (8 heads
+  // of 64, 24 rows, 1000 keys: whole 12.9 us, shared by four 10.3; 300 rows, 16384
+  // keys: 145 and 34; 56 heads, 700 rows: 287 and 328.)
+  const bool narrow = p.D <= 64;
   auto consider = [&](int pack, int n, int resident) {
     const Work w = {pack, KEYS / pack, (n ? 1 : 2) * (KEYS / pack)};
-    const double per = q / w.item_tokens, items = p.B * (per > 1 ? per : 1) * (p.heads_q / pack);
-    const double rounds = items > resident ? items / resident : 1;
-    // Microseconds.
-    const double t = n ? rounds * (key_tiles / n * 0.6 + 5.0 + (n > 1 ? 2.0 : 0.0)) : rounds * (key_tiles * 1.15 + 3.0);
+    const double per = std::ceil(q / w.item_tokens), rounds = std::ceil(p.B * per * (p.heads_q / pack) / resident);
+    const double t = n ? rounds * (std::ceil(key_tiles / n) * (narrow ? 0.70 : 0.83) + (narrow ? 7.5 : 8.5) + 0.7 * n)
+                       : rounds * (std::ceil(key_tiles) * (q > w.tps ? (narrow ? 1.11 : 1.38) : (narrow ? 1.0 : 1.24)) + 3.6) + 2.5;
     if (least == 0 || t < least) {
       least = t;
       best = w;

@@ -1,54 +1,72 @@
-// convrot_attention and convrot_paged_attention: few rows per K head, and the
-// C-ABI entry points.
+// convrot_attention and convrot_paged_attention, few rows per K head: single
+// tokens, or a few, over a cache.
 //
-// Single tokens over a long cache: each key and value is read once, and the bytes
-// bound it.  A cluster of up to 8 CTAs shares the keys of one sequence's K head,
-// a CTA's eight warps take blocks of 16 keys in turn, and a block goes from
-// memory into registers, the next one's loads under way while it is used.
+// Each key and value is read once and used for 1 to 16 rows, so their bytes
+// bound it and have to be kept coming: a warp asks for tiles of 64 keys by TMA,
+// up to three ahead (192 KB per SM on their way or in use), and four warps take
+// 16 keys of each.  A cluster of up to 16 CTAs shares the keys of a sequence's K
+// head; their parts are joined through distributed shared memory in a fixed
+// order.
 //
 // The products run on the warp-level tensor instruction (mma.sync m16n8k16) with
 // the keys as its 16-row operand and the query rows, eight to a tile, as the
 // other one: S^T = K Q^T, then O^T = V^T P^T.  At one to 16 rows a tcgen05 tile
-// would be mostly padding.  Which column of the head an operand's slot holds
-// does not matter as long as both operands agree, so a lane feeds K from 16
-// contiguous bytes of a key; V's pairs of neighbouring keys come from two rows'
-// 16 bytes by byte permutes, and P^T from S^T by an 8 x 8 transposition in
-// registers.  Softmax as in attention.cu: a reference per row that follows the
-// maximum once it has grown by 2^kLag, FP32 sums, weights rounded for the
-// product.  Warps and CTAs are joined in a fixed order through (distributed)
-// shared memory.
+// would be mostly padding.  The tiles lie swizzled in shared memory; K's operand
+// is read by ldmatrix, V's by its transposing form, and P^T comes from S^T by an
+// 8 x 8 transposition in registers.  Softmax as in attention.cu: a reference per
+// row that follows the maximum once it has grown by 2^kLag, FP32 sums, weights
+// rounded for the product.
+//
+// 19989 keys x 56 heads of 128, one token, BF16, pages of 64: 83 us (6.9 TB/s,
+// 103% of the copy bandwidth); 64 tokens over up to 8191 keys, 32 heads on 8: 213
+// us (6.4 TB/s).  Before, every warp loaded its blocks of 16 keys into registers
+// one ahead: 100 and 256 us, and 45 us where this takes 20 (2 K heads of 32768
+// keys: few CTAs, and a block took the memory's latency twice).
 #include <atomic>
 #include <cstdint>
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include "../../include/convrot.h"
 #include "attention.cuh"
-#include "attention_check.h"
-#include "attention_many.cuh"
+#include "attention_kernels.cuh"
+#include "attention_map.cuh"
 #include "errors.h"
 #include "pdl.cuh"
+#include "tcgen05.cuh"
 
 namespace cratt {
 
-static __device__ int g_error = 0;
+using namespace crgemm;
 
-constexpr int FEW_WARPS = 8;
-constexpr int FEW_ROWS = 16;             // most rows per K head that are taken here at once
-constexpr int FEW_SLICES = 8;
+constexpr int TILE_KEYS = 64;
+constexpr int FEW_WARPS = 4;                       // 16 keys of a tile each
+constexpr int FEW_THREADS = 32 * (FEW_WARPS + 1);
 
 template <int DP, int NT>
 struct FewLayout {
   static constexpr int ROWS = 8 * NT, PITCH = DP + 4;
-  static constexpr int PARTS = FEW_WARPS * ROWS * PITCH, JOINED = ROWS * PITCH;       // floats
-  static constexpr int SMEM = 4 * (PARTS + JOINED) + 8 * (FEW_WARPS + 1) * ROWS;
+  static constexpr int BOX = TILE_KEYS * 128, TILE = TILE_KEYS * DP * 2;     // a 64-wide column block; K or V
+  static constexpr int MOST_STAGES = DP == 128 ? 3 : 6;
+  static constexpr int PART = ROWS * PITCH * 4;
+  static constexpr int AUX = 1024;                    // barriers, then the parts' statistics
+  static constexpr int STATS = 256;
+  // the parts to be joined take the tiles' place at the end
+  static constexpr int space(int stages) {
+    return stages * 2 * TILE > (FEW_WARPS + 1) * PART ? stages * 2 * TILE : ((FEW_WARPS + 1) * PART + 1023) / 1024 * 1024;
+  }
+  static constexpr int smem(int stages) { return space(stages) + AUX + 1024; }
+  static_assert(STATS + (FEW_WARPS + 1) * ROWS * 8 <= AUX && 2 * MOST_STAGES * 8 + 8 <= STATS, "aux");
+  static_assert(2 * (smem(MOST_STAGES) + 1024) <= 233472, "two CTAs per SM");
 };
 
-// 16 bytes of a key or value: read once, kept out of L1.
-__device__ __forceinline__ uint4 load_once(const char* p) {
-  uint4 v;
-  asm volatile("ld.global.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
-      : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
-  return v;
+__device__ __forceinline__ void ldmatrix4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
 }
 
 template <int DT>
@@ -99,265 +117,321 @@ __device__ __forceinline__ void join(float2& total, float2 part, float c, float&
   total = make_float2(top, total.y * keep + part.y * take);
 }
 
+// Joins the warps' parts (parts [warp][row][pitch], with their references and sums), then, through distributed shared
+// memory, the cluster's CTAs', in a fixed order, and writes the rows.  Every thread of the CTA; `joined` is one part more.
+// Rows r0 .. r0 + held - 1 of the sequence's rows x group of K head head_kv.
+template <int DT>
+__device__ __forceinline__ void join_parts(const Problem& p, const Sequence& s, int64_t r0, int head_kv, int held, int slices,
+                                           int rank, int warps, const float* parts, float* joined, const float2* part_stats,
+                                           float2* joined_stats, int part_rows, int pitch) {
+  const int group = p.heads_q / p.heads_k;
+  auto finish = [&](int r, int col, float2 total, const float (&y)[4]) {
+    const float f = total.y == 0.f ? 0.f : 1.f / total.y;
+    float z[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) z[j] = total.y == 0.f ? 0.f : y[j] * f;
+    const int64_t at = r0 + r;
+    char* dst = static_cast<char*>(p.out) +
+                2 * ((s.q_start + at / group) * p.out_tok + (head_kv * group + at % group) * p.out_head + col);
+    asm volatile("st.global.v2.b32 [%0], {%1, %2};" ::"l"(dst), "r"(pack2<DT>(z[0], z[1])), "r"(pack2<DT>(z[2], z[3])) : "memory");
+  };
+  auto add = [&](float2& total, float (&y)[4], float2 stats, const float4& part) {
+    float keep, take;
+    join(total, stats, p.scale_log2, keep, take);
+    y[0] = y[0] * keep + part.x * take;
+    y[1] = y[1] * keep + part.y * take;
+    y[2] = y[2] * keep + part.z * take;
+    y[3] = y[3] * keep + part.w * take;
+  };
+  const int cols4 = p.D / 4;
+  for (int i = threadIdx.x; i < held * cols4; i += blockDim.x) {
+    const int r = i / cols4, col = 4 * (i % cols4);
+    float2 total = make_float2(-INFINITY, 0.f);
+    float y[4] = {};
+#pragma unroll 4
+    for (int j = 0; j < warps; ++j)
+      add(total, y, part_stats[j * part_rows + r], *reinterpret_cast<const float4*>(parts + (j * part_rows + r) * pitch + col));
+    if (slices == 1) {
+      finish(r, col, total, y);
+    } else {
+      *reinterpret_cast<float4*>(joined + r * pitch + col) = make_float4(y[0], y[1], y[2], y[3]);
+      if (col == 0) joined_stats[r] = total;
+    }
+  }
+  if (slices == 1) {
+    __syncthreads();
+    return;
+  }
+  cluster_barrier();
+  // the cluster's CTAs take the rows' columns in turn
+  for (int i = rank + slices * threadIdx.x; i < held * cols4; i += slices * blockDim.x) {
+    const int r = i / cols4, col = 4 * (i % cols4);
+    float2 total = make_float2(-INFINITY, 0.f);
+    float y[4] = {};
+    for (int j = 0; j < slices; ++j)
+      add(total, y, load_cluster2(shared_of_rank(joined_stats + r, j)), load_cluster4(shared_of_rank(joined + r * pitch + col, j)));
+    finish(r, col, total, y);
+  }
+  cluster_barrier();                     // no CTA leaves, or begins again, while another still reads from it
+}
+
 template <int DT, int DP, int NT, bool PAGED>
-__global__ void __launch_bounds__(32 * FEW_WARPS, NT == 1 ? 2 : 1)
-few_kernel(const __grid_constant__ Problem p, const int slices) {
+__global__ void __launch_bounds__(FEW_THREADS, NT == 1 ? 3 : 2)      // (three where one or two stages are enough)
+few_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+              const __grid_constant__ Problem p, const int slices, const uint32_t stages) {
   using L = FewLayout<DP, NT>;
-  constexpr int KP = DP / 32, VP = DP / 64;                 // 16-byte pieces of a lane: per key of K, per key of V
-  extern __shared__ float few_smem[];
-  float* parts = few_smem;                                  // [warp][row][PITCH]
-  float* joined = few_smem + L::PARTS;                      // [row][PITCH]
-  float2* part_stats = reinterpret_cast<float2*>(few_smem + L::PARTS + L::JOINED);       // [warp][row]
-  float2* joined_stats = part_stats + FEW_WARPS * L::ROWS;                               // [row]
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, quad = lane >> 2, i4 = lane & 3;
+  constexpr int KK = DP / 16;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* tiles = smem_raw + (1024 - (smem_u32(smem_raw) & 1023)) % 1024;
+  uint8_t* aux = tiles + L::space(stages);
+  const uint32_t full0 = smem_u32(aux), empty0 = full0 + 8 * L::MOST_STAGES;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(aux + 16 * L::MOST_STAGES);
+  float* parts = reinterpret_cast<float*>(tiles);
+  float* joined = parts + FEW_WARPS * L::ROWS * L::PITCH;
+  float2* part_stats = reinterpret_cast<float2*>(aux + L::STATS);
+  float2* joined_stats = part_stats + FEW_WARPS * L::ROWS;
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
+  const int quad = lane >> 2, i4 = lane & 3;
   const int rank = blockIdx.x % slices, head_kv = blockIdx.x / slices, b = blockIdx.y;
   const int group = p.heads_q / p.heads_k;
-  convrot::after_previous_kernel();
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (threadIdx.x == 0) {
+    for (uint32_t i = 0; i < stages; ++i) {
+      mbar_init(full0 + 8 * i, 1);
+      mbar_init(empty0 + 8 * i, FEW_WARPS);
+    }
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  __syncthreads();
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const Sequence s = load_sequence(p, b, &g_error);
   const int64_t rows = static_cast<int64_t>(s.q_len) * group;
-  const int base = PAGED ? s.k_start & ~15 : s.k_start, lo = s.k_start - base, hi = lo + s.k_len;
-  const char* k_head = static_cast<const char*>(p.k) + 2 * head_kv * p.k_head;
-  const char* v_head = static_cast<const char*>(p.v) + 2 * head_kv * p.v_head;
-  const int pieces = p.D / 8;
-  const int32_t* table = PAGED ? p.pages + b * p.ld_pages : nullptr;
+  const int box_rows = PAGED ? min(1 << p.page_log2, TILE_KEYS) : TILE_KEYS;
+  const int base = PAGED ? s.k_start / box_rows * box_rows : s.k_start, lo = s.k_start - base, hi = lo + s.k_len;
+  uint32_t stage = 0, phase = 0;
+  bool ok = true;
 
   for (int64_t r0 = 0; r0 < rows; r0 += L::ROWS) {
     const int held = static_cast<int>(rows - r0 < L::ROWS ? rows - r0 : L::ROWS);
-    // Q^T: row quad of tile n, 16 bytes at piece 4 kp + i4
-    uint4 q[NT][KP];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const int r = 8 * n + quad;
-      const int64_t at = r0 + r;
-      const char* src = static_cast<const char*>(p.q) + 2 * ((s.q_start + at / group) * p.q_tok +
-                                                             (head_kv * group + at % group) * p.q_head);
-#pragma unroll
-      for (int kp = 0; kp < KP; ++kp)
-        q[n][kp] = r < held && 4 * kp + i4 < pieces ? convrot::load_global(reinterpret_cast<const uint4*>(src) + 4 * kp + i4)
-                                                    : make_uint4(0, 0, 0, 0);
-    }
-    // first key that this lane's rows (2 i4, 2 i4 + 1 of each tile) do not see; of the first and last row
-    int limit[NT][2];
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int e = 0; e < 2; ++e)
-        limit[n][e] = lo + seen(p, s, static_cast<int>((r0 + 8 * n + 2 * i4 + e) / group));
-    const int all = lo + seen(p, s, static_cast<int>(r0 / group));
-    const int last = min(hi, lo + seen(p, s, static_cast<int>((r0 + held - 1) / group)));
-    const int blocks = last > lo ? (last + 15) / 16 : 0;
-    const int first = static_cast<int>(static_cast<int64_t>(blocks) * rank / slices) + warp;
-    const int end = static_cast<int>(static_cast<int64_t>(blocks) * (rank + 1) / slices);
-
-    uint4 k[2][KP], v[4][VP];
-    auto page_of = [&](int blk) { return PAGED && blk < end ? convrot::load_global(table + ((base + 16 * blk) >> p.page_log2)) : 0; };
-    int page = page_of(first), page_next = page_of(first + FEW_WARPS);
-    // where a block's keys begin; a page out of range reads as no keys
-    auto usable = [&](int pg) {
-      if (!PAGED || (pg >= 0 && pg < p.num_pages)) return true;
-      atomicCAS(&g_error, 0, ERR_PAGE);
-      return false;
-    };
-    auto load_k = [&](int blk, int pg) {
-      const bool ok = usable(pg);
-      const int64_t row = PAGED ? (base + 16 * blk) & ((1 << p.page_log2) - 1) : static_cast<int64_t>(base) + 16 * blk;
-      const char* src = k_head + 2 * ((PAGED ? pg * p.k_page : 0) + row * p.k_row);
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int key = quad + 8 * h;
-        const bool in = ok && 16 * blk + key >= lo && 16 * blk + key < hi;
-#pragma unroll
-        for (int kp = 0; kp < KP; ++kp)
-          k[h][kp] = in && 4 * kp + i4 < pieces ? load_once(src + 2 * key * p.k_row + 16 * (4 * kp + i4)) : make_uint4(0, 0, 0, 0);
-      }
-    };
-    auto load_v = [&](int blk, int pg) {
-      const bool ok = usable(pg);
-      const int64_t row = PAGED ? (base + 16 * blk) & ((1 << p.page_log2) - 1) : static_cast<int64_t>(base) + 16 * blk;
-      const char* src = v_head + 2 * ((PAGED ? pg * p.v_page : 0) + row * p.v_row);
-#pragma unroll
-      for (int h = 0; h < 4; ++h) {
-        const int key = 2 * i4 + (h & 1) + 8 * (h >> 1);
-        const bool in = ok && 16 * blk + key >= lo && 16 * blk + key < hi;
-#pragma unroll
-        for (int c = 0; c < VP; ++c)
-          v[h][c] = in && 8 * c + quad < pieces ? load_once(src + 2 * key * p.v_row + 16 * (8 * c + quad)) : make_uint4(0, 0, 0, 0);
-      }
-    };
-    float o[NT][VP][4][4] = {};          // O^T: tile (c, u) holds columns 64 c + 8 quad + 2 u (+1), rows 2 i4 (+1)
-    float m[NT][2], l[NT][2];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) m[n][0] = m[n][1] = -INFINITY, l[n][0] = l[n][1] = 0.f;
-    if (first < end) {
-      load_k(first, page);
-      load_v(first, page);
-    }
-    for (int blk = first; blk < end; blk += FEW_WARPS) {
-      const int next = blk + FEW_WARPS;
-      const int page_after = page_of(next + FEW_WARPS);
-      float x[NT][4] = {};               // S^T: keys quad, quad + 8 of rows 2 i4, 2 i4 + 1
-#pragma unroll
-      for (int kp = 0; kp < KP; ++kp)
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          mma<DT>(x[n], k[0][kp].x, k[1][kp].x, k[0][kp].y, k[1][kp].y, q[n][kp].x, q[n][kp].y);
-          mma<DT>(x[n], k[0][kp].z, k[1][kp].z, k[0][kp].w, k[1][kp].w, q[n][kp].z, q[n][kp].w);
-        }
-      if (next < end) load_k(next, page_next);
-      bool grown = false;
-      const bool whole = 16 * blk + 16 <= all && !(blk == 0 && lo > 0);
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        if (!whole) {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int key = 16 * blk + quad + 8 * (j >> 1);
-            if (key < lo || key >= limit[n][j & 1]) x[n][j] = -INFINITY;
+    const int last = min(hi, lo + seen(p, s, static_cast<int>((r0 + held - 1) / group)));       // keys that the last row sees
+    const int64_t n = last > lo ? (last + TILE_KEYS - 1) / TILE_KEYS : 0;
+    const int t0 = static_cast<int>(n * rank / slices), t1 = static_cast<int>(n * (rank + 1) / slices);
+    if (warp == FEW_WARPS) {
+      // -------------------------------------------------------------- loads
+      const int boxes = TILE_KEYS / box_rows, at = lane % boxes * box_rows, col = lane / boxes % (DP / 64);
+      const bool is_v = lane / boxes >= DP / 64, issues = lane < 2 * boxes * (DP / 64);
+      auto page_of = [&](int t) {
+        const int64_t pos = static_cast<int64_t>(base) + static_cast<int64_t>(t) * TILE_KEYS + at;
+        return PAGED && pos < static_cast<int64_t>(base) + hi ? convrot::load_global(p.pages + b * p.ld_pages + (pos >> p.page_log2)) : -1;
+      };
+      int page = t0 < t1 ? page_of(t0) : -1;
+      uint32_t issued = 0, issued_phase = 0;
+      for (int t = t0; ok && !p.starve && t < t1; ++t) {
+        const int page_next = t + 1 < t1 ? page_of(t + 1) : -1;
+        ok = __all_sync(0xffffffffu, mbar_wait(empty0 + 8 * stage, phase ^ 1u, ERR_WAIT_EMPTY, abort_flag));
+        if (!ok) break;
+        const int wanted = PAGED ? min(boxes, (hi - t * TILE_KEYS + box_rows - 1) / box_rows) : 1;
+        if (lane == 0) mbar_arrive_expect_tx(full0 + 8 * stage, 2 * wanted * box_rows * DP * 2);
+        __syncwarp();
+        if (issues && lane % boxes < wanted) {
+          const uint32_t dst = smem_u32(tiles) + (2 * stage + is_v) * L::TILE + col * L::BOX + at * 128;
+          const CUtensorMap* map = is_v ? &map_v : &map_k;
+          const int pos = base + t * TILE_KEYS + at;
+          if (PAGED) {
+            if (page < 0 || page >= p.num_pages) {
+              atomicCAS(&g_error, 0, ERR_PAGE);
+              page = p.num_pages;                      // past the last one: reads as zeros
+            }
+            load_box_4d(dst, map, full0 + 8 * stage, 64 * col, head_kv, pos & ((1 << p.page_log2) - 1), page);
+          } else {
+            load_box_3d(dst, map, full0 + 8 * stage, 64 * col, head_kv, pos);
           }
         }
-#pragma unroll
-        for (int e = 0; e < 2; ++e) grown |= (fmaxf(x[n][e], x[n][2 + e]) - m[n][e]) * p.scale_log2 > kLag;
+        __syncwarp();
+        issued |= 1u << stage;
+        issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
+        page = page_next;
+        if (++stage == stages) { stage = 0; phase ^= 1u; }
       }
-      if (__any_sync(0xffffffffu, grown)) {
+      if (!ok) {
+        const uint64_t t_start = globaltimer();        // what is still in flight lands before the CTA can exit
+        for (uint32_t i = 0; i < stages; ++i)
+          while ((issued >> i & 1u) && !mbar_try_wait(full0 + 8 * i, issued_phase >> i & 1u) && globaltimer() - t_start < kWaitLimitNs) {}
+      }
+    } else {
+      // -------------------------------------------------------------- rows
+      // Q^T: row quad of tile n, columns 16 kk + 2 i4 (+1) and those + 8
+      uint32_t q[NT][KK][2];
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+      for (int j = 0; j < NT; ++j) {
+        const int r = 8 * j + quad;
+        const int64_t qr = r0 + r;
+        const char* src = static_cast<const char*>(p.q) + 2 * ((s.q_start + qr / group) * p.q_tok +
+                                                               (head_kv * group + qr % group) * p.q_head);
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float top = fmaxf(m[n][e], fmaxf(x[n][e], x[n][2 + e]));
+        for (int kk = 0; kk < KK; ++kk)
 #pragma unroll
-            for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-            const float f = top == m[n][e] ? 1.f : exp2_approx((m[n][e] - top) * p.scale_log2);
-            m[n][e] = top;
-            l[n][e] *= f;
+          for (int h = 0; h < 2; ++h) {
+            const int c = 16 * kk + 8 * h + 2 * i4;
+            q[j][kk][h] = r < held && c < p.D ? static_cast<uint32_t>(convrot::load_global(reinterpret_cast<const int32_t*>(src + 2 * c))) : 0u;
+          }
+      }
+      // first key that this lane's rows (2 i4, 2 i4 + 1 of each tile) do not see
+      int limit[NT][2];
 #pragma unroll
-            for (int c = 0; c < VP; ++c)
+      for (int j = 0; j < NT; ++j)
 #pragma unroll
-              for (int u = 0; u < 4; ++u) {
-                o[n][c][u][e] *= f;
-                o[n][c][u][2 + e] *= f;
+        for (int e = 0; e < 2; ++e) limit[j][e] = lo + seen(p, s, static_cast<int>((r0 + 8 * j + 2 * i4 + e) / group));
+      const int all = lo + seen(p, s, static_cast<int>(r0 / group));
+      float o[NT][KK][4] = {};                         // O^T: columns 16 u + quad (+8), rows 2 i4 (+1)
+      float m[NT][2], l[NT][2];
+#pragma unroll
+      for (int j = 0; j < NT; ++j) m[j][0] = m[j][1] = -INFINITY, l[j][0] = l[j][1] = 0.f;
+      // ldmatrix: this lane's row of the warp's 16 keys, and its 16-byte piece's low bit
+      const int k_row = 16 * warp + (lane & 7) + (lane & 8), k_piece = lane >> 4;
+      const int v_row = 16 * warp + (lane & 7) + (lane >> 4 << 3), v_piece = lane >> 3 & 1;
+      for (int t = t0; t < t1; ++t) {
+        ok = __all_sync(0xffffffffu, mbar_wait(full0 + 8 * stage, phase, ERR_WAIT_FULL, abort_flag));
+        if (!ok) break;
+        const int k0 = t * TILE_KEYS + 16 * warp;      // the warp's first key
+        const uint32_t kt = smem_u32(tiles) + 2 * stage * L::TILE, vt = kt + L::TILE;
+        if (k0 < last) {
+          float x[NT][2][4] = {};                      // S^T in two sums: keys quad, quad + 8 of rows 2 i4, 2 i4 + 1
+#pragma unroll
+          for (int kk = 0; kk < KK; ++kk) {
+            uint32_t a[4];
+            const int piece = 2 * kk + k_piece;
+            ldmatrix4(kt + piece / 8 * L::BOX + k_row * 128 + ((piece & 7) ^ (k_row & 7)) * 16, a);
+#pragma unroll
+            for (int j = 0; j < NT; ++j) mma<DT>(x[j][kk & 1], a[0], a[1], a[2], a[3], q[j][kk][0], q[j][kk][1]);
+          }
+          const bool edge = k0 + 16 > hi || k0 < lo;   // keys that are not the sequence's
+          const bool whole = k0 + 16 <= all && !edge;
+          bool grown = false;
+#pragma unroll
+          for (int j = 0; j < NT; ++j) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[j][0][i] += x[j][1][i];
+            if (!whole) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int key = k0 + quad + 8 * (i >> 1);
+                if (key < lo || key >= limit[j][i & 1]) x[j][0][i] = -INFINITY;
+              }
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) grown |= (fmaxf(x[j][0][e], x[j][0][2 + e]) - m[j][e]) * p.scale_log2 > kLag;
+          }
+          if (__any_sync(0xffffffffu, grown)) {
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                float top = fmaxf(m[j][e], fmaxf(x[j][0][e], x[j][0][2 + e]));
+#pragma unroll
+                for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+                const float f = top == m[j][e] ? 1.f : exp2_approx((m[j][e] - top) * p.scale_log2);
+                m[j][e] = top;
+                l[j][e] *= f;
+#pragma unroll
+                for (int u = 0; u < KK; ++u) {
+                  o[j][u][e] *= f;
+                  o[j][u][2 + e] *= f;
+                }
               }
           }
-      }
-      uint32_t w[NT][2];                 // P^T: row quad, keys 2 i4 (+1) and those + 8
+          uint32_t w[NT][2];                           // P^T: row quad, keys 2 i4 (+1) and those + 8
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        float e[4];
+          for (int j = 0; j < NT; ++j) {
+            float e[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float r = m[n][j & 1];
-          e[j] = exp2_approx(fmaf(x[n][j], p.scale_log2, kLift<DT> - (r == -INFINITY ? 0.f : r * p.scale_log2)));
+            for (int i = 0; i < 4; ++i) {
+              const float r = m[j][i & 1];
+              e[i] = exp2_approx(fmaf(x[j][0][i], p.scale_log2, kLift<DT> - (r == -INFINITY ? 0.f : r * p.scale_log2)));
+            }
+            l[j][0] += e[0] + e[2];
+            l[j][1] += e[1] + e[3];
+            w[j][0] = transpose(pack2<DT>(e[0], e[1]));
+            w[j][1] = transpose(pack2<DT>(e[2], e[3]));
+          }
+          // keys outside the sequence: their values are cleared (0 x NaN), pairs of keys 2 i4 (+1) and those + 8
+          uint32_t keep[2] = {0xffffffffu, 0xffffffffu};
+          if (edge) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int key = k0 + 8 * h + 2 * i4;
+              keep[h] = (key >= lo && key < hi ? 0xffffu : 0u) | (key + 1 >= lo && key + 1 < hi ? 0xffff0000u : 0u);
+            }
+          }
+#pragma unroll
+          for (int u = 0; u < KK; ++u) {
+            uint32_t a[4];
+            const int piece = 2 * u + v_piece;
+            ldmatrix4_trans(vt + piece / 8 * L::BOX + v_row * 128 + ((piece & 7) ^ (v_row & 7)) * 16, a);
+            if (edge) {
+              a[0] &= keep[0];
+              a[1] &= keep[0];
+              a[2] &= keep[1];
+              a[3] &= keep[1];
+            }
+#pragma unroll
+            for (int j = 0; j < NT; ++j) mma<DT>(o[j][u], a[0], a[1], a[2], a[3], w[j][0], w[j][1]);
+          }
         }
-        l[n][0] += e[0] + e[2];
-        l[n][1] += e[1] + e[3];
-        w[n][0] = transpose(pack2<DT>(e[0], e[1]));
-        w[n][1] = transpose(pack2<DT>(e[2], e[3]));
+        __syncwarp();
+        if (lane == 0) mbar_arrive_local(empty0 + 8 * stage);
+        if (++stage == stages) { stage = 0; phase ^= 1u; }
       }
+      // the warps' parts, where the tiles were: every warp is done with them
+      asm volatile("bar.sync 1, %0;" ::"n"(32 * FEW_WARPS) : "memory");
 #pragma unroll
-      for (int c = 0; c < VP; ++c)
+      for (int j = 0; j < NT; ++j)
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const uint32_t r0_ = (&v[0][c].x)[u], r1_ = (&v[1][c].x)[u], r2_ = (&v[2][c].x)[u], r3_ = (&v[3][c].x)[u];
-          const uint32_t a0 = __byte_perm(r0_, r1_, 0x5410), a1 = __byte_perm(r0_, r1_, 0x7632);
-          const uint32_t a2 = __byte_perm(r2_, r3_, 0x5410), a3 = __byte_perm(r2_, r3_, 0x7632);
+        for (int e = 0; e < 2; ++e) {
 #pragma unroll
-          for (int n = 0; n < NT; ++n) mma<DT>(o[n][c][u], a0, a1, a2, a3, w[n][0], w[n][1]);
+          for (int d = 4; d < 32; d <<= 1) l[j][e] += __shfl_xor_sync(0xffffffffu, l[j][e], d);
+          const int r = 8 * j + 2 * i4 + e;
+          if (r < held) {
+            if (quad == 0) part_stats[warp * L::ROWS + r] = make_float2(m[j][e], l[j][e]);
+            float* dst = parts + (warp * L::ROWS + r) * L::PITCH + quad;
+#pragma unroll
+            for (int u = 0; u < KK; ++u) {
+              dst[16 * u] = o[j][u][e];
+              dst[16 * u + 8] = o[j][u][2 + e];
+            }
+          }
         }
-      if (next < end) load_v(next, page_next);
-      page_next = page_after;
     }
-    // the warps' parts
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-#pragma unroll
-        for (int d = 4; d < 32; d <<= 1) l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], d);
-        const int r = 8 * n + 2 * i4 + e;
-        if (r < held) {
-          if (quad == 0) part_stats[warp * L::ROWS + r] = make_float2(m[n][e], l[n][e]);
-          float* dst = parts + (warp * L::ROWS + r) * L::PITCH + 8 * quad;
-#pragma unroll
-          for (int c = 0; c < VP; ++c)
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-              *reinterpret_cast<float4*>(dst + 64 * c + 4 * h) = make_float4(o[n][c][2 * h][e], o[n][c][2 * h][2 + e],
-                                                                             o[n][c][2 * h + 1][e], o[n][c][2 * h + 1][2 + e]);
-        }
-      }
     __syncthreads();
-    auto finish = [&](int r, int col, float2 total, const float (&y)[4]) {
-      const float f = total.y == 0.f ? 0.f : 1.f / total.y;
-      float z[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) z[j] = total.y == 0.f ? 0.f : y[j] * f;
-      const int64_t at = r0 + r;
-      char* dst = static_cast<char*>(p.out) +
-                  2 * ((s.q_start + at / group) * p.out_tok + (head_kv * group + at % group) * p.out_head + col);
-      asm volatile("st.global.v2.b32 [%0], {%1, %2};" ::"l"(dst), "r"(pack2<DT>(z[0], z[1])), "r"(pack2<DT>(z[2], z[3])) : "memory");
-    };
-    const int cols4 = p.D / 4;
-    for (int i = threadIdx.x; i < held * cols4; i += 32 * FEW_WARPS) {
-      const int r = i / cols4, col = 4 * (i % cols4);
-      float2 total = make_float2(-INFINITY, 0.f);
-      float y[4] = {};
-#pragma unroll
-      for (int j = 0; j < FEW_WARPS; ++j) {
-        float keep, take;
-        join(total, part_stats[j * L::ROWS + r], p.scale_log2, keep, take);
-        const float4 part = *reinterpret_cast<const float4*>(parts + (j * L::ROWS + r) * L::PITCH + col);
-        y[0] = y[0] * keep + part.x * take;
-        y[1] = y[1] * keep + part.y * take;
-        y[2] = y[2] * keep + part.z * take;
-        y[3] = y[3] * keep + part.w * take;
-      }
-      if (slices == 1) {
-        finish(r, col, total, y);
-      } else {
-        *reinterpret_cast<float4*>(joined + r * L::PITCH + col) = make_float4(y[0], y[1], y[2], y[3]);
-        if (col == 0) joined_stats[r] = total;
-      }
-    }
-    if (slices > 1) {
-      cluster_barrier();
-      // the cluster's CTAs take the row's columns in turn
-      for (int i = rank + slices * threadIdx.x; i < held * cols4; i += slices * 32 * FEW_WARPS) {
-        const int r = i / cols4, col = 4 * (i % cols4);
-        float2 total = make_float2(-INFINITY, 0.f);
-        float y[4] = {};
-        for (int j = 0; j < slices; ++j) {
-          float keep, take;
-          join(total, load_cluster2(shared_of_rank(joined_stats + r, j)), p.scale_log2, keep, take);
-          const float4 part = load_cluster4(shared_of_rank(joined + r * L::PITCH + col, j));
-          y[0] = y[0] * keep + part.x * take;
-          y[1] = y[1] * keep + part.y * take;
-          y[2] = y[2] * keep + part.z * take;
-          y[3] = y[3] * keep + part.w * take;
-        }
-        finish(r, col, total, y);
-      }
-      cluster_barrier();                 // no CTA leaves, or begins again, while another still reads from it
-    } else {
-      __syncthreads();
-    }
+    join_parts<DT>(p, s, r0, head_kv, held, slices, rank, FEW_WARPS, parts, joined, part_stats, joined_stats, L::ROWS, L::PITCH);
+    fence_proxy_async_smem();            // the next rows' tiles come where the parts were
+    __syncthreads();
+    ok = *abort_flag == 0;
   }
 }
 
 // ------------------------------------------------------------------ host side
 template <int DT, int DP, int NT, bool PAGED>
 static int launch_few(const Problem& p, int slices, cudaStream_t st) {
-  constexpr int smem = FewLayout<DP, NT>::SMEM;
+  using L = FewLayout<DP, NT>;
   auto k = few_kernel<DT, DP, NT, PAGED>;
-  if (smem > 48 * 1024) {
-    static std::atomic<bool> known[64] = {};       // set up on this device (two threads may both do it)
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess && (dev >= 64 || !known[dev])) {
-      e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-      if (e == cudaSuccess && dev < 64) known[dev] = true;
-    }
-    if (e != cudaSuccess) return convrot::record_cuda_error("attention set-up", e);
+  static std::atomic<bool> known[64] = {};       // set up on this device (two threads may both do it)
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess && (dev >= 64 || !known[dev])) {
+    e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, L::smem(L::MOST_STAGES));
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e == cudaSuccess && dev < 64) known[dev] = true;
   }
-  const cudaError_t e = convrot::launch_after(k, dim3(p.heads_k * slices, p.B), 32 * FEW_WARPS, smem, slices, st, p, slices);
+  if (e != cudaSuccess) return convrot::record_cuda_error("attention set-up", e);
+  CUtensorMap mk, mv;
+  if (!make_key_maps<DT, PAGED>(&mk, &mv, p, TILE_KEYS)) return convrot::record_error("cuTensorMapEncodeTiled failed for k or v");
+  // no more stages than tiles: short keys leave room for more CTAs
+  const int64_t tiles = (static_cast<int64_t>(p.keys) + TILE_KEYS - 1) / TILE_KEYS, share = (tiles + slices - 1) / slices;
+  const int stages = static_cast<int>(share < 1 ? 1 : share < L::MOST_STAGES ? share : L::MOST_STAGES);
+  e = convrot::launch_after(k, dim3(p.heads_k * slices, p.B), FEW_THREADS, L::smem(stages), slices, st, mk, mv, p, slices,
+                            static_cast<uint32_t>(stages));
   return e == cudaSuccess ? CONVROT_OK : convrot::record_cuda_error("attention launch", e);
 }
 
@@ -366,151 +440,33 @@ static int launch_few(const Problem& p, int slices, cudaStream_t st) {
   return p.pages ? launch_few<DT, DP, NT, true>(p, slices, st) : launch_few<DT, DP, NT, false>(p, slices, st);
 }
 
-template <int DT>
-static int few(const Problem& p, bool many_rows, int slices, cudaStream_t st) {
-  if (p.D <= 64) return many_rows ? launch_few<DT, 64, 2>(p, slices, st) : launch_few<DT, 64, 1>(p, slices, st);
-  return many_rows ? launch_few<DT, 128, 2>(p, slices, st) : launch_few<DT, 128, 1>(p, slices, st);
+// CTAs that share the keys of a sequence's K head: as many as fit the SMs twice
+// (one token, 56 heads x 19989 keys: 4 or 5 CTAs 83 us, 2 97 us, 6, which take
+// two rounds, 99 us; 2 heads x 32768 keys: 16 CTAs 20 us, 8 33 us), two tiles or
+// more for each; with more heads than that, four where the keys are long, so that
+// the last round is short (512 x 8191 keys: 213 us, whole 242 us; 512 x 512: 26 to
+// 41 us in parts, whole 16 us).
+static int few_slices(const Problem& p) {
+  const int64_t units = static_cast<int64_t>(p.heads_k) * p.B;
+  const int64_t keys = p.seqs && !p.pages ? (p.keys + p.B - 1) / p.B : p.keys, tiles = (keys + TILE_KEYS - 1) / TILE_KEYS;
+  int64_t n = 2 * 152 / units, most = tiles / 2;
+  if (n < 2) n = 4, most = tiles / 32;
+  // larger clusters than eight fit less well: only where they have the SMs for themselves (30 heads x 4096 keys: by
+  // eight 10 us, by ten 18 us)
+  if (n > 8) n = 152 / units > 8 ? 152 / units : 8;
+  n = n < most ? n : most;
+  return static_cast<int>(n < 1 ? 1 : n > MOST_FEW_SLICES ? MOST_FEW_SLICES : n);
 }
 
 template <int DT>
-static int run(const Problem& p, const Variant& variant, cudaStream_t st) {
-  const int64_t group = p.heads_q / p.heads_k, rows = (p.rows + p.B - 1) / p.B * group;    // an average sequence's rows per K head
-  const bool is_few = variant.kernel == FEW || (variant.kernel == CHOSEN && rows <= FEW_ROWS);
-  if (!is_few) return attention_many<DT>(p, variant, st);
-  int slices = variant.slices;
-  if (variant.kernel == CHOSEN) {
-    // CTAs for twice the SMs (two fit each), every warp with a block of keys or more
-    const int64_t units = static_cast<int64_t>(p.heads_k) * p.B, keys = p.seqs && !p.pages ? p.keys / p.B : p.keys;
-    int64_t n = 2 * 152 / units;
-    const int64_t most = (keys + 16 * FEW_WARPS - 1) / (16 * FEW_WARPS);
-    n = n < most ? n : most;
-    slices = static_cast<int>(n < 1 ? 1 : n > FEW_SLICES ? FEW_SLICES : n);
-  }
-  return few<DT>(p, rows > 8, slices, st);
+int attention_few(const Problem& p, int64_t rows, const Variant& variant, cudaStream_t st) {
+  const int slices = variant.kernel == CHOSEN ? few_slices(p) : variant.slices;
+  if (p.D <= 64) return rows > 8 ? launch_few<DT, 64, 2>(p, slices, st) : launch_few<DT, 64, 1>(p, slices, st);
+  return rows > 8 ? launch_few<DT, 128, 2>(p, slices, st) : launch_few<DT, 128, 1>(p, slices, st);
 }
+template int attention_few<CONVROT_BF16>(const Problem&, int64_t, const Variant&, cudaStream_t);
+template int attention_few<CONVROT_FP16>(const Problem&, int64_t, const Variant&, cudaStream_t);
 
-static int call(Problem p, convrot_dtype dtype, const int32_t* seqs, float scale, const Variant& variant, cudaStream_t st) {
-  if (!(scale > 0.f) || scale > 3.4e38f) return CONVROT_ERR_INVALID_ARG;
-  if (reinterpret_cast<uintptr_t>(seqs) % 16) return CONVROT_ERR_MISALIGNED;
-  p.seqs = reinterpret_cast<const int4*>(seqs);
-  p.scale_log2 = static_cast<float>(scale * 1.4426950408889634);
-  return dtype == CONVROT_BF16 ? run<CONVROT_BF16>(p, variant, st) : run<CONVROT_FP16>(p, variant, st);
-}
-
-static int check_rows(const Problem& p) {
-  const Extent q[3] = {{p.heads_q, p.q_head}, {p.rows, p.q_tok}, {1, 0}}, out[3] = {{p.heads_q, p.out_head}, {p.rows, p.out_tok}, {1, 0}};
-  const int st = check_input(p.q, p.D, q);
-  return st != CONVROT_OK ? st : check_output(p.out, p.D, out);
-}
-
-static int rows_call(Problem p, convrot_dtype dtype, const int32_t* seqs, float scale, const Variant& variant, cudaStream_t st) {
-  int e = check_heads(dtype, p.rows, p.heads_q, p.heads_k, p.D, p.B);
-  if (e != CONVROT_OK) return e;
-  if (p.keys < 0) return CONVROT_ERR_INVALID_ARG;
-  if (p.keys > kMostRows) return CONVROT_ERR_UNSUPPORTED;
-  if (!seqs) p.B = 1;
-  if (p.rows == 0 || p.B == 0) return CONVROT_OK;
-  if ((e = check_rows(p)) != CONVROT_OK) return e;
-  const Extent k[3] = {{p.heads_k, p.k_head}, {p.keys, p.k_row}, {1, 0}}, v[3] = {{p.heads_k, p.v_head}, {p.keys, p.v_row}, {1, 0}};
-  if (p.keys > 0 && ((e = check_input(p.k, p.D, k)) != CONVROT_OK || (e = check_input(p.v, p.D, v)) != CONVROT_OK)) return e;
-  return call(p, dtype, seqs, scale, variant, st);
-}
-
-static int pages_call(Problem p, convrot_dtype dtype, int page_size, const int32_t* pages, int pages_per_seq,
-                      const int32_t* seqs, float scale, const Variant& variant, cudaStream_t st) {
-  Table t = {pages, p.ld_pages, pages_per_seq, p.num_pages, page_size, 0, 0};
-  int e = check_heads(dtype, p.rows, p.heads_q, p.heads_k, p.D, p.B);
-  if (e == CONVROT_OK) e = check_table(&t, p.B);
-  if (e != CONVROT_OK) return e;
-  if (p.rows == 0 || p.B == 0) return CONVROT_OK;
-  if (!seqs) return CONVROT_ERR_INVALID_ARG;
-  if ((e = check_rows(p)) != CONVROT_OK) return e;
-  const Extent k[3] = {{p.heads_k, p.k_head}, {page_size, p.k_row}, {p.num_pages, p.k_page}},
-               v[3] = {{p.heads_k, p.v_head}, {page_size, p.v_row}, {p.num_pages, p.v_page}};
-  if (p.num_pages > 0 && ((e = check_input(p.k, p.D, k)) != CONVROT_OK || (e = check_input(p.v, p.D, v)) != CONVROT_OK)) return e;
-  p.keys = t.positions;
-  p.page_log2 = t.page_log2;
-  if (p.keys > 0) {
-    p.pages = pages;
-  } else {
-    p.k = p.v = nullptr;                       // no positions at all: every row is empty
-  }
-  return call(p, dtype, seqs, scale, variant, st);
-}
-
-cudaError_t take_write_error(int* v);
+cudaError_t take_few_error(int* v) { return crgemm::take_error_word(v); }
 
 }  // namespace cratt
-
-using namespace cratt;
-
-extern "C" int convrot_attention(const void* q, int64_t q_row, int64_t q_head, const void* k, int64_t k_row, int64_t k_head,
-                                 const void* v, int64_t v_row, int64_t v_head, void* out, int64_t out_row,
-                                 int64_t out_head, convrot_dtype dtype, int rows, int keys, int heads_q, int heads_k, int D,
-                                 const int32_t* seqs, int B, float scale, int causal, cudaStream_t stream) {
-  Problem p = {};
-  p.q = q, p.q_tok = q_row, p.q_head = q_head;
-  p.k = k, p.k_row = k_row, p.k_head = k_head;
-  p.v = v, p.v_row = v_row, p.v_head = v_head;
-  p.out = out, p.out_tok = out_row, p.out_head = out_head;
-  p.rows = rows, p.keys = keys, p.heads_q = heads_q, p.heads_k = heads_k, p.D = D, p.B = B, p.causal = causal != 0;
-  return rows_call(p, dtype, seqs, scale, {CHOSEN, 0}, stream);
-}
-
-extern "C" int convrot_paged_attention(const void* q, int64_t q_row, int64_t q_head, const void* k_cache, int64_t k_page,
-                                       int64_t k_row, int64_t k_head, const void* v_cache, int64_t v_page, int64_t v_row,
-                                       int64_t v_head, void* out, int64_t out_row, int64_t out_head, convrot_dtype dtype,
-                                       int rows, int heads_q, int heads_k, int D, int num_pages, int page_size,
-                                       const int32_t* pages, int64_t ld_pages, int pages_per_seq, const int32_t* seqs, int B,
-                                       float scale, int causal, cudaStream_t stream) {
-  Problem p = {};
-  p.q = q, p.q_tok = q_row, p.q_head = q_head;
-  p.k = k_cache, p.k_page = k_page, p.k_row = k_row, p.k_head = k_head;
-  p.v = v_cache, p.v_page = v_page, p.v_row = v_row, p.v_head = v_head;
-  p.out = out, p.out_tok = out_row, p.out_head = out_head;
-  p.rows = rows, p.heads_q = heads_q, p.heads_k = heads_k, p.D = D, p.B = B, p.causal = causal != 0;
-  p.num_pages = num_pages, p.ld_pages = ld_pages;
-  return pages_call(p, dtype, page_size, pages, pages_per_seq, seqs, scale, {CHOSEN, 0}, stream);
-}
-
-extern "C" int convrot_attention_selftest(const void* q, int64_t q_row, int64_t q_head, const void* k, int64_t k_page,
-                                          int64_t k_row, int64_t k_head, const void* v, int64_t v_page, int64_t v_row,
-                                          int64_t v_head, void* out, int64_t out_row, int64_t out_head, convrot_dtype dtype,
-                                          int rows, int heads_q, int heads_k, int D, int num_pages, int page_size, int paged,
-                                          const int32_t* pages, int64_t ld_pages, int pages_per_seq, const int32_t* seqs, int B,
-                                          float scale, int causal, int kernel, int slices, int starve, cudaStream_t stream) {
-  if (kernel < FEW || kernel > SHARED || slices < 1 || slices > FEW_SLICES || (kernel == WHOLE && slices != 1) ||
-      (kernel == FEW && starve))
-    return CONVROT_ERR_INVALID_ARG;
-  Problem p = {};
-  p.q = q, p.q_tok = q_row, p.q_head = q_head;
-  p.k = k, p.k_page = k_page, p.k_row = k_row, p.k_head = k_head;
-  p.v = v, p.v_page = v_page, p.v_row = v_row, p.v_head = v_head;
-  p.out = out, p.out_tok = out_row, p.out_head = out_head;
-  p.rows = rows, p.heads_q = heads_q, p.heads_k = heads_k, p.D = D, p.B = B, p.causal = causal != 0, p.starve = starve != 0;
-  const Variant variant = {kernel, slices};
-  if (!paged) {
-    p.keys = num_pages;
-    return rows_call(p, dtype, seqs, scale, variant, stream);
-  }
-  p.num_pages = num_pages, p.ld_pages = ld_pages;
-  return pages_call(p, dtype, page_size, pages, pages_per_seq, seqs, scale, variant, stream);
-}
-
-namespace convrot {
-cudaError_t take_attention_error_word(int* v) {
-  int each[4] = {};
-  cudaError_t e = take_attention_error<CONVROT_BF16>(&each[0]);
-  if (e == cudaSuccess) e = take_attention_error<CONVROT_FP16>(&each[1]);
-  if (e == cudaSuccess) e = take_write_error(&each[2]);
-  if (e == cudaSuccess) e = cudaMemcpyFromSymbol(&each[3], g_error, sizeof(int));
-  if (e == cudaSuccess && each[3] != 0) {
-    const int zero = 0;
-    e = cudaMemcpyToSymbol(g_error, &zero, sizeof(int));
-  }
-  *v = 0;
-  for (int i = 0; i < 4; ++i)
-    if (*v == 0) *v = each[i];
-  return e;
-}
-}  // namespace convrot

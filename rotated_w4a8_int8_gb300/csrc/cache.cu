@@ -9,6 +9,7 @@
 #include "../../include/convrot.h"
 #include "attention.cuh"
 #include "attention_check.h"
+#include "attention_kernels.cuh"
 #include "errors.h"
 #include "pdl.cuh"
 

@@ -90,8 +90,8 @@ def test_selftest_arguments():
     def call(kernel, slices, starve=0):
         return lib.convrot_attention_selftest(P, 512, 64, P, 0, 128, 64, P, 0, 128, 64, P, 512, 64, 0, 0, 8, 2, 64, 5, 0, 0,
                                               None, 0, 0, None, 1, 0.125, 0, kernel, slices, starve, None)
-    assert call(1, 8) == 0 and call(2, 1) == 0 and call(3, 7, 1) == 0
-    for kernel, slices, starve in ((0, 1, 0), (4, 1, 0), (1, 0, 0), (1, 9, 0), (2, 2, 0), (3, 9, 0), (1, 1, 1)):
+    assert call(1, 16) == 0 and call(1, 3, 1) == 0 and call(2, 1) == 0 and call(3, 7, 1) == 0
+    for kernel, slices, starve in ((0, 1, 0), (4, 1, 0), (1, 0, 0), (1, 17, 0), (2, 2, 0), (3, 9, 0)):
         assert call(kernel, slices, starve) == 1
 
 

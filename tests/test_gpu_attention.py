@@ -14,7 +14,7 @@ pytestmark = [pytest.mark.gpu,
 
 BF, HF = torch.bfloat16, torch.float16
 FEW, WHOLE, SHARED = 1, 2, 3
-KERNELS = [(FEW, 1), (FEW, 3), (FEW, 8), (WHOLE, 1), (SHARED, 1), (SHARED, 2), (SHARED, 5), (SHARED, 8)]
+KERNELS = [(FEW, 1), (FEW, 3), (FEW, 8), (FEW, 16), (WHOLE, 1), (SHARED, 1), (SHARED, 2), (SHARED, 5), (SHARED, 8)]
 
 
 @pytest.fixture(scope="module", autouse=True)
