@@ -1,0 +1,275 @@
+"""attention, paged_attention and cache_write where calls meet: captured and replayed on new lengths, on other streams and
+two at once, one launched while the one before still runs; offsets past 2^31 elements, many sequences, values that are no
+numbers, waits that run out.  The bound is derived in attention_util.py."""
+import math
+import time
+
+import pytest
+import torch
+
+from attention_util import check, paged, reference
+from gpu_util import DEV, ensure_built
+
+pytestmark = [pytest.mark.gpu,
+              pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a CUDA GPU")]
+
+BF, HF = torch.bfloat16, torch.float16
+EACH = [(1, 1), (1, 4), (2, 1), (3, 1), (3, 4)]        # kernel, CTAs that share keys
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    ensure_built()
+
+
+def rand(*shape, seed=0, dtype=BF):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    return torch.randn(*shape, generator=g, device=DEV).to(dtype)
+
+
+def i32(rows):
+    return torch.tensor(rows, dtype=torch.int32, device=DEV)
+
+
+@pytest.mark.parametrize("rows,heads_q,heads_k", [(3, 4, 2), (200, 4, 4), (700, 2, 1)])
+def test_captured_and_replayed_on_new_lengths(rows, heads_q, heads_k):
+    """The graph holds no length: seqs, tables and contents are read at each replay."""
+    import rotated_w4a8_int8_gb300 as cr
+    D, page = 64, 32
+    q, k, v = rand(rows, heads_q, D), rand(900, heads_k, D, seed=1), rand(900, heads_k, D, seed=2)
+    kc, vc = (torch.full((64, page, heads_k, D), math.nan, dtype=BF, device=DEV) for _ in range(2))
+    table, seqs, out = torch.zeros(2, 30, dtype=torch.int32, device=DEV), torch.zeros(2, 4, dtype=torch.int32, device=DEV), torch.zeros_like(q)
+    run = lambda: cr.paged_attention(q, kc, vc, table, seqs, out, causal=True)
+    run()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run()
+    for lens, window in [(((1, 1), (rows - 1, rows)), 0), (((rows - 2, rows + 100), (2, 800 - rows)), 0), (((0, 0), (rows, 777)), 45)]:
+        where, a, f = [], 0, 0
+        for n, m in lens:
+            where.append((a, n, f, m))
+            a, f = a + n, f + max(m, 0)
+        nk, nv, t, w = paged(k, v, where, page, window)
+        kc[:nk.shape[0]], vc[:nv.shape[0]] = nk, nv
+        table.zero_()
+        table[:, :t.shape[1]] = t
+        seqs.copy_(w)
+        out.fill_(3.0)
+        want = reference(q, k, v, where, D ** -0.5, True, out)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert cr.device_error() == 0
+        check(out, *want)
+
+
+def test_streams():
+    """The given stream is used, and two calls may run at once."""
+    import rotated_w4a8_int8_gb300 as cr
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    sets = [(rand(300, 4, 128, seed=s), rand(2000, 4, 128, seed=s + 10), rand(2000, 4, 128, seed=s + 20)) for s in range(2)]
+    small = [(rand(1, 4, 128, seed=s), k, v) for s, (_, k, v) in enumerate(sets)]
+    outs = [torch.zeros_like(q) for q, _, _ in sets + small]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for i, (q, k, v) in enumerate(sets + small):
+            cr.attention(q, k, v, outs[i], stream=(a, b)[i % 2])
+    torch.cuda.synchronize()
+    for o, (q, k, v) in zip(outs, sets + small):
+        check(o, *reference(q, k, v, [(0, q.shape[0], 0, 2000)], 128 ** -0.5, False, o))
+
+
+@pytest.mark.parametrize("rows,page", [(1, 16), (40, 64), (300, 64)])
+def test_chain_equals_synchronised_calls(rows, page):
+    """Every call is launched while the one before it still runs, reads what that one writes and overwrites what it
+    reads: rotary positions in place, keys and values into the cache, attention over them, whose output is the next
+    layer's input."""
+    import rotated_w4a8_int8_gb300 as cr
+    H, D, layers = 4, 64, 10
+    x0 = rand(rows, H, D)
+    x, y, out = (torch.empty_like(x0) for _ in range(3))
+    caches = [torch.empty(60, page, H, D, dtype=BF, device=DEV) for _ in range(2)]
+    start = [rand(60, page, H, D, seed=s) for s in (3, 4)]
+    table = torch.arange(59, -1, -1, dtype=torch.int32, device=DEV).view(1, 60)
+    seqs = [i32([(0, rows, 0, 100 + rows * (i + 1))]) for i in range(2)]
+    pos = torch.arange(rows, dtype=torch.int32, device=DEV).view(-1, 1)
+    freq = torch.tensor(cr.rope_inv_freq([32]), dtype=torch.float64, device=DEV)
+
+    def run(after=lambda: None):
+        x.copy_(x0)
+        for c, s in zip(caches, start):
+            c.copy_(s)
+        after()
+        for i in range(layers):
+            cr.qk_norm_rope(x, x, pos, freq, [32], y, out)
+            after()
+            cr.cache_write(out, x, *caches, table, seqs[i % 2])
+            after()
+            cr.paged_attention(y, *caches, table, seqs[i % 2], x, scale=0.02)
+            after()
+            cr.attention(y, out, x, out2, scale=1.0)
+            after()
+            x.copy_(out2)
+        return x
+
+    out2 = torch.empty_like(x0)
+    want = run(torch.cuda.synchronize).clone()
+    assert bool(torch.isfinite(want.float()).all()) and not torch.equal(want, x0)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run()
+    for _ in range(20):
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(x, want)
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(x, want) and cr.device_error() == 0
+
+
+@pytest.mark.parametrize("kernel", EACH)
+def test_runs_agree_bit_for_bit(kernel):
+    import rotated_w4a8_int8_gb300 as cr
+    q, k, v = rand(150, 8, 96, dtype=HF), rand(1500, 2, 96, seed=1, dtype=HF), rand(1500, 2, 96, seed=2, dtype=HF)
+    outs = [torch.empty_like(q) for _ in range(4)]
+    for o in outs:
+        cr.attention_selftest(q, k, v, o, *kernel)
+    torch.cuda.synchronize()
+    assert all(torch.equal(outs[0], o) for o in outs)
+
+
+@pytest.mark.parametrize("kernel", EACH)
+def test_offsets_past_32_bits(kernel):
+    """Pages 2^30 elements apart and rows 2^24: the last ones lie more than 2^31 elements behind the first."""
+    import rotated_w4a8_int8_gb300 as cr
+    D, H, page = 64, 2, 64
+    far = torch.empty(7 * 2 ** 29 + 2 ** 14, dtype=BF, device=DEV)
+    pages = far.as_strided((4, page, H, D), (2 ** 30, H * D, D, 1))
+    vpages = far.as_strided((4, page, H, D), (2 ** 30, H * D, D, 1), 2 ** 13)      # after the keys of the same page
+    k, v = rand(4 * page, H, D, seed=1), rand(4 * page, H, D, seed=2)
+    rows = far.as_strided((200, H, D), (2 ** 24, D, 1), 2 ** 15)
+    q = rand(200, H, D)
+    rows.copy_(q)
+    out = far.as_strided((200, H, D), (2 ** 24, D, 1), 2 ** 16)
+    out.fill_(7.0)
+    table, seqs = i32([[2, 0, 3, 1]]), i32([(0, 200, 0, 4 * page)])
+    cr.cache_write(k[56:], v[56:], pages, vpages, table, seqs)           # the last 200 tokens
+    cr.cache_write(k[:56], v[:56], pages, vpages, table, i32([(0, 56, 0, 56)]))
+    cr.attention_selftest(rows, pages, vpages, out, *kernel, pages=table, seqs=seqs)
+    torch.cuda.synchronize()
+    assert cr.device_error() == 0
+    for i, p in enumerate([2, 0, 3, 1]):
+        assert torch.equal(pages[p], k[i * page:(i + 1) * page]) and torch.equal(vpages[p], v[i * page:(i + 1) * page])
+    check(out, *reference(q, k, v, [(0, 200, 0, 4 * page)], D ** -0.5, False, out))
+    # the same rows as keys and values
+    cr.attention_selftest(rows[:5], rows, rows, out[:5], *kernel)
+    torch.cuda.synchronize()
+    check(out[:5], *reference(q[:5], q, q, [(0, 5, 0, 200)], D ** -0.5, False, out[:5]))
+
+
+@pytest.mark.parametrize("kernel", [(1, 2), (2, 1), (3, 2), None])
+def test_many_sequences(kernel):
+    import rotated_w4a8_int8_gb300 as cr
+    g = torch.Generator().manual_seed(4)
+    lens = [(int(n), int(m)) for n, m in zip(torch.randint(0, 9, (500,), generator=g), torch.randint(0, 70, (500,), generator=g))]
+    lens[77] = (300, 400)
+    order = torch.randperm(500, generator=g).tolist()      # rows of the sequences in no order
+    at, seqs, f = 0, [None] * 500, 0
+    for b in order:
+        n, m = lens[b]
+        seqs[b] = (at, n, f, m)
+        at, f = at + n, f + m
+    q, k, v = rand(at, 2, 64), rand(f, 1, 64, seed=1), rand(f, 1, 64, seed=2)
+    out = torch.empty_like(q)
+    if kernel:
+        cr.attention_selftest(q, k, v, out, *kernel, seqs=i32(seqs), causal=True)
+    else:
+        cr.attention(q, k, v, out, seqs=i32(seqs), causal=True)
+    torch.cuda.synchronize()
+    assert cr.device_error() == 0
+    check(out, *reference(q, k, v, seqs, 0.125, True, out))
+
+
+@pytest.mark.parametrize("kernel", EACH)
+def test_values_that_are_no_numbers(kernel):
+    """A row of q that is NaN stays alone; an Inf or NaN among the values shows in its column of every row that sees the
+    key, a NaN key in every row."""
+    import rotated_w4a8_int8_gb300 as cr
+    q, k, v = rand(40, 2, 64), rand(300, 2, 64, seed=1), rand(300, 2, 64, seed=2)
+    clean, out = torch.empty_like(q), torch.empty_like(q)
+    cr.attention_selftest(q, k, v, clean, *kernel)
+    bad = q.clone()
+    bad[7, 1, 3] = math.nan
+    cr.attention_selftest(bad, k, v, out, *kernel)
+    torch.cuda.synchronize()
+    assert bool(out[7, 1].isnan().all())
+    out[7, 1] = clean[7, 1]
+    assert torch.equal(out, clean)
+    bad = v.clone()
+    bad[123, 0, 5], bad[299, 1, 6] = math.inf, math.nan
+    cr.attention_selftest(q, k, bad, out, *kernel)
+    torch.cuda.synchronize()
+    assert bool((out[:, 0, 5] == math.inf).all()) and bool(out[:, 1, 6].isnan().all())
+    out[:, 0, 5], out[:, 1, 6] = clean[:, 0, 5], clean[:, 1, 6]
+    assert torch.equal(out, clean)
+    bad = k.clone()
+    bad[200, 1, 0] = math.nan
+    cr.attention_selftest(q, bad, v, out, *kernel)
+    torch.cuda.synchronize()
+    assert bool(out[:, 1].isnan().all()) and torch.equal(out[:, 0], clean[:, 0])
+
+
+@pytest.mark.parametrize("kernel", EACH)
+@pytest.mark.parametrize("dtype", [BF, HF])
+def test_equal_weights_of_many_keys(kernel, dtype):
+    """All scores zero: every weight is 1 / n, the smallest that n keys can share."""
+    import rotated_w4a8_int8_gb300 as cr
+    n = 30000
+    q, k, v = torch.zeros(130, 1, 64, dtype=dtype, device=DEV), rand(n, 1, 64, dtype=dtype), rand(n, 1, 64, seed=1, dtype=dtype) + 1
+    out = torch.empty_like(q)
+    cr.attention_selftest(q, k, v, out, *kernel)
+    torch.cuda.synchronize()
+    check(out, *reference(q, k, v, [(0, 130, 0, n)], 0.125, False, out))
+
+
+@pytest.mark.parametrize("kernel", [(1, 2), (2, 1), (3, 2)])
+def test_wait_that_runs_out_is_reported(kernel):
+    import rotated_w4a8_int8_gb300 as cr
+    assert cr.device_error() == 0
+    q, k, v = rand(9, 2, 64), rand(300, 2, 64, seed=1), rand(300, 2, 64, seed=2)
+    out = torch.empty_like(q)
+    t0 = time.time()
+    cr.attention_selftest(q, k, v, out, *kernel, starve=True)
+    code = cr.device_error()              # synchronises
+    assert code not in (0, 16, 17) and 1.0 < time.time() - t0 < 30.0
+    assert cr.device_error() == 0         # reading clears the word
+    cr.attention_selftest(q, k, v, out, *kernel)
+    torch.cuda.synchronize()
+    assert cr.device_error() == 0
+    check(out, *reference(q, k, v, [(0, 9, 0, 300)], 0.125, False, out))
+
+
+def test_heads_outermost():
+    """[heads, rows, D] tensors, seen as [rows, heads, D]."""
+    import rotated_w4a8_int8_gb300 as cr
+    q, k, v = (rand(4, n, 72, seed=n).transpose(0, 1) for n in (150, 333, 333))
+    out = torch.empty(4, 150, 72, dtype=BF, device=DEV).transpose(0, 1)
+    for rows in (150, 2):
+        cr.attention(q[:rows], k, v, out[:rows])
+        torch.cuda.synchronize()
+        check(out[:rows], *reference(q[:rows], k, v, [(0, rows, 0, 333)], 72 ** -0.5, False, out[:rows]))
+
+
+def test_errors_leave_outputs():
+    import rotated_w4a8_int8_gb300 as cr
+    q, k = rand(4, 2, 64), rand(8, 2, 64)
+    out = torch.full_like(q, 5.0)
+    for bad in (rand(4, 2, 65)[:, :, 1:], rand(4, 2, 68)[:, :, :64]):          # rows off 16 bytes
+        with pytest.raises(cr.ConvRotError, match="misaligned"):
+            cr.attention(bad, k, k, out)
+    with pytest.raises(cr.ConvRotError, match="unsupported"):
+        cr.attention(rand(4, 2, 144), rand(8, 2, 144), rand(8, 2, 144), rand(4, 2, 144))
+    with pytest.raises(cr.ConvRotError, match="invalid"):
+        cr.attention(q, rand(8, 2, 64)[:, :1].expand(8, 2, 64), k, out)        # heads on top of each other
+    torch.cuda.synchronize()
+    assert bool((out == 5).all())
