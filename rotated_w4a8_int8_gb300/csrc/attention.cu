@@ -250,17 +250,19 @@ __device__ __forceinline__ void find_tile(const Problem& p, const Work& w, int64
 }
 
 // ------------------------------------------------------------------ kernel
-template <int DT, int DP, bool PAGED, bool SPLIT>
+// KK: steps of 16 columns that a head takes (4, 5, 6 or 8), in tiles of 64 or 128 columns.  (Heads of 80 as 128: TODO.)
+template <int DT, int KK, bool PAGED, bool SPLIT>
 __global__ void __launch_bounds__(THREADS, 1)
 attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                  const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_out,
                  const __grid_constant__ Problem p, const Work w, const int slices) {
+  constexpr int DP = KK > 4 ? 128 : 64;
   using L = Layout<DP, SPLIT>;
   constexpr int STAGES = L::STAGES;
-  // FP32 accumulators; operands BF16 or FP16; M = 128, N = 128 keys or DP columns; V is not transposed (bit 16)
+  // FP32 accumulators; operands BF16 or FP16; M = 128, N = 128 keys or the head's columns; V is not transposed (bit 16)
   constexpr uint32_t KIND = (1u << 4) | (DT == CONVROT_BF16 ? (1u << 7) | (1u << 10) : 0u) | (static_cast<uint32_t>(128 >> 4) << 24);
   constexpr uint32_t IDESC_S = KIND | (static_cast<uint32_t>(KEYS >> 3) << 17);
-  constexpr uint32_t IDESC_O = KIND | (static_cast<uint32_t>(DP >> 3) << 17) | (1u << 16);
+  constexpr uint32_t IDESC_O = KIND | (static_cast<uint32_t>(KK * 2) << 17) | (1u << 16);
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* aux = smem_raw + (1024 - (smem_u32(smem_raw) & 1023)) % 1024;
@@ -494,7 +496,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
       tc_fence_after();
       const uint32_t a = desc_low(q_tiles + (SPLIT ? 0 : s) * L::TILE), b = desc_low(stages + stage * L::TILE);
 #pragma unroll
-      for (int kk = 0; kk < DP / 16; ++kk) {
+      for (int kk = 0; kk < KK; ++kk) {
         const uint32_t at = (kk / 4) * (L::BOX >> 4) + (kk % 4) * 2;
         mma_ss(tmem + L::S_COL + s * KEYS, a + at, b + at, DESC_HIGH, IDESC_S, kk > 0, leader);
       }
@@ -685,7 +687,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
           l0 *= f;
           l1 *= f;
 #pragma unroll 1
-          for (int c = 0; c < DP / 32; ++c) {
+          for (int c = 0; c < (KK + 1) / 2; ++c) {
             uint32_t o[32];
             tmem_ld32(o_addr + 32 * c, o);
             tmem_ld_wait();
@@ -803,7 +805,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
         const int rows = (128 + slices - 1) / slices, source = 2 * rank + slot;
         const uint32_t to = map_to_rank(smem_u32(tiles) + ((source * rows + row / slices) * L::PITCH) * 4, row % slices);
 #pragma unroll 1
-        for (int c = 0; c < DP / 32; ++c) {
+        for (int c = 0; c < (KK + 1) / 2; ++c) {
           uint32_t o[32];
           if (ok && any) {
             tmem_ld32(o_addr + 32 * c, o);
@@ -860,7 +862,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
 constexpr int kMaxDevices = 64;
 
 // Clusters of `slices` CTAs of this kernel that are resident at once (0: none of this size).
-template <int DT, int DP, bool PAGED, bool SPLIT>
+template <int DT, int KK, bool PAGED, bool SPLIT>
 static cudaError_t resident_clusters(int slices, int* out) {
   static std::atomic<int> known[kMaxDevices][MAX_SPLIT + 1] = {};    // 0: not set up (two threads may both do it)
   int dev = 0;
@@ -868,8 +870,8 @@ static cudaError_t resident_clusters(int slices, int* out) {
   if (e != cudaSuccess) return e;
   int n = dev < kMaxDevices ? known[dev][slices].load() : 0;
   if (n == 0) {
-    auto k = attention_kernel<DT, DP, PAGED, SPLIT>;
-    constexpr int smem = Layout<DP, SPLIT>::SMEM;
+    auto k = attention_kernel<DT, KK, PAGED, SPLIT>;
+    constexpr int smem = Layout<(KK > 4 ? 128 : 64), SPLIT>::SMEM;
     if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return e;
     int sms = 0;
     if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
@@ -897,9 +899,9 @@ static cudaError_t resident_clusters(int slices, int* out) {
   return cudaSuccess;
 }
 
-template <int DT, int DP, bool PAGED, bool SPLIT>
+template <int DT, int KK, bool PAGED, bool SPLIT>
 static int launch(const Problem& p, const Work& w, int slices, int64_t items, cudaStream_t st) {
-  using L = Layout<DP, SPLIT>;
+  using L = Layout<(KK > 4 ? 128 : 64), SPLIT>;
   static_assert(L::SMEM >= L::AUX + (L::QTILES + L::STAGES) * L::TILE + 1023, "shared memory");
   CUtensorMap mq, mk, mv, mo;
   const int64_t q_dims[3] = {p.heads_q, p.rows, 1}, q_strides[3] = {p.q_head, p.q_tok, 0};
@@ -909,12 +911,12 @@ static int launch(const Problem& p, const Work& w, int slices, int64_t items, cu
   made = made && make_key_maps<DT, PAGED>(&mk, &mv, p, KEYS);
   if (!made) return convrot::record_error("cuTensorMapEncodeTiled failed for q, k, v or out");
   int resident = 0;
-  cudaError_t e = resident_clusters<DT, DP, PAGED, SPLIT>(slices, &resident);
+  cudaError_t e = resident_clusters<DT, KK, PAGED, SPLIT>(slices, &resident);
   if (e != cudaSuccess) return convrot::record_cuda_error("attention set-up", e);
   if (resident <= 0) return CONVROT_ERR_UNSUPPORTED;
   const int64_t clusters = SPLIT ? items : items < resident ? items : resident;
   if (clusters * slices > INT32_MAX) return CONVROT_ERR_UNSUPPORTED;
-  e = convrot::launch_after(attention_kernel<DT, DP, PAGED, SPLIT>, dim3(static_cast<unsigned>(clusters * slices)), THREADS,
+  e = convrot::launch_after(attention_kernel<DT, KK, PAGED, SPLIT>, dim3(static_cast<unsigned>(clusters * slices)), THREADS,
                             L::SMEM, slices, st, mq, mk, mv, mo, p, w, slices);
   return e == cudaSuccess ? CONVROT_OK : convrot::record_cuda_error("attention launch", e);
 }
@@ -925,7 +927,7 @@ static int64_t most_items(const Problem& p, int tokens) {
   return B == 1 ? (rows + tokens - 1) / tokens : (rows + B * (tokens - 1)) / tokens;
 }
 
-template <int DT, int DP, bool PAGED>
+template <int DT, int KK, bool PAGED>
 static int choose(const Problem& p, const Variant& variant, cudaStream_t st) {
   const int group = p.heads_q / p.heads_k;
   // Lengths are on the device: every sequence is taken for an average one, with
@@ -958,15 +960,15 @@ static int choose(const Problem& p, const Variant& variant, cudaStream_t st) {
       if (variant.kernel == WHOLE && n != 0) break;
       if (variant.kernel == SHARED && n != variant.slices) continue;
       int resident = 0;
-      const cudaError_t e = n ? resident_clusters<DT, DP, PAGED, true>(n, &resident)
-                              : resident_clusters<DT, DP, PAGED, false>(1, &resident);
+      const cudaError_t e = n ? resident_clusters<DT, KK, PAGED, true>(n, &resident)
+                              : resident_clusters<DT, KK, PAGED, false>(1, &resident);
       if (e != cudaSuccess) return convrot::record_cuda_error("attention set-up", e);
       if (resident > 0) consider(pack, n, resident);
     }
     if (group == 1) break;
   }
   const int64_t items = most_items(p, best.item_tokens) * (p.heads_q / best.pack);
-  return slices ? launch<DT, DP, PAGED, true>(p, best, slices, items, st) : launch<DT, DP, PAGED, false>(p, best, 1, items, st);
+  return slices ? launch<DT, KK, PAGED, true>(p, best, slices, items, st) : launch<DT, KK, PAGED, false>(p, best, 1, items, st);
 }
 
 // This file is compiled once per type of q, k and v (CONVROT_ATTENTION_TYPE).
@@ -977,8 +979,12 @@ static int choose(const Problem& p, const Variant& variant, cudaStream_t st) {
 template <>
 int attention_many<CONVROT_ATTENTION_TYPE>(const Problem& p, const Variant& variant, cudaStream_t st) {
   constexpr int DT = CONVROT_ATTENTION_TYPE;
-  if (p.pages) return p.D <= 64 ? choose<DT, 64, true>(p, variant, st) : choose<DT, 128, true>(p, variant, st);
-  return p.D <= 64 ? choose<DT, 64, false>(p, variant, st) : choose<DT, 128, false>(p, variant, st);
+  const int steps = (p.D + 15) / 16;
+  if (p.pages)
+    return steps <= 4 ? choose<DT, 4, true>(p, variant, st) : steps == 5 ? choose<DT, 5, true>(p, variant, st)
+           : steps == 6 ? choose<DT, 6, true>(p, variant, st) : choose<DT, 8, true>(p, variant, st);
+  return steps <= 4 ? choose<DT, 4, false>(p, variant, st) : steps == 5 ? choose<DT, 5, false>(p, variant, st)
+         : steps == 6 ? choose<DT, 6, false>(p, variant, st) : choose<DT, 8, false>(p, variant, st);
 }
 
 template <>

@@ -84,6 +84,15 @@ template <> __device__ __forceinline__ uint32_t pack2<CONVROT_FP16>(float lo, fl
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+template <int DT>
+__device__ __forceinline__ float2 unpack2(uint32_t v);
+template <> __device__ __forceinline__ float2 unpack2<CONVROT_BF16>(uint32_t v) {
+  return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
+}
+template <> __device__ __forceinline__ float2 unpack2<CONVROT_FP16>(uint32_t v) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&v));
+}
+
 // 16 bytes of outputs.
 __device__ __forceinline__ void store_global(void* p, uint4 v) {
   asm volatile("st.global.v4.b32 [%0], {%1, %2, %3, %4};" ::"l"(p), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");

@@ -14,8 +14,10 @@
 // would be mostly padding.  The tiles lie swizzled in shared memory; K's operand
 // is read by ldmatrix, V's by its transposing form, and P^T comes from S^T by an
 // 8 x 8 transposition in registers.  Softmax as in attention.cu: a reference per
-// row that follows the maximum once it has grown by 2^kLag, FP32 sums, weights
-// rounded for the product.
+// row that follows the maximum once it has grown by 2^kLag, FP32 sums.  The weights
+// go into the product as two values of the operands' type, rounded and what that
+// left: the bytes bound this kernel, and a second product costs nothing that shows
+// (one token: 83.6 and 83.2 us), while one row's error grew by half with one.
 //
 // 19989 keys x 56 heads of 128, one token, BF16, pages of 64: 83 us (6.9 TB/s,
 // 103% of the copy bandwidth); 64 tokens over up to 8191 keys, 32 heads on 8: 213
@@ -341,7 +343,8 @@ few_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CU
                 }
               }
           }
-          uint32_t w[NT][2];                           // P^T: row quad, keys 2 i4 (+1) and those + 8
+          // P^T: row quad, keys 2 i4 (+1) and those + 8; rounded, and what the rounding left
+          uint32_t w[NT][2], rest[NT][2];
 #pragma unroll
           for (int j = 0; j < NT; ++j) {
             float e[4];
@@ -352,8 +355,13 @@ few_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CU
             }
             l[j][0] += e[0] + e[2];
             l[j][1] += e[1] + e[3];
-            w[j][0] = transpose(pack2<DT>(e[0], e[1]));
-            w[j][1] = transpose(pack2<DT>(e[2], e[3]));
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const uint32_t near = pack2<DT>(e[2 * h], e[2 * h + 1]);
+              const float2 back = unpack2<DT>(near);
+              w[j][h] = transpose(near);
+              rest[j][h] = transpose(pack2<DT>(e[2 * h] - back.x, e[2 * h + 1] - back.y));
+            }
           }
           // keys outside the sequence: their values are cleared (0 x NaN), pairs of keys 2 i4 (+1) and those + 8
           uint32_t keep[2] = {0xffffffffu, 0xffffffffu};
@@ -376,7 +384,10 @@ few_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CU
               a[3] &= keep[1];
             }
 #pragma unroll
-            for (int j = 0; j < NT; ++j) mma<DT>(o[j][u], a[0], a[1], a[2], a[3], w[j][0], w[j][1]);
+            for (int j = 0; j < NT; ++j) {
+              mma<DT>(o[j][u], a[0], a[1], a[2], a[3], w[j][0], w[j][1]);
+              mma<DT>(o[j][u], a[0], a[1], a[2], a[3], rest[j][0], rest[j][1]);
+            }
           }
         }
         __syncwarp();
