@@ -15,7 +15,7 @@
 // is read by ldmatrix, V's by its transposing form, and P^T comes from S^T by an
 // 8 x 8 transposition in registers.  Softmax as in attention.cu: a reference per
 // row that follows the maximum once it has grown by 2^kLag, FP32 sums.  The weights
-// go into the product as two values of the operands' type, rounded and what that
+// go into the product as two values of the operands' type, cut off and what that
 // left: the bytes bound this kernel, and a second product costs nothing that shows
 // (one token: 83.6 and 83.2 us), while one row's error grew by half with one.
 //
@@ -79,6 +79,21 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uin
   else
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Two values cut to the type (towards zero), and what that leaves of one: never below zero, and above it for every weight
+// above zero, so that an infinite value times both parts is the same infinity.
+template <int DT>
+__device__ __forceinline__ uint32_t truncate2(float lo, float hi) {
+  uint32_t v;
+  if constexpr (DT == CONVROT_BF16) asm("cvt.rz.bf16x2.f32 %0, %1, %2;" : "=r"(v) : "f"(hi), "f"(lo));
+  else asm("cvt.rz.f16x2.f32 %0, %1, %2;" : "=r"(v) : "f"(hi), "f"(lo));
+  return v;
+}
+template <int DT>
+__device__ __forceinline__ float left_over(float e, float cut) {
+  constexpr float least = DT == CONVROT_BF16 ? 1.1754943508222875e-38f : 5.9604644775390625e-8f;      // 2^-126, 2^-24
+  return e == cut && e > 0.f ? least : e - cut;
 }
 
 // 8 x 8 matrix of 16-bit values, transposed over the warp.
@@ -343,7 +358,7 @@ few_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CU
                 }
               }
           }
-          // P^T: row quad, keys 2 i4 (+1) and those + 8; rounded, and what the rounding left
+          // P^T: row quad, keys 2 i4 (+1) and those + 8; cut off, and what that left
           uint32_t w[NT][2], rest[NT][2];
 #pragma unroll
           for (int j = 0; j < NT; ++j) {
@@ -357,10 +372,10 @@ few_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CU
             l[j][1] += e[1] + e[3];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              const uint32_t near = pack2<DT>(e[2 * h], e[2 * h + 1]);
-              const float2 back = unpack2<DT>(near);
-              w[j][h] = transpose(near);
-              rest[j][h] = transpose(pack2<DT>(e[2 * h] - back.x, e[2 * h + 1] - back.y));
+              const uint32_t below = truncate2<DT>(e[2 * h], e[2 * h + 1]);
+              const float2 back = unpack2<DT>(below);
+              w[j][h] = transpose(below);
+              rest[j][h] = transpose(pack2<DT>(left_over<DT>(e[2 * h], back.x), left_over<DT>(e[2 * h + 1], back.y)));
             }
           }
           // keys outside the sequence: their values are cleared (0 x NaN), pairs of keys 2 i4 (+1) and those + 8
