@@ -398,11 +398,13 @@ int convrot_gemm_fused_selftest(const void* a_q, int64_t ld_aq,
  *   scale   > 0 and finite.
  *
  * Scores, maximum, sum and outputs are FP32; the weights p are rounded to
- * `dtype` for their product with v, and the result once.  An Inf or NaN in v
- * (or in a row of scores) shows in the rows that see that key; with `causal` it
- * may also show in earlier rows of the same sequence.  The result does not
- * depend on other sequences of the call, nor on the run; it may change in its
- * last bits with the sizes of the call (how the keys are split).
+ * `dtype` for their product with v (with up to 16 rows per K head held as two
+ * such values), and the result once.  An Inf or NaN in v shows in its column of
+ * the rows that see that key, one in a row's scores in that row; with `causal`
+ * one in v may also show in earlier rows of the same sequence.  The result does
+ * not depend on other sequences of the call, nor on the run; it may change in
+ * its last bits with the sizes of the call (how the keys are split).
+ * Limits: rows, keys <= 2^30, heads_q <= 65536, strides < 2^39 elements.
  * Alignment: every pointer 16-byte aligned, row and head strides multiples of 8
  * elements and not below D (where that dimension is more than one long).
  */

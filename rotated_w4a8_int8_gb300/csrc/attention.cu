@@ -27,6 +27,16 @@
 // true): both slots hold the same rows and take the key tiles in turn, and a
 // cluster of up to eight CTAs shares the keys; sums and outputs are joined
 // through distributed shared memory in a fixed order.
+//
+// What bounds it.  A step of a slot is its rows' turn (200 clocks to read S, 330
+// for the maximum, 930 for the weights) and its products (PV's second half and
+// QK, 1000 to 1200 with the hand-overs); the two slots' steps overlap, 2700
+// clocks for both where the products alone take 2048.  19989 rows x 19989 keys x
+// 56 heads of 128 in BF16: 6.2 to 6.5 ms, 1760 to 1840 TFLOP/s, the power cap in
+// it (cuBLAS sustains 1734); narrower heads are bound by the rows' turns (64: 15%
+// faster than 128).  Few keys: an item's start and end take 2 to 3 us beside its
+// tiles, about the time of reading its Q and writing its rows (19989 x 512: 205
+// us, 1430 TFLOP/s).
 #include <atomic>
 #include <cmath>
 #include <cstdint>
@@ -48,8 +58,8 @@ using namespace crgemm;
 constexpr int THREADS = 384;              // warps 0-7: rows (two slots), 8: loads, 9: products, 10: ragged V tiles (11 gives registers)
 // Registers of a thread: a row's 128 scores need more than an equal share of the
 // SM's (168, with which they spilled).  2 x 128 x 208 + 128 x 80 <= 384 x 168.
-constexpr int ROW_REGISTERS = 208, OTHER_REGISTERS = 80;
-static_assert(256 * ROW_REGISTERS + 128 * OTHER_REGISTERS <= THREADS * 168, "registers");
+constexpr int ROW_REGISTERS = 208, OTHER_REGISTERS = 80, LAUNCH_REGISTERS = 168;
+static_assert(256 * ROW_REGISTERS + 128 * OTHER_REGISTERS <= THREADS * LAUNCH_REGISTERS, "registers");
 constexpr int MAX_SPLIT = MOST_SLICES;
 
 template <int DP, bool SPLIT>
@@ -250,7 +260,8 @@ __device__ __forceinline__ void find_tile(const Problem& p, const Work& w, int64
 }
 
 // ------------------------------------------------------------------ kernel
-// KK: steps of 16 columns that a head takes (4, 5, 6 or 8), in tiles of 64 or 128 columns.  (Heads of 80 as 128: TODO.)
+// KK: steps of 16 columns that the products take of a head (4, 5, 6 or 8), in tiles of 64 or 128 columns (20000 rows x 2048
+// keys x 8 heads of 80: 104 us, with the steps of 128 columns 114; of 96: 107 and 115; of 128: 115).
 template <int DT, int KK, bool PAGED, bool SPLIT>
 __global__ void __launch_bounds__(THREADS, 1)
 attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
@@ -873,6 +884,10 @@ static cudaError_t resident_clusters(int slices, int* out) {
     auto k = attention_kernel<DT, KK, PAGED, SPLIT>;
     constexpr int smem = Layout<(KK > 4 ? 128 : 64), SPLIT>::SMEM;
     if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return e;
+    // the rows' larger share comes out of what the launch has: a kernel built with fewer registers would wait for it
+    cudaFuncAttributes attributes;
+    if ((e = cudaFuncGetAttributes(&attributes, k)) != cudaSuccess) return e;
+    if (attributes.numRegs < LAUNCH_REGISTERS) return cudaErrorLaunchOutOfResources;
     int sms = 0;
     if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
     n = sms;
@@ -945,7 +960,8 @@ static int choose(const Problem& p, const Variant& variant, cudaStream_t st) {
   const bool narrow = p.D <= 64;
   auto consider = [&](int pack, int n, int resident) {
     const Work w = {pack, KEYS / pack, (n ? 1 : 2) * (KEYS / pack)};
-    const double per = std::ceil(q / w.item_tokens), rounds = std::ceil(p.B * per * (p.heads_q / pack) / resident);
+    const double per = std::ceil(q / w.item_tokens), load = p.B * per * (p.heads_q / pack) / resident;
+    const double rounds = p.B <= 8 ? std::ceil(load) : load > 0.75 ? load + 0.25 : 1;      // (many lengths fill the last one)
     const double t = n ? rounds * (std::ceil(key_tiles / n) * (narrow ? 0.70 : 0.83) + (narrow ? 7.5 : 8.5) + 0.7 * n)
                        : rounds * (std::ceil(key_tiles) * (q > w.tps ? (narrow ? 1.11 : 1.38) : (narrow ? 1.0 : 1.24)) + 3.6) + 2.5;
     if (least == 0 || t < least) {
