@@ -386,7 +386,7 @@ int convrot_gemm_fused_selftest(const void* a_q, int64_t ld_aq,
  *           heads_q is a multiple of heads_k.  out overlaps no input, and its
  *           heads and rows do not overlap.
  *   D       a multiple of 8, 8 .. CONVROT_MAX_ATT_HEAD.
- *   seqs    NULL: one sequence of all rows and all keys.  Otherwise device
+ *   seqs    NULL (B = 1): one sequence of all rows and all keys.  Otherwise device
  *           int32 [B][4] (16-byte aligned; B <= CONVROT_MAX_SEQUENCES), for every
  *           sequence q_start, q_len,
  *           k_start, k_len: rows q_start .. q_start + q_len - 1 attend to keys
@@ -400,8 +400,10 @@ int convrot_gemm_fused_selftest(const void* a_q, int64_t ld_aq,
  * Scores, maximum, sum and outputs are FP32; the weights p are rounded to
  * `dtype` for their product with v (with up to 16 rows per K head held as two
  * such values), and the result once.  An Inf or NaN in v shows in its column of
- * the rows that see that key, one in a row's scores in that row; with `causal`
- * one in v may also show in earlier rows of the same sequence.  The result does
+ * the rows that see that key, a NaN or +Inf among a row's scores in that row;
+ * with `causal` one in v may also show in earlier rows of the same sequence.
+ * Lengths being on the device, the kernel is chosen for rows / B rows and an
+ * equal share of the keys per sequence; other lengths cost time, no more.  The result does
  * not depend on other sequences of the call, nor on the run; it may change in
  * its last bits with the sizes of the call (how the keys are split).
  * Limits: rows, keys <= 2^30, heads_q <= 65536, strides < 2^39 elements.

@@ -22,8 +22,8 @@
 // sequence are zeroed in shared memory (0 x NaN).
 //
 // Whole items (SPLIT false): the slots are neighbouring tiles of rows and share
-// every K and V tile; CTAs stay and take items in turn, the loads and products
-// of the next item running into the output phase of the last.  Few rows (SPLIT
+// every K and V tile; CTAs stay and take items in turn, the next item's first
+// loads running into the output phase of the last.  Few rows (SPLIT
 // true): both slots hold the same rows and take the key tiles in turn, and a
 // cluster of up to eight CTAs shares the keys; sums and outputs are joined
 // through distributed shared memory in a fixed order.
@@ -34,7 +34,10 @@
 // clocks for both where the products alone take 2048.  19989 rows x 19989 keys x
 // 56 heads of 128 in BF16: 6.2 to 6.5 ms, 1760 to 1840 TFLOP/s, the power cap in
 // it (cuBLAS sustains 1734); narrower heads are bound by the rows' turns (64: 15%
-// faster than 128).  Few keys: an item's start and end take 2 to 3 us beside its
+// faster than 128).  Tried against it, and slower: two threads a row (5 to 8%), a
+// products' warp for each slot (3 to 14%: the slots' products then delay each
+// other), parts of 64 keys turned while the next part's scores are computed (13%),
+// the next item's scores before this one's outputs (2 to 10%).  Few keys: an item's start and end take 2 to 3 us beside its
 // tiles, about the time of reading its Q and writing its rows (19989 x 512: 205
 // us, 1430 TFLOP/s).
 #include <atomic>

@@ -27,6 +27,7 @@ static int call(Problem p, convrot_dtype dtype, const int32_t* seqs, float scale
 
 static int check_rows(const Problem& p) {
   const Extent q[3] = {{p.heads_q, p.q_head}, {p.rows, p.q_tok}, {1, 0}}, out[3] = {{p.heads_q, p.out_head}, {p.rows, p.out_tok}, {1, 0}};
+  if (p.out && (p.out == p.q || p.out == p.k || p.out == p.v)) return CONVROT_ERR_INVALID_ARG;     // read while it is written
   const int st = check_input(p.q, p.D, q);
   return st != CONVROT_OK ? st : check_output(p.out, p.D, out);
 }
@@ -36,8 +37,8 @@ static int rows_call(Problem p, convrot_dtype dtype, const int32_t* seqs, float 
   if (e != CONVROT_OK) return e;
   if (p.keys < 0) return CONVROT_ERR_INVALID_ARG;
   if (p.keys > kMostRows) return CONVROT_ERR_UNSUPPORTED;
-  if (!seqs) p.B = 1;
   if (p.rows == 0 || p.B == 0) return CONVROT_OK;
+  if (!seqs) p.B = 1;
   if ((e = check_rows(p)) != CONVROT_OK) return e;
   const Extent k[3] = {{p.heads_k, p.k_head}, {p.keys, p.k_row}, {1, 0}}, v[3] = {{p.heads_k, p.v_head}, {p.keys, p.v_row}, {1, 0}};
   if (p.keys > 0 && ((e = check_input(p.k, p.D, k)) != CONVROT_OK || (e = check_input(p.v, p.D, v)) != CONVROT_OK)) return e;
@@ -56,7 +57,7 @@ static int pages_call(Problem p, convrot_dtype dtype, int page_size, const int32
   const Extent k[3] = {{p.heads_k, p.k_head}, {page_size, p.k_row}, {p.num_pages, p.k_page}},
                v[3] = {{p.heads_k, p.v_head}, {page_size, p.v_row}, {p.num_pages, p.v_page}};
   if (p.num_pages > 0 && ((e = check_input(p.k, p.D, k)) != CONVROT_OK || (e = check_input(p.v, p.D, v)) != CONVROT_OK)) return e;
-  p.keys = t.positions;
+  p.keys = p.num_pages > 0 ? t.positions : 0;       // (without pages no entry of the table names one)
   p.page_log2 = t.page_log2;
   if (p.keys > 0) {
     p.pages = pages;

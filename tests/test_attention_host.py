@@ -19,7 +19,7 @@ def built():
 
 
 def rows_call(**kw):
-    a = dict(q=P, qr=512, qh=64, k=P, kr=128, kh=64, v=P, vr=128, vh=64, o=P, orow=512, oh=64, dt=0, rows=0, keys=5, hq=8,
+    a = dict(q=P, qr=512, qh=64, k=P, kr=128, kh=64, v=P, vr=128, vh=64, o=2 * P, orow=512, oh=64, dt=0, rows=0, keys=5, hq=8,
              hk=2, D=64, seqs=None, B=1, scale=0.125, causal=0)
     a.update(kw)
     return cr.load_library().convrot_attention(
@@ -30,6 +30,7 @@ def rows_call(**kw):
 def test_attention_arguments():
     assert rows_call() == 0                                   # no rows: nothing to do
     assert rows_call(rows=4, seqs=P, B=0) == 0                # no sequences
+    assert rows_call(rows=4, seqs=None, B=0) == 0             # (an empty tensor has no address)
     assert rows_call(dt=2) == 3 and rows_call(dt=7) == 3      # FP32 is not taken
     assert rows_call(rows=-1) == 1 and rows_call(keys=-1) == 1 and rows_call(B=-1) == 1
     assert rows_call(hq=0) == 1 and rows_call(hk=0) == 1 and rows_call(hq=7) == 1
@@ -45,13 +46,15 @@ def test_attention_arguments():
         assert rows_call(rows=4, **{name: -512}) == 1
         assert rows_call(rows=4, **{name: 1028}) == 2         # no whole 16-byte pieces
         assert rows_call(rows=4, **{name: 1 << 39}) == 3
+    for name in ("q", "k", "v"):
+        assert rows_call(rows=4, **{n: P + (1 << 20) * (n == name) for n in ("q", "k", "v")}, o=P + (1 << 20)) == 1   # in place
     assert rows_call(rows=4, orow=64, oh=64) == 1             # outputs overlap
     assert rows_call(rows=4, orow=128, oh=64) == 1
     assert rows_call(rows=4, seqs=P + 4) == 2
 
 
 def pages_call(fn="paged", **kw):
-    a = dict(q=P, qr=512, qh=64, k=P, kp=2048, kr=128, kh=64, v=P, vp=2048, vr=128, vh=64, o=P, orow=512, oh=64, dt=1,
+    a = dict(q=P, qr=512, qh=64, k=P, kp=2048, kr=128, kh=64, v=P, vp=2048, vr=128, vh=64, o=2 * P, orow=512, oh=64, dt=1,
              rows=4, hq=8, hk=2, D=64, n=9, size=16, t=P, ld=5, per=5, seqs=P, B=3, scale=0.125, causal=0)
     a.update(kw)
     lib = cr.load_library()
@@ -88,7 +91,7 @@ def test_selftest_arguments():
     lib = cr.load_library()
 
     def call(kernel, slices, starve=0):
-        return lib.convrot_attention_selftest(P, 512, 64, P, 0, 128, 64, P, 0, 128, 64, P, 512, 64, 0, 0, 8, 2, 64, 5, 0, 0,
+        return lib.convrot_attention_selftest(P, 512, 64, P, 0, 128, 64, P, 0, 128, 64, 2 * P, 512, 64, 0, 0, 8, 2, 64, 5, 0, 0,
                                               None, 0, 0, None, 1, 0.125, 0, kernel, slices, starve, None)
     assert call(1, 16) == 0 and call(1, 3, 1) == 0 and call(2, 1) == 0 and call(3, 7, 1) == 0
     for kernel, slices, starve in ((0, 1, 0), (4, 1, 0), (1, 0, 0), (1, 17, 0), (2, 2, 0), (3, 9, 0)):

@@ -273,3 +273,25 @@ def test_errors_leave_outputs():
         cr.attention(q, rand(8, 2, 64)[:, :1].expand(8, 2, 64), k, out)        # heads on top of each other
     torch.cuda.synchronize()
     assert bool((out == 5).all())
+
+
+def test_nothing_to_attend_to():
+    """No pages, no table, no sequences: rows without keys become zeros, a sequence that has some is reported, rows in
+    no sequence stay."""
+    import rotated_w4a8_int8_gb300 as cr
+    q = rand(6, 2, 64)
+    none = torch.empty(0, 16, 2, 64, dtype=BF, device=DEV)
+    for caches, table in (((none, none), torch.zeros(2, 3, dtype=torch.int32, device=DEV)),
+                          ([rand(4, 16, 2, 64)] * 2, torch.zeros(2, 0, dtype=torch.int32, device=DEV))):
+        out = torch.full_like(q, 5.0)
+        cr.paged_attention(q, *caches, table, i32([(0, 2, 0, 0), (2, 3, 0, 7)]), out)
+        assert cr.device_error() == 16
+        assert bool((out[:2] == 0).all()) and bool((out[2:] == 5).all())
+    k = rand(4, 2, 64)
+    cr.cache_write(k, k, none, none, torch.zeros(1, 3, dtype=torch.int32, device=DEV), i32([(0, 4, 0, 4)]))
+    assert cr.device_error() == 17
+    out = torch.full_like(q, 5.0)
+    cr.attention(q, k, k, out, seqs=torch.empty(0, 4, dtype=torch.int32, device=DEV))
+    cr.attention(q[:0], k, k, out[:0])
+    torch.cuda.synchronize()
+    assert cr.device_error() == 0 and bool((out == 5).all())
