@@ -406,7 +406,8 @@ int convrot_gemm_fused_selftest(const void* a_q, int64_t ld_aq,
  * equal share of the keys per sequence; other lengths cost time, no more.  The result does
  * not depend on other sequences of the call, nor on the run; it may change in
  * its last bits with the sizes of the call (how the keys are split).
- * Limits: rows, keys <= 2^30, heads_q <= 65536, strides < 2^39 elements.
+ * Limits: rows <= 2^30, keys and positions <= 2^26, heads_q <= 65536, strides
+ * < 2^39 elements.
  * Alignment: every pointer 16-byte aligned, row and head strides multiples of 8
  * elements and not below D (where that dimension is more than one long).
  */

@@ -48,6 +48,7 @@
 
 #include "../../include/convrot.h"
 #include "attention.cuh"
+#include "attention_check.h"
 #include "attention_kernels.cuh"
 #include "attention_map.cuh"
 #include "errors.h"
@@ -105,8 +106,13 @@ static_assert(sizeof(Item) <= 128, "item area");
 
 // A V tile that holds rows outside its sequence: rows before `first` and from `end` on are to be zero.
 struct Ragged {
-  int stage, first, end;   // stage < 0: no more
+  int stage, first, end;   // stage NO_TILE: none for a while; NO_MORE: the end
 };
+enum : int { NO_MORE = -1, NO_TILE = -2 };
+// The warp that waits for them is told at least once in so many tiles that there was none: no wait lasts longer than
+// these and one item's tiles take (kMostKeys: at 1.4 us a tile less than a second, half a wait's limit).
+constexpr int QUIET_TILES = 1 << 17;
+static_assert(QUIET_TILES + kMostKeys / KEYS <= 700000, "waits that nothing is wrong with");
 
 // ------------------------------------------------------------------ PTX
 __device__ __forceinline__ void store_box_3d(const CUtensorMap* map, uint32_t src, int x, int y, int z) {
@@ -333,6 +339,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
     uint32_t stage = 0, phase = 0;
     uint32_t issued = 0, issued_phase = 0;       // outstanding loads, for an abort
     uint32_t n_items = 0, n_ragged = 0;
+    int quiet = 0;                               // tiles since the last ragged one
     bool ok = true, q_out = false;
     auto find = [&](int64_t i) {
       Item it = {};
@@ -396,6 +403,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
           if (n_ragged > 0 && !wait_all(raw_free, (n_ragged - 1) & 1u)) return false;
           if (lane == 0) *ragged = {static_cast<int>(stage), first, end};
           ++n_ragged;
+          quiet = 0;
         }
         const uint32_t bar = raw ? v_raw : full0 + 8 * stage, dst = stages + stage * L::TILE;
         const CUtensorMap* map = is_v ? &map_v : &map_k;
@@ -460,6 +468,17 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
         if (!SPLIT && t == t0) find_next();        // while this item's first tiles are on their way
       }
       if (!ok) break;
+      quiet += t1 - t0;
+      if (quiet >= QUIET_TILES) {
+        if (n_ragged > 0 && !(ok = wait_all(raw_free, (n_ragged - 1) & 1u))) break;
+        if (lane == 0) {
+          ragged->stage = NO_TILE;
+          mbar_arrive_local(v_raw);
+        }
+        __syncwarp();
+        ++n_ragged;
+        quiet = 0;
+      }
       if (!SPLIT && t0 >= t1) find_next();
       it = next;                                                   // (SPLIT: there is one item)
       i += gridDim.x;
@@ -467,7 +486,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
     if (ok) {
       if (n_ragged > 0) ok = wait_all(raw_free, (n_ragged - 1) & 1u);
       if (ok && lane == 0) {
-        ragged->stage = -1;
+        ragged->stage = NO_MORE;
         mbar_arrive_local(v_raw);
       }
       // the products' last commits arrive on the empty barriers: wait for them before leaving
@@ -614,7 +633,12 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
       for (uint32_t n = 0;; ++n) {
         if (!__all_sync(0xffffffffu, mbar_wait(v_raw, n & 1u, ERR_WAIT_FULL, abort_flag))) break;
         const Ragged r = *ragged;
-        if (r.stage < 0) break;
+        if (r.stage == NO_MORE) break;
+        if (r.stage == NO_TILE) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive_local(raw_free);
+          continue;
+        }
         uint8_t* tile = tiles + (L::QTILES + r.stage) * L::TILE;
         constexpr int PIECES = DP / 8;                     // 16-byte pieces of a row; a lane zeroes one of every 32 / PIECES rows
         uint8_t* at = tile + lane % PIECES / 8 * L::BOX + lane % 8 * 16;

@@ -36,7 +36,7 @@ static int rows_call(Problem p, convrot_dtype dtype, const int32_t* seqs, float 
   int e = check_heads(dtype, p.rows, p.heads_q, p.heads_k, p.D, p.B);
   if (e != CONVROT_OK) return e;
   if (p.keys < 0) return CONVROT_ERR_INVALID_ARG;
-  if (p.keys > kMostRows) return CONVROT_ERR_UNSUPPORTED;
+  if (p.keys > kMostKeys) return CONVROT_ERR_UNSUPPORTED;
   if (p.rows == 0 || p.B == 0) return CONVROT_OK;
   if (!seqs) p.B = 1;
   if ((e = check_rows(p)) != CONVROT_OK) return e;

@@ -7,8 +7,9 @@
 
 namespace cratt {
 
-// Most rows, keys or positions of a call: positions and lengths are int32 in the kernels.
-constexpr int kMostRows = 1 << 30;
+// Most rows of a call, and most keys or positions: lengths are int32 in the kernels, and what one item of the many-row
+// kernel takes stays below its waits' limit.
+constexpr int kMostRows = 1 << 30, kMostKeys = 1 << 26;
 
 // Elements of a dimension and their stride (in elements of the type).
 struct Extent {
@@ -69,7 +70,7 @@ struct Table {
   if (reinterpret_cast<uintptr_t>(t->pages) % 4) return CONVROT_ERR_MISALIGNED;
   while ((1 << t->page_log2) < t->page_size) ++t->page_log2;
   const int64_t n = static_cast<int64_t>(t->per_seq) * t->page_size;
-  t->positions = static_cast<int>(n < kMostRows ? n : kMostRows);
+  t->positions = static_cast<int>(n < kMostKeys ? n : kMostKeys);
   return CONVROT_OK;
 }
 

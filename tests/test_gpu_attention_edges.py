@@ -295,3 +295,23 @@ def test_nothing_to_attend_to():
     cr.attention(q[:0], k, k, out[:0])
     torch.cuda.synchronize()
     assert cr.device_error() == 0 and bool((out == 5).all())
+
+
+def test_a_call_longer_than_a_wait_may_last():
+    """2^18 rows by 2^18 keys, 128 heads: more than the two seconds after which a wait is given up.  No tile is ragged, so
+    the warp that looks after those waits all the time."""
+    import rotated_w4a8_int8_gb300 as cr
+    n, H, D = 2 ** 18, 128, 128
+    g = torch.Generator(device=DEV).manual_seed(3)
+    q, k, v = (torch.empty(n, H, D, dtype=BF, device=DEV).normal_(generator=g) for _ in range(3))
+    out = torch.empty_like(q)
+    begin, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    begin.record()
+    cr.attention(q, k, v, out)
+    end.record()
+    torch.cuda.synchronize()
+    assert begin.elapsed_time(end) > 2100
+    assert cr.device_error() == 0
+    for row, head in ((0, 0), (n // 2 + 77, 63), (n - 1, H - 1)):
+        at = slice(row, row + 1), slice(head, head + 1)
+        check(out[at], *reference(q[at], k[:, at[1]], v[:, at[1]], [(0, 1, 0, n)], D ** -0.5, False, out[at]))
