@@ -221,6 +221,7 @@ __device__ __forceinline__ uint32_t desc_low(uint32_t saddr, uint32_t block = 16
 struct Work {
   int pack, tps;             // heads per tile, tokens per tile of 128 rows
   int item_tokens;           // tokens per item: tps, or 2 tps
+  int rest;                  // the last items that whole items leave to clusters that share keys (each as two of theirs)
 };
 
 // Tiles of all sequences (a warp together).
@@ -344,13 +345,20 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
     auto find = [&](int64_t i) {
       Item it = {};
       it.q_row = -1;
-      if (i >= num_items) return it;
+      int half = 0;
+      if (SPLIT && w.rest > 0) {
+        half = static_cast<int>(i & 1);
+        i = num_items - w.rest + (i >> 1);
+      }
+      if (i < 0 || i >= num_items - (SPLIT ? 0 : w.rest)) return it;
       Sequence s;
       int token;
       const int unit = static_cast<int>(i / num_tiles);
       find_tile(p, w, i % num_tiles, lane, &g_error, s, it.seq, token);
+      token += half * w.tps;
+      if (token >= s.q_len) return it;
       it.q_row = s.q_start + token;
-      it.tokens = min(w.item_tokens, s.q_len - token);
+      it.tokens = min(SPLIT ? w.tps : w.item_tokens, s.q_len - token);
       it.head0 = unit * w.pack;
       it.head_kv = it.head0 / group;
       it.base = PAGED ? s.k_start / box_rows * box_rows : s.k_start;
@@ -976,7 +984,7 @@ static int choose(const Problem& p, const Variant& variant, cudaStream_t st) {
   // the whole table in use.
   const double q = static_cast<double>(p.rows) / p.B, k = p.seqs && !p.pages ? static_cast<double>(p.keys) / p.B : p.keys;
   const double key_tiles = k > KEYS ? k / KEYS : 1;
-  Work best = {1, KEYS, 2 * KEYS};
+  Work best = {1, KEYS, 2 * KEYS, 0};
   int slices = 0;                            // 0: whole items
   double least = 0;
   // Microseconds, fitted to runs of 1 to 700 rows per sequence over 64 to 16384
@@ -985,12 +993,13 @@ static int choose(const Problem& p, const Variant& variant, cudaStream_t st) {
   // of 64, 24 rows, 1000 keys: whole 12.9 us, shared by four 10.3; 300 rows, 16384
   // keys: 145 and 34; 56 heads, 700 rows: 287 and 328.)
   const bool narrow = p.D <= 64;
+  auto shared_round = [&](int n) { return std::ceil(key_tiles / n) * (narrow ? 0.70 : 0.83) + (narrow ? 7.5 : 8.5) + 0.7 * n; };
+  auto whole_round = [&](bool both) { return std::ceil(key_tiles) * (both ? (narrow ? 1.11 : 1.38) : (narrow ? 1.0 : 1.24)) + 3.6; };
   auto consider = [&](int pack, int n, int resident) {
-    const Work w = {pack, KEYS / pack, (n ? 1 : 2) * (KEYS / pack)};
+    const Work w = {pack, KEYS / pack, (n ? 1 : 2) * (KEYS / pack), 0};
     const double per = std::ceil(q / w.item_tokens), load = p.B * per * (p.heads_q / pack) / resident;
     const double rounds = p.B <= 8 ? std::ceil(load) : load > 0.75 ? load + 0.25 : 1;      // (many lengths fill the last one)
-    const double t = n ? rounds * (std::ceil(key_tiles / n) * (narrow ? 0.70 : 0.83) + (narrow ? 7.5 : 8.5) + 0.7 * n)
-                       : rounds * (std::ceil(key_tiles) * (q > w.tps ? (narrow ? 1.11 : 1.38) : (narrow ? 1.0 : 1.24)) + 3.6) + 2.5;
+    const double t = n ? rounds * shared_round(n) : rounds * whole_round(q > w.tps) + 2.5;
     if (least == 0 || t < least) {
       least = t;
       best = w;
@@ -1011,7 +1020,30 @@ static int choose(const Problem& p, const Variant& variant, cudaStream_t st) {
     if (group == 1) break;
   }
   const int64_t items = most_items(p, best.item_tokens) * (p.heads_q / best.pack);
-  return slices ? launch<DT, KK, PAGED, true>(p, best, slices, items, st) : launch<DT, KK, PAGED, false>(p, best, 1, items, st);
+  if (slices) return launch<DT, KK, PAGED, true>(p, best, slices, items, st);
+  // Whole items in full rounds, and a last round that is not: its items by clusters that share keys, in a launch of their
+  // own, where that is sooner done.  (2304 rows x 19989 keys x 56 heads, 3.3 rounds: 838 -> 806 us.)
+  int sms = 0, tail_slices = 0;
+  cudaError_t e = resident_clusters<DT, KK, PAGED, false>(1, &sms);
+  if (e != cudaSuccess) return convrot::record_cuda_error("attention set-up", e);
+  const int64_t left = sms > 0 ? items % sms : 0;
+  if (variant.kernel == CHOSEN && p.B == 1 && items > left && left > 0) {
+    double soonest = whole_round(true) - 5.0;                  // a second launch, and that nothing overlaps at its start
+    for (int n = 1; n <= MAX_SPLIT; ++n) {
+      int resident = 0;
+      if ((e = resident_clusters<DT, KK, PAGED, true>(n, &resident)) != cudaSuccess)
+        return convrot::record_cuda_error("attention set-up", e);
+      if (resident <= 0) continue;
+      const double t = std::ceil(2.0 * left / resident) * shared_round(n);
+      if (t < soonest) {
+        soonest = t;
+        tail_slices = n;
+      }
+    }
+  }
+  if (tail_slices) best.rest = static_cast<int>(left);
+  const int status = launch<DT, KK, PAGED, false>(p, best, 1, items, st);
+  return tail_slices && status == CONVROT_OK ? launch<DT, KK, PAGED, true>(p, best, tail_slices, 2 * left, st) : status;
 }
 
 // This file is compiled once per type of q, k and v (CONVROT_ATTENTION_TYPE).

@@ -315,3 +315,23 @@ def test_a_call_longer_than_a_wait_may_last():
     for row, head in ((0, 0), (n // 2 + 77, 63), (n - 1, H - 1)):
         at = slice(row, row + 1), slice(head, head + 1)
         check(out[at], *reference(q[at], k[:, at[1]], v[:, at[1]], [(0, 1, 0, n)], D ** -0.5, False, out[at]))
+
+
+@pytest.mark.parametrize("D,causal,page", [(128, False, 0), (128, True, 64), (64, False, 0), (96, True, 0)])
+@pytest.mark.parametrize("q_len", [2048, 2000, 1500, 300])
+def test_items_left_to_a_second_launch(D, causal, page, q_len):
+    """2048 rows of 20 heads are 160 items of 256 rows, eight more than the SMs: with many keys these are shared.  The
+    sequence may have fewer rows than the host counted on."""
+    import rotated_w4a8_int8_gb300 as cr
+    m = 6001
+    q, k, v = rand(2048, 20, D), rand(m, 4, D, seed=1), rand(m, 4, D, seed=2)
+    seqs, out = [(5, q_len, 0, m)] if q_len < 2048 else [(0, q_len, 0, m)], torch.full_like(q, 3.0)
+    want = reference(q, k, v, seqs, D ** -0.5, causal, out)
+    if page:
+        kc, vc, table, where = paged(k, v, seqs, page, 9)
+        cr.paged_attention(q, kc, vc, table, where, out, causal=causal)
+    else:
+        cr.attention(q, k, v, out, seqs=i32(seqs), causal=causal)
+    torch.cuda.synchronize()
+    assert cr.device_error() == 0
+    check(out, *want)
