@@ -76,10 +76,10 @@ struct Layout {
   static constexpr int S_COL = 0, O_COL = 256;               // tensor memory: S of both slots, O of both slots
   static constexpr int PITCH = DP + 4;                       // floats per row of a joined partial
   // barriers and small things, then the tiles
-  static constexpr int ITEM = 256, STATS = 512, SUMS = STATS + 2 * 128 * 8, AUX = SPLIT ? 3072 : 1024;
+  static constexpr int ITEM = 256, STATS = 512, SUMS = STATS + 2 * 128 * 8, AUX = (SPLIT ? 3 : 1) * 1024;
   static constexpr int SMEM = (QTILES + STAGES) * TILE + STAGING + AUX + 1024;
   static_assert(SMEM <= 232448, "shared memory");
-  static_assert((2 * STAGES + 13) * 8 + 8 <= ITEM && SUMS + 512 <= 3072, "barrier area");
+  static_assert((2 * STAGES + 13) * 8 + 8 <= ITEM && SUMS + 512 <= 3 * 1024, "barrier area");
   // partials that a CTA receives: 2 slots of every CTA x its share of the 128 rows
   static constexpr int PARTS = 2 * MAX_SPLIT * ((128 + MAX_SPLIT - 1) / MAX_SPLIT) + 2 * MAX_SPLIT;
   static_assert(!SPLIT || PARTS * PITCH * 4 <= (QTILES + STAGES) * TILE, "joined partials");

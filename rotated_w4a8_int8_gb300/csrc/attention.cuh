@@ -13,7 +13,6 @@
 namespace cratt {
 
 constexpr int KEYS = 128;                 // keys of a tile of the many-row kernel
-constexpr int MAX_D = CONVROT_MAX_ATT_HEAD;
 
 // Codes in the device error word (beside the waits' own): an entry of `seqs`
 // reaches past its tensors, or a needed entry of `pages` names no page.
