@@ -743,7 +743,21 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
           }
         }
         // a row that has seen no key yet keeps -inf, its weights are exp2(-inf) = 0
-        const float ref = kLift<DT> - (m == -INFINITY ? 0.f : m * p.scale_log2);
+        const float zero = m == -INFINITY ? 0.f : m;
+        float ref = kLift<DT> - zero * p.scale_log2;
+        // This product's rounding moves all weights of the row by one factor, 2 to the 2^-24th of it: of no account below
+        // 2^16, past a type's range from some 2^25 on.  There the scores' differences are taken first.
+        const bool large = fabsf(zero * p.scale_log2) > 65536.f;
+        if (__any_sync(0xffffffffu, large)) {
+          const float2 less = make_float2(large ? -zero : 0.f, large ? -zero : 0.f);
+          if (large) ref = kLift<DT>;
+#pragma unroll
+          for (int j = 0; j < KEYS; j += 2) {
+            const float2 d = add2(make_float2(x[j], x[j + 1]), less);
+            x[j] = d.x;
+            x[j + 1] = d.y;
+          }
+        }
         const float2 r2 = make_float2(ref, ref);
         float2 sum = make_float2(l0, l1);
         auto weights = [&](int c) {                        // of 32 keys

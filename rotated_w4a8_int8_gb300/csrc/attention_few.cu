@@ -366,7 +366,8 @@ few_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CU
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const float r = m[j][i & 1];
-              e[i] = exp2_approx(fmaf(x[j][0][i], p.scale_log2, kLift<DT> - (r == -INFINITY ? 0.f : r * p.scale_log2)));
+              // (the difference first: a rounded product of r would be past the types' range with scores of 2^25 and more)
+              e[i] = exp2_approx(fmaf(x[j][0][i] - (r == -INFINITY ? 0.f : r), p.scale_log2, kLift<DT>));
             }
             l[j][0] += e[0] + e[2];
             l[j][1] += e[1] + e[3];

@@ -232,6 +232,30 @@ def test_equal_weights_of_many_keys(kernel, dtype):
     check(out, *reference(q, k, v, [(0, 130, 0, n)], 0.125, False, out))
 
 
+@pytest.mark.parametrize("kernel", EACH)
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("rows", [4, 150])
+def test_large_scores(kernel, dtype, rows):
+    """Scores up to 2^37, whose FP32 sums are exact (whole numbers below 2^14, times a power of two): what is left is the
+    weights of the largest ones, equal where there are several.  Rows past the first half have ordinary scores."""
+    import rotated_w4a8_int8_gb300 as cr
+    g = torch.Generator(device=DEV).manual_seed(rows)
+    whole = lambda *shape: torch.randint(-8, 9, shape, generator=g, device=DEV).to(dtype)
+    q, k, v = whole(rows, 2, 128) * 2.0 ** 12, whole(700, 2, 128) * 2.0 ** 12, rand(700, 2, 128, seed=1, dtype=dtype)
+    q[rows // 2:] *= 2.0 ** -25 if dtype == BF else 2.0 ** -24
+    assert bool((k * 2.0 ** -12 == (k * 2.0 ** -12).round()).all()) and float(q[:rows // 2].abs().max()) == 2.0 ** 15
+    out = torch.empty_like(q)
+    cr.attention_selftest(q, k, v, out, *kernel, scale=0.125)
+    torch.cuda.synchronize()
+    want, bound = reference(q, k, v, [(0, rows, 0, 700)], 0.125, False, out)
+    # exact scores: only the weights' and the output's rounding (and, for FP32 sums and the exponential, 2^-18 of both)
+    p_v = reference(q, k, v.abs(), [(0, rows, 0, 700)], 0.125, False, out)[0]
+    u, half = torch.finfo(dtype).eps / 2, rows // 2
+    tight = (u + 2.0 ** -18) * (p_v + want.abs())
+    bound[:half] = tight[:half]
+    check(out, want, bound)
+
+
 @pytest.mark.parametrize("kernel", [(1, 2), (2, 1), (3, 2)])
 def test_wait_that_runs_out_is_reported(kernel):
     import rotated_w4a8_int8_gb300 as cr
