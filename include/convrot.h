@@ -395,7 +395,7 @@ int convrot_gemm_fused_selftest(const void* a_q, int64_t ld_aq,
  *           no sequence are left as they were, and keys in none are not used,
  *           whatever they hold (Inf or NaN too).  A sequence that reaches past
  *           its tensors is skipped and reported by convrot_device_error.
- *   scale   > 0 and finite.
+ *   scale   > 0, at most 2^126.
  *
  * Scores, maximum, sum and outputs are FP32; the weights p are rounded to
  * `dtype` for their product with v (with up to 16 rows per K head held as two

@@ -18,7 +18,7 @@ static int run(const Problem& p, const Variant& variant, cudaStream_t st) {
 }
 
 static int call(Problem p, convrot_dtype dtype, const int32_t* seqs, float scale, const Variant& variant, cudaStream_t st) {
-  if (!(scale > 0.f) || scale > 3.4e38f) return CONVROT_ERR_INVALID_ARG;
+  if (!(scale > 0.f) || scale > 0x1p126f) return CONVROT_ERR_INVALID_ARG;      // (scale * log2(e) is finite)
   if (reinterpret_cast<uintptr_t>(seqs) % 16) return CONVROT_ERR_MISALIGNED;
   p.seqs = reinterpret_cast<const int4*>(seqs);
   p.scale_log2 = static_cast<float>(scale * 1.4426950408889634);

@@ -27,6 +27,12 @@ def rows_call(**kw):
         a["rows"], a["keys"], a["hq"], a["hk"], a["D"], a["seqs"], a["B"], a["scale"], a["causal"], None)
 
 
+def test_largest_scale():
+    """scale * log2(e), which the kernels use, is finite too."""
+    assert rows_call(rows=4, scale=2.0 ** 127) == 1 and rows_call(rows=4, scale=3.4e38) == 1
+    assert rows_call(rows=4, seqs=P + 8, scale=2.0 ** 126) == 2       # (refused for an address that is looked at after it)
+
+
 def test_attention_arguments():
     assert rows_call() == 0                                   # no rows: nothing to do
     assert rows_call(rows=4, seqs=P, B=0) == 0                # no sequences
