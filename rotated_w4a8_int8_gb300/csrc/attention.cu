@@ -746,7 +746,8 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
         const float zero = m == -INFINITY ? 0.f : m;
         float ref = kLift<DT> - zero * p.scale_log2;
         // This product's rounding moves all weights of the row by one factor, 2 to the 2^-24th of it: of no account below
-        // 2^16, past a type's range from some 2^25 on.  There the scores' differences are taken first.
+        // 2^16, past a type's range from some 2^25 on.  There the scores' differences are taken first (2304 rows x 19989
+        // keys x 56 heads: without this 802 us, with the vote 808, differences in all rows 821).
         const bool large = fabsf(zero * p.scale_log2) > 65536.f;
         if (__any_sync(0xffffffffu, large)) {
           const float2 less = make_float2(large ? -zero : 0.f, large ? -zero : 0.f);
