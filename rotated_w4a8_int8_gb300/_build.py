@@ -21,14 +21,15 @@ LIB = os.path.join(HERE, "libconvrot.so")
 MARSHAL = os.path.join(HERE, "_marshal" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
 # (source, object, defines): quant.cu is compiled twice, once without and once
 # with the kernels that write code-norm bounds; gemm_fused.cu once per output type, attention.cu
-# once per type of its operands
+# once per type of its operands for short sequences and once for long ones
 SOURCES = [("api.cu", "api", []), ("quant.cu", "quant", []),
            ("quant.cu", "quant_norm", ["-DCONVROT_QUANT_NORM=1"]), ("gemm.cu", "gemm", []),
            ("int8_probe.cu", "int8_probe", []), ("decode_gemm_probe.cu", "decode_gemm_probe", []),
            ("norm_quant.cu", "norm_quant", []), ("rope.cu", "rope", []), ("gemm_few.cu", "gemm_few", []),
            ("attention_api.cu", "attention_api", []), ("attention_few.cu", "attention_few", []), ("cache.cu", "cache", []),
-           *(("attention.cu", f"attention_{name}", [f"-DCONVROT_ATTENTION_TYPE=CONVROT_{name.upper()}"])
-             for name in ("bf16", "fp16")),
+           *(("attention.cu", f"attention_{name}{'_long' * long}",
+              [f"-DCONVROT_ATTENTION_TYPE=CONVROT_{name.upper()}", f"-DCONVROT_ATTENTION_LONG={long}"])
+             for name in ("bf16", "fp16") for long in (0, 1)),
            *(("gemm_fused.cu", f"gemm_fused_{name}", [f"-DCONVROT_FUSED_OUT=CONVROT_{name.upper()}"])
              for name in ("bf16", "fp16", "fp32"))]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

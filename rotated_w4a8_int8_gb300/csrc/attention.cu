@@ -14,7 +14,9 @@
 // the sum are then scaled (rarely after the first tile), otherwise m stays and
 // weights above one are kept as they are.  The sum adds the FP32 weights; P is
 // rounded to the operands' type for the product (half a step of that type each,
-// at random: the result's error grows by about its own rounding's).
+// at random: the result's error grows by about its own rounding's).  A tile's
+// weights are added to one another before they join the row's sum, and after
+// kKeepKeys keys O and the sum move to sums of their own (Kept).
 //
 // Rows of a slot: `pack` heads that share a K head for each of `tps` tokens (one
 // head for many tokens).  Masks are applied where a tile crosses a row's last
@@ -269,10 +271,42 @@ __device__ __forceinline__ void find_tile(const Problem& p, const Work& w, int64
   }
 }
 
+// What is kept of a row of long keys besides O: outputs and their sum, with their reference (in local memory: O fills tensor
+// memory, and shared memory has no room for a second one).
+template <int DP>
+struct Kept {
+  float o[DP], m, l;
+};
+// Adds O (32 x `n` columns), whose reference is m, and the row's sum l to what is kept and clears O; or (end) takes the
+// whole as O.  Returns the new sum.  (Not inlined: in the rows' loop it cost short items up to 10%.)
+template <int DP>
+static __device__ __noinline__ float move_kept(Kept<DP>* kept, uint32_t o_addr, int n, float m, float l, float c, bool first, bool end) {
+  const float f = first ? 0.f : move_reference(kept->m, m, c);
+  const float sum = first ? l : kept->l * f + l;
+  kept->m = m;
+  kept->l = sum;
+#pragma unroll 1
+  for (int i = 0; i < n; ++i) {
+    uint32_t o[32];
+    tmem_ld32(o_addr + 32 * i, o);
+    tmem_ld_wait();
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+      const float y = __uint_as_float(o[j]) + (first ? 0.f : kept->o[32 * i + j] * f);
+      kept->o[32 * i + j] = y;
+      o[j] = end ? __float_as_uint(y) : 0u;
+    }
+    tmem_st32(o_addr + 32 * i, o);
+  }
+  tmem_st_wait();
+  return end ? sum : 0.f;
+}
+
 // ------------------------------------------------------------------ kernel
 // KK: steps of 16 columns that the products take of a head (4, 5, 6 or 8), in tiles of 64 or 128 columns (20000 rows x 2048
 // keys x 8 heads of 80: 104 us, with the steps of 128 columns 114; of 96: 107 and 115; of 128: 115).
-template <int DT, int KK, bool PAGED, bool SPLIT>
+// LONG: a sequence may have more than kKeepKeys keys.  (Calls of short items take 1 to 5% longer with it.)
+template <int DT, int KK, bool PAGED, bool SPLIT, bool LONG>
 __global__ void __launch_bounds__(THREADS, 1)
 attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                  const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_out,
@@ -693,7 +727,17 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
       const int whole = it.limit(SPLIT ? 0 : slot * w.tps, p.causal) / KEYS;
       float m = -INFINITY, l0 = 0.f, l1 = 0.f;             // reference and sum (in two parts) of this row
       const bool any = t0 < t1;
+      constexpr int KEEP = kKeepKeys<DT> / KEYS * step, COLUMNS = (KK + 1) / 2;      // tiles; O in 32 columns
+      Kept<LONG ? DP : 1> kept;
       for (int t = t0; t < t1; t += step) {
+        if (LONG && t != t0 && ((t - t0) & (KEEP - 1)) == 0) {
+          // O is whole once the next scores are there: its products came before them
+          ok = __all_sync(0xffffffffu, mbar_wait(s_full0 + 8 * slot, s_phase, ERR_WAIT_ACC_FULL, abort_flag));
+          if (!ok) break;
+          tc_fence_after();
+          l0 = move_kept(&kept, o_addr, COLUMNS, m, l0 + l1, p.scale_log2, t - t0 == KEEP, false);
+          l1 = 0.f;
+        }
         ok = __all_sync(0xffffffffu, mbar_wait(s_full0 + 8 * slot, s_phase, ERR_WAIT_ACC_FULL, abort_flag));
         if (!ok) break;
         s_phase ^= 1u;
@@ -794,6 +838,10 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
         ok = __all_sync(0xffffffffu, mbar_wait(o_full0 + 8 * slot, o_phase, ERR_WAIT_ACC_FULL, abort_flag));
         o_phase ^= 1u;
         tc_fence_after();
+        if (LONG && t1 - t0 > KEEP) {
+          l0 = move_kept(&kept, o_addr, COLUMNS, m, l0 + l1, p.scale_log2, false, true);
+          l1 = 0.f;
+        }
       }
       const float l = l0 + l1;
       const bool mine = ok && it.q_row >= 0 && held && my_token < it.tokens;
@@ -925,7 +973,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
 constexpr int kMaxDevices = 64;
 
 // Clusters of `slices` CTAs of this kernel that are resident at once (0: none of this size).
-template <int DT, int KK, bool PAGED, bool SPLIT>
+template <int DT, int KK, bool PAGED, bool SPLIT, bool LONG>
 static cudaError_t resident_clusters(int slices, int* out) {
   static std::atomic<int> known[kMaxDevices][MAX_SPLIT + 1] = {};    // 0: not set up (two threads may both do it)
   int dev = 0;
@@ -933,7 +981,7 @@ static cudaError_t resident_clusters(int slices, int* out) {
   if (e != cudaSuccess) return e;
   int n = dev < kMaxDevices ? known[dev][slices].load() : 0;
   if (n == 0) {
-    auto k = attention_kernel<DT, KK, PAGED, SPLIT>;
+    auto k = attention_kernel<DT, KK, PAGED, SPLIT, LONG>;
     constexpr int smem = Layout<(KK > 4 ? 128 : 64), SPLIT>::SMEM;
     if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return e;
     // the rows' larger share comes out of what the launch has: a kernel built with fewer registers would wait for it
@@ -966,7 +1014,7 @@ static cudaError_t resident_clusters(int slices, int* out) {
   return cudaSuccess;
 }
 
-template <int DT, int KK, bool PAGED, bool SPLIT>
+template <int DT, int KK, bool PAGED, bool SPLIT, bool LONG>
 static int launch(const Problem& p, const Work& w, int slices, int64_t items, cudaStream_t st) {
   using L = Layout<(KK > 4 ? 128 : 64), SPLIT>;
   static_assert(L::SMEM >= L::AUX + (L::QTILES + L::STAGES) * L::TILE + 1023, "shared memory");
@@ -978,12 +1026,12 @@ static int launch(const Problem& p, const Work& w, int slices, int64_t items, cu
   made = made && make_key_maps<DT, PAGED>(&mk, &mv, p, KEYS);
   if (!made) return convrot::record_error("cuTensorMapEncodeTiled failed for q, k, v or out");
   int resident = 0;
-  cudaError_t e = resident_clusters<DT, KK, PAGED, SPLIT>(slices, &resident);
+  cudaError_t e = resident_clusters<DT, KK, PAGED, SPLIT, LONG>(slices, &resident);
   if (e != cudaSuccess) return convrot::record_cuda_error("attention set-up", e);
   if (resident <= 0) return CONVROT_ERR_UNSUPPORTED;
   const int64_t clusters = SPLIT ? items : items < resident ? items : resident;
   if (clusters * slices > INT32_MAX) return CONVROT_ERR_UNSUPPORTED;
-  e = convrot::launch_after(attention_kernel<DT, KK, PAGED, SPLIT>, dim3(static_cast<unsigned>(clusters * slices)), THREADS,
+  e = convrot::launch_after(attention_kernel<DT, KK, PAGED, SPLIT, LONG>, dim3(static_cast<unsigned>(clusters * slices)), THREADS,
                             L::SMEM, slices, st, mq, mk, mv, mo, p, w, slices);
   return e == cudaSuccess ? CONVROT_OK : convrot::record_cuda_error("attention launch", e);
 }
@@ -994,7 +1042,7 @@ static int64_t most_items(const Problem& p, int tokens) {
   return B == 1 ? (rows + tokens - 1) / tokens : (rows + B * (tokens - 1)) / tokens;
 }
 
-template <int DT, int KK, bool PAGED>
+template <int DT, int KK, bool PAGED, bool LONG>
 static int choose(const Problem& p, const Variant& variant, cudaStream_t st) {
   const int group = p.heads_q / p.heads_k;
   // Lengths are on the device: every sequence is taken for an average one, with
@@ -1029,26 +1077,26 @@ static int choose(const Problem& p, const Variant& variant, cudaStream_t st) {
       if (variant.kernel == WHOLE && n != 0) break;
       if (variant.kernel == SHARED && n != variant.slices) continue;
       int resident = 0;
-      const cudaError_t e = n ? resident_clusters<DT, KK, PAGED, true>(n, &resident)
-                              : resident_clusters<DT, KK, PAGED, false>(1, &resident);
+      const cudaError_t e = n ? resident_clusters<DT, KK, PAGED, true, LONG>(n, &resident)
+                              : resident_clusters<DT, KK, PAGED, false, LONG>(1, &resident);
       if (e != cudaSuccess) return convrot::record_cuda_error("attention set-up", e);
       if (resident > 0) consider(pack, n, resident);
     }
     if (group == 1) break;
   }
   const int64_t items = most_items(p, best.item_tokens) * (p.heads_q / best.pack);
-  if (slices) return launch<DT, KK, PAGED, true>(p, best, slices, items, st);
+  if (slices) return launch<DT, KK, PAGED, true, LONG>(p, best, slices, items, st);
   // Whole items in full rounds, and a last round that is not: its items by clusters that share keys, in a launch of their
   // own, where that is sooner done.  (2304 rows x 19989 keys x 56 heads, 3.3 rounds: 838 -> 806 us.)
   int sms = 0, tail_slices = 0;
-  cudaError_t e = resident_clusters<DT, KK, PAGED, false>(1, &sms);
+  cudaError_t e = resident_clusters<DT, KK, PAGED, false, LONG>(1, &sms);
   if (e != cudaSuccess) return convrot::record_cuda_error("attention set-up", e);
   const int64_t left = sms > 0 ? items % sms : 0;
   if (variant.kernel == CHOSEN && p.B == 1 && items > left && left > 0) {
     double soonest = whole_round(true) - 5.0;                  // a second launch, and that nothing overlaps at its start
     for (int n = 1; n <= MAX_SPLIT; ++n) {
       int resident = 0;
-      if ((e = resident_clusters<DT, KK, PAGED, true>(n, &resident)) != cudaSuccess)
+      if ((e = resident_clusters<DT, KK, PAGED, true, LONG>(n, &resident)) != cudaSuccess)
         return convrot::record_cuda_error("attention set-up", e);
       if (resident <= 0) continue;
       const double t = std::ceil(2.0 * left / resident) * shared_round(n);
@@ -1059,27 +1107,35 @@ static int choose(const Problem& p, const Variant& variant, cudaStream_t st) {
     }
   }
   if (tail_slices) best.rest = static_cast<int>(left);
-  const int status = launch<DT, KK, PAGED, false>(p, best, 1, items, st);
-  return tail_slices && status == CONVROT_OK ? launch<DT, KK, PAGED, true>(p, best, tail_slices, 2 * left, st) : status;
+  const int status = launch<DT, KK, PAGED, false, LONG>(p, best, 1, items, st);
+  return tail_slices && status == CONVROT_OK ? launch<DT, KK, PAGED, true, LONG>(p, best, tail_slices, 2 * left, st) : status;
 }
 
-// This file is compiled once per type of q, k and v (CONVROT_ATTENTION_TYPE).
-#ifndef CONVROT_ATTENTION_TYPE
-#error "compile with -DCONVROT_ATTENTION_TYPE=<convrot_dtype>"
+// This file is compiled for each type of q, k and v (CONVROT_ATTENTION_TYPE), once for sequences of at most kKeepKeys keys
+// and once for longer ones (CONVROT_ATTENTION_LONG 0, 1).
+#if !defined(CONVROT_ATTENTION_TYPE) || !defined(CONVROT_ATTENTION_LONG)
+#error "compile with -DCONVROT_ATTENTION_TYPE=<convrot_dtype> -DCONVROT_ATTENTION_LONG=<0 or 1>"
 #endif
 
-template <>
-int attention_many<CONVROT_ATTENTION_TYPE>(const Problem& p, const Variant& variant, cudaStream_t st) {
-  constexpr int DT = CONVROT_ATTENTION_TYPE;
-  const int steps = (p.D + 15) / 16;
-  if (p.pages)
-    return steps <= 4 ? choose<DT, 4, true>(p, variant, st) : steps == 5 ? choose<DT, 5, true>(p, variant, st)
-           : steps == 6 ? choose<DT, 6, true>(p, variant, st) : choose<DT, 8, true>(p, variant, st);
-  return steps <= 4 ? choose<DT, 4, false>(p, variant, st) : steps == 5 ? choose<DT, 5, false>(p, variant, st)
-         : steps == 6 ? choose<DT, 6, false>(p, variant, st) : choose<DT, 8, false>(p, variant, st);
+template <int DT, int KK, bool LONG>
+static int choose_pages(const Problem& p, const Variant& variant, cudaStream_t st) {
+  return p.pages ? choose<DT, KK, true, LONG>(p, variant, st) : choose<DT, KK, false, LONG>(p, variant, st);
 }
 
 template <>
-cudaError_t take_attention_error<CONVROT_ATTENTION_TYPE>(int* v) { return crgemm::take_error_word(v); }
+int attention_many<CONVROT_ATTENTION_TYPE, CONVROT_ATTENTION_LONG>(const Problem& p, const Variant& variant, cudaStream_t st) {
+  constexpr int DT = CONVROT_ATTENTION_TYPE;
+  constexpr bool LONG = CONVROT_ATTENTION_LONG;
+  const int steps = (p.D + 15) / 16;
+  if (steps <= 4) return choose_pages<DT, 4, LONG>(p, variant, st);
+  if constexpr (!LONG) {
+    if (steps == 5) return choose_pages<DT, 5, LONG>(p, variant, st);
+    if (steps == 6) return choose_pages<DT, 6, LONG>(p, variant, st);
+  }
+  return choose_pages<DT, 8, LONG>(p, variant, st);
+}
+
+template <>
+cudaError_t take_attention_error<CONVROT_ATTENTION_TYPE, CONVROT_ATTENTION_LONG>(int* v) { return crgemm::take_error_word(v); }
 
 }  // namespace cratt

@@ -72,6 +72,18 @@ constexpr float kLag = 8.f;
 template <int DT>
 constexpr float kLift = DT == CONVROT_FP16 ? 6.f : 0.f;
 
+// Keys after which a row's output leaves the tensor core's accumulators for FP32 sums of its own, rounded to nearest.
+// The accumulators are cut towards zero, as measured by 2^-27 of themselves for every key that they take (equal weights
+// of 2^20 keys: 0.66% short, in mma.sync 0.14% where four warps share the keys), at most by 2^-25 (four cuts for 16
+// keys): over this many keys by a fifth of half a step of the type, at most by half a step.
+template <int DT>
+constexpr int kKeepKeys = DT == CONVROT_FP16 ? 1 << 14 : 1 << 17;
+
+// exp2((from - to) * c): the factor that moves a sum from one reference to another (-inf: nothing summed yet).
+__device__ __forceinline__ float move_reference(float from, float to, float c) {
+  return from == to ? 1.f : exp2_approx((from - to) * c);
+}
+
 template <int DT>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi);
 template <> __device__ __forceinline__ uint32_t pack2<CONVROT_BF16>(float lo, float hi) {

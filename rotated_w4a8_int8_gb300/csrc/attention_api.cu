@@ -14,7 +14,7 @@ template <int DT>
 static int run(const Problem& p, const Variant& variant, cudaStream_t st) {
   const int64_t group = p.heads_q / p.heads_k, rows = (p.rows + p.B - 1) / p.B * group;    // an average sequence's rows per K head
   if (variant.kernel == FEW || (variant.kernel == CHOSEN && rows <= FEW_ROWS)) return attention_few<DT>(p, rows, variant, st);
-  return attention_many<DT>(p, variant, st);
+  return p.keys > kKeepKeys<DT> ? attention_many<DT, true>(p, variant, st) : attention_many<DT, false>(p, variant, st);
 }
 
 static int call(Problem p, convrot_dtype dtype, const int32_t* seqs, float scale, const Variant& variant, cudaStream_t st) {
@@ -126,13 +126,15 @@ extern "C" int convrot_attention_selftest(const void* q, int64_t q_row, int64_t 
 
 namespace convrot {
 cudaError_t take_attention_error_word(int* v) {
-  int each[4] = {};
-  cudaError_t e = take_attention_error<CONVROT_BF16>(&each[0]);
-  if (e == cudaSuccess) e = take_attention_error<CONVROT_FP16>(&each[1]);
-  if (e == cudaSuccess) e = take_few_error(&each[2]);
-  if (e == cudaSuccess) e = take_write_error(&each[3]);
+  int each[6] = {};
+  cudaError_t e = take_attention_error<CONVROT_BF16, false>(&each[0]);
+  if (e == cudaSuccess) e = take_attention_error<CONVROT_BF16, true>(&each[1]);
+  if (e == cudaSuccess) e = take_attention_error<CONVROT_FP16, false>(&each[2]);
+  if (e == cudaSuccess) e = take_attention_error<CONVROT_FP16, true>(&each[3]);
+  if (e == cudaSuccess) e = take_few_error(&each[4]);
+  if (e == cudaSuccess) e = take_write_error(&each[5]);
   *v = 0;
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < 6; ++i)
     if (*v == 0) *v = each[i];
   return e;
 }
