@@ -14,7 +14,8 @@
 // would be mostly padding.  The tiles lie swizzled in shared memory; K's operand
 // is read by ldmatrix, V's by its transposing form, and P^T comes from S^T by an
 // 8 x 8 transposition in registers.  Softmax as in attention.cu: a reference per
-// row that follows the maximum once it has grown by 2^kLag, FP32 sums.  The weights
+// row that follows the maximum once it has grown by 2^kLag, FP32 sums, which O too
+// moves to after kKeepKeys keys of a warp.  The weights
 // go into the product as two values of the operands' type, cut off and what that
 // left: the bytes bound this kernel, and a second product costs nothing that shows
 // (one token: 83.6 and 83.2 us), while one row's error grew by half with one.
@@ -192,7 +193,18 @@ __device__ __forceinline__ void join_parts(const Problem& p, const Sequence& s, 
   cluster_barrier();                     // no CTA leaves, or begins again, while another still reads from it
 }
 
-template <int DT, int DP, int NT, bool PAGED>
+// What is kept of a thread's part of O and the sums of long keys, with its reference (in local memory).
+template <int KK, int NT>
+struct FewKept {
+  volatile float o[NT][KK][4], m[NT][2], l[NT][2];
+};
+// Tiles after which a warp, which takes 16 keys of each, has had kKeepKeys.
+template <int DT>
+constexpr int KEEP_TILES = kKeepKeys<DT> / (TILE_KEYS / FEW_WARPS);
+
+// LONG: a CTA may have more than KEEP_TILES tiles.  (In 45 calls of 1 to 16 rows that need no LONG it took 3.4% longer in
+// the mean, at most 11%.)
+template <int DT, int DP, int NT, bool PAGED, bool LONG>
 __global__ void __launch_bounds__(FEW_THREADS, NT == 1 ? 3 : 2)      // (three where one or two stages are enough)
 few_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
               const __grid_constant__ Problem p, const int slices, const uint32_t stages) {
@@ -308,7 +320,30 @@ few_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CU
       // ldmatrix: this lane's row of the warp's 16 keys, and its 16-byte piece's low bit
       const int k_row = 16 * warp + (lane & 7) + (lane & 8), k_piece = lane >> 4;
       const int v_row = 16 * warp + (lane & 7) + (lane >> 4 << 3), v_piece = lane >> 3 & 1;
+      [[maybe_unused]] FewKept<KK, NT> kept;
+      // adds O and the sums to what is kept and starts those again, or (end) takes the whole as O and the sums
+      [[maybe_unused]] auto keep = [&](bool first, bool end) {
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float f = first ? 0.f : move_reference(kept.m[j][e], m[j][e], p.scale_log2);
+            auto move = [&](float& now, volatile float& before) {
+              const float both = first ? now : before * f + now;
+              before = both;
+              now = end ? both : 0.f;
+            };
+            kept.m[j][e] = m[j][e];
+            move(l[j][e], kept.l[j][e]);
+#pragma unroll
+            for (int u = 0; u < KK; ++u) {
+              move(o[j][u][e], kept.o[j][u][e]);
+              move(o[j][u][2 + e], kept.o[j][u][2 + e]);
+            }
+          }
+      };
       for (int t = t0; t < t1; ++t) {
+        if (LONG && t != t0 && (t - t0) % KEEP_TILES<DT> == 0) keep(t - t0 == KEEP_TILES<DT>, false);
         ok = __all_sync(0xffffffffu, mbar_wait(full0 + 8 * stage, phase, ERR_WAIT_FULL, abort_flag));
         if (!ok) break;
         const int k0 = t * TILE_KEYS + 16 * warp;      // the warp's first key
@@ -410,6 +445,7 @@ few_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CU
         if (lane == 0) mbar_arrive_local(empty0 + 8 * stage);
         if (++stage == stages) { stage = 0; phase ^= 1u; }
       }
+      if (LONG && t1 - t0 > KEEP_TILES<DT>) keep(false, true);
       // the warps' parts, where the tiles were: every warp is done with them
       asm volatile("bar.sync 1, %0;" ::"n"(32 * FEW_WARPS) : "memory");
 #pragma unroll
@@ -439,10 +475,10 @@ few_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CU
 }
 
 // ------------------------------------------------------------------ host side
-template <int DT, int DP, int NT, bool PAGED>
+template <int DT, int DP, int NT, bool PAGED, bool LONG>
 static int launch_few(const Problem& p, int slices, cudaStream_t st) {
   using L = FewLayout<DP, NT>;
-  auto k = few_kernel<DT, DP, NT, PAGED>;
+  auto k = few_kernel<DT, DP, NT, PAGED, LONG>;
   static std::atomic<bool> known[64] = {};       // set up on this device (two threads may both do it)
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -464,7 +500,10 @@ static int launch_few(const Problem& p, int slices, cudaStream_t st) {
 
 template <int DT, int DP, int NT>
 static int launch_few(const Problem& p, int slices, cudaStream_t st) {
-  return p.pages ? launch_few<DT, DP, NT, true>(p, slices, st) : launch_few<DT, DP, NT, false>(p, slices, st);
+  // (tiles that a CTA has at most: one more where the first key lies inside a tile)
+  const bool is_long = ((static_cast<int64_t>(p.keys) + TILE_KEYS - 1) / TILE_KEYS + slices) / slices > KEEP_TILES<DT>;
+  if (p.pages) return is_long ? launch_few<DT, DP, NT, true, true>(p, slices, st) : launch_few<DT, DP, NT, true, false>(p, slices, st);
+  return is_long ? launch_few<DT, DP, NT, false, true>(p, slices, st) : launch_few<DT, DP, NT, false, false>(p, slices, st);
 }
 
 // CTAs that share the keys of a sequence's K head: as many as fit the SMs twice

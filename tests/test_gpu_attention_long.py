@@ -5,7 +5,8 @@ The roundings that the bounds count, with u half a step of the type (finfo.eps /
 (their exponents' one rounded product and the exponential); the row's sum, FP32: weights of a tile of 128 keys are added to
 one another (in two halves of 64), tiles' sums to the row's, 2^-24 of the sum for every addition one after another; the
 tensor core's accumulators, which are cut towards zero: at most 2^-25 of the sum for every key (four cuts for 16 keys) until
-it is added to FP32 sums after 2^14 keys in FP16, 2^17 in BF16: u; and those sums, 2^-24 for each addition.
+it is added to FP32 sums after 2^14 keys in FP16, 2^17 in BF16: u (kernel 1, which has two products for each key: 2 u); and
+those sums, 2^-24 for each addition.
 """
 import math
 
@@ -67,7 +68,7 @@ def values():
     made.clear()
 
 
-@pytest.mark.parametrize("dtype,kernel", [(t, k) for t in (BF, HF) for k in KERNELS if k[0] != 1])
+@pytest.mark.parametrize("dtype,kernel", [(t, k) for t in (BF, HF) for k in KERNELS])
 def test_sum_of_values(values, dtype, kernel):
     """All scores zero: the weights and their sum are exact, the output is the values' mean."""
     import rotated_w4a8_int8_gb300 as cr
@@ -77,13 +78,13 @@ def test_sum_of_values(values, dtype, kernel):
     cr.attention_selftest(q, v, v, out, *kernel)
     torch.cuda.synchronize()
     u, held = torch.finfo(dtype).eps / 2, 2 ** 24 // (2 ** 14 if dtype == HF else 2 ** 17)
-    assert float((out.double() / want - 1).abs().max()) <= 2 * u + held * 2.0 ** -24
+    assert float((out.double() / want - 1).abs().max()) <= (3 if kernel[0] == 1 else 2) * u + held * 2.0 ** -24
 
 
-def within(q, k, v, seqs, causal, out, got):
-    """check() with the accumulators' term: u times the sum of p |v|."""
+def within(q, k, v, seqs, causal, out, got, cuts=1):
+    """check() with the accumulators' term: `cuts` u times the sum of p |v|."""
     want, bound = reference(q, k, v, seqs, q.shape[2] ** -0.5, causal, out)
-    check(got, want, bound + torch.finfo(q.dtype).eps / 2 * reference(q, k, v.abs(), seqs, q.shape[2] ** -0.5, causal, out)[0])
+    check(got, want, bound + cuts * torch.finfo(q.dtype).eps / 2 * reference(q, k, v.abs(), seqs, q.shape[2] ** -0.5, causal, out)[0])
 
 
 @pytest.mark.parametrize("kernel", KERNELS)
@@ -105,7 +106,7 @@ def test_references_that_move(kernel, dtype, causal, grows):
     cr.attention_selftest(q, kc, vc, out, *kernel, pages=table, seqs=where, causal=causal)
     torch.cuda.synchronize()
     assert cr.device_error() == 0
-    within(q, k, v, seqs, causal, before, out)
+    within(q, k, v, seqs, causal, before, out, 2 if kernel[0] == 1 else 1)
 
 
 def test_long_and_short_items_in_turn():
