@@ -789,10 +789,11 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
         // a row that has seen no key yet keeps -inf, its weights are exp2(-inf) = 0
         const float zero = m == -INFINITY ? 0.f : m;
         float ref = kLift<DT> - zero * p.scale_log2;
-        // This product's rounding moves all weights of the row by one factor, 2 to the 2^-24th of it: of no account below
-        // 2^16, past a type's range from some 2^25 on.  There the scores' differences are taken first (2304 rows x 19989
-        // keys x 56 heads: without this 802 us, with the vote 808, differences in all rows 821).
-        const bool large = fabsf(zero * p.scale_log2) > 65536.f;
+        // This product's rounding moves all weights that are taken from this reference by one factor, 2 to the 2^-25th of it:
+        // below 2^10 by at most 2^-15.5, which parts of a row with other references do not share; from some 2^25 on past
+        // a type's range.  Past 2^10 the scores' differences are taken first (2304 rows x 19989 keys x 56 heads: without
+        // this 802 us, with the vote 808, differences in all rows 821).
+        const bool large = fabsf(zero * p.scale_log2) > 1024.f;
         if (__any_sync(0xffffffffu, large)) {
           const float2 less = make_float2(large ? -zero : 0.f, large ? -zero : 0.f);
           if (large) ref = kLift<DT>;

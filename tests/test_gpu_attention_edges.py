@@ -256,6 +256,33 @@ def test_large_scores(kernel, dtype, rows):
     check(out, want, bound)
 
 
+@pytest.mark.parametrize("kernel", EACH)
+@pytest.mark.parametrize("dtype", [BF, HF])
+def test_references_of_one_row_agree(kernel, dtype):
+    """Weights of one row are taken from several references: of the slots and CTAs that share its keys, and before and
+    after one has moved.  Scores are whole numbers (times a power of two) of 2^13 to 2^16 powers of two, that grow by
+    less than one from tile to tile while every 32nd row's growth moves its warp's references; the values' signs alternate
+    with the tiles, so that what is left shows a factor between them.  The bound has only roundings: of the weights and the
+    output, and 2^-18 for sums and the exponential."""
+    import rotated_w4a8_int8_gb300 as cr
+    rows, n, D = 130, 1024, 64
+    g = torch.Generator(device=DEV).manual_seed(9)
+    r, j = torch.arange(rows, device=DEV), torch.arange(n, device=DEV)
+    q, k = torch.zeros(rows, 1, D, device=DEV), torch.zeros(n, 1, D, device=DEV)
+    base = (45000 + 2000 * r + 77 * r * r) % 300000 + 46000                   # 0.18 powers of two each
+    q[:, 0, 0], q[:, 0, 1], q[:, 0, 2] = base // 4096, base % 4096 // 16, base % 16
+    q[:, 0, 3], q[:, 0, 4] = torch.where(r % 32 == 0, 64.0, 0.0), 1.0
+    k[:, 0, 0], k[:, 0, 1], k[:, 0, 2], k[:, 0, 3], k[:, 0, 4] = 4096.0, 16.0, 1.0, (j // 128).float(), (j // 128 + j % 3).float()
+    v = torch.randn(n, 1, D, generator=g, device=DEV).abs() * torch.where(j // 128 % 2 == 0, 1.0, -1.0)[:, None, None]
+    q, k, v = q.to(dtype), k.to(dtype), v.to(dtype)
+    out = torch.empty_like(q)
+    cr.attention_selftest(q, k, v, out, *kernel, scale=0.125)
+    torch.cuda.synchronize()
+    want = reference(q, k, v, [(0, rows, 0, n)], 0.125, False, out)[0]
+    p_v = reference(q, k, v.abs(), [(0, rows, 0, n)], 0.125, False, out)[0]
+    check(out, want, (torch.finfo(dtype).eps / 2 + 2.0 ** -18) * (p_v + want.abs()))
+
+
 @pytest.mark.parametrize("kernel", [(1, 2), (2, 1), (3, 2)])
 def test_wait_that_runs_out_is_reported(kernel):
     import rotated_w4a8_int8_gb300 as cr
