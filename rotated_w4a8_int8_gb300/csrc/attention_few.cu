@@ -82,8 +82,9 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uin
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Two values cut to the type (towards zero), and what that leaves of one: never below zero, and above it for every weight
-// above zero, so that an infinite value times both parts is the same infinity.
+// A weight as two values of the type: cut off (towards zero) a little below it, and what that leaves, neither of which
+// then rounds to zero (FP16: from 2^-23 on, 2^-29 of the largest weight), so that an infinite value times both is the same
+// infinity.  The first takes 2^-12 (BF16: 2^-9) of the weight less, FP16 at least a subnormal step.
 template <int DT>
 __device__ __forceinline__ uint32_t truncate2(float lo, float hi) {
   uint32_t v;
@@ -92,9 +93,9 @@ __device__ __forceinline__ uint32_t truncate2(float lo, float hi) {
   return v;
 }
 template <int DT>
-__device__ __forceinline__ float left_over(float e, float cut) {
-  constexpr float least = DT == CONVROT_BF16 ? 1.1754943508222875e-38f : 5.9604644775390625e-8f;      // 2^-126, 2^-24
-  return e == cut && e > 0.f ? least : e - cut;
+__device__ __forceinline__ float below(float e) {
+  if constexpr (DT == CONVROT_BF16) return e - e * 0x1p-9f;
+  return fmaxf(e - fmaxf(e * 0x1p-12f, 0x1p-24f), 0.f);
 }
 
 // 8 x 8 matrix of 16-bit values, transposed over the warp.
@@ -408,10 +409,10 @@ few_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CU
             l[j][1] += e[1] + e[3];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              const uint32_t below = truncate2<DT>(e[2 * h], e[2 * h + 1]);
-              const float2 back = unpack2<DT>(below);
-              w[j][h] = transpose(below);
-              rest[j][h] = transpose(pack2<DT>(left_over<DT>(e[2 * h], back.x), left_over<DT>(e[2 * h + 1], back.y)));
+              const uint32_t cut = truncate2<DT>(below<DT>(e[2 * h]), below<DT>(e[2 * h + 1]));
+              const float2 back = unpack2<DT>(cut);
+              w[j][h] = transpose(cut);
+              rest[j][h] = transpose(pack2<DT>(e[2 * h] - back.x, e[2 * h + 1] - back.y));
             }
           }
           // keys outside the sequence: their values are cleared (0 x NaN), pairs of keys 2 i4 (+1) and those + 8

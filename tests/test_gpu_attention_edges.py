@@ -221,6 +221,28 @@ def test_values_that_are_no_numbers(kernel):
 
 @pytest.mark.parametrize("kernel", EACH)
 @pytest.mark.parametrize("dtype", [BF, HF])
+def test_infinite_values_of_light_keys(kernel, dtype):
+    """Weights down to 2^-22 of the largest one: an infinite value stays the infinity that it is."""
+    import rotated_w4a8_int8_gb300 as cr
+    n, D = 320, 64
+    g = torch.Generator(device=DEV).manual_seed(6)
+    q, k = torch.zeros(20, 1, D, dtype=dtype, device=DEV), torch.zeros(n, 1, D, dtype=dtype, device=DEV)
+    q[:, 0, :3] = 1.0
+    q[:, 0, 3] = torch.arange(20, device=DEV).to(dtype) / 20
+    k[:, 0, 0] = -(torch.rand(n, generator=g, device=DEV) * 14).to(dtype)            # exp(-15.25) = 2^-22
+    k[:, 0, 3] = -torch.rand(n, generator=g, device=DEV).to(dtype)
+    k[0] = 0.0
+    out = torch.empty_like(q)
+    for first in range(0, n, D):
+        v, d = torch.ones(n, 1, D, dtype=dtype, device=DEV), torch.arange(D, device=DEV)
+        v[first + d, 0, d] = torch.where(d % 2 == 0, math.inf, -math.inf).to(dtype)
+        cr.attention_selftest(q, k, v, out, *kernel, scale=1.0)
+        torch.cuda.synchronize()
+        assert bool((out[:, 0, 0::2] == math.inf).all()) and bool((out[:, 0, 1::2] == -math.inf).all())
+
+
+@pytest.mark.parametrize("kernel", EACH)
+@pytest.mark.parametrize("dtype", [BF, HF])
 def test_equal_weights_of_many_keys(kernel, dtype):
     """All scores zero: every weight is 1 / n, the smallest that n keys can share."""
     import rotated_w4a8_int8_gb300 as cr
