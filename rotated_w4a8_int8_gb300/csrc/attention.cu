@@ -853,7 +853,8 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
         // Through shared memory, 32 rows x 64 columns at a time (16-byte pieces swizzled by the row): by a TMA store
         // where the warp's rows are all the item's, else copied, four rows of 128 bytes at a time.  (From the threads'
         // own rows a store covered 32 rows of 16 bytes; copies alone took the warp 3300 clocks, the row's scores wait.)
-        const float f = l == 0.f ? 0.f : 1.f / l;
+        const float f = 1.f / l;                           // (scores all -inf: 0 / 0)
+        const bool none = limit <= it.lo;                  // no key is seen
         const unsigned rows = __ballot_sync(0xffffffffu, mine);
         const bool whole_box = rows == 0xffffffffu && w.pack == 1;
         uint4* box = reinterpret_cast<uint4*>(tiles + (L::QTILES + STAGES) * L::TILE + warp * 4096);
@@ -866,7 +867,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
 #pragma unroll
           for (int j = 0; j < 32; ++j) {
             const uint32_t two = pack2<DT>(__uint_as_float(o[2 * j]) * f, __uint_as_float(o[2 * j + 1]) * f);
-            v[j] = l == 0.f ? 0u : two;
+            v[j] = none ? 0u : two;
           }
           if (lane == 0) bulk_wait_read<0>();              // the box's last store has read it
           __syncwarp();
@@ -913,7 +914,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
           top = high;
         }
         const float f = m == -INFINITY ? 0.f : exp2_approx((m - top) * p.scale_log2);
-        if (slot == 0) inverse[row] = total == 0.f ? 0.f : 1.f / total;
+        if (slot == 0) inverse[row] = limit <= it.lo ? 0.f : 1.f / total;      // (scores all -inf: 0 / 0)
         const int rows = (128 + slices - 1) / slices, source = 2 * rank + slot;
         const uint32_t to = map_to_rank(smem_u32(tiles) + ((source * rows + row / slices) * L::PITCH) * 4, row % slices);
 #pragma unroll 1

@@ -145,11 +145,12 @@ __device__ __forceinline__ void join_parts(const Problem& p, const Sequence& s, 
                                            float2* joined_stats, int part_rows, int pitch) {
   const int group = p.heads_q / p.heads_k;
   auto finish = [&](int r, int col, float2 total, const float (&y)[4]) {
-    const float f = total.y == 0.f ? 0.f : 1.f / total.y;
+    const int64_t at = r0 + r;
+    const float f = 1.f / total.y;                         // (scores all -inf: 0 / 0)
+    const bool none = seen(p, s, static_cast<int>(at / group)) <= 0;
     float z[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) z[j] = total.y == 0.f ? 0.f : y[j] * f;
-    const int64_t at = r0 + r;
+    for (int j = 0; j < 4; ++j) z[j] = none ? 0.f : y[j] * f;
     char* dst = static_cast<char*>(p.out) +
                 2 * ((s.q_start + at / group) * p.out_tok + (head_kv * group + at % group) * p.out_head + col);
     asm volatile("st.global.v2.b32 [%0], {%1, %2};" ::"l"(dst), "r"(pack2<DT>(z[0], z[1])), "r"(pack2<DT>(z[2], z[3])) : "memory");

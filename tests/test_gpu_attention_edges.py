@@ -221,6 +221,29 @@ def test_values_that_are_no_numbers(kernel):
 
 @pytest.mark.parametrize("kernel", EACH)
 @pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("page", [0, 16])
+def test_scores_of_minus_infinity(kernel, dtype, page):
+    """Keys with such a score have no weight; a row with no other key is 0 / 0, a row that sees no key zeros."""
+    import rotated_w4a8_int8_gb300 as cr
+    q, k, v = (rand(n, h, 64, seed=n + h, dtype=dtype) for n, h in ((50, 4), (400, 2), (400, 2)))
+    q[:, :, 0] = 1.0
+    k[:200, :, 0], k[200:300, :, 0] = -math.inf, -math.inf             # all of the first 200, 100 of the others
+    seqs = [(0, 20, 0, 200), (20, 10, 200, 200), (30, 0, 5, 5), (30, 20, 390, 10)]
+    table, where, kk, vv = None, i32(seqs), k, v
+    if page:
+        kk, vv, table, where = paged(k, v, seqs, page, 5)
+    out = torch.full_like(q, 3.0)
+    cr.attention_selftest(q, kk, vv, out, *kernel, pages=table, seqs=where, causal=True)
+    torch.cuda.synchronize()
+    assert cr.device_error() == 0
+    assert bool(out[:20].isnan().all()) and bool((out[30:40] == 0).all())
+    finite = [(20, 10, 300, 100), (30, 20, 390, 10)]
+    want, bound = reference(q, k, v, finite, 0.125, True, torch.zeros_like(out))
+    check(out[20:], want[20:], bound[20:])
+
+
+@pytest.mark.parametrize("kernel", EACH)
+@pytest.mark.parametrize("dtype", [BF, HF])
 def test_infinite_values_of_light_keys(kernel, dtype):
     """Weights down to 2^-22 of the largest one: an infinite value stays the infinity that it is."""
     import rotated_w4a8_int8_gb300 as cr
