@@ -477,60 +477,86 @@ few_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CU
 }
 
 // ------------------------------------------------------------------ host side
+// Sets the kernel up on the current device: its SMs, and the largest cluster of its CTAs that can be resident there.
+template <int DT, int DP, int NT, bool PAGED, bool LONG>
+static cudaError_t set_up(int* sms, int* largest) {
+  using L = FewLayout<DP, NT>;
+  static std::atomic<int> known[64] = {};        // SMs * 32 + the largest cluster; 0: not set up (two threads may both do it)
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  int both = dev < 64 ? known[dev].load() : 0;
+  if (both == 0) {
+    auto k = few_kernel<DT, DP, NT, PAGED, LONG>;
+    constexpr int smem = L::smem(L::MOST_STAGES);
+    if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return e;
+    if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess) return e;
+    int n = 0, size = MOST_FEW_SLICES;
+    if ((e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
+    for (; size > 8; --size) {                   // (eight is portable)
+      cudaLaunchConfig_t cfg = {};
+      cudaLaunchAttribute attr[1];
+      attr[0].id = cudaLaunchAttributeClusterDimension;
+      attr[0].val.clusterDim.x = size;
+      attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+      cfg.blockDim = dim3(FEW_THREADS);
+      cfg.dynamicSmemBytes = smem;
+      cfg.gridDim = dim3(size);
+      cfg.attrs = attr;
+      cfg.numAttrs = 1;
+      int clusters = 0;
+      if (cudaOccupancyMaxActiveClusters(&clusters, k, &cfg) == cudaSuccess && clusters > 0) break;
+      (void)cudaGetLastError();
+    }
+    both = n * 32 + size;
+    if (dev < 64) known[dev] = both;
+  }
+  *sms = both / 32;
+  *largest = both % 32;
+  return cudaSuccess;
+}
+
+static int64_t tiles_of(int64_t keys) { return (keys + TILE_KEYS - 1) / TILE_KEYS; }
+
 template <int DT, int DP, int NT, bool PAGED, bool LONG>
 static int launch_few(const Problem& p, int slices, cudaStream_t st) {
   using L = FewLayout<DP, NT>;
-  auto k = few_kernel<DT, DP, NT, PAGED, LONG>;
-  static std::atomic<bool> known[64] = {};       // set up on this device (two threads may both do it)
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess && (dev >= 64 || !known[dev])) {
-    e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, L::smem(L::MOST_STAGES));
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e == cudaSuccess && dev < 64) known[dev] = true;
-  }
+  int sms, largest;
+  cudaError_t e = set_up<DT, DP, NT, PAGED, LONG>(&sms, &largest);
   if (e != cudaSuccess) return convrot::record_cuda_error("attention set-up", e);
   CUtensorMap mk, mv;
   if (!make_key_maps<DT, PAGED>(&mk, &mv, p, TILE_KEYS)) return convrot::record_error("cuTensorMapEncodeTiled failed for k or v");
   // no more stages than tiles: short keys leave room for more CTAs
-  const int64_t tiles = (static_cast<int64_t>(p.keys) + TILE_KEYS - 1) / TILE_KEYS, share = (tiles + slices - 1) / slices;
+  const int64_t share = (tiles_of(p.keys) + slices - 1) / slices;
   const int stages = static_cast<int>(share < 1 ? 1 : share < L::MOST_STAGES ? share : L::MOST_STAGES);
-  e = convrot::launch_after(k, dim3(p.heads_k * slices, p.B), FEW_THREADS, L::smem(stages), slices, st, mk, mv, p, slices,
-                            static_cast<uint32_t>(stages));
+  e = convrot::launch_after(few_kernel<DT, DP, NT, PAGED, LONG>, dim3(p.heads_k * slices, p.B), FEW_THREADS, L::smem(stages), slices,
+                            st, mk, mv, p, slices, static_cast<uint32_t>(stages));
   return e == cudaSuccess ? CONVROT_OK : convrot::record_cuda_error("attention launch", e);
 }
 
-template <int DT, int DP, int NT>
-static int launch_few(const Problem& p, int slices, cudaStream_t st) {
+template <int DT, int DP, int NT, bool PAGED>
+static int launch_few(const Problem& p, const Variant& variant, cudaStream_t st) {
+  int sms, largest;
+  const cudaError_t e = set_up<DT, DP, NT, PAGED, false>(&sms, &largest);
+  if (e != cudaSuccess) return convrot::record_cuda_error("attention set-up", e);
+  const int64_t keys = p.seqs && !p.pages ? (p.keys + p.B - 1) / p.B : p.keys;
+  const int slices = variant.kernel == CHOSEN ? few_slices(static_cast<int64_t>(p.heads_k) * p.B, tiles_of(keys), sms, largest)
+                                              : variant.slices;
+  if (slices > largest) return CONVROT_ERR_UNSUPPORTED;
   // (tiles that a CTA has at most: one more where the first key lies inside a tile)
-  const bool is_long = ((static_cast<int64_t>(p.keys) + TILE_KEYS - 1) / TILE_KEYS + slices) / slices > KEEP_TILES<DT>;
-  if (p.pages) return is_long ? launch_few<DT, DP, NT, true, true>(p, slices, st) : launch_few<DT, DP, NT, true, false>(p, slices, st);
-  return is_long ? launch_few<DT, DP, NT, false, true>(p, slices, st) : launch_few<DT, DP, NT, false, false>(p, slices, st);
+  const bool is_long = (tiles_of(p.keys) + slices) / slices > KEEP_TILES<DT>;
+  return is_long ? launch_few<DT, DP, NT, PAGED, true>(p, slices, st) : launch_few<DT, DP, NT, PAGED, false>(p, slices, st);
 }
 
-// CTAs that share the keys of a sequence's K head: as many as fit the SMs twice
-// (one token, 56 heads x 19989 keys: 4 or 5 CTAs 83 us, 2 97 us, 6, which take
-// two rounds, 99 us; 2 heads x 32768 keys: 16 CTAs 20 us, 8 33 us), two tiles or
-// more for each; with more heads than that, four where the keys are long, so that
-// the last round is short (512 x 8191 keys: 213 us, whole 242 us; 512 x 512: 26 to
-// 41 us in parts, whole 16 us).
-static int few_slices(const Problem& p) {
-  const int64_t units = static_cast<int64_t>(p.heads_k) * p.B;
-  const int64_t keys = p.seqs && !p.pages ? (p.keys + p.B - 1) / p.B : p.keys, tiles = (keys + TILE_KEYS - 1) / TILE_KEYS;
-  int64_t n = 2 * 152 / units, most = tiles / 2;
-  if (n < 2) n = 4, most = tiles / 32;
-  // larger clusters than eight fit less well: only where they have the SMs for themselves (30 heads x 4096 keys: by
-  // eight 10 us, by ten 18 us)
-  if (n > 8) n = 152 / units > 8 ? 152 / units : 8;
-  n = n < most ? n : most;
-  return static_cast<int>(n < 1 ? 1 : n > MOST_FEW_SLICES ? MOST_FEW_SLICES : n);
+template <int DT, int DP, int NT>
+static int launch_few(const Problem& p, const Variant& variant, cudaStream_t st) {
+  return p.pages ? launch_few<DT, DP, NT, true>(p, variant, st) : launch_few<DT, DP, NT, false>(p, variant, st);
 }
 
 template <int DT>
 int attention_few(const Problem& p, int64_t rows, const Variant& variant, cudaStream_t st) {
-  const int slices = variant.kernel == CHOSEN ? few_slices(p) : variant.slices;
-  if (p.D <= 64) return rows > 8 ? launch_few<DT, 64, 2>(p, slices, st) : launch_few<DT, 64, 1>(p, slices, st);
-  return rows > 8 ? launch_few<DT, 128, 2>(p, slices, st) : launch_few<DT, 128, 1>(p, slices, st);
+  if (p.D <= 64) return rows > 8 ? launch_few<DT, 64, 2>(p, variant, st) : launch_few<DT, 64, 1>(p, variant, st);
+  return rows > 8 ? launch_few<DT, 128, 2>(p, variant, st) : launch_few<DT, 128, 1>(p, variant, st);
 }
 template int attention_few<CONVROT_BF16>(const Problem&, int64_t, const Variant&, cudaStream_t);
 template int attention_few<CONVROT_FP16>(const Problem&, int64_t, const Variant&, cudaStream_t);

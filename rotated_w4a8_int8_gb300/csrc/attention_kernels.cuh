@@ -7,11 +7,12 @@
 #include <cuda_runtime.h>
 
 #include "attention.cuh"
+#include "attention_choice.h"
 
 namespace cratt {
 
 constexpr int FEW_ROWS = 16;                  // rows per K head up to which the kernel for few is taken
-constexpr int MOST_FEW_SLICES = 16, MOST_SLICES = 8;
+constexpr int MOST_SLICES = 8;
 
 // Which kernel computes a call, and how many CTAs share keys (FEW, SHARED).
 enum Kernel : int { CHOSEN = 0, FEW = 1, WHOLE = 2, SHARED = 3 };

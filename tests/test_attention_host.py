@@ -224,3 +224,40 @@ def test_other_threads_run_while_a_call_waits(marshal, tmp_path, call, names):
     t.start()
     assert call(marshal, [0] * len(names)) == 0
     t.join()
+
+
+CHOICE = """
+#include "attention_choice.h"
+extern "C" int few_slices(long long units, long long tiles, int sms, int largest) {
+  return cratt::few_slices(units, tiles, sms, largest);
+}
+"""
+
+
+def test_ctas_that_share_keys(tmp_path):
+    """As many as were chosen for 152 SMs when that was written into the code; never a larger cluster than the device
+    takes, and fewer on fewer SMs."""
+    import os
+    import subprocess
+    src, so = tmp_path / "choice.cpp", tmp_path / "choice.so"
+    src.write_text(CHOICE)
+    subprocess.run(["g++", "-std=c++17", "-O1", "-shared", "-fPIC", "-I", os.path.join(os.path.dirname(cr.LIB_PATH), "csrc"),
+                    str(src), "-o", str(so)], check=True)
+    slices = ctypes.CDLL(str(so)).few_slices
+    slices.argtypes = [ctypes.c_longlong] * 2 + [ctypes.c_int] * 2
+
+    def as_before(units, tiles):
+        n, most = 304 // units, tiles // 2
+        if n < 2:
+            n, most = 4, tiles // 32
+        if n > 8:
+            n = max(152 // units, 8)
+        return max(1, min(n, most, 16))
+    for units in (1, 2, 7, 8, 9, 16, 17, 19, 20, 30, 38, 56, 76, 150, 152, 153, 304, 305, 4096, 65535 * 8):
+        for tiles in (0, 1, 2, 3, 17, 31, 32, 64, 129, 313, 1 << 20):
+            want = as_before(units, tiles)
+            assert slices(units, tiles, 152, 16) == want
+            for largest in (1, 8, 11):
+                assert slices(units, tiles, 152, largest) == min(want, largest)
+            assert slices(units, tiles, 19, 16) <= max(8, 19 // units)
+    assert slices(2, 1 << 20, 19, 16) == 9 and slices(1, 1 << 20, 8, 16) == 8
