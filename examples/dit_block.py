@@ -54,6 +54,9 @@ class FrameCache:
 
     def extend(self, n: int) -> torch.Tensor:
         """Room for n more tokens; the call's seqs: every token in the window, the new ones at the end."""
+        if n > self.window or self.length + n > self.table.shape[1] * self.page:
+            raise ValueError(f"{n} tokens after {self.length}: more than the window ({self.window}) or the table "
+                             f"({self.table.shape[1] * self.page}) holds")
         self.length += n
         first = max(0, self.length - self.window)
         for i in [i for i in self.held if (i + 1) * self.page <= first]:

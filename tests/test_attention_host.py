@@ -261,3 +261,19 @@ def test_ctas_that_share_keys(tmp_path):
                 assert slices(units, tiles, 152, largest) == min(want, largest)
             assert slices(units, tiles, 19, 16) <= max(8, 19 // units)
     assert slices(2, 1 << 20, 19, 16) == 9 and slices(1, 1 << 20, 8, 16) == 8
+
+
+def test_frame_cache_refuses_what_it_cannot_hold():
+    """A frame longer than the window, or one past the table, is refused, and the cache is as before."""
+    import os
+    import sys
+    sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
+    import dit_block
+    cache = dit_block.FrameCache(tokens=64, window=40, heads=1, head_dim=8, page=16, device="cpu")
+    with pytest.raises(ValueError, match="window"):
+        cache.extend(41)
+    assert cache.extend(40).tolist() == [[0, 40, 0, 40]]
+    assert cache.extend(24).tolist() == [[0, 24, 24, 40]]
+    with pytest.raises(ValueError, match="table"):
+        cache.extend(1)
+    assert cache.length == 64 and sorted(cache.held) == [1, 2, 3]
