@@ -126,3 +126,13 @@ def test_all_rows_and_keys_without_sequences():
     cr.attention(q, k, v, out)
     torch.cuda.synchronize()
     check(out, *reference(q, k, v, [(0, 300, 0, 200)], 0.125, False, out))
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+@pytest.mark.parametrize("D,dtype", [(104, BF), (112, HF), (120, BF)])
+@pytest.mark.parametrize("page", [0, 32])
+def test_widths_below_the_widest(kernel, D, dtype, page):
+    # computed as 128 columns; the next head's and the next row's values lie right behind
+    seqs = [(0, 3, 0, 130), (3, 140, 130, 300)]
+    q, k, v = inputs(143, 430, 4, 2, D, dtype, seed=D)
+    run(q, k, v, seqs, kernel, True, page, 21 if page else 0)
