@@ -277,35 +277,36 @@ template <int DP>
 struct Kept {
   float o[DP], m, l;
 };
-// Adds O (32 x `n` columns), whose reference is m, and the row's sum l to what is kept and clears O; or (end) takes the
-// whole as O.  Returns the new sum.  (Not inlined: in the rows' loop it cost short items up to 10%.)
-template <int DP>
-static __device__ __noinline__ float move_kept(Kept<DP>* kept, uint32_t o_addr, int n, float m, float l, float c, bool first, bool end) {
-  const float f = first ? 0.f : move_reference(kept->m, m, c);
-  const float sum = first ? l : kept->l * f + l;
+enum Move : int { FIRST, NEXT, LAST };
+// Adds O (32 x N columns), whose reference is m, and the row's sum l to what is kept (FIRST: nothing yet) and clears O; or
+// (LAST) adds what is kept to O.  Returns the new sum.  (Not inlined: in the rows' loop it cost short items up to 10%.)
+template <int MOVE, int N, int DP>
+static __device__ __noinline__ float move_kept(Kept<DP>* kept, uint32_t o_addr, float m, float l, float c) {
+  __builtin_assume(__isLocal(kept));
+  const float f = MOVE == FIRST ? 0.f : move_reference(kept->m, m, c), sum = MOVE == FIRST ? l : kept->l * f + l;
   kept->m = m;
   kept->l = sum;
 #pragma unroll 1
-  for (int i = 0; i < n; ++i) {
+  for (int i = 0; i < N; ++i) {
     uint32_t o[32];
     tmem_ld32(o_addr + 32 * i, o);
     tmem_ld_wait();
 #pragma unroll
     for (int j = 0; j < 32; ++j) {
-      const float y = __uint_as_float(o[j]) + (first ? 0.f : kept->o[32 * i + j] * f);
-      kept->o[32 * i + j] = y;
-      o[j] = end ? __float_as_uint(y) : 0u;
+      const float y = MOVE == FIRST ? __uint_as_float(o[j]) : kept->o[32 * i + j] * f + __uint_as_float(o[j]);
+      if (MOVE != LAST) kept->o[32 * i + j] = y;
+      o[j] = MOVE == LAST ? __float_as_uint(y) : 0u;
     }
     tmem_st32(o_addr + 32 * i, o);
   }
   tmem_st_wait();
-  return end ? sum : 0.f;
+  return MOVE == LAST ? sum : 0.f;
 }
 
 // ------------------------------------------------------------------ kernel
 // KK: steps of 16 columns that the products take of a head (4, 5, 6 or 8), in tiles of 64 or 128 columns (20000 rows x 2048
 // keys x 8 heads of 80: 104 us, with the steps of 128 columns 114; of 96: 107 and 115; of 128: 115).
-// LONG: a sequence may have more than kKeepKeys keys.  (Calls of short items take 1 to 5% longer with it.)
+// LONG: a sequence may have more than kKeepKeys keys.  (Calls of short items take up to 5% longer with it.)
 template <int DT, int KK, bool PAGED, bool SPLIT, bool LONG>
 __global__ void __launch_bounds__(THREADS, 1)
 attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
@@ -735,7 +736,8 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
           ok = __all_sync(0xffffffffu, mbar_wait(s_full0 + 8 * slot, s_phase, ERR_WAIT_ACC_FULL, abort_flag));
           if (!ok) break;
           tc_fence_after();
-          l0 = move_kept(&kept, o_addr, COLUMNS, m, l0 + l1, p.scale_log2, t - t0 == KEEP, false);
+          l0 = t - t0 == KEEP ? move_kept<FIRST, COLUMNS>(&kept, o_addr, m, l0 + l1, p.scale_log2)
+                              : move_kept<NEXT, COLUMNS>(&kept, o_addr, m, l0 + l1, p.scale_log2);
           l1 = 0.f;
         }
         ok = __all_sync(0xffffffffu, mbar_wait(s_full0 + 8 * slot, s_phase, ERR_WAIT_ACC_FULL, abort_flag));
@@ -805,9 +807,9 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
           }
         }
         const float2 r2 = make_float2(ref, ref);
-        // A tile's sum starts from zero: added one by one to the row's, equal weights would all be rounded the same way
-        // (2^20 keys: up to 0.7% of the sum; at 2^25 a half's sum no longer grew).
-        float2 sum = make_float2(0.f, 0.f);
+        // A tile's sum starts anew: added one by one to the row's, equal weights would all be rounded the same way (2^20
+        // keys: up to 0.7% of the sum; at 2^25 a half's sum no longer grew).
+        float2 sum;
         auto weights = [&](int c) {                        // of 32 keys
           uint32_t packed[16];
 #pragma unroll
@@ -815,7 +817,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
             float2 e = fma2(make_float2(x[32 * c + 2 * j], x[32 * c + 2 * j + 1]), c2, r2);
             e.x = exp2_approx(e.x);
             e.y = exp2_approx(e.y);
-            sum = add2(sum, e);
+            sum = c == 0 && j == 0 ? e : add2(sum, e);
             packed[j] = pack2<DT>(e.x, e.y);
           }
           tmem_st16(s_addr + 16 * c, packed);
@@ -832,15 +834,16 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
         weights(2);
         weights(3);
         hand_over(1);
-        l0 += sum.x;
-        l1 += sum.y;
+        sum = add2(make_float2(l0, l1), sum);
+        l0 = sum.x;
+        l1 = sum.y;
       }
       if (ok && any) {
         ok = __all_sync(0xffffffffu, mbar_wait(o_full0 + 8 * slot, o_phase, ERR_WAIT_ACC_FULL, abort_flag));
         o_phase ^= 1u;
         tc_fence_after();
         if (LONG && t1 - t0 > KEEP) {
-          l0 = move_kept(&kept, o_addr, COLUMNS, m, l0 + l1, p.scale_log2, false, true);
+          l0 = move_kept<LAST, COLUMNS>(&kept, o_addr, m, l0 + l1, p.scale_log2);
           l1 = 0.f;
         }
       }
@@ -1129,12 +1132,10 @@ int attention_many<CONVROT_ATTENTION_TYPE, CONVROT_ATTENTION_LONG>(const Problem
   constexpr int DT = CONVROT_ATTENTION_TYPE;
   constexpr bool LONG = CONVROT_ATTENTION_LONG;
   const int steps = (p.D + 15) / 16;
-  if (steps <= 4) return choose_pages<DT, 4, LONG>(p, variant, st);
-  if constexpr (!LONG) {
-    if (steps == 5) return choose_pages<DT, 5, LONG>(p, variant, st);
-    if (steps == 6) return choose_pages<DT, 6, LONG>(p, variant, st);
-  }
-  return choose_pages<DT, 8, LONG>(p, variant, st);
+  return steps <= 4   ? choose_pages<DT, 4, LONG>(p, variant, st)
+         : steps == 5 ? choose_pages<DT, 5, LONG>(p, variant, st)
+         : steps == 6 ? choose_pages<DT, 6, LONG>(p, variant, st)
+                      : choose_pages<DT, 8, LONG>(p, variant, st);
 }
 
 template <>

@@ -4,9 +4,9 @@ under test is exact or bounded by a few roundings.
 The roundings that the bounds count, with u half a step of the type (finfo.eps / 2): the output's u; the weights' own 2^-20
 (their exponents' one rounded product and the exponential); the row's sum, FP32: weights of a tile of 128 keys are added to
 one another (in two halves of 64), tiles' sums to the row's, 2^-24 of the sum for every addition one after another; the
-tensor core's accumulators, which are cut towards zero: at most 2^-25 of the sum for every key (four cuts for 16 keys) until
-it is added to FP32 sums after 2^14 keys in FP16, 2^17 in BF16: u (kernel 1, which has two products for each key: 2 u); and
-those sums, 2^-24 for each addition.
+tensor core's accumulators, which are cut towards zero: at most 2^-26 of a sum that grows evenly for every key (four cuts
+for 16 keys, each less than 2^-23 of what has been summed by then) until it is added to FP32 sums after 2^15 keys in FP16, 2^17
+in BF16: u (kernel 1, which has two products for each key: 2 u); and those sums, 2^-24 for each addition.
 """
 import math
 
@@ -122,3 +122,35 @@ def test_long_and_short_items_in_turn():
     for h in range(0, 160, 40):
         part = slice(h, h + 40)
         within(q[:, part], k, v, seqs, False, torch.zeros_like(q[:, part]), out[:, part])
+
+
+@pytest.mark.parametrize("rows,dtype,keys", [(4, HF, 300000), (4, BF, 2200000), (200, HF, 70000), (400, BF, 140000)])
+def test_captured_and_at_once(rows, dtype, keys):
+    """Long keys through the chosen kernels: on two streams at once and replayed from two graphs, the same bits as one
+    call alone."""
+    import rotated_w4a8_int8_gb300 as cr
+    g = torch.Generator(device=DEV).manual_seed(rows)
+    sets = [[torch.randn(n, h, 64, generator=g, device=DEV).to(dtype) for n, h in ((rows, 8), (keys, 2), (keys, 2))] for _ in range(2)]
+    want, out = ([torch.zeros_like(q) for q, _, _ in sets] for _ in range(2))
+    for o, s in zip(want, sets):
+        cr.attention(*s, o)
+        torch.cuda.synchronize()
+    part = slice(0, 4)
+    within(sets[0][0][part], *sets[0][1:], [(0, 4, 0, keys)], False, torch.zeros_like(want[0][part]), want[0][part], 2)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(3):
+        for st, o, s in zip(streams, out, sets):
+            cr.attention(*s, o, stream=st)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(want, out))
+    graphs = [torch.cuda.CUDAGraph() for _ in range(2)]
+    for graph, o, s in zip(graphs, out, sets):
+        o.zero_()
+        with torch.cuda.graph(graph):
+            cr.attention(*s, o)
+            cr.attention(*s, o)
+    for st, graph in zip(streams, graphs):
+        with torch.cuda.stream(st):
+            graph.replay()
+    torch.cuda.synchronize()
+    assert cr.device_error() == 0 and all(torch.equal(a, b) for a, b in zip(want, out))
