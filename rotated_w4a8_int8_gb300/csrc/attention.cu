@@ -203,11 +203,6 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
       : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
   return d;
 }
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-  return v;
-}
 __device__ __forceinline__ void st_cluster_f32x4(uint32_t addr, float a, float b, float c, float d) {
   asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(a), "f"(b), "f"(c), "f"(d) : "memory");
 }
@@ -907,8 +902,8 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
         cluster_sync();              // statistics are there, and all tiles have been used
         float top = -INFINITY, total = 0.f;
         for (int i = 0; i < 2 * slices; ++i) {
-          const uint32_t a = map_to_rank(smem_u32(stats + (i & 1) * 128 + row), i >> 1);
-          const float mi = ld_cluster_f32(a), li = ld_cluster_f32(a + 4), high = fmaxf(top, mi);
+          const float2 part = load_cluster2(map_to_rank(smem_u32(stats + (i & 1) * 128 + row), i >> 1));
+          const float mi = part.x, li = part.y, high = fmaxf(top, mi);
           if (high == -INFINITY) {                        // no key so far (or nothing but NaN)
             total += li;
             continue;

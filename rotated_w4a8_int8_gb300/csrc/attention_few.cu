@@ -105,26 +105,6 @@ __device__ __forceinline__ uint32_t transpose(uint32_t x) {
   return y;
 }
 
-__device__ __forceinline__ uint32_t shared_of_rank(const void* p, uint32_t rank) {
-  uint32_t r;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(p))), "r"(rank));
-  return r;
-}
-__device__ __forceinline__ float4 load_cluster4(uint32_t addr) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
-  return v;
-}
-__device__ __forceinline__ float2 load_cluster2(uint32_t addr) {
-  float2 v;
-  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
-  return v;
-}
-__device__ __forceinline__ void cluster_barrier() {
-  __syncwarp();
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
 // Adds a partial with reference m and sum l to the running ones; the factors of both sides.
 __device__ __forceinline__ void join(float2& total, float2 part, float c, float& keep, float& take) {
   const float top = fmaxf(total.x, part.x);
@@ -182,17 +162,18 @@ __device__ __forceinline__ void join_parts(const Problem& p, const Sequence& s, 
     __syncthreads();
     return;
   }
-  cluster_barrier();
+  cluster_sync();
   // the cluster's CTAs take the rows' columns in turn
   for (int i = rank + slices * threadIdx.x; i < held * cols4; i += slices * blockDim.x) {
     const int r = i / cols4, col = 4 * (i % cols4);
     float2 total = make_float2(-INFINITY, 0.f);
     float y[4] = {};
     for (int j = 0; j < slices; ++j)
-      add(total, y, load_cluster2(shared_of_rank(joined_stats + r, j)), load_cluster4(shared_of_rank(joined + r * pitch + col, j)));
+      add(total, y, load_cluster2(map_to_rank(smem_u32(joined_stats + r), j)),
+          load_cluster4(map_to_rank(smem_u32(joined + r * pitch + col), j)));
     finish(r, col, total, y);
   }
-  cluster_barrier();                     // no CTA leaves, or begins again, while another still reads from it
+  cluster_sync();                     // no CTA leaves, or begins again, while another still reads from it
 }
 
 // What is kept of a thread's part of O and the sums of long keys, with its reference (in local memory).

@@ -190,6 +190,38 @@ def test_many_sequences(kernel):
     check(out, *reference(q, k, v, seqs, 0.125, True, out))
 
 
+@pytest.mark.parametrize("kernel", [(1, 1), (1, 2), (2, 1), (3, 2), None])
+def test_most_sequences(kernel):
+    """As many sequences as a call takes, their rows in no order: a page each, written and attended to."""
+    import rotated_w4a8_int8_gb300 as cr
+    B, n, m, D, page = 65535, 3, 5, 64, 16
+    order = torch.randperm(B, generator=torch.Generator().manual_seed(8)).to(DEV)
+    q, k, v = rand(B * n, 1, D), rand(B * n, 1, D, seed=1), rand(B * n, 1, D, seed=2)
+    kc, vc = rand(B, page, 1, D, seed=3), rand(B, page, 1, D, seed=4)
+    table = torch.arange(B - 1, -1, -1, dtype=torch.int32, device=DEV).view(B, 1)
+    seqs = torch.stack([order * n, torch.full_like(order, n), order % 11, torch.full_like(order, m)], 1).to(torch.int32)
+    want_k, want_v = kc.clone(), vc.clone()
+    where = (table[:, :1].long(), (order % 11)[:, None] + m - n + torch.arange(n, device=DEV))
+    rows = order[:, None] * n + torch.arange(n, device=DEV)
+    want_k[where], want_v[where] = k[rows], v[rows]
+    cr.cache_write(k, v, kc, vc, table, seqs)
+    out = torch.empty_like(q)
+    if kernel:
+        cr.attention_selftest(q, kc, vc, out, *kernel, pages=table, seqs=seqs, causal=True)
+    else:
+        cr.paged_attention(q, kc, vc, table, seqs, out, causal=True)
+    torch.cuda.synchronize()
+    assert cr.device_error() == 0 and torch.equal(kc, want_k) and torch.equal(vc, want_v)
+    keys = (table[:, :1].long(), (order % 11)[:, None] + torch.arange(m, device=DEV))
+    kk, vv, qq = want_k[keys][:, :, 0].double(), want_v[keys][:, :, 0].double(), q[rows][:, :, 0].double()
+    s, size = torch.matmul(qq, kk.transpose(1, 2)) / 8, torch.matmul(qq.abs(), kk.abs().transpose(1, 2)) / 8
+    hidden = torch.arange(m, device=DEV) > m - n + torch.arange(n, device=DEV)[:, None]
+    p = torch.softmax(s.masked_fill(hidden, -math.inf), 2)
+    y, A, u = p @ vv, p @ vv.abs(), torch.finfo(BF).eps / 2
+    e = size.amax(2, keepdim=True) * (D * 2.0 ** -23 + 2.0 ** -20) + 2.0 ** -20
+    check(out[rows][:, :, 0], y, u * (A + y.abs()) + 2 * e * A + torch.finfo(BF).tiny * u)
+
+
 @pytest.mark.parametrize("kernel", EACH)
 def test_values_that_are_no_numbers(kernel):
     """A row of q that is NaN stays alone; an Inf or NaN among the values shows in its column of every row that sees the
