@@ -768,7 +768,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
         const float now = fmaxf(fmaxf(m, fmaxf(top[0], top[1])), fmaxf(top[2], top[3]));
         if (t == t0) {
           m = now;                                        // nothing summed yet
-        } else if (__any_sync(0xffffffffu, (now - m) * p.scale_log2 > kLag)) {
+        } else if (__any_sync(0xffffffffu, (now - m) * p.scale_log2 > kLag<DT, LONG>)) {
           const float f = now == m ? 1.f : exp2_approx((m - now) * p.scale_log2);
           m = now;
           l0 *= f;
@@ -785,7 +785,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
         }
         // a row that has seen no key yet keeps -inf, its weights are exp2(-inf) = 0
         const float zero = m == -INFINITY ? 0.f : m;
-        float ref = kLift<DT> - zero * p.scale_log2;
+        float ref = kLift<DT, LONG> - zero * p.scale_log2;
         // This product's rounding moves all weights that are taken from this reference by one factor, 2 to the 2^-25th of it:
         // below 2^10 by at most 2^-15.5, which parts of a row with other references do not share; from some 2^25 on past
         // a type's range.  Past 2^10 the scores' differences are taken first (2304 rows x 19989 keys x 56 heads: without
@@ -793,7 +793,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
         const bool large = fabsf(zero * p.scale_log2) > 1024.f;
         if (__any_sync(0xffffffffu, large)) {
           const float2 less = make_float2(large ? -zero : 0.f, large ? -zero : 0.f);
-          if (large) ref = kLift<DT>;
+          if (large) ref = kLift<DT, LONG>;
 #pragma unroll
           for (int j = 0; j < KEYS; j += 2) {
             const float2 d = add2(make_float2(x[j], x[j + 1]), less);

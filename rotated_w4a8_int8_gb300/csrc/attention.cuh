@@ -63,14 +63,16 @@ __device__ __forceinline__ float exp2_approx(float x) {
   return y;
 }
 
-// Weights are held in the operands' type for the second product, as powers of
-// two around the running maximum: at most 2^kLag above it (the maximum is only
-// followed once it has grown by more).  FP16's narrow range gets them 2^6 higher
-// (at most 2^14), which puts its subnormals below 2^-20 of the largest weight;
-// the factor leaves with the sum.
-constexpr float kLag = 8.f;
-template <int DT>
-constexpr float kLift = DT == CONVROT_FP16 ? 6.f : 0.f;
+// Weights are held in the operands' type for the second product, as powers of two around the running maximum: at most
+// 2^kLag above it (the maximum is only followed once it has grown by more).  FP16's narrow range gets them 2^kLift higher:
+// its subnormals are steps of 2^-24, so a key's weight is off by up to 2^-(25 + kLift) of the largest one, and many light
+// keys by as much each.  Few keys (many rows of at most kKeepKeys): 2^6 higher and 2^8 above the maximum, 2^-16 for all
+// 2^15 of them.  MANY: 2^12 and 2^3 (at most 2^15), 2^-11 for 2^26 keys where that would be 3%; the maximum is followed
+// more often, which costs many rows 1 to 6% (most where keys are few) and few rows up to 3%.  The factor leaves with the sum.
+template <int DT, bool MANY>
+constexpr float kLag = DT == CONVROT_FP16 && MANY ? 3.f : 8.f;
+template <int DT, bool MANY>
+constexpr float kLift = DT == CONVROT_FP16 ? MANY ? 12.f : 6.f : 0.f;
 
 // Keys after which a row's output leaves the tensor core's accumulators for FP32 sums of its own, rounded to nearest.
 // The accumulators are cut towards zero, as measured by 2^-27 of the sum for every key that they take (equal weights of

@@ -83,7 +83,7 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uin
 }
 
 // A weight as two values of the type: cut off (towards zero) a little below it, and what that leaves, neither of which
-// then rounds to zero (FP16: from 2^-23 on, 2^-29 of the largest weight), so that an infinite value times both is the same
+// then rounds to zero (FP16: from 2^-23 on, 2^-35 of the largest weight), so that an infinite value times both is the same
 // infinity.  The first takes 2^-12 (BF16: 2^-9) of the weight less, FP16 at least a subnormal step.
 template <int DT>
 __device__ __forceinline__ uint32_t truncate2(float lo, float hi) {
@@ -356,7 +356,7 @@ few_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CU
               }
             }
 #pragma unroll
-            for (int e = 0; e < 2; ++e) grown |= (fmaxf(x[j][0][e], x[j][0][2 + e]) - m[j][e]) * p.scale_log2 > kLag;
+            for (int e = 0; e < 2; ++e) grown |= (fmaxf(x[j][0][e], x[j][0][2 + e]) - m[j][e]) * p.scale_log2 > kLag<DT, true>;
           }
           if (__any_sync(0xffffffffu, grown)) {
 #pragma unroll
@@ -385,7 +385,7 @@ few_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CU
             for (int i = 0; i < 4; ++i) {
               const float r = m[j][i & 1];
               // (the difference first: a rounded product of r would be past the types' range with scores of 2^25 and more)
-              e[i] = exp2_approx(fmaf(x[j][0][i] - (r == -INFINITY ? 0.f : r), p.scale_log2, kLift<DT>));
+              e[i] = exp2_approx(fmaf(x[j][0][i] - (r == -INFINITY ? 0.f : r), p.scale_log2, kLift<DT, true>));
             }
             l[j][0] += e[0] + e[2];
             l[j][1] += e[1] + e[3];

@@ -154,3 +154,23 @@ def test_captured_and_at_once(rows, dtype, keys):
             graph.replay()
     torch.cuda.synchronize()
     assert cr.device_error() == 0 and all(torch.equal(a, b) for a, b in zip(want, out))
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+@pytest.mark.parametrize("light", [28.5, 29.51, 31.2])
+def test_many_light_keys(kernel, light):
+    """2^22 keys, each of 2^-light of the weight of the first, whose value is zero, in FP16: steps of its subnormals are
+    2^-24, the largest weight is at least 2^12, so a key's weight is off by at most 2^-37.  (The exponent: one product, FP32,
+    of up to 32.)"""
+    import rotated_w4a8_int8_gb300 as cr
+    q = torch.ones(20, 1, 64, dtype=HF, device=DEV)
+    k, v = torch.zeros(N, 1, 64, dtype=HF, device=DEV), torch.ones(N, 1, 64, dtype=HF, device=DEV)
+    k[1:, 0, 0] = -1.0
+    v[0] = 0.0
+    scale = float(torch.tensor(light * math.log(2), dtype=torch.float32))
+    out = torch.empty_like(q)
+    cr.attention_selftest(q, k, v, out, *kernel, scale=scale)
+    torch.cuda.synchronize()
+    mass = (N - 1) * math.exp(-scale)
+    want = mass / (1 + mass)
+    assert float((out.double() - want).abs().max()) <= (N - 1) * 2.0 ** -37 + want * (3 * torch.finfo(HF).eps / 2 + 2.0 ** -18)
