@@ -723,6 +723,16 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
       const int whole = it.limit(SPLIT ? 0 : slot * w.tps, p.causal) / KEYS;
       float m = -INFINITY, l0 = 0.f, l1 = 0.f;             // reference and sum (in two parts) of this row
       const bool any = t0 < t1;
+      // Rows of the tile that are not the item's (another sequence's, or none's) have no say in its warps' votes: their lanes
+      // are masked out, with heads of up to 64 columns their growth is multiplied by zero.  (Paged chunks of heads of 64 take
+      // up to 8% longer with the mask, 1 to 3% with the factor; wider ones 0.8% with the factor, with the mask none.)
+      const bool votes = held && my_token < it.tokens;
+      const unsigned voters = __ballot_sync(0xffffffffu, votes);
+      const float growth = votes ? p.scale_log2 : 0.f;
+      auto grown = [&](float by) {
+        if constexpr (KK > 4) return (__ballot_sync(0xffffffffu, by * p.scale_log2 > kLag<DT, LONG>) & voters) != 0;
+        return __any_sync(0xffffffffu, by * growth > kLag<DT, LONG>) != 0;
+      };
       constexpr int KEEP = kKeepKeys<DT> / KEYS * step, COLUMNS = (KK + 1) / 2;      // tiles; O in 32 columns
       Kept<LONG ? DP : 1> kept;
       for (int t = t0; t < t1; t += step) {
@@ -768,7 +778,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
         const float now = fmaxf(fmaxf(m, fmaxf(top[0], top[1])), fmaxf(top[2], top[3]));
         if (t == t0) {
           m = now;                                        // nothing summed yet
-        } else if (__any_sync(0xffffffffu, (now - m) * p.scale_log2 > kLag<DT, LONG>)) {
+        } else if (grown(now - m)) {
           const float f = now == m ? 1.f : exp2_approx((m - now) * p.scale_log2);
           m = now;
           l0 *= f;
@@ -785,12 +795,13 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
         }
         // a row that has seen no key yet keeps -inf, its weights are exp2(-inf) = 0
         const float zero = m == -INFINITY ? 0.f : m;
-        float ref = kLift<DT, LONG> - zero * p.scale_log2;
+        const float scaled = __fmul_rn(zero, p.scale_log2);
+        float ref = __fsub_rn(kLift<DT, LONG>, scaled);      // (never fused: the same on either path below)
         // This product's rounding moves all weights that are taken from this reference by one factor, 2 to the 2^-25th of it:
         // below 2^10 by at most 2^-15.5, which parts of a row with other references do not share; from some 2^25 on past
         // a type's range.  Past 2^10 the scores' differences are taken first (2304 rows x 19989 keys x 56 heads: without
         // this 802 us, with the vote 808, differences in all rows 821).
-        const bool large = fabsf(zero * p.scale_log2) > 1024.f;
+        const bool large = fabsf(scaled) > 1024.f;
         if (__any_sync(0xffffffffu, large)) {
           const float2 less = make_float2(large ? -zero : 0.f, large ? -zero : 0.f);
           if (large) ref = kLift<DT, LONG>;
@@ -843,7 +854,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
         }
       }
       const float l = l0 + l1;
-      const bool mine = ok && it.q_row >= 0 && held && my_token < it.tokens;
+      const bool mine = ok && it.q_row >= 0 && votes;
       char* const out_row = static_cast<char*>(p.out) +
                             2 * ((static_cast<int64_t>(it.q_row) + my_token) * p.out_tok + (it.head0 + my_head) * p.out_head);
       if constexpr (!SPLIT) {

@@ -190,6 +190,26 @@ def test_many_sequences(kernel):
     check(out, *reference(q, k, v, seqs, 0.125, True, out))
 
 
+@pytest.mark.parametrize("kernel", EACH)
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("heads_q", [2, 6])
+def test_rows_behind_a_sequence_have_no_say(kernel, dtype, heads_q):
+    """The same bits whatever the next sequence's rows, and rows in no sequence, hold: they lie in the same tiles."""
+    import rotated_w4a8_int8_gb300 as cr
+    q, k, v = rand(300, heads_q, 64, dtype=dtype), rand(900, 2, 64, seed=1, dtype=dtype), rand(900, 2, 64, seed=2, dtype=dtype)
+    k = (k * torch.linspace(0.5, 1.5, 900, device=DEV)[:, None, None]).to(dtype)
+    seqs, outs = [(0, 21, 0, 600), (21, 137, 600, 300), (170, 100, 0, 900)], []
+    for factor in (1.0, 30.0, -1000.0, math.inf, math.nan):
+        x = q.clone()
+        for a, n in ((21, 137), (158, 12), (270, 30)):
+            x[a:a + n] *= factor
+        out = torch.zeros_like(q)
+        cr.attention_selftest(x, k, v, out, *kernel, seqs=i32(seqs))
+        outs.append(torch.cat([out[:21], out[170:270]]))
+    torch.cuda.synchronize()
+    assert cr.device_error() == 0 and bool(torch.isfinite(outs[0]).all()) and all(torch.equal(outs[0], o) for o in outs)
+
+
 @pytest.mark.parametrize("kernel", [(1, 1), (1, 2), (2, 1), (3, 2), None])
 def test_most_sequences(kernel):
     """As many sequences as a call takes, their rows in no order: a page each, written and attended to."""
