@@ -404,6 +404,8 @@ int convrot_gemm_fused_selftest(const void* a_q, int64_t ld_aq,
  * 2^-29 of the row's largest, in BF16 2^-100, else maybe as NaN), a NaN or +Inf
  * among a row's scores in that row, and a row whose scores are all -Inf becomes
  * NaN; with `causal` one in v may also show in earlier rows of the same sequence.
+ * The sum of p v before its division, the largest weight of a row between 1 and
+ * 2^8 (BF16), has to stay within FP32's range: values below 2^94 always do.
  * Lengths being on the device, the kernel is chosen for rows / B rows and an
  * equal share of the keys per sequence; other lengths cost time, no more.  The result does
  * not depend on other sequences of the call, nor on the run; it may change in

@@ -34,14 +34,15 @@
 // for the maximum, 930 for the weights) and its products (PV's second half and
 // QK, 1000 to 1200 with the hand-overs); the two slots' steps overlap, 2700
 // clocks for both where the products alone take 2048.  19989 rows x 19989 keys x
-// 56 heads of 128 in BF16: 6.2 to 6.5 ms, 1760 to 1840 TFLOP/s, the power cap in
-// it (cuBLAS sustains 1734); narrower heads are bound by the rows' turns (64: 15%
-// faster than 128).  Tried against it, and slower: two threads a row (5 to 8%), a
-// products' warp for each slot (3 to 14%: the slots' products then delay each
-// other), parts of 64 keys turned while the next part's scores are computed (13%),
-// the next item's scores before this one's outputs (2 to 10%).  Few keys: an item's start and end take 2 to 3 us beside its
-// tiles, about the time of reading its Q and writing its rows (19989 x 512: 205
-// us, 1430 TFLOP/s).
+// 56 heads of 128 in BF16: 6.7 ms, 1710 TFLOP/s, with inputs that change from call
+// to call (6.5 ms over one set), the power cap in it (cuBLAS sustains 1734);
+// narrower heads are bound by the rows' turns (64: 15% faster than 128).  Tried
+// against it, and slower: two threads a row (5 to 8%), a products' warp for each
+// slot (3 to 14%: the slots' products then delay each other), parts of 64 keys
+// turned while the next part's scores are computed (13%), the next item's scores
+// before this one's outputs (2 to 10%).  Few keys: an item's start and end take 2
+// to 3 us beside its tiles, about the time of reading its Q and writing its rows
+// (19989 x 512: 220 us, 1330 TFLOP/s; 209 us over one set of inputs).
 #include <atomic>
 #include <cmath>
 #include <cstdint>
@@ -797,10 +798,10 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
         const float zero = m == -INFINITY ? 0.f : m;
         const float scaled = __fmul_rn(zero, p.scale_log2);
         float ref = __fsub_rn(kLift<DT, LONG>, scaled);      // (never fused: the same on either path below)
-        // This product's rounding moves all weights that are taken from this reference by one factor, 2 to the 2^-25th of it:
-        // below 2^10 by at most 2^-15.5, which parts of a row with other references do not share; from some 2^25 on past
-        // a type's range.  Past 2^10 the scores' differences are taken first (2304 rows x 19989 keys x 56 heads: without
-        // this 802 us, with the vote 808, differences in all rows 821).
+        // Its two roundings move all weights that are taken from this reference by one factor, 2 to the 2^-24th of it: below
+        // 2^10 by at most 2^-14.5, which parts of a row with other references do not share; from some 2^25 on past
+        // a type's range.  Past 2^10 the scores' differences are taken first (2304 rows x 19989 keys x 56 heads, one set of
+        // inputs: without this 802 us, with the vote 808, differences in all rows 821).
         const bool large = fabsf(scaled) > 1024.f;
         if (__any_sync(0xffffffffu, large)) {
           const float2 less = make_float2(large ? -zero : 0.f, large ? -zero : 0.f);
@@ -1098,7 +1099,7 @@ static int choose(const Problem& p, const Variant& variant, cudaStream_t st) {
   const int64_t items = most_items(p, best.item_tokens) * (p.heads_q / best.pack);
   if (slices) return launch<DT, KK, PAGED, true, LONG>(p, best, slices, items, st);
   // Whole items in full rounds, and a last round that is not: its items by clusters that share keys, in a launch of their
-  // own, where that is sooner done.  (2304 rows x 19989 keys x 56 heads, 3.3 rounds: 838 -> 806 us.)
+  // own, where that is sooner done.  (2304 rows x 19989 keys x 56 heads, 3.3 rounds, one set of inputs: 838 -> 806 us.)
   int sms = 0, tail_slices = 0;
   cudaError_t e = resident_clusters<DT, KK, PAGED, false, LONG>(1, &sms);
   if (e != cudaSuccess) return convrot::record_cuda_error("attention set-up", e);

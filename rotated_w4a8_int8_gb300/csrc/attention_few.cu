@@ -15,16 +15,17 @@
 // is read by ldmatrix, V's by its transposing form, and P^T comes from S^T by an
 // 8 x 8 transposition in registers.  Softmax as in attention.cu: a reference per
 // row that follows the maximum once it has grown by 2^kLag, FP32 sums, which O too
-// moves to after kKeepKeys keys of a warp.  The weights
-// go into the product as two values of the operands' type, cut off and what that
-// left: the bytes bound this kernel, and a second product costs nothing that shows
-// (one token: 83.6 and 83.2 us), while one row's error grew by half with one.
+// moves to after kKeepKeys keys of a warp.  The weights go into the product as two
+// values of the operands' type, cut off and what that left: the bytes bound this
+// kernel, and a second product costs nothing that shows (one token: 83.6 and 83.2
+// us), while one row's error grew by half with one.
 //
-// 19989 keys x 56 heads of 128, one token, BF16, pages of 64: 83 us (6.9 TB/s,
-// 103% of the copy bandwidth); 64 tokens over up to 8191 keys, 32 heads on 8: 213
-// us (6.4 TB/s).  Before, every warp loaded its blocks of 16 keys into registers
-// one ahead: 100 and 256 us, and 45 us where this takes 20 (2 K heads of 32768
-// keys: few CTAs, and a block took the memory's latency twice).
+// 19989 keys x 56 heads of 128, one token, BF16, pages of 64: 84.5 us (6.8 TB/s,
+// 101% of the copy bandwidth); 64 tokens over up to 8191 keys, 32 heads on 8: 219
+// us (6.3 TB/s), both with inputs that change from call to call.  Before, every
+// warp loaded its blocks of 16 keys into registers one ahead: 100 and 256 us, and
+// 45 us where this takes 20 (2 K heads of 32768 keys: few CTAs, and a block took
+// the memory's latency twice).
 #include <atomic>
 #include <cstdint>
 #include <cuda.h>
