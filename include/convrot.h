@@ -460,8 +460,8 @@ int convrot_paged_attention(const void* q, int64_t q_row, int64_t q_head,
  *
  *   k, v    [rows][heads_k][D] in `dtype` (BF16 or FP16), row and head strides
  *           in elements (views of the packed qkv output).
- *   k_cache, v_cache, pages, seqs   as above; the caches overlap no input, their
- *           heads, rows and pages do not overlap, and no two tokens of a call go
+ *   k_cache, v_cache, pages, seqs   as above; the caches overlap no input and
+ *           not each other, their heads, rows and pages do not overlap, and no two tokens of a call go
  *           to the same place (a page that is written belongs to one sequence).
  *           A token whose page entry names no page is left out and reported by
  *           convrot_device_error, as is a sequence with q_len > k_len.

@@ -115,6 +115,8 @@ extern "C" int convrot_cache_write(const void* k, int64_t k_row, int64_t k_head,
   }
   if (!seqs) return CONVROT_ERR_INVALID_ARG;
   if (reinterpret_cast<uintptr_t>(seqs) % 16) return CONVROT_ERR_MISALIGNED;
+  if (num_pages > 0 && (k_cache == v_cache || k_cache == k || k_cache == v || v_cache == k || v_cache == v))
+    return CONVROT_ERR_INVALID_ARG;              // written twice, or read while it is written
   Write w = {};
   w.k = static_cast<const char*>(k);
   w.v = static_cast<const char*>(v);

@@ -93,6 +93,17 @@ def test_paged_arguments(fn):
         assert call(kp=1024) == 1 and call(vr=64) == 1        # what is written does not overlap
 
 
+def test_caches_are_written_once():
+    """The same memory as both caches, or as a cache and an input, is refused."""
+    lib, at = cr.load_library(), [P * n for n in (1, 2, 3, 4)]
+
+    def call(k, v, kc, vc):
+        return lib.convrot_cache_write(k, 512, 64, v, 512, 64, kc, 2048, 128, 64, vc, 2048, 128, 64, 0, 4, 2, 64, 9, 16, P, 5, 5,
+                                       P, 3, None)
+    for same in ((0, 1, 2, 2), (0, 1, 0, 2), (0, 1, 1, 2), (0, 1, 2, 0), (0, 1, 2, 1)):
+        assert call(*(at[i] for i in same)) == 1
+
+
 def test_selftest_arguments():
     lib = cr.load_library()
 
